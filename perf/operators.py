@@ -102,7 +102,7 @@ def _lengths(case, seed):
 def _quantise(x):
     """x [pages, tokens, heads, D] as e4m3 with the least power-of-two scale a page and head under which it fits."""
     m, e = torch.frexp(x.abs().amax(dim=(1, 3)))
-    e = torch.where(m > 0.875, e - 8, e - 9).clamp(MIN_EXP, MAX_EXP)
+    e = torch.where(m > 0.875, e - 8, e - 9).masked_fill(m == 0, MIN_EXP).clamp(MIN_EXP, MAX_EXP)
     scale = torch.ldexp(torch.ones_like(m), e)
     return (x / scale[:, None, :, None]).clamp(-448, 448).to(E4M3), scale
 
@@ -249,7 +249,8 @@ def _append(s):
         p, begin = page[first], row[first]
         most = torch.zeros_like(scale).index_reduce_(0, page, x.abs().amax(-1), "amax")[p]
         m, e = torch.frexp(most)
-        need = torch.ldexp(torch.ones_like(m), torch.where(m > 0.875, e - 8, e - 9).clamp(MIN_EXP, MAX_EXP))
+        e = torch.where(m > 0.875, e - 8, e - 9).masked_fill(m == 0, MIN_EXP).clamp(MIN_EXP, MAX_EXP)
+        need = torch.ldexp(torch.ones_like(m), e)
         old = torch.where((begin > 0)[:, None], scale[p], need)
         now = torch.maximum(old, need)
         scale[p] = now
