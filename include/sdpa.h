@@ -334,6 +334,137 @@ SDPA_API sdpa_status sdpa_sparse_compact(const int32_t* idx_local, int64_t idx_l
                                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
                                          int64_t n_docs, int is_causal, void* stream);
 
+/*
+ * Paged key/value caches.  The pages' text has no counterpart: these are the
+ * operators that a program needs to answer with a model token by token, next
+ * to the forwards above.  A cache is a pool of pages of page_size tokens; a
+ * sequence's tokens [i * page_size, ...) lie in page table[i], in any order
+ * and shared between sequences at will.  sdpa_cache_append writes new tokens'
+ * keys and values, sdpa_paged_forward attends to them.
+ *
+ * k, v         : DEVICE [n_pages, page_size, n_kv_heads, head_dim], strides in
+ *                ELEMENTS for (page, token, head); the last stride is 1, the
+ *                others are multiples of 16 bytes.  16-byte aligned.
+ * elem         : SDPA_CACHE_BF16, SDPA_CACHE_FP16 (the type of the tokens and
+ *                queries used with it), or SDPA_CACHE_E4M3: 8-bit codes, used
+ *                with tokens and queries of either 16-bit type.
+ * k_scale,
+ * v_scale      : SDPA_CACHE_E4M3: DEVICE fp32 [n_pages, n_kv_heads]; the
+ *                values are code * scale.  Scales are positive, in [2^-50,
+ *                2^50]; others are taken as the nearest of these (0 and NaN as
+ *                the least).  NULL for 16-bit caches.
+ * page_size    : 16, 32, 64, 128, 256, 512 or 1024.
+ * head_dim     : 64 or 128.
+ */
+typedef enum sdpa_cache_elem {
+  SDPA_CACHE_BF16 = 0,
+  SDPA_CACHE_FP16 = 1,
+  SDPA_CACHE_E4M3 = 2
+} sdpa_cache_elem;
+
+typedef struct sdpa_paged_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t n_pages, page_size, n_kv_heads, head_dim;
+  int64_t k_stride[3], v_stride[3];
+  int32_t elem;
+} sdpa_paged_cache;
+
+/*
+ * sdpa_cache_append -- write new tokens' keys and values into a paged cache,
+ * the keys rotated by their positions on the way, and the queries of the same
+ * tokens if they are given.  One kernel launch, asynchronous on `stream`.
+ *
+ * k, v         : DEVICE [total, n_kv_heads, head_dim] of `dtype`; 2 strides in
+ *                ELEMENTS (token, head), multiples of 8.  Sequence b's new
+ *                tokens are rows [cu_seqlens[b], cu_seqlens[b+1]).
+ * cu_seqlens   : DEVICE int32 [n_seqs + 1], nondecreasing, or NULL: every
+ *                sequence has total / n_seqs new tokens (which must divide).
+ * kv_lens      : DEVICE int32 [n_seqs], the sequences' lengths WITH the new
+ *                tokens: token i of n has position kv_lens[b] - n + i.
+ * page_table   : DEVICE int32 [n_seqs, max_pages], row stride
+ *                page_table_stride >= max_pages.  No two sequences may append
+ *                to one page.
+ * cos, sin     : both NULL (no rotation), or DEVICE fp32 [n_pos, rot_dim / 2]
+ *                contiguous, 16-byte aligned: entry (pos, j) turns pair j of
+ *                every key (and query) head: (x1, x2) -> (x1 cos - x2 sin,
+ *                x2 cos + x1 sin).  rot_dim: a multiple of 8 up to head_dim;
+ *                later elements are left as they are.  Pair j is elements
+ *                (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved != 0.
+ * q, q_out     : both NULL, or DEVICE [total, n_heads, head_dim] of `dtype`
+ *                (2 strides each): q_out receives the rotated queries.  q_out
+ *                may be q with q's strides (in place).
+ *
+ * A token whose position is negative or not below max_pages * page_size or
+ * n_pos is left out: none of its rows is written.  A page entry outside [0,
+ * n_pages) leaves the token's key and value out.  Rows of tokens beyond the
+ * last sequence are not touched.
+ *
+ * 16-bit caches: the rotated key is rounded once.  SDPA_CACHE_E4M3: the scale
+ * of a (page, head) is the least power of two, in range, under which every
+ * finite value appended to it so far fits into +-448; a page's first token
+ * (row 0) starts it anew.  When it grows, the page's earlier codes are
+ * multiplied by old / new in place (exact but for codes below the type's
+ * least normal).  Values beyond the range become +-448, NaN stays NaN.
+ *
+ * Errors: NULL; DTYPE (elem of a 16-bit cache is not dtype); SHAPE (an extent
+ * < 1 or too large, page_size, head_dim, rot_dim, total not divisible);
+ * LAYOUT; ARG (an output overlaps an input or the cache); CUDA; DEVICE.
+ */
+SDPA_API sdpa_status sdpa_cache_append(
+    const sdpa_paged_cache* cache, const void* k, const void* v, sdpa_dtype dtype, int64_t total,
+    const int64_t* k_stride, const int64_t* v_stride, const int32_t* page_table,
+    int64_t page_table_stride, int64_t max_pages, const int32_t* kv_lens,
+    const int32_t* cu_seqlens, int64_t n_seqs, const float* cos, const float* sin, int64_t n_pos,
+    int64_t rot_dim, int interleaved, const void* q, void* q_out, int64_t n_heads,
+    const int64_t* q_stride, const int64_t* q_out_stride, void* stream);
+
+/*
+ * sdpa_paged_forward -- attention of each sequence's new tokens over its pages.
+ *
+ * q, out       : DEVICE [total_q, n_heads, head_dim] of `dtype`; 2 strides in
+ *                ELEMENTS (token, head), multiples of 8.  n_heads is a
+ *                multiple of the cache's n_kv_heads; query head h reads
+ *                key/value head h / (n_heads / n_kv_heads).
+ * cu_seqlens_q : DEVICE int32 [n_seqs + 1] (rows of q of each sequence,
+ *                nondecreasing), or NULL: total_q / n_seqs rows each.
+ * kv_lens      : DEVICE int32 [n_seqs], cached tokens of each sequence (the
+ *                new ones among them), clamped to [0, max_pages * page_size].
+ * is_causal    : nonzero: row i of n sees keys j <= kv_lens[b] - n + i, i.e.
+ *                the new tokens are the sequence's last ones; zero: all keys.
+ * lse          : NULL or DEVICE fp32 [total_q, n_heads] (2 strides).
+ * max_seqlen_q : an upper bound on the sequences' rows, used to choose a
+ *                kernel; a smaller value costs time, never results.
+ * scale        : multiplier of q.k; NaN selects 1/sqrt(head_dim).
+ * workspace    : DEVICE scratch, 16-byte aligned, of at least
+ *                sdpa_paged_workspace_bytes(...) bytes, whatever it holds.
+ *                Calls that may run at the same time need one each.
+ *
+ * A row that sees no key gives zeros and lse = -inf; rows of q outside every
+ * sequence are not written.  A page entry outside [0, n_pages) removes its
+ * tokens' keys.  What pages hold beyond a sequence's length is not used (it
+ * may be anything, NaN too).  Products on tensor cores with fp32 sums, softmax
+ * in fp32; each key's weight, times its value's scale, is rounded to 16 bits
+ * (bf16 for a bf16 cache, else fp16) before the second product.  Results do
+ * not depend on timing.  Asynchronous on `stream`.  Errors as above, and ARG
+ * for an infinite scale or too small a workspace.
+ */
+SDPA_API sdpa_status sdpa_paged_forward(
+    const void* q, void* out, float* lse, sdpa_dtype dtype, const sdpa_paged_cache* cache,
+    int64_t total_q, int64_t n_heads, const int64_t* q_stride, const int64_t* o_stride,
+    const int64_t* lse_stride, const int32_t* page_table, int64_t page_table_stride,
+    int64_t max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens_q, int64_t n_seqs,
+    int64_t max_seqlen_q, int is_causal, float scale, void* workspace, uint64_t workspace_bytes,
+    void* stream);
+
+/* Bytes of workspace that sdpa_paged_forward needs on the current device (a
+ * bound that depends on the device and these arguments alone, not on lengths
+ * or batch); 0 when there is no sm_103 device or an argument is out of range. */
+SDPA_API uint64_t sdpa_paged_workspace_bytes(int64_t head_dim, int64_t n_heads,
+                                             int64_t n_kv_heads, int64_t max_seqlen_q);
+
 /* Adds (lse != NULL) or removes (lse == NULL) the log-sum-exp output of a
  * plan; same layout rules as sdpa_forward_lse. */
 SDPA_API sdpa_status sdpa_plan_set_lse(sdpa_plan* plan, float* lse, const int64_t* lse_stride);

@@ -22,7 +22,7 @@ __all__ = ["sdpa_forward", "sdpa_forward_raw", "sdpa_status_string", "sdpa_last_
            "sdpa_debug_set_wait_limit_ns", "sdpa_debug_withhold_q_load",
            "sdpa_forward_varlen", "sdpa_sparse_forward", "sdpa_sparse_compact", "SdpaPlan",
            "sdpa_mask_tiles", "sdpa_forward_masked_noalloc", "head_range",
-           "sdpa_forward_heads"]
+           "sdpa_forward_heads", "SdpaPagedCache", "sdpa_cache_append", "sdpa_paged_forward"]
 
 LIB_PATH = _build.LIB_PATH
 
@@ -32,12 +32,21 @@ STATUS = {
     8: "SDPA_ERR_DEVICE_TIMEOUT", 9: "SDPA_ERR_DEVICE",
 }
 SDPA_BF16, SDPA_FP16 = 0, 1
+SDPA_CACHE_E4M3 = 2
 
 
 class SdpaError(RuntimeError):
     def __init__(self, status: int, where: str = "sdpa_forward"):
         self.status = int(status)
         super().__init__(f"{where}: {sdpa_status_string(status)} (status {status})")
+
+
+class _PagedCacheStruct(ctypes.Structure):
+    """sdpa_paged_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("elem", ctypes.c_int32)]
 
 
 _lib = None
@@ -105,6 +114,15 @@ def load_library(path: str | None = None):
     lib.sdpa_forward_masked_noalloc.argtypes = [vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, i64p,
                                                 i64p, i64p, i64p, i64p, vp, ctypes.c_float, vp]
     lib.sdpa_forward_masked_noalloc.restype = ctypes.c_int
+    i64, cp = ctypes.c_int64, ctypes.POINTER(_PagedCacheStruct)
+    lib.sdpa_cache_append.argtypes = [cp, vp, vp, ctypes.c_int, i64, i64p, i64p, vp, i64, i64, vp, vp, i64, vp, vp,
+                                      i64, i64, ctypes.c_int, vp, vp, i64, i64p, i64p, vp]
+    lib.sdpa_cache_append.restype = ctypes.c_int
+    lib.sdpa_paged_forward.argtypes = [vp, vp, vp, ctypes.c_int, cp, i64, i64, i64p, i64p, i64p, vp, i64, i64, vp, vp,
+                                       i64, i64, ctypes.c_int, ctypes.c_float, vp, ctypes.c_uint64, vp]
+    lib.sdpa_paged_forward.restype = ctypes.c_int
+    lib.sdpa_paged_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.sdpa_paged_workspace_bytes.restype = ctypes.c_uint64
     if path is None:
         _lib = lib
     return lib
@@ -450,6 +468,211 @@ class SdpaPlan:
             self.close()
         except Exception:  # pragma: no cover - interpreter shutdown
             pass
+
+
+class SdpaPagedCache:
+    """A paged key/value cache (sdpa_paged_cache): ``k`` and ``v`` are the
+    caller's tensors [n_pages, page_size, n_kv_heads, head_dim], bf16, fp16 or
+    float8_e4m3fn, any strides with the last one 1 (multiples of 16 bytes);
+    an 8-bit cache also has ``k_scale`` and ``v_scale``, contiguous fp32
+    [n_pages, n_kv_heads] (values are code * scale).  The handle keeps the
+    tensors and describes them once for sdpa_cache_append and
+    sdpa_paged_forward; it owns no device memory of its own."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+
+        elem = {torch.bfloat16: SDPA_BF16, torch.float16: SDPA_FP16, torch.float8_e4m3fn: SDPA_CACHE_E4M3}.get(k.dtype)
+        if elem is None or v.dtype != k.dtype:
+            raise SdpaError(4, "SdpaPagedCache")
+        if k.dim() != 4 or k.shape != v.shape or min(k.shape) < 1:
+            raise SdpaError(3, "SdpaPagedCache")
+        if k.stride(3) != 1 or v.stride(3) != 1:
+            raise SdpaError(5, "SdpaPagedCache")
+        n_pages, page_size, n_kv, dim = k.shape
+        if dim not in (64, 128) or page_size not in (16, 32, 64, 128, 256, 512, 1024):
+            raise SdpaError(3, "SdpaPagedCache")
+        scales = (k_scale, v_scale)
+        if elem == SDPA_CACHE_E4M3:
+            if k_scale is None or v_scale is None:
+                raise SdpaError(1, "SdpaPagedCache")
+            for s in scales:
+                if s.dtype != torch.float32:
+                    raise SdpaError(4, "SdpaPagedCache")
+                if tuple(s.shape) != (n_pages, n_kv):
+                    raise SdpaError(3, "SdpaPagedCache")
+                if not s.is_contiguous():
+                    raise SdpaError(5, "SdpaPagedCache")
+        elif k_scale is not None or v_scale is not None:
+            raise SdpaError(6, "SdpaPagedCache")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.elem, self.device = elem, k.get_device()
+        if any(t is not None and t.get_device() != self.device for t in (v, k_scale, v_scale)):
+            raise SdpaError(6, "SdpaPagedCache")
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv, dim
+        ptr = [t.data_ptr() if t is not None else None for t in (k, v, k_scale, v_scale)]
+        self._struct = _PagedCacheStruct(*ptr, n_pages, page_size, n_kv, dim, k.stride()[:3], v.stride()[:3], elem)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, rows):
+    """Checks what append and forward share; (n_seqs, max_pages, int type code)."""
+    import torch
+
+    i32 = torch.int32
+    if page_table.dtype != i32 or kv_lens.dtype != i32 or (cu_seqlens is not None and cu_seqlens.dtype != i32):
+        raise SdpaError(4, where)
+    n_seqs = kv_lens.numel()
+    if kv_lens.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != n_seqs or \
+            (cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() != n_seqs + 1)):
+        raise SdpaError(3, where)
+    if not kv_lens.is_contiguous() or page_table.stride(1) != 1 or \
+            (cu_seqlens is not None and not cu_seqlens.is_contiguous()):
+        raise SdpaError(5, where)
+    dt = _dtype_code(rows)
+    if cache.elem not in (dt, SDPA_CACHE_E4M3):
+        raise SdpaError(4, where)
+    return n_seqs, page_table.shape[1], dt
+
+
+def _two_strides(t, where):
+    st = t.stride()
+    if st[2] != 1:
+        raise SdpaError(5, where)
+    return (ctypes.c_int64 * 2)(st[0], st[1])
+
+
+def _same_device(device, where, *tensors):
+    """All tensors on the cache's CUDA device (a host pointer would fault)."""
+    if device < 0:
+        raise SdpaError(6, where)
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise SdpaError(6, where)
+
+
+def _on_device(device, stream, call):
+    """call(stream handle) with ``device`` current, memory that it allocates
+    belonging to the stream it launches on."""
+    import torch
+
+    if stream is not None:
+        if stream.device_index != device:
+            raise SdpaError(6)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream(device).cuda_stream)
+    return call(torch.cuda.current_stream(device).cuda_stream)
+
+
+def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=None, sin=None,
+                      interleaved: bool = False, q=None, q_out=None, stream=None):
+    """Append new tokens' keys and values to a paged cache (sdpa_cache_append).
+
+    k, v: [total, n_kv_heads, head_dim] bf16/fp16, the sequences' new tokens
+    one after another; cu_seqlens: int32 [n_seqs + 1] row offsets (None: the
+    same number for each sequence); kv_lens: int32 [n_seqs] lengths with the
+    new tokens; page_table: int32 [n_seqs, max_pages].  cos, sin: fp32 [n_pos,
+    rot_dim / 2] rotation tables (None: no rotation), pairs (j, j + rot_dim /
+    2), or neighbours when ``interleaved``.  q: the tokens' queries [total,
+    n_heads, head_dim], rotated too, into ``q_out`` (allocated if None; may be
+    ``q``).  Returns ``q_out`` (None without q)."""
+    import torch
+
+    where = "sdpa_cache_append"
+    n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, k)
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype) or (q_out is not None and q_out.dtype != k.dtype):
+        raise SdpaError(4, where)
+    total = k.shape[0]
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1] != cache.n_kv_heads or k.shape[2] != cache.head_dim:
+        raise SdpaError(3, where)
+    if (cos is None) != (sin is None) or (q is None and q_out is not None):
+        raise SdpaError(1, where)
+    if q is not None and (q.dim() != 3 or q.shape[0] != total or q.shape[2] != cache.head_dim or
+                          (q_out is not None and q_out.shape != q.shape)):
+        raise SdpaError(3, where)
+    n_pos = rot = 0
+    if cos is not None:
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32:
+            raise SdpaError(4, where)
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise SdpaError(3, where)
+        if not cos.is_contiguous() or not sin.is_contiguous():
+            raise SdpaError(5, where)
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    ks, vs = _two_strides(k, where), _two_strides(v, where)
+    _same_device(cache.device, where, k, v, page_table, kv_lens, cu_seqlens, cos, sin, q, q_out)
+
+    def call(st):
+        qo = torch.empty_like(q, memory_format=torch.contiguous_format) if q is not None and q_out is None else q_out
+        rc = load_library().sdpa_cache_append(
+            cache._ref, k.data_ptr(), v.data_ptr(), dt, total, ks, vs, page_table.data_ptr(), page_table.stride(0),
+            max_pages, kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None, n_seqs,
+            cos.data_ptr() if cos is not None else None, sin.data_ptr() if sin is not None else None, n_pos, rot,
+            1 if interleaved else 0, q.data_ptr() if q is not None else None,
+            qo.data_ptr() if q is not None else None, q.shape[1] if q is not None else 0,
+            _two_strides(q, where) if q is not None else None, _two_strides(qo, where) if q is not None else None, st)
+        if rc != 0:
+            raise SdpaError(rc, where)
+        return qo
+
+    return _on_device(cache.device, stream, call)
+
+
+def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seqlen_q=None, out=None, *,
+                       is_causal: bool = False, scale=None, stream=None, return_lse: bool = False, lse=None):
+    """Attention of new tokens over a paged cache (sdpa_paged_forward).
+
+    q: [total_q, n_heads, head_dim] bf16/fp16, the sequences' rows one after
+    another; cu_seqlens_q: int32 [n_seqs + 1] offsets of the rows, with
+    max_seqlen_q an upper bound on their number a sequence (None: the same
+    number of rows for each sequence, one for a decoding step); kv_lens: int32
+    [n_seqs] cached tokens, the new ones among them; page_table: int32
+    [n_seqs, max_pages].  is_causal: row i of n sees keys up to kv_lens - n +
+    i.  Returns ``out`` [total_q, n_heads, head_dim], or ``(out, lse)`` with
+    lse fp32 [total_q, n_heads].  The workspace is allocated from torch's
+    pool for this call and stream."""
+    import torch
+
+    where = "sdpa_paged_forward"
+    n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens_q, q)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.n_kv_heads != 0:
+        raise SdpaError(3, where)
+    total, heads = q.shape[0], q.shape[1]
+    if cu_seqlens_q is None:
+        if n_seqs == 0 or total % n_seqs != 0:
+            raise SdpaError(3, where)
+        max_seqlen_q = total // n_seqs
+    elif max_seqlen_q is None:
+        raise SdpaError(1, where)
+    if out is not None and (out.dtype != q.dtype or out.shape != q.shape):
+        raise SdpaError(3, where)
+    want_lse = return_lse or lse is not None
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total, heads)):
+        raise SdpaError(3, where)
+    qs = _two_strides(q, where)
+    _same_device(cache.device, where, q, page_table, kv_lens, cu_seqlens_q, out, lse)
+    s = float("nan") if scale is None else float(scale)
+
+    def call(st):
+        lib = load_library()
+        o = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+        ls = torch.empty((total, heads), dtype=torch.float32, device=q.device) if want_lse and lse is None else lse
+        size = lib.sdpa_paged_workspace_bytes(cache.head_dim, heads, cache.n_kv_heads, max_seqlen_q)
+        work = torch.empty(size, dtype=torch.uint8, device=q.device)
+        rc = lib.sdpa_paged_forward(
+            q.data_ptr(), o.data_ptr(), ls.data_ptr() if want_lse else None, dt, cache._ref, total, heads, qs,
+            _two_strides(o, where), _arr(ls.stride()) if want_lse else None, page_table.data_ptr(),
+            page_table.stride(0), max_pages, kv_lens.data_ptr(),
+            cu_seqlens_q.data_ptr() if cu_seqlens_q is not None else None, n_seqs, max_seqlen_q,
+            1 if is_causal else 0, s, work.data_ptr(), size, st)
+        if rc != 0:
+            raise SdpaError(rc, where)
+        return (o, ls) if want_lse else o
+
+    return _on_device(cache.device, stream, call)
 
 
 def sdpa_last_device_status(stream=None):

@@ -372,6 +372,18 @@ void span(const void* a, uint64_t bytes, uintptr_t* lo, uintptr_t* hi) {
 
 }  // namespace
 
+namespace sdpa_impl {
+
+int current_device(int* device, int* sms) {
+  const sdpa_status s = check_device();
+  if (s != SDPA_OK) return s;
+  if (cudaGetDevice(device) != cudaSuccess) return SDPA_ERR_CUDA;
+  *sms = g_device_sms[*device].load(std::memory_order_relaxed);
+  return SDPA_OK;
+}
+
+}  // namespace sdpa_impl
+
 struct sdpa_plan {
   Prepared pr;
   int64_t shape[4];

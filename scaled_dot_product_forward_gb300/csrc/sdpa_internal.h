@@ -122,6 +122,70 @@ constexpr int kNoAllocMaxTiles = 32;
 constexpr int kNoAllocMaxDevices = 64;
 cudaError_t noalloc_mask_tiles(int device, const uint4** tile_bits, const uint8_t** tile_class);
 
+// Attention over a paged cache (e4m3 or 16-bit).
+struct PagedParams {
+  const void* q;            // [total_q, H, D], element strides below
+  int64_t q_st, q_sh;
+  void* out;                // [total_q, H, D]
+  int64_t o_st, o_sh;
+  float* lse;               // optional [total_q, H]
+  int64_t lse_st, lse_sh;
+  const uint8_t* k;         // pages, BYTE strides below
+  const uint8_t* v;
+  int64_t k_sp, k_st, k_sh, v_sp, v_st, v_sh;
+  const float* k_scale;     // e4m3: [n_pages, n_kv] (null for 16-bit caches)
+  const float* v_scale;
+  const int* table;         // [n_seqs, max_pages]
+  int64_t table_st;
+  const int* kv_lens;       // [n_seqs]
+  const int* cu;            // [n_seqs + 1], or null: total_q / n_seqs tokens each
+  int total_q, n_seqs, n_kv, G, n_pages, max_len;
+  int page_shift;           // page size = 1 << page_shift
+  int is_causal;
+  int min_rows, max_rows;   // sequences of this launch: min_rows < nq * G <= max_rows
+  float scale_log2;
+  float* part;              // workspace: [n_ctas][2][RT] rows of D + 2 floats
+  int n_ctas;               // ranges of the division (grid of the main kernel)
+  int device;               // the current device (below 64)
+};
+
+// Appending to a paged cache.
+struct AppendParams {
+  const void* k;            // [total, n_kv, D] 16-bit, element strides
+  const void* v;
+  const void* q;            // optional [total, H, D]
+  void* q_out;
+  int64_t k_st, k_sh, v_st, v_sh, q_st, q_sh, qo_st, qo_sh;
+  uint8_t* ck;              // pages, BYTE strides
+  uint8_t* cv;
+  int64_t ck_sp, ck_st, ck_sh, cv_sp, cv_st, cv_sh;
+  float* k_scale;           // e4m3: [n_pages, n_kv]
+  float* v_scale;
+  const float* cos;         // [n_pos, rot / 2], null: no rotation
+  const float* sin;
+  const int* table;
+  int64_t table_st;
+  const int* kv_lens;
+  const int* cu;
+  int total, n_seqs, n_kv, H, n_pages, max_len, n_pos, rot, interleaved, page_shift;
+};
+
+// The scales a cache may hold: positive, 2^-50 .. 2^50 (others are taken as
+// the nearest of these, NaN and zero as the least).
+constexpr int kScaleMinExp = -50, kScaleMaxExp = 50;
+
+cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, bool e4m3, int sms,
+                                cudaStream_t stream);
+// The division's CTAs and rows of a tile for a launch of launch_paged.
+int paged_ctas(int sms);
+int paged_tile_rows(int64_t max_rows);
+cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile_rows,
+                         cudaStream_t stream);
+
+// The current device and its SM count; the status of the check that it is an
+// sm_103 GPU (an sdpa_status as an int).
+int current_device(int* device, int* sms);
+
 // Reads and clears the device status word (nonzero = a barrier wait timed out).
 cudaError_t read_and_clear_device_status(cudaStream_t stream, unsigned int* status);
 
