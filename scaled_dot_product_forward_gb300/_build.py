@@ -18,7 +18,8 @@ LIB_NAME = "libsdpa_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["sdpa_fwd_sm103a.cu", "sdpa_fwd64_sm103a.cu", "sdpa_sparse_sm103a.cu",
-           "sdpa_cache_sm103a.cu", "sdpa_paged_sm103a.cu", "sdpa_api.cpp", "sdpa_paged_api.cpp"]
+           "sdpa_cache_sm103a.cu", "sdpa_paged_sm103a.cu", "sdpa_paged_tc_sm103a.cu",
+           "sdpa_api.cpp", "sdpa_paged_api.cpp"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
           "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]

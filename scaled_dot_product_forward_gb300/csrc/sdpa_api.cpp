@@ -382,6 +382,28 @@ int current_device(int* device, int* sms) {
   return SDPA_OK;
 }
 
+int encode_pages(const void* ptr, bool e4m3, bool bf16, const int64_t* extents, const int64_t* byte_strides,
+                 int box_tokens, int swizzle, CUtensorMap* map) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return SDPA_ERR_CUDA;
+  cuuint64_t gdim[4], gstride[3];
+  for (int i = 0; i < 4; ++i) gdim[i] = static_cast<cuuint64_t>(extents[i]);
+  // a dimension of one has no stride of its own: any valid one serves
+  for (int i = 0; i < 3; ++i) gstride[i] = static_cast<cuuint64_t>(extents[i + 1] > 1 ? byte_strides[i] : 256);
+  const cuuint32_t box[4] = {e4m3 ? static_cast<cuuint32_t>(extents[0]) : 64u, static_cast<cuuint32_t>(box_tokens), 1, 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  const CUresult r =
+      enc(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+          4, const_cast<void*>(ptr), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          swizzle == 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SDPA_OK : SDPA_ERR_LAYOUT;
+}
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
+int withhold_q() { return g_withhold_q.load(std::memory_order_relaxed); }
+
 }  // namespace sdpa_impl
 
 struct sdpa_plan {
@@ -821,13 +843,14 @@ const char* sdpa_status_string(sdpa_status status) {
 }
 
 sdpa_status sdpa_last_device_status_detail(void* stream, uint32_t* detail) {
-  unsigned int st = 0, st64 = 0, st_sparse = 0;
+  unsigned int st = 0, st64 = 0, st_sparse = 0, st_paged = 0;
   if (sdpa_impl::read_and_clear_device_status(static_cast<cudaStream_t>(stream), &st) !=
           cudaSuccess ||
       sdpa_impl::read_and_clear_fwd64_status(&st64) != cudaSuccess ||
-      sdpa_impl::read_and_clear_sparse_status(&st_sparse) != cudaSuccess)
+      sdpa_impl::read_and_clear_sparse_status(&st_sparse) != cudaSuccess ||
+      sdpa_impl::read_and_clear_paged_status(&st_paged) != cudaSuccess)
     return SDPA_ERR_CUDA;
-  st |= st64 | st_sparse;
+  st |= st64 | st_sparse | st_paged;
   if (detail) *detail = st;
   return st == 0 ? SDPA_OK : SDPA_ERR_DEVICE_TIMEOUT;
 }

@@ -142,11 +142,12 @@ struct PagedParams {
   int total_q, n_seqs, n_kv, G, n_pages, max_len;
   int page_shift;           // page size = 1 << page_shift
   int is_causal;
-  int min_rows, max_rows;   // sequences of this launch: min_rows < nq * G <= max_rows
   float scale_log2;
   float* part;              // workspace: [n_ctas][2][RT] rows of D + 2 floats
   int n_ctas;               // ranges of the division (grid of the main kernel)
   int device;               // the current device (below 64)
+  int debug_withhold_q;     // test hook: 1 = no products are issued, so the waits run out
+  uint64_t wait_limit_ns;
 };
 
 // Appending to a paged cache.
@@ -176,11 +177,36 @@ constexpr int kScaleMinExp = -50, kScaleMaxExp = 50;
 
 cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, bool e4m3, int sms,
                                 cudaStream_t stream);
-// The division's CTAs and rows of a tile for a launch of launch_paged.
-int paged_ctas(int sms);
-int paged_tile_rows(int64_t max_rows);
+// How a launch is divided: CTAs, rows of a unit, and whether it is the form
+// for many rows (paged_tc).
+struct PagedForm {
+  int ctas, rows;
+  bool tc;
+};
+inline PagedForm paged_form(int64_t max_rows, int sms) {
+  if (max_rows <= 16) return {2 * sms, 16, false};
+  if (max_rows <= 32) return {2 * sms, 32, false};
+  return {sms, 256, true};
+}
 cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile_rows,
                          cudaStream_t stream);
+// The form for many rows; tm_k, tm_v: 4-D maps of the pages (D, token, head,
+// page), box min(page size, 128) tokens by 64 16-bit elements with the 128-byte
+// swizzle, or by D codes, the keys' with the swizzle of D bytes, the values'
+// without.
+cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, bool bf16, bool e4m3, const CUtensorMap& tm_k,
+                            const CUtensorMap& tm_v, cudaStream_t stream);
+// Joins the units that a division into steps of 128 keys cuts.
+cudaError_t launch_paged_join128(const PagedParams& p, int head_dim, bool bf16, int tile_rows,
+                                 cudaStream_t stream);
+cudaError_t read_and_clear_paged_status(unsigned int* status);
+
+// Tiled map of a cache's pages (the driver's encoder); an sdpa_status as an int.
+int encode_pages(const void* ptr, bool e4m3, bool bf16, const int64_t* extents, const int64_t* byte_strides,
+                 int box_tokens, int swizzle, CUtensorMap* map);
+// The test hooks' settings.
+uint64_t wait_limit_ns();
+int withhold_q();
 
 // The current device and its SM count; the status of the check that it is an
 // sm_103 GPU (an sdpa_status as an int).

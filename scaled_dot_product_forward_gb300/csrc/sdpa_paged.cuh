@@ -67,8 +67,7 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, int rt) {
   }
   s.nq = q1 - s.q0;
   s.len = min(max(__ldg(p.kv_lens + b), 0), p.max_len);
-  const int rows = s.nq * p.G;
-  s.nt = (rows > p.min_rows && rows <= p.max_rows) ? (rows + rt - 1) / rt : 0;
+  s.nt = (s.nq * p.G + rt - 1) / rt;
   return s;
 }
 
@@ -82,14 +81,6 @@ template <int KT>
 __device__ __forceinline__ int unit_steps(const PagedParams& p, const Seq& s, int t, int rt) {
   return max((unit_keys(p, s, t, rt) + KT - 1) / KT, 1);
 }
-template <int KT>
-__device__ __forceinline__ long long head_steps(const PagedParams& p, const Seq& s, int rt) {
-  if (s.nt == 0) return 0;
-  if (!p.is_causal) return static_cast<long long>(s.nt) * unit_steps<KT>(p, s, 0, rt);
-  long long sum = 0;
-  for (int t = 0; t < s.nt; ++t) sum += unit_steps<KT>(p, s, t, rt);
-  return sum;
-}
 
 // A position in the division: unit (b, h, t), whose steps begin at u0.
 struct Cursor {
@@ -98,81 +89,106 @@ struct Cursor {
   Seq s;
 };
 
-// Shared scratch of locate().
-struct LocateScratch {
+// Shared scratch of divide().
+struct DivideScratch {
   long long warp_sum[16];
-  long long total;
   int found_b;
-  long long found_u0;
+  long long found_u0, found_steps;
 };
 
-// Total steps of the batch; every thread of the block calls it.
-template <int KT, int NT>
-__device__ __forceinline__ long long batch_steps(const PagedParams& p, int rt, LocateScratch* sc) {
-  long long sum = 0;
-  for (int b = threadIdx.x; b < p.n_seqs; b += NT)
-    sum += head_steps<KT>(p, load_seq(p, b, rt), rt);
-  sum *= p.n_kv;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sc->warp_sum[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) total += sc->warp_sum[w];
-  return total;
+// First step of range i of the n equal ones of `total` steps.
+__device__ __forceinline__ long long range_start(long long total, int i, int n) {
+  return total * i / n;
 }
 
-// The unit that holds step v (v < the batch's total); every thread of the
-// block calls it.
-template <int KT, int NT>
-__device__ __forceinline__ Cursor locate(const PagedParams& p, int rt, long long v,
-                                         LocateScratch* sc) {
-  long long base = 0;
-  for (int b0 = 0; b0 < p.n_seqs; b0 += NT) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    long long mine = 0;
-    if (b < p.n_seqs) mine = head_steps<KT>(p, load_seq(p, b, rt), rt) * p.n_kv;
-    long long incl = mine;
+// The batch's total of steps, and the unit that holds step `at(total)` when
+// that is below the total (returns it; -1 otherwise).  Every thread of the
+// block calls it.  A group of W lanes adds up a sequence's units, as many
+// sequences at a time as the block has groups; a batch of at most that many is
+// read once.
+template <int KT, int NT, class At>
+__device__ __forceinline__ long long divide(const PagedParams& p, int rt, DivideScratch* sc, At&& at,
+                                            long long& total, Cursor& c) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  int w = 1;
+  if (p.is_causal)
+    while (w < 32 && p.n_seqs * w * 2 <= NT) w *= 2;
+  const int per = NT / w, sub = tid % w;
+  // this thread's part of sequence b0 + tid / w; inclusive sum over the block
+  // of the sequences' steps, at each group's first lane
+  long long mine, incl, all;
+  auto chunk = [&](int b0) {
+    const int b = b0 + tid / w;
+    mine = 0;
+    if (b < p.n_seqs) {
+      const Seq s = load_seq(p, b, rt);
+      if (!p.is_causal)
+        mine = s.nt == 0 ? 0 : static_cast<long long>(s.nt) * unit_steps<KT>(p, s, 0, rt);
+      else
+        for (int t = sub; t < s.nt; t += w) mine += unit_steps<KT>(p, s, t, rt);
+    }
+    for (int o = 1; o < w; o <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    incl = sub == 0 ? mine * p.n_kv : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (static_cast<int>(threadIdx.x & 31) >= o) incl += x;
+      if (lane >= o) incl += x;
     }
     __syncthreads();
-    if ((threadIdx.x & 31) == 31) sc->warp_sum[threadIdx.x >> 5] = incl;
+    if (lane == 31) sc->warp_sum[warp] = incl;
     __syncthreads();
-    long long before = base, all = base;
+    all = 0;
+    long long before = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-      if (w < static_cast<int>(threadIdx.x >> 5)) before += sc->warp_sum[w];
-      all += sc->warp_sum[w];
+    for (int k = 0; k < NT / 32; ++k) {
+      if (k < warp) before += sc->warp_sum[k];
+      all += sc->warp_sum[k];
     }
-    const long long u = before + incl - mine;
-    if (mine > 0 && v >= u && v < u + mine) {
-      sc->found_b = b;
-      sc->found_u0 = u;
+    incl += before;
+  };
+  total = 0;
+  const int chunks = (p.n_seqs + per - 1) / per;
+  for (int k = 0; k < chunks; ++k) {
+    chunk(k * per);
+    total += all;
+  }
+  const long long v = at(total);
+  if (v >= total) return -1;
+  long long base = 0;
+  for (int k = 0; k < chunks; ++k) {
+    if (chunks > 1) chunk(k * per);
+    const long long u1 = base + incl, u0 = u1 - mine * p.n_kv;
+    if (sub == 0 && mine > 0 && v >= u0 && v < u1) {
+      sc->found_b = k * per + tid / w;
+      sc->found_u0 = u0;
+      sc->found_steps = mine;
     }
-    base = all;
-    if (v < all) break;
+    base += all;
+    if (v < base) break;
   }
   __syncthreads();
-  Cursor c;
   c.b = sc->found_b;
   c.s = load_seq(p, c.b, rt);
-  const long long per_head = head_steps<KT>(p, c.s, rt);
-  const long long off = v - sc->found_u0;
-  c.h = static_cast<int>(off / per_head);
-  c.u0 = sc->found_u0 + c.h * per_head;
-  c.t = 0;
-  while (true) {
-    const int n = unit_steps<KT>(p, c.s, c.t, rt);
-    if (v < c.u0 + n) break;
-    c.u0 += n;
-    ++c.t;
+  c.h = static_cast<int>((v - sc->found_u0) / sc->found_steps);
+  c.u0 = sc->found_u0 + c.h * sc->found_steps;
+  for (int t0 = 0;; t0 += 32) {
+    const long long n = t0 + lane < c.s.nt ? unit_steps<KT>(p, c.s, t0 + lane, rt) : 0;
+    long long sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, v < c.u0 + sum);
+    if (hit != 0 || t0 + 32 >= c.s.nt) {
+      const int k = hit != 0 ? __ffs(static_cast<int>(hit)) - 1 : 31;
+      c.t = t0 + k;
+      c.u0 += __shfl_sync(0xffffffffu, sum - n, k);
+      break;
+    }
+    c.u0 += __shfl_sync(0xffffffffu, sum, 31);
   }
-  return c;
+  return v;
 }
 
 // The next unit (its steps begin where this one's end).
@@ -188,11 +204,6 @@ __device__ __forceinline__ void advance(const PagedParams& p, int rt, Cursor& c)
     if (c.b >= p.n_seqs) return;
     c.s = load_seq(p, c.b, rt);
   } while (c.s.nt == 0);
-}
-
-// First step of range i of the n equal ones of `total` steps.
-__device__ __forceinline__ long long range_start(long long total, int i, int n) {
-  return total * i / n;
 }
 
 // Partial rows of slot s of CTA i.

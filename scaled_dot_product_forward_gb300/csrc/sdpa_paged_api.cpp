@@ -120,10 +120,8 @@ void byte_strides(const sdpa_paged_cache* c, const int64_t* st, int64_t* sp, int
   *sh = c->n_kv_heads > 1 ? st[2] * bytes : 0;
 }
 
-uint64_t workspace_bytes(int sms, int64_t head_dim, int64_t max_rows) {
-  return static_cast<uint64_t>(sdpa_impl::paged_ctas(sms)) * 2u *
-         static_cast<uint64_t>(sdpa_impl::paged_tile_rows(max_rows)) *
-         static_cast<uint64_t>(head_dim + 2) * 4u;
+uint64_t workspace_bytes(const sdpa_impl::PagedForm& f, int64_t head_dim) {
+  return static_cast<uint64_t>(f.ctas) * 2u * static_cast<uint64_t>(f.rows) * static_cast<uint64_t>(head_dim + 2) * 4u;
 }
 
 }  // namespace
@@ -237,7 +235,7 @@ uint64_t sdpa_paged_workspace_bytes(int64_t head_dim, int64_t n_heads, int64_t n
     return 0;
   int dev = 0, sms = 0;
   if (sdpa_impl::current_device(&dev, &sms) != SDPA_OK) return 0;
-  return workspace_bytes(sms, head_dim, max_seqlen_q * (n_heads / n_kv_heads));
+  return workspace_bytes(sdpa_impl::paged_form(max_seqlen_q * (n_heads / n_kv_heads), sms), head_dim);
 }
 
 sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype dtype,
@@ -271,8 +269,8 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
     ls = span_of(lse, 4ull * static_cast<uint64_t>((total_q - 1) * lt + (n_heads - 1) * lh + 1));
   }
   if (std::isinf(scale)) return SDPA_ERR_ARG;
+  const bool e4m3 = cache->elem == SDPA_CACHE_E4M3;
   {
-    const bool e4m3 = cache->elem == SDPA_CACHE_E4M3;
     const uint64_t sb = 4ull * static_cast<uint64_t>(cache->n_pages) * static_cast<uint64_t>(hkv);
     const Span ins[8] = {rq.span(),
                          cache_span(cache, cache->k, cache->k_stride),
@@ -291,8 +289,8 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   int dev = 0, sms = 0;
   s = static_cast<sdpa_status>(sdpa_impl::current_device(&dev, &sms));
   if (s != SDPA_OK) return s;
-  const int64_t rows = (max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
-  if (workspace_size < workspace_bytes(sms, D, rows)) return SDPA_ERR_ARG;
+  const sdpa_impl::PagedForm form = sdpa_impl::paged_form((max_seqlen_q < total_q ? max_seqlen_q : total_q) * G, sms);
+  if (workspace_size < workspace_bytes(form, D)) return SDPA_ERR_ARG;
   sdpa_impl::PagedParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = q;
@@ -319,18 +317,35 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   p.max_len = static_cast<int>(max_pages * cache->page_size);
   p.page_shift = log2_of(cache->page_size);
   p.is_causal = is_causal ? 1 : 0;
-  p.min_rows = 0;
-  p.max_rows = static_cast<int>(kIntMax);
   const double sc = std::isnan(scale) ? 1.0 / std::sqrt(static_cast<double>(D)) : static_cast<double>(scale);
   p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);  // log2(e)
   p.part = static_cast<float*>(workspace);
-  p.n_ctas = sdpa_impl::paged_ctas(sms);
+  p.n_ctas = form.ctas;
   p.device = dev;
-  return sdpa_impl::launch_paged(p, static_cast<int>(D), dtype == SDPA_BF16,
-                                 cache->elem == SDPA_CACHE_E4M3, sdpa_impl::paged_tile_rows(rows),
-                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? SDPA_OK
-             : SDPA_ERR_CUDA;
+  cudaError_t e;
+  if (form.tc) {
+    // a zero scale: the smallest normal multiplier rounds every finite score
+    // to 0 and keeps a removed one infinite (its sign does not matter)
+    if (p.scale_log2 == 0.0f) p.scale_log2 = FLT_MIN;
+    p.debug_withhold_q = sdpa_impl::withhold_q();
+    p.wait_limit_ns = sdpa_impl::wait_limit_ns();
+    CUtensorMap tm_k, tm_v;
+    const int64_t ext[4] = {D, cache->page_size, hkv, cache->n_pages};
+    const int64_t ks[3] = {p.k_st, p.k_sh, p.k_sp}, vs[3] = {p.v_st, p.v_sh, p.v_sp};
+    const int box = static_cast<int>(cache->page_size < 128 ? cache->page_size : 128);
+    const bool bf16 = dtype == SDPA_BF16;
+    s = static_cast<sdpa_status>(sdpa_impl::encode_pages(cache->k, e4m3, bf16, ext, ks, box,
+                                                         e4m3 ? static_cast<int>(D) : 128, &tm_k));
+    if (s == SDPA_OK)
+      s = static_cast<sdpa_status>(sdpa_impl::encode_pages(cache->v, e4m3, bf16, ext, vs, box, e4m3 ? 0 : 128, &tm_v));
+    if (s != SDPA_OK) return s;
+    e = sdpa_impl::launch_paged_tc(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, tm_k, tm_v,
+                                   static_cast<cudaStream_t>(stream));
+  } else {
+    e = sdpa_impl::launch_paged(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, form.rows,
+                                static_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
 }  // extern "C"

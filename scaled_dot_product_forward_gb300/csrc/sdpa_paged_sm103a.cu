@@ -124,8 +124,8 @@ struct Smem {
   static constexpr int kBulk = kRings > kJoin ? kRings : kJoin;
   static constexpr int kNotes = kBulk;
   static constexpr int kMl = kNotes + static_cast<int>(sizeof(WarpScratch)) * kWarps;
-  static constexpr int kLocate = (kMl + kWarps * RT * 8 + 15) / 16 * 16;
-  static constexpr int kTotal = kLocate + static_cast<int>(sizeof(LocateScratch));
+  static constexpr int kDivide = (kMl + kWarps * RT * 8 + 15) / 16 * 16;
+  static constexpr int kTotal = kDivide + static_cast<int>(sizeof(DivideScratch));
 };
 
 // Writes a finished element group (4 values of row r from column d) of a unit.
@@ -164,16 +164,18 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t ring_addr = smem_addr(ring);
   WarpScratch* notes = reinterpret_cast<WarpScratch*>(smem + S::kNotes) + warp;
   float* ml = reinterpret_cast<float*>(smem + S::kMl);  // [warp][RT][2]
-  LocateScratch* sc = reinterpret_cast<LocateScratch*>(smem + S::kLocate);
+  DivideScratch* sc = reinterpret_cast<DivideScratch*>(smem + S::kDivide);
 
   grid_dependency_wait();
   grid_launch_dependents();
 
-  const long long total = batch_steps<KT, kThreads>(p, RT, sc);
-  long long v = range_start(total, blockIdx.x, p.n_ctas);
-  const long long v_end = range_start(total, blockIdx.x + 1, p.n_ctas);
-  if (v >= v_end) return;
-  Cursor c = locate<KT, kThreads>(p, RT, v, sc);
+  const int cta = static_cast<int>(blockIdx.x);
+  long long total;
+  Cursor c;
+  long long v = divide<KT, kThreads>(
+      p, RT, sc, [&](long long all) { return range_start(all, cta, p.n_ctas); }, total, c);
+  const long long v_end = range_start(total, cta + 1, p.n_ctas);
+  if (v < 0 || v >= v_end) return;
   bool first_segment = true;
 
   while (true) {
@@ -537,26 +539,24 @@ __global__ void __launch_bounds__(kThreads)
 // Joins a unit that several CTAs worked on: block i looks at the boundary
 // between ranges i and i + 1, and takes the unit it cuts if it is the first
 // boundary inside that unit.
-template <int D, bool BF16>
+template <int D, bool BF16, int STEP>
 __global__ void __launch_bounds__(kThreads)
     paged_join_kernel(const __grid_constant__ PagedParams p, int RT) {
-  __shared__ LocateScratch sc;
+  __shared__ DivideScratch sc;
   grid_dependency_wait();
   grid_launch_dependents();
   const int n = p.n_ctas, i = static_cast<int>(blockIdx.x);
-  const long long total = batch_steps<KT, kThreads>(p, RT, &sc);
-  const long long v = range_start(total, i + 1, n), from = range_start(total, i, n);
-  if (v >= total || v == 0) return;
-  const Cursor c = locate<KT, kThreads>(p, RT, v, &sc);
-  if (v == c.u0 || from > c.u0) {
-    // cuts no unit, or an earlier boundary (a non-empty range ended there)
-    // lies inside it too
-    return;
-  }
-  if (from == v) return;
-  const long long u1 = c.u0 + unit_steps<KT>(p, c.s, c.t, RT);
+  long long total;
+  Cursor c;
+  const long long v = divide<STEP, kThreads>(
+      p, RT, &sc, [&](long long all) { return range_start(all, i + 1, n); }, total, c);
+  if (v < 0) return;
+  // cuts no unit, or an earlier boundary lies inside it too
+  if (v == c.u0 || range_start(total, i, n) > c.u0) return;
+  const long long u1 = c.u0 + unit_steps<STEP>(p, c.s, c.t, RT);
   const int rows = min(RT, c.s.nq * p.G - c.t * RT);
-  for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
+  for (int e = static_cast<int>(blockIdx.y * kThreads + threadIdx.x); e < rows * (D / 4);
+       e += static_cast<int>(gridDim.y) * kThreads) {
     const int r = e / (D / 4), d = (e % (D / 4)) * 4;
     float mx = -INFINITY, ls = 0.0f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -587,9 +587,9 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <class K, class... A>
-cudaError_t launch_pdl(K kern, unsigned grid, int smem, cudaStream_t stream, const A&... args) {
+cudaError_t launch_pdl(K kern, dim3 grid, int smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -599,6 +599,13 @@ cudaError_t launch_pdl(K kern, unsigned grid, int smem, cudaStream_t stream, con
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D, bool BF16, int STEP>
+cudaError_t launch_join(const PagedParams& p, int rt, cudaStream_t stream) {
+  if (p.n_ctas < 2) return cudaSuccess;
+  return launch_pdl(paged_join_kernel<D, BF16, STEP>, dim3(static_cast<unsigned>(p.n_ctas - 1), rt / 16), 0,
+                    stream, p, rt);
 }
 
 template <int D, bool E4M3, bool BF16, int MT>
@@ -613,9 +620,9 @@ cudaError_t launch_one(const PagedParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
-  e = launch_pdl(kern, static_cast<unsigned>(p.n_ctas), S::kTotal, stream, p);
-  if (e != cudaSuccess || p.n_ctas < 2) return e;
-  return launch_pdl(paged_join_kernel<D, BF16>, static_cast<unsigned>(p.n_ctas - 1), 0, stream, p, S::RT);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(p.n_ctas)), S::kTotal, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_join<D, BF16, KT>(p, S::RT, stream);
 }
 
 template <int D, bool E4M3, bool BF16>
@@ -634,13 +641,16 @@ cudaError_t launch_dim(const PagedParams& p, int rt, bool bf16, bool e4m3, cudaS
 
 namespace sdpa_impl {
 
-int paged_ctas(int sms) { return 2 * sms; }
-int paged_tile_rows(int64_t max_rows) { return max_rows <= 16 ? 16 : 32; }
-
 cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int rt,
                          cudaStream_t stream) {
   return head_dim == 64 ? launch_dim<64>(p, rt, bf16, e4m3, stream)
                         : launch_dim<128>(p, rt, bf16, e4m3, stream);
+}
+
+cudaError_t launch_paged_join128(const PagedParams& p, int head_dim, bool bf16, int rt, cudaStream_t stream) {
+  if (head_dim == 64)
+    return bf16 ? launch_join<64, true, 128>(p, rt, stream) : launch_join<64, false, 128>(p, rt, stream);
+  return bf16 ? launch_join<128, true, 128>(p, rt, stream) : launch_join<128, false, 128>(p, rt, stream);
 }
 
 }  // namespace sdpa_impl

@@ -1,0 +1,998 @@
+// sdpa_paged_tc_sm103a.cu -- attention of many new tokens a sequence over a
+// paged key/value cache, on the fifth-generation tensor cores (sm_103a): the
+// rows of a key/value head (tokens times the query heads that share it) are
+// more than the few that sdpa_paged_sm103a.cu is made for.
+//
+// Same mathematics as there, tiles as in the dense forward: a step is 128
+// keys; S = Q K^T and O += P V are M = 128 tcgen05 products with S, P and O
+// in tensor memory, two softmax warpgroups (one row a thread) alternate on
+// the tensor core.  A unit is up to 256 rows of a sequence and head:
+//   * more than 128: warpgroup t owns rows 128 t .. of the unit, both read
+//     every key tile;
+//   * at most 128: both own the same rows and take the key tiles in turn
+//     (even steps, odd steps), so that a unit with few rows, bound by memory
+//     or by the softmax's latency, still keeps both at work; their sums are
+//     joined at the end through tensor memory, each thread of one reading the
+//     other's lane.
+// Pages arrive by TMA (one box a page and 128-byte column chunk; an entry that
+// is no page lies out of the map's bounds and reads as zeros).  16-bit pages
+// land in the 128-byte-swizzled layout that the products read.  e4m3 pages
+// land as they are in a small ring, and two warps turn them into fp16 tiles
+// (exact); a key's weight carries its page's value scale, so the scales touch
+// eight constants a row and step, not the elements.
+//
+// The steps of all units are divided equally over the CTAs (one an SM), the
+// two cut units of a CTA joined by a second kernel (sdpa_paged.cuh).  Every
+// wait is bounded in time; on expiry the CTA records a status bit, stops, lets
+// what it issued land and frees its tensor memory.
+#include <atomic>
+
+#include <cuda_fp8.h>
+
+#include "sdpa_paged.cuh"
+#include "sdpa_sched.cuh"
+
+using namespace sdpa_dev;
+using namespace sdpa_paged;
+
+__device__ unsigned int g_sdpa_paged_status = 0;
+
+namespace {
+
+constexpr int kThreads = 384;  // warp 0 loads, 1 products, 2-3 conversion; WG1, WG2 softmax
+constexpr int KT = 128;        // keys a step
+constexpr int RT = 256;        // rows a unit
+// Register split: 128 * 88 + 256 * 208 <= 384 * 168 needs 80 for the first
+// warpgroup.
+constexpr uint32_t kLaunchRegs = 168, kRegsControl = 80, kRegsSoftmax = 208;
+static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr float kRescaleLog2 = 8.0f;
+constexpr uint32_t kTmemCols = 512;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
+constexpr int kGroups = KT / 16;     // 16 keys lie in one page
+
+// Terms of a query row in e4m3 for products with e4m3 keys: four significant
+// bits each, so two carry a bf16 value and three an fp16 one.
+__host__ __device__ constexpr int q_terms(bool e4m3, bool bf16) { return !e4m3 ? 1 : bf16 ? 2 : 3; }
+
+template <int D, bool E4M3, bool BF16>
+struct Lay {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kChunkBytes = KT * 128;
+  static constexpr int kTile = kChunks * kChunkBytes;      // 128 rows of 16-bit elements
+  static constexpr int kCodes = KT * D;                    // 128 rows of codes
+  static constexpr int kQTile = q_terms(E4M3, BF16) * (E4M3 ? kCodes : kTile);
+  static constexpr int kKTile = E4M3 ? kCodes : kTile;
+  static constexpr int kKStages = E4M3 ? (D == 128 ? (BF16 ? 3 : 2) : 4) : (D == 128 ? 3 : 4);
+  static constexpr int kVStages = D == 128 ? 2 : (E4M3 ? 3 : 4);
+  static constexpr int kRawStages = !E4M3 ? 0 : (D == 128 ? (BF16 ? 3 : 2) : 4);  // V's codes
+  // Notes on a step (its pages' scales), written when step x's keys have been
+  // asked for: S of step x - K stages is complete then, and so (S is issued
+  // behind the product that needs the weights of two steps before, at most)
+  // the softmax of every step up to x - K stages - 2.
+  static constexpr int kNotes = 8;
+  static_assert(kNotes >= kKStages + 2, "notes are rewritten before they are read");
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kQTile;
+  static constexpr int kV = kK + kKStages * kKTile;
+  static constexpr int kRaw = kV + kVStages * kTile;
+  static constexpr int kNote = kRaw + kRawStages * kCodes;
+  static constexpr int kBar = kNote + (E4M3 ? kNotes * kGroups * 16 : 0);
+  static constexpr int kCursors = kBar + 512;   // the softmax warps' places (8 x 64 bytes)
+  static constexpr int kTotal = kCursors + 512 + 1024;
+  static_assert(kTotal <= 227 * 1024, "shared memory over the per-CTA limit");
+};
+
+struct Bars {
+  uint64_t q_full;      // both warpgroups: Q written, the last unit's rows read out
+  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t sums;        // alternating steps: both warpgroups' sums are in tensor memory
+  uint64_t fin;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], raw_full[6], raw_empty[6];
+  uint64_t note[8];
+  uint32_t bad[8];      // a step's groups of 16 keys without a page
+  uint32_t tmem_base, abort_flag;
+};
+
+enum Site : unsigned int {
+  kSiteQ = 1u << 1, kSiteK = 1u << 2, kSiteEmpty = 1u << 3, kSiteS = 1u << 4, kSiteP = 1u << 5,
+  kSiteO = 1u << 6, kSiteDrain = 1u << 7, kSiteV = 1u << 8, kSiteNote = 1u << 9, kSiteSums = 1u << 10,
+};
+
+__device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, Bars* bars, uint64_t limit,
+                                         unsigned int site, bool honour_abort = true) {
+  return sdpa_sched::wait_phase(bar, parity, &bars->abort_flag, &g_sdpa_paged_status, limit, site,
+                                honour_abort);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* bars, uint64_t limit,
+                                          unsigned int site) {
+  return __all_sync(0xffffffffu, wait_any(bar, parity, bars, limit, site));
+}
+
+// A position in a ring of N slots.
+template <int N>
+struct RingAt {
+  int idx = 0;
+  uint32_t phase = 0;
+  bool lapped = false;
+  __device__ __forceinline__ void next() {
+    if (++idx == N) {
+      idx = 0;
+      phase ^= 1u;
+      lapped = true;
+    }
+  }
+};
+
+// One CTA's share of one unit: steps [s0, s1) of c's unit.
+struct Segment {
+  int s0, s1, rows;
+  bool whole, split, first;
+};
+
+__device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor& c, long long v, long long v_end,
+                                              bool first) {
+  const int steps = unit_steps<KT>(p, c.s, c.t, RT);
+  Segment g;
+  g.s0 = static_cast<int>(v - c.u0);
+  g.s1 = static_cast<int>(min(static_cast<long long>(steps), v_end - c.u0));
+  g.rows = min(RT, c.s.nq * p.G - c.t * RT);
+  g.whole = g.s0 == 0 && g.s1 == steps;
+  g.split = g.rows <= 128;
+  g.first = first;
+  return g;
+}
+
+// Calls f(cursor, segment) for the CTA's segments in order until it returns
+// false.
+template <class F>
+__device__ __forceinline__ void for_each_segment(const PagedParams& p, Cursor c, long long v,
+                                                 long long v_end, F&& f) {
+  bool first = true;
+  while (v < v_end) {
+    const Segment g = segment_of(p, c, v, v_end, first);
+    if (!f(c, g)) return;
+    first = false;
+    v = c.u0 + g.s1;
+    if (v < v_end) advance<KT>(p, RT, c);
+  }
+}
+
+// A softmax warp's place in the division, in shared memory: its registers
+// hold a row of scores.
+struct Place {
+  Cursor c;
+  long long v, v_end;
+};
+static_assert(sizeof(Place) <= 64, "place");
+
+// Four e4m3 codes as four fp16 values, in the arithmetic units: the code's
+// exponent and mantissa bits moved to fp16's place are the value times 2^-8,
+// subnormals too.  (The conversion instruction shares the unit of the base-2
+// exponential, which the softmax fills.)  Codes of NaN come out as +-480.
+__device__ __forceinline__ uint2 halves_of(uint32_t w) {
+  const __half2 up = __float2half2_rn(256.0f);
+  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+  const uint32_t x = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
+  const uint32_t y = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
+  const __half2 hx = __hmul2(*reinterpret_cast<const __half2*>(&x), up);
+  const __half2 hy = __hmul2(*reinterpret_cast<const __half2*>(&y), up);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&hx), *reinterpret_cast<const uint32_t*>(&hy));
+}
+// Bytes of w that are NaN codes (0x7f, 0xff): their top bits.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// +-480 back to NaN where code e of w was one.
+__device__ __forceinline__ uint2 with_nan(uint2 h, uint32_t w) {
+  const uint32_t n = nan_codes(w);
+  if (n & 0x00000080u) h.x = (h.x & 0xffff0000u) | 0x7fffu;
+  if (n & 0x00008000u) h.x = (h.x & 0x0000ffffu) | 0x7fff0000u;
+  if (n & 0x00800000u) h.y = (h.y & 0xffff0000u) | 0x7fffu;
+  if (n & 0x80000000u) h.y = (h.y & 0x0000ffffu) | 0x7fff0000u;
+  return h;
+}
+
+// Converter warp w (0, 1): its half of a value tile's 128 rows from codes to
+// fp16 in the swizzled layout; rows from `valid` on become zeros.  Eight lanes
+// take two rows at a time, so that both the 16-byte reads and the writes of
+// each eight touch all banks.  TAIL: rows may be past `valid` and codes may be
+// NaN; otherwise returns whether a NaN code was met (the tile is then done
+// again with TAIL, so that the loop that always runs has no branch in it).
+template <int D, bool TAIL>
+__device__ __forceinline__ bool convert_rows(const uint8_t* raw, uint8_t* tile, int w, int lane, int valid) {
+  constexpr int kUnits = D / 16;  // 16-byte units of a raw row
+  constexpr int kChunkBytes = KT * 128;
+  const int sub = lane & 7;
+  uint32_t nan = 0;
+#pragma unroll(TAIL ? 1 : 4)
+  for (int i = 0; i < 64 * kUnits / 32; ++i) {
+    int row, unit;
+    if constexpr (D == 128) {
+      row = w * 64 + (i >> 1) * 8 + (lane >> 3) * 2 + (sub >> 2);
+      unit = (i & 1) ? sub ^ 4 : sub;
+    } else {
+      row = w * 64 + i * 8 + (lane >> 3) * 2 + (sub >> 2);
+      unit = sub & 3;
+    }
+    uint4 x = *reinterpret_cast<const uint4*>(raw + row * D + unit * 16);
+    if (TAIL && row >= valid) x = make_uint4(0u, 0u, 0u, 0u);
+    uint2 h0 = halves_of(x.x), h1 = halves_of(x.y), h2 = halves_of(x.z), h3 = halves_of(x.w);
+    if constexpr (TAIL) {
+      h0 = with_nan(h0, x.x);
+      h1 = with_nan(h1, x.y);
+      h2 = with_nan(h2, x.z);
+      h3 = with_nan(h3, x.w);
+    } else {
+      nan |= nan_codes(x.x) | nan_codes(x.y) | nan_codes(x.z) | nan_codes(x.w);
+    }
+    uint8_t* dst = tile + (unit >> 2) * kChunkBytes + row * 128;
+    const int q = (unit & 3) * 2;
+    *reinterpret_cast<uint4*>(dst + ((q ^ (row & 7)) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+    *reinterpret_cast<uint4*>(dst + (((q + 1) ^ (row & 7)) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+  }
+  return nan != 0;
+}
+template <int D>
+__device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* tile, int w, int lane, int valid) {
+  if (valid >= KT && !__any_sync(0xffffffffu, convert_rows<D, false>(raw, tile, w, lane, valid))) return;
+  convert_rows<D, true>(raw, tile, w, lane, valid);
+}
+
+// A row's 128 scores (raw, in s; -inf: removed) to weights: 2^(f s - m), and
+// with groups of 16 keys that have scales of their own 2^(f ks s + log2 vs -
+// m).  f >= 0.  Returns the factor that the earlier sums have to take (need:
+// it is not 1).
+template <bool E4M3, bool MBF>
+__device__ __forceinline__ float weights(float (&s)[KT], float f, const float4* note, float& m, float& l,
+                                         bool& need, uint32_t (&pk)[KT / 2]) {
+  float top = -INFINITY;
+  // never zero: a removed score, an infinity, has to stay one
+  auto mul = [&](int g) { return fmaxf(f * note[g].x, 1.17549435e-38f); };
+  if constexpr (E4M3) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const float* x = s + g * 16;
+      const float a = max3f(x[0], x[1], x[2]), b = max3f(x[3], x[4], x[5]), c = max3f(x[6], x[7], x[8]);
+      const float d = max3f(x[9], x[10], x[11]), e = max3f(x[12], x[13], x[14]);
+      top = fmaxf(top, fmaf(fmaxf(max3f(a, b, c), max3f(d, e, x[15])), mul(g), note[g].y));
+    }
+  } else {
+    float e8[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e8[i] = s[i];
+#pragma unroll
+    for (int c = 8; c < KT; c += 16)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e8[i] = max3f(e8[i], s[c + i], s[c + 8 + i < KT ? c + 8 + i : c + i]);
+    e8[0] = fmaxf(max3f(e8[0], e8[1], e8[2]), max3f(e8[3], e8[4], e8[5]));
+    top = max3f(e8[0], e8[6], e8[7]) * f;
+  }
+  need = top > m + kRescaleLog2;
+  float alpha = 1.0f;
+  if (need) {
+    alpha = ex2(m - top);
+    m = top;
+    l *= alpha;
+  }
+  const float neg_m = m == -INFINITY ? 0.0f : -m;
+  if constexpr (E4M3) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const float a = mul(g), b = note[g].y + neg_m;
+#pragma unroll
+      for (int c = 16 * g; c < 16 * g + 16; c += 2) fma2_bcast(s[c], s[c + 1], s[c], s[c + 1], a, b);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < KT; c += 2) fma2_bcast(s[c], s[c + 1], s[c], s[c + 1], f, neg_m);
+  }
+#pragma unroll
+  for (int c = 0; c < KT; ++c) s[c] = ex2(s[c]);
+  if constexpr (E4M3) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int e = 16 * g + 2 * c;
+        add2_acc(r[2 * (c & 1)], r[2 * (c & 1) + 1], s[e], s[e + 1]);
+        pk[e / 2] = pack2<MBF>(s[e], s[e + 1]);
+      }
+      add2_acc(r[0], r[1], r[2], r[3]);
+      l = fmaf(r[0] + r[1], note[g].z, l);
+    }
+  } else {
+    float rs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rs[i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < KT / 2; ++c) {
+      add2_acc(rs[2 * (c & 3)], rs[2 * (c & 3) + 1], s[2 * c], s[2 * c + 1]);
+      pk[c] = pack2<MBF>(s[2 * c], s[2 * c + 1]);
+    }
+    add2_acc(rs[0], rs[1], rs[2], rs[3]);
+    add2_acc(rs[4], rs[5], rs[6], rs[7]);
+    add2_acc(rs[0], rs[1], rs[4], rs[5]);
+    l += rs[0] + rs[1];
+  }
+  return alpha;
+}
+
+// Where 16-byte piece c of row r of a tile of ROW_BYTES-wide rows lies: the
+// 128-byte swizzle, or the 64-byte one.
+template <int ROW_BYTES>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  return ROW_BYTES == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 128 + ((c ^ (r & 7)) << 4);
+}
+
+// Thread's row of Q to its warpgroup's shared tile (zeros when it has none),
+// negated for a negative scale; returns the (positive) multiplier of the
+// scores, |scale| * log2(e).  For e4m3 keys the row is brought by a power of
+// two to a largest element in [2^7, 2^8) (the factor goes into the
+// multiplier) and split into e4m3 terms, each what the earlier ones leave: a
+// bf16 value is exact in two, an fp16 one in three, down to 2^-10 in that
+// scale, 2^-17 of the row's largest element.
+template <int D, bool E4M3, bool BF16>
+__device__ __forceinline__ float store_query(const PagedParams& p, const uint16_t* src, bool live, uint8_t* tile,
+                                             int r) {
+  uint4 w[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+    w[i] = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t* x = reinterpret_cast<uint32_t*>(w);
+  const float f = fabsf(p.scale_log2);
+  if (p.scale_log2 < 0.0f) {
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) x[i] ^= 0x80008000u;
+  }
+  if constexpr (!E4M3) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      *reinterpret_cast<uint4*>(tile + (i >> 3) * (KT * 128) + swizzled<128>(r, i & 7)) = w[i];
+    return f;
+  } else {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) {
+      const float2 a = unpack2<BF16>(x[i]);
+      top = max3f(top, fabsf(a.x), fabsf(a.y));
+    }
+    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
+    // (an infinite element makes the row NaN)
+    const float up = top < INFINITY ? __int_as_float((127 + 7 - e) << 23) : NAN;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t term[3][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v[4];
+        const float2 a = unpack2<BF16>(x[8 * i + 2 * (k)]), b = unpack2<BF16>(x[8 * i + 2 * k + 1]);
+        v[0] = a.x * up, v[1] = a.y * up, v[2] = b.x * up, v[3] = b.y * up;
+#pragma unroll
+        for (int n = 0; n < q_terms(E4M3, BF16); ++n) {
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+          term[n][k] = lo | (hi << 16);
+          const uint2 h = with_nan(halves_of(term[n][k]), term[n][k]);
+          const float2 g0 = unpack2<false>(h.x), g1 = unpack2<false>(h.y);
+          v[0] -= g0.x, v[1] -= g0.y, v[2] -= g1.x, v[3] -= g1.y;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < q_terms(E4M3, BF16); ++n)
+        *reinterpret_cast<uint4*>(tile + n * (KT * D) + swizzled<D>(r, i)) =
+            make_uint4(term[n][0], term[n][1], term[n][2], term[n][3]);
+    }
+    return f * __int_as_float((127 - 7 + e) << 23);
+  }
+}
+
+// Four consecutive K-steps (32 codes each) of D[tmem] (+)= A[smem] * B[smem]^T
+// with e4m3 operands, in one elected issue; see mma_ss_x4.
+template <uint32_t HI, int STEPS>
+__device__ __forceinline__ void mma_codes(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t acc) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo + 2u * k), "r"(b_lo + 2u * k), "r"(idesc), "r"(k > 0 ? 1u : acc), "n"(HI)
+        : "memory");
+}
+
+template <int D, bool E4M3, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v) {
+  using L = Lay<D, E4M3, BF16>;
+  constexpr bool MBF = BF16 && !E4M3;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem + L::kQ;
+  uint8_t* sK = smem + L::kK;
+  uint8_t* sV = smem + L::kV;
+  float4* notes = reinterpret_cast<float4*>(smem + L::kNote);
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBar);
+  static_assert(sizeof(Bars) <= 512, "barriers");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = p.wait_limit_ns;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 8);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_ready[t], 4);
+      mbar_init(&bars->o_done[t], 1);
+    }
+    mbar_init(&bars->sums, 8);
+    mbar_init(&bars->fin, 1);
+    for (int i = 0; i < L::kKStages; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 1);
+    }
+    for (int i = 0; i < L::kVStages; ++i) {
+      mbar_init(&bars->v_full[i], E4M3 ? 2 : 1);
+      mbar_init(&bars->v_empty[i], 1);
+    }
+    for (int i = 0; i < L::kRawStages; ++i) {
+      mbar_init(&bars->raw_full[i], 1);
+      mbar_init(&bars->raw_empty[i], 2);
+    }
+    for (int i = 0; i < L::kNotes; ++i) mbar_init(&bars->note[i], 1);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t tmem = bars->tmem_base;
+
+  // the division, in the scratch of the Q tiles
+  const int cta = static_cast<int>(blockIdx.x);
+  long long total;
+  Cursor c0{};
+  const long long v0 = divide<KT, kThreads>(
+      p, RT, reinterpret_cast<DivideScratch*>(sQ),
+      [&](long long all) { return range_start(all, cta, p.n_ctas); }, total, c0);
+  const long long v1 = v0 < 0 ? v0 : range_start(total, cta + 1, p.n_ctas);
+  __syncthreads();
+
+  if (warp >= 4) {
+    // -------------------------------------------------------- softmax
+    regs_increase<kRegsSoftmax>();
+    const int t = (warp - 4) >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + (t ? 128u : 0u) + lane_off;
+    const uint32_t tO = tmem + (t ? 384u : 256u) + lane_off;
+    uint32_t n_s = 0, n_sums = 0;   // completions consumed
+    RingAt<L::kNotes> note_at;
+    volatile Place* vplace = reinterpret_cast<volatile Place*>(smem + L::kCursors) + (warp - 4);
+    auto save = [&](const Cursor& c, long long v) {
+      if (lane == 0) {
+        vplace->c.b = c.b, vplace->c.h = c.h, vplace->c.t = c.t, vplace->c.u0 = c.u0;
+        vplace->c.s.q0 = c.s.q0, vplace->c.s.nq = c.s.nq, vplace->c.s.len = c.s.len, vplace->c.s.nt = c.s.nt;
+        vplace->v = v, vplace->v_end = v1;
+      }
+      __syncwarp();
+    };
+    auto load = [&](Cursor& c, long long& v, long long& v_end) {
+      c.b = vplace->c.b, c.h = vplace->c.h, c.t = vplace->c.t, c.u0 = vplace->c.u0;
+      c.s.q0 = vplace->c.s.q0, c.s.nq = vplace->c.s.nq, c.s.len = vplace->c.s.len, c.s.nt = vplace->c.s.nt;
+      v = vplace->v, v_end = vplace->v_end;
+    };
+    // the row's token and query head
+    auto place = [&](const Cursor& c, int ru, int64_t& token, int64_t& head) {
+      const int rr = c.t * RT + ru, tok = rr / p.G;
+      token = static_cast<int64_t>(c.s.q0) + tok;
+      head = static_cast<int64_t>(c.h) * p.G + (rr - tok * p.G);
+      return tok;
+    };
+    save(c0, v0);
+    bool first = true;
+    for (bool ok = v0 < v1; ok;) {
+      float f;
+      int seen, s0, s1;
+      bool split;
+      {
+        Cursor c;
+        long long v, v_end;
+        load(c, v, v_end);
+        const Segment g = segment_of(p, c, v, v_end, first);
+        s0 = g.s0, s1 = g.s1, split = g.split;
+        const int ru = split ? r : t * 128 + r;   // row of the unit
+        int64_t token, head;
+        const int tok = place(c, ru, token, head);
+        const bool live = ru < g.rows;
+        seen = !live ? 0 : p.is_causal ? min(max(c.s.len - c.s.nq + tok + 1, 0), c.s.len) : c.s.len;
+        f = store_query<D, E4M3, BF16>(
+            p, reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh, live, sQ + t * L::kQTile, r);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_full);
+      float m = -INFINITY, l = 0.0f;
+      int mine = 0;
+      for (int s = s0; s < s1; ++s) {
+        const int slot = note_at.idx;
+        const uint32_t note_phase = note_at.phase;
+        note_at.next();
+        if (split && ((s - s0) & 1) != t) continue;
+        if (!warp_wait(&bars->note[slot], note_phase, bars, limit, kSiteNote)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&bars->bad[slot]);
+        if (!warp_wait(&bars->s_full[t], n_s & 1, bars, limit, kSiteS)) {
+          ok = false;
+          break;
+        }
+        ++n_s;
+        tc_fence_after();
+        float x[KT];
+        {
+          uint32_t u[KT];
+#pragma unroll
+          for (int i = 0; i < KT / 32; ++i) tmem_ld32(tS + i * 32, u + i * 32);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < KT; ++i) x[i] = __uint_as_float(u[i]);
+        }
+        const int left = seen - s * KT;   // keys of this tile that the row sees
+        if (__any_sync(0xffffffffu, left < KT) || bad != 0u) {
+#pragma unroll
+          for (int i = 0; i < KT; ++i) x[i] = (i >= left || ((bad >> (i >> 4)) & 1u)) ? -INFINITY : x[i];
+        }
+        bool need;
+        uint32_t pk[KT / 2];
+        const float alpha = weights<E4M3, MBF>(x, f, notes + slot * kGroups, m, l, need, pk);
+        if (mine > 0 && __any_sync(0xffffffffu, need)) {
+          // the earlier products of this tile are complete: S of this step was
+          // issued behind them
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tmem_ld32(tO + i * 32, o);
+            tmem_ld_wait();
+            float* of = reinterpret_cast<float*>(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mul2_bcast(of[e], of[e + 1], alpha);
+            tmem_st32(tO + i * 32, o);
+          }
+        }
+        tmem_st32(tS, pk);
+        tmem_st32(tS + 32, pk + 32);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_ready[t]);
+        ++mine;
+      }
+      // n_s completions of s_full[t] so far, as many of o_done[t]
+      if (!ok || (mine > 0 && !warp_wait(&bars->o_done[t], (n_s - 1) & 1, bars, limit, kSiteO))) break;
+      tc_fence_after();
+      float fa = 1.0f, fb = 0.0f;
+      if (split) {
+        // join the two warpgroups' sums: each leaves (m, l) behind its P and
+        // writes half of the columns
+        uint32_t ml[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) ml[i] = 0u;
+        ml[0] = __float_as_uint(m);
+        ml[1] = __float_as_uint(l);
+        tmem_st32(tS + 96, ml);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->sums);
+        if (!warp_wait(&bars->sums, n_sums & 1, bars, limit, kSiteSums)) {
+          ok = false;
+          break;
+        }
+        ++n_sums;
+        tc_fence_after();
+        tmem_ld32(tmem + (t ? 0u : 128u) + lane_off + 96, ml);
+        tmem_ld_wait();
+        const float mo = __uint_as_float(ml[0]), lo = __uint_as_float(ml[1]);
+        const float mx = fmaxf(m, mo), base = mx == -INFINITY ? 0.0f : mx;
+        fa = ex2(m - base);
+        fb = ex2(mo - base);
+        l = l * fa + lo * fb;
+        m = mx;
+      }
+      Cursor c;
+      long long v, v_end;
+      load(c, v, v_end);
+      const Segment g = segment_of(p, c, v, v_end, first);
+      const int ru = g.split ? r : t * 128 + r;
+      const bool live = ru < g.rows;
+      int64_t token, head;
+      place(c, ru, token, head);
+      // O is undefined where no step was taken; otherwise (no key seen) zeros
+      const bool own = mine > 0, other = g.split && (t == 0 ? g.s1 - g.s0 > 1 : true);
+      const float inv = !g.whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      fa *= inv;
+      fb *= inv;
+      uint16_t* orow = reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh;
+      float* prow = part_rows<D>(p, blockIdx.x, g.first ? 0 : 1, RT) + static_cast<int64_t>(ru) * (D + 2);
+      const int i0 = g.split ? t * (D / 64) : 0, i1 = g.split ? i0 + D / 64 : D / 32;
+      for (int i = i0; i < i1; ++i) {
+        uint32_t o[32];
+        tmem_ld32(tO + i * 32, o);
+        tmem_ld_wait();
+        float* of = reinterpret_cast<float*>(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) of[e] = own ? of[e] * fa : 0.0f;
+        if (other) {
+          uint32_t o2[32];
+          tmem_ld32(tmem + (t ? 256u : 384u) + lane_off + i * 32, o2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) of[e] = fmaf(__uint_as_float(o2[e]), fb, of[e]);
+        }
+        if (live) {
+          if (g.whole) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(orow + i * 32 + e * 8) =
+                  make_uint4(pack2<BF16>(of[8 * e], of[8 * e + 1]), pack2<BF16>(of[8 * e + 2], of[8 * e + 3]),
+                             pack2<BF16>(of[8 * e + 4], of[8 * e + 5]), pack2<BF16>(of[8 * e + 6], of[8 * e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              *reinterpret_cast<float2*>(prow + i * 32 + e) = make_float2(of[e], of[e + 1]);
+          }
+        }
+      }
+      if (live && (!g.split || t == 0)) {
+        if (!g.whole) {
+          *reinterpret_cast<float2*>(prow + D) = make_float2(m, l);
+        } else if (p.lse != nullptr) {
+          constexpr float kLn2 = 0.693147180559945309f;
+          p.lse[token * p.lse_st + head * p.lse_sh] = l == 0.0f ? -INFINITY : (log2f(l) + m) * kLn2;
+        }
+      }
+      tc_fence_before();
+      first = false;
+      v = c.u0 + g.s1;
+      if (v >= v_end) break;
+      advance<KT>(p, RT, c);
+      __syncwarp();
+      save(c, v);
+    }
+    tc_fence_before();
+  } else {
+    regs_decrease<kRegsControl>();
+    if (warp == 0 || (!E4M3 && warp == 2)) {
+      // ----------------------------------------------------------- loads
+      // (16-bit pages: warp 0 the keys', warp 2 the values')
+      const bool keys = warp == 0;
+      RingAt<L::kKStages> k_at;
+      RingAt<E4M3 ? L::kRawStages : L::kVStages> v_at;
+      RingAt<L::kNotes> note_at;
+      int k_end = 0, v_end = 0;   // tiles issued
+      const int P = 1 << p.page_shift;
+      const int box = P < KT ? P : KT, per_step = KT / box;
+      for_each_segment(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
+        const int* trow = p.table + static_cast<int64_t>(c.b) * p.table_st;
+        const int n_entries = (c.s.len + P - 1) >> p.page_shift;
+        // a window of 32 page entries in the lanes, the next one behind it; an
+        // entry that is no page becomes n_pages, out of the map's bounds
+        int win0 = (g.s0 * KT) >> p.page_shift;
+        auto entries = [&](int from) {
+          const int id = from + lane < n_entries ? __ldg(trow + from + lane) : -1;
+          return id >= 0 && id < p.n_pages ? id : p.n_pages;
+        };
+        int ids = entries(win0), ids_next = entries(win0 + 32);
+        for (int s = g.s0; s < g.s1; ++s) {
+          const int e0 = (s * KT) >> p.page_shift;
+          if (e0 - win0 >= 32) {
+            win0 += 32;
+            ids = ids_next;
+            ids_next = entries(win0 + 32);
+          }
+          const int row0 = (s * KT) & (P - 1);
+          // one elected lane issues a tile's boxes
+          auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full) {
+            int id[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) id[i] = __shfl_sync(0xffffffffu, ids, (e0 - win0 + i) & 31);
+            if (elect_one()) {
+              mbar_arrive_expect_tx(full, E4M3 ? L::kCodes : L::kTile);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (i >= per_step) break;
+                if constexpr (E4M3) {
+                  tma_load_4d(dst + i * box * D, map, full, 0, row0, c.h, id[i]);
+                } else {
+#pragma unroll
+                  for (int ch = 0; ch < L::kChunks; ++ch)
+                    tma_load_4d(dst + ch * L::kChunkBytes + i * box * 128, map, full, ch * 64, row0, c.h, id[i]);
+                }
+              }
+            }
+            __syncwarp();
+          };
+          if (keys) {
+            if (k_at.lapped && !warp_wait(&bars->k_empty[k_at.idx], k_at.phase ^ 1u, bars, limit, kSiteEmpty))
+              return false;
+            load(&tm_k, sK + k_at.idx * L::kKTile, &bars->k_full[k_at.idx]);
+            k_at.next();
+            ++k_end;
+          }
+          if (E4M3 || !keys) {
+            uint64_t* empty = E4M3 ? &bars->raw_empty[v_at.idx] : &bars->v_empty[v_at.idx];
+            if (v_at.lapped && !warp_wait(empty, v_at.phase ^ 1u, bars, limit, kSiteEmpty)) return false;
+            load(&tm_v, E4M3 ? smem + L::kRaw + v_at.idx * L::kCodes : sV + v_at.idx * L::kTile,
+                 E4M3 ? &bars->raw_full[v_at.idx] : &bars->v_full[v_at.idx]);
+            v_at.next();
+            ++v_end;
+          }
+          if (!keys) continue;
+          // notes: lane i < 8 looks after keys 16 i .. of the step
+          {
+            const int e = min((s * KT + (lane & 7) * 16) >> p.page_shift, win0 + 31);
+            const int id = __shfl_sync(0xffffffffu, ids, e - win0);
+            const bool is_page = id < p.n_pages;
+            const uint32_t bad = __ballot_sync(0xffffffffu, !is_page) & 0xffu;
+            if (lane < 8) {
+              if constexpr (E4M3) {
+                float4 n = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+                if (is_page) {
+                  const int64_t at = static_cast<int64_t>(id) * p.n_kv + c.h;
+                  const float vs = clamp_scale(__ldg(p.v_scale + at));
+                  n = make_float4(clamp_scale(__ldg(p.k_scale + at)), __log2f(vs), 1.0f / vs, 0.0f);
+                }
+                notes[note_at.idx * kGroups + lane] = n;
+              }
+              if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&bars->bad[note_at.idx]) = bad;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->note[note_at.idx]);
+            note_at.next();
+          }
+        }
+        return true;
+      });
+      // what was issued must land before shared memory is released
+      constexpr int kN = E4M3 ? L::kRawStages : L::kVStages;
+      for (int j = max(0, k_end - L::kKStages); j < k_end; ++j)
+        wait_any(&bars->k_full[j % L::kKStages], (j / L::kKStages) & 1, bars, limit, kSiteDrain, false);
+      for (int j = max(0, v_end - kN); j < v_end; ++j)
+        wait_any(E4M3 ? &bars->raw_full[j % kN] : &bars->v_full[j % kN], (j / kN) & 1, bars, limit, kSiteDrain, false);
+    } else if (warp == 1) {
+      // -------------------------------------------------------- products
+      constexpr uint32_t idS = idesc_f16_f32acc(MBF, false, 128, KT);
+      constexpr uint32_t idPV = idesc_f16_f32acc(MBF, true, 128, D);
+      constexpr uint32_t kHi = desc_hi_sw128(1024);
+      // e4m3 operands (type 0 in the descriptor's fields, D = fp32), rows of D
+      // bytes: the 128-byte swizzle, or the 64-byte one (mode 4)
+      constexpr uint32_t idCodes = (1u << 4) | ((KT >> 3) << 17) | ((128 >> 4) << 24);
+      constexpr uint32_t kHiCodes = D == 128 ? kHi : ((512u >> 4) | (1u << 14) | (4u << 29));
+      const uint32_t q_lo = desc_lo_sw128(smem_addr(sQ), 16);
+      const uint32_t k_lo = desc_lo_sw128(smem_addr(sK), 16);
+      const uint32_t v_lo = desc_lo_sw128(smem_addr(sV), L::kChunkBytes);
+      RingAt<L::kKStages> k_at;
+      RingAt<L::kVStages> v_at;
+      uint32_t n_p[2] = {0, 0}, n_seg = 0;
+      bool issued = false;
+      auto issue_s = [&](int t) {
+        const uint32_t a0 = q_lo + static_cast<uint32_t>(t * (L::kQTile >> 4));
+        const uint32_t b0 = k_lo + static_cast<uint32_t>(k_at.idx * (L::kKTile >> 4));
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int n = 0; n < q_terms(E4M3, BF16); ++n)
+            mma_codes<kHiCodes, D / 32>(tmem + (t ? 128u : 0u), a0 + n * (L::kCodes >> 4), b0, idCodes, n > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int ch = 0; ch < L::kChunks; ++ch) {
+            const uint32_t off = static_cast<uint32_t>(ch * L::kChunkBytes) >> 4;
+            mma_ss_x4<kHi, kHi>(tmem + (t ? 128u : 0u), a0 + off, b0 + off, 2u, 2u, idS, ch > 0 ? 1u : 0u);
+          }
+        }
+        mma_commit_elect(&bars->s_full[t]);
+      };
+      auto issue_pv = [&](int t, bool more) {
+        const uint32_t b0 = v_lo + static_cast<uint32_t>(v_at.idx * (L::kTile >> 4));
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          mma_ts_x4<kHi>(tmem + (t ? 384u : 256u), tmem + (t ? 128u : 0u) + hf * 32,
+                         b0 + hf * ((64 * 128) >> 4), 8u, (16 * 128) >> 4, idPV, (more || hf > 0) ? 1u : 0u);
+        mma_commit_elect(&bars->o_done[t]);
+      };
+      auto next_k = [&]() {
+        if (!warp_wait(&bars->k_full[k_at.idx], k_at.phase, bars, limit, kSiteK)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto done_k = [&]() {
+        mma_commit_elect(&bars->k_empty[k_at.idx]);
+        k_at.next();
+      };
+      // V of the step: rows past the sequence's end are made zeros (their
+      // weights are, but a stale NaN must not meet them)
+      auto next_v = [&](int valid) {
+        if (!warp_wait(&bars->v_full[v_at.idx], v_at.phase, bars, limit, kSiteV)) return false;
+        if (!E4M3 && valid < KT) {
+          uint8_t* tile = sV + v_at.idx * L::kTile;
+          for (int i = max(valid, 0) * 8 + lane; i < KT * 8; i += 32)
+#pragma unroll
+            for (int ch = 0; ch < L::kChunks; ++ch)
+              *reinterpret_cast<uint4*>(tile + ch * L::kChunkBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        return true;
+      };
+      auto next_p = [&](int t) {
+        if (!warp_wait(&bars->p_ready[t], n_p[t] & 1, bars, limit, kSiteP)) return false;
+        ++n_p[t];
+        tc_fence_after();
+        return true;
+      };
+      for_each_segment(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
+        if (p.debug_withhold_q) return false;
+        if (!warp_wait(&bars->q_full, n_seg & 1, bars, limit, kSiteQ)) return false;
+        ++n_seg;
+        tc_fence_after();
+        const int n = g.s1 - g.s0;
+        if (!next_k()) return false;
+        issued = true;
+        if (g.split) {
+          issue_s(0);
+          done_k();
+          if (n > 1) {
+            if (!next_k()) return false;
+            issue_s(1);
+            done_k();
+          }
+          for (int j = 0; j < n; ++j) {
+            const int t = j & 1;
+            if (!next_v(c.s.len - (g.s0 + j) * KT) || !next_p(t)) return false;
+            issue_pv(t, j > 1);
+            mma_commit_elect(&bars->v_empty[v_at.idx]);
+            v_at.next();
+            if (j + 2 < n) {
+              if (!next_k()) return false;
+              issue_s(t);
+              done_k();
+            }
+          }
+        } else {
+          issue_s(0);
+          issue_s(1);
+          done_k();
+          for (int j = 0; j < n; ++j) {
+            if (!next_v(c.s.len - (g.s0 + j) * KT) || !next_p(0)) return false;
+            issue_pv(0, j > 0);
+            if (j + 1 < n) {
+              if (!next_k()) return false;
+              issue_s(0);
+            }
+            if (!next_p(1)) return false;
+            issue_pv(1, j > 0);
+            mma_commit_elect(&bars->v_empty[v_at.idx]);
+            v_at.next();
+            if (j + 1 < n) {
+              issue_s(1);
+              done_k();
+            }
+          }
+        }
+        return true;
+      });
+      if (issued) {
+        mma_commit_elect(&bars->fin);
+        wait_any(&bars->fin, 0, bars, limit, kSiteDrain, false);
+      }
+    } else if constexpr (E4M3) {
+      // ------------------------------------------------------ conversion
+      RingAt<L::kVStages> v_at;
+      RingAt<L::kRawStages> raw_at;
+      for_each_segment(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
+        for (int s = g.s0; s < g.s1; ++s) {
+          if (!warp_wait(&bars->raw_full[raw_at.idx], raw_at.phase, bars, limit, kSiteK)) return false;
+          if (v_at.lapped && !warp_wait(&bars->v_empty[v_at.idx], v_at.phase ^ 1u, bars, limit, kSiteEmpty))
+            return false;
+          convert_tile<D>(smem + L::kRaw + raw_at.idx * L::kCodes, sV + v_at.idx * L::kTile, warp - 2, lane,
+                          c.s.len - s * KT);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars->raw_empty[raw_at.idx]);
+            mbar_arrive(&bars->v_full[v_at.idx]);
+          }
+          raw_at.next();
+          v_at.next();
+        }
+        return true;
+      });
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool E4M3, bool BF16>
+cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
+  auto kern = paged_tc_kernel<D, E4M3, BF16>;
+  static std::atomic<uint64_t> configured{0};  // a bit a device
+  const uint64_t bit = 1ull << p.device;
+  cudaError_t e = cudaSuccess;
+  if ((configured.load(std::memory_order_relaxed) & bit) == 0) {
+    // the register split assumes kLaunchRegs a thread at launch: never start a
+    // build where that does not hold (setmaxnreg would wait)
+    cudaFuncAttributes fa{};
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, E4M3, BF16>::kTotal);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Lay<D, E4M3, BF16>::kTotal;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p, tm_k, tm_v);
+  if (e != cudaSuccess) return e;
+  return sdpa_impl::launch_paged_join128(p, D, BF16, RT, stream);
+}
+
+template <int D>
+cudaError_t launch_dim(const PagedParams& p, bool bf16, bool e4m3, const CUtensorMap& k, const CUtensorMap& v,
+                       cudaStream_t s) {
+  if (e4m3) return bf16 ? launch_one<D, true, true>(p, k, v, s) : launch_one<D, true, false>(p, k, v, s);
+  return bf16 ? launch_one<D, false, true>(p, k, v, s) : launch_one<D, false, false>(p, k, v, s);
+}
+
+}  // namespace
+
+namespace sdpa_impl {
+
+cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, bool bf16, bool e4m3, const CUtensorMap& tm_k,
+                            const CUtensorMap& tm_v, cudaStream_t stream) {
+  return head_dim == 64 ? launch_dim<64>(p, bf16, e4m3, tm_k, tm_v, stream)
+                        : launch_dim<128>(p, bf16, e4m3, tm_k, tm_v, stream);
+}
+
+cudaError_t read_and_clear_paged_status(unsigned int* status) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_sdpa_paged_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  if (*status != 0) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_sdpa_paged_status, &zero, sizeof(unsigned int));
+  }
+  return e;
+}
+
+}  // namespace sdpa_impl
