@@ -143,7 +143,8 @@ struct PagedParams {
   int page_shift;           // page size = 1 << page_shift
   int is_causal;
   float scale_log2;
-  float* part;              // workspace: [n_ctas][2][RT] rows of D + 2 floats
+  int max_rows;             // the caller's bound on a sequence's rows a head (>= 1)
+  float* part;              // workspace: n_ctas notes, [n_ctas][2][rows of a unit][D + 2] floats
   int n_ctas;               // ranges of the division (grid of the main kernel)
   int device;               // the current device (below 64)
   int debug_withhold_q;     // test hook: 1 = no products are issued, so the waits run out
@@ -177,6 +178,8 @@ constexpr int kScaleMinExp = -50, kScaleMaxExp = 50;
 
 cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, bool e4m3, int sms,
                                 cudaStream_t stream);
+constexpr int kJoinNoteBytes = 32;  // a CTA's note at the workspace's start
+
 // How a launch is divided: CTAs, rows of a unit, and whether it is the form
 // for many rows (paged_tc).
 struct PagedForm {
@@ -196,8 +199,8 @@ cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m
 // without.
 cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, bool bf16, bool e4m3, const CUtensorMap& tm_k,
                             const CUtensorMap& tm_v, cudaStream_t stream);
-// Joins the units that a division into steps of 128 keys cuts.
-cudaError_t launch_paged_join128(const PagedParams& p, int head_dim, bool bf16, int tile_rows,
+// Joins the units that the division cut.
+cudaError_t launch_paged_join(const PagedParams& p, int head_dim, bool bf16, int tile_rows,
                                  cudaStream_t stream);
 cudaError_t read_and_clear_paged_status(unsigned int* status);
 

@@ -96,9 +96,14 @@ struct DivideScratch {
   long long found_u0, found_steps;
 };
 
+// Ranges of a division into at most n: never an empty one.
+__device__ __forceinline__ int range_count(long long total, int n) {
+  return total < n ? static_cast<int>(total) : n;
+}
 // First step of range i of the n equal ones of `total` steps.
 __device__ __forceinline__ long long range_start(long long total, int i, int n) {
-  return total * i / n;
+  const long long q = total < (1ll << 31) ? static_cast<int>(total) / n : total / n;
+  return q * i + static_cast<int>(total - q * n) * i / n;   // both factors below n
 }
 
 // The batch's total of steps, and the unit that holds step `at(total)` when
@@ -169,7 +174,9 @@ __device__ __forceinline__ long long divide(const PagedParams& p, int rt, Divide
   __syncthreads();
   c.b = sc->found_b;
   c.s = load_seq(p, c.b, rt);
-  c.h = static_cast<int>((v - sc->found_u0) / sc->found_steps);
+  const long long off = v - sc->found_u0;
+  c.h = static_cast<int>(off < (1ll << 31) ? static_cast<int>(off) / static_cast<int>(min(sc->found_steps, 0x7fffffffll))
+                                           : off / sc->found_steps);
   c.u0 = sc->found_u0 + c.h * sc->found_steps;
   for (int t0 = 0;; t0 += 32) {
     const long long n = t0 + lane < c.s.nt ? unit_steps<KT>(p, c.s, t0 + lane, rt) : 0;
@@ -206,10 +213,41 @@ __device__ __forceinline__ void advance(const PagedParams& p, int rt, Cursor& c)
   } while (c.s.nt == 0);
 }
 
-// Partial rows of slot s of CTA i.
+// The workspace: what to join, a note of each CTA's, then the partial units,
+// two a CTA of rt rows of D sums and their maximum and sum.
+struct JoinNote {
+  int pieces;        // 0: no unit begins in this CTA's range and ends behind it
+  int slot;          // of its piece here; the following CTAs' pieces are their first
+  int rows, row0;    // the unit's rows, the first one's number in the sequence
+  int q0, head0;     // the sequence's first row of q, the unit's first query head
+  int unused[2];
+};
+static_assert(sizeof(JoinNote) == sdpa_impl::kJoinNoteBytes, "workspace layout");
+
 template <int D>
 __device__ __forceinline__ float* part_rows(const PagedParams& p, int i, int slot, int rt) {
-  return p.part + (static_cast<int64_t>(i) * 2 + slot) * rt * (D + 2);
+  return p.part + static_cast<int64_t>(p.n_ctas) * (sizeof(JoinNote) / 4) +
+         (static_cast<int64_t>(i) * 2 + slot) * rt * (D + 2);
+}
+
+// CTA i's note: its last unit, if that begins here (with its first or a later
+// segment) and goes on behind its range.
+template <int KT>
+__device__ __forceinline__ void leave_note(const PagedParams& p, int i, long long total, int n, int rt,
+                                           const Cursor& c, int s0, int s1, bool first) {
+  JoinNote j{};
+  const int steps = unit_steps<KT>(p, c.s, c.t, rt);
+  if (s0 == 0 && s1 < steps) {
+    // the range that holds the unit's last step
+    const long long last = ((c.u0 + steps) * n - 1) / total;
+    j.pieces = static_cast<int>(last) - i + 1;
+    j.slot = first ? 0 : 1;
+    j.rows = min(rt, c.s.nq * p.G - c.t * rt);
+    j.row0 = c.t * rt;
+    j.q0 = c.s.q0;
+    j.head0 = c.h * p.G;
+  }
+  reinterpret_cast<JoinNote*>(p.part)[i] = j;
 }
 
 }  // namespace sdpa_paged

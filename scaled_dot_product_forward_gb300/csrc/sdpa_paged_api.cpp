@@ -121,7 +121,8 @@ void byte_strides(const sdpa_paged_cache* c, const int64_t* st, int64_t* sp, int
 }
 
 uint64_t workspace_bytes(const sdpa_impl::PagedForm& f, int64_t head_dim) {
-  return static_cast<uint64_t>(f.ctas) * 2u * static_cast<uint64_t>(f.rows) * static_cast<uint64_t>(head_dim + 2) * 4u;
+  return static_cast<uint64_t>(f.ctas) *
+         (sdpa_impl::kJoinNoteBytes + 2u * static_cast<uint64_t>(f.rows) * static_cast<uint64_t>(head_dim + 2) * 4u);
 }
 
 }  // namespace
@@ -289,7 +290,8 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   int dev = 0, sms = 0;
   s = static_cast<sdpa_status>(sdpa_impl::current_device(&dev, &sms));
   if (s != SDPA_OK) return s;
-  const sdpa_impl::PagedForm form = sdpa_impl::paged_form((max_seqlen_q < total_q ? max_seqlen_q : total_q) * G, sms);
+  const int64_t max_rows = (max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
+  const sdpa_impl::PagedForm form = sdpa_impl::paged_form(max_rows, sms);
   if (workspace_size < workspace_bytes(form, D)) return SDPA_ERR_ARG;
   sdpa_impl::PagedParams p;
   std::memset(&p, 0, sizeof(p));
@@ -321,6 +323,7 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);  // log2(e)
   p.part = static_cast<float*>(workspace);
   p.n_ctas = form.ctas;
+  p.max_rows = static_cast<int>(max_rows);
   p.device = dev;
   cudaError_t e;
   if (form.tc) {

@@ -125,7 +125,11 @@ struct Smem {
   static constexpr int kNotes = kBulk;
   static constexpr int kMl = kNotes + static_cast<int>(sizeof(WarpScratch)) * kWarps;
   static constexpr int kDivide = (kMl + kWarps * RT * 8 + 15) / 16 * 16;
-  static constexpr int kTotal = kDivide + static_cast<int>(sizeof(DivideScratch));
+  // Not below 80 KB: two CTAs an SM and never three, or the kernel's equal
+  // shares land on some SMs three at a time and on others one.
+  static constexpr int kNeed = kDivide + static_cast<int>(sizeof(DivideScratch));
+  static constexpr int kTotal = kNeed > 80 * 1024 ? kNeed : 80 * 1024;
+  static_assert(2 * (kTotal + 1024) <= 227 * 1024, "two CTAs an SM");
 };
 
 // Writes a finished element group (4 values of row r from column d) of a unit.
@@ -173,9 +177,19 @@ __global__ void __launch_bounds__(kThreads)
   long long total;
   Cursor c;
   long long v = divide<KT, kThreads>(
-      p, RT, sc, [&](long long all) { return range_start(all, cta, p.n_ctas); }, total, c);
-  const long long v_end = range_start(total, cta + 1, p.n_ctas);
-  if (v < 0 || v >= v_end) return;
+      p, RT, sc,
+      [&](long long all) {
+        const int n = range_count(all, p.n_ctas);
+        return cta < n ? range_start(all, cta, n) : all;
+      },
+      total, c);
+  const int n_ranges = range_count(total, p.n_ctas);
+  if (v < 0) {
+    // more CTAs than steps
+    if (threadIdx.x == 0) reinterpret_cast<JoinNote*>(p.part)[cta].pieces = 0;
+    return;
+  }
+  const long long v_end = range_start(total, cta + 1, n_ranges);
   bool first_segment = true;
 
   while (true) {
@@ -528,61 +542,60 @@ __global__ void __launch_bounds__(kThreads)
         if (d == 0) *reinterpret_cast<float2*>(row + D) = make_float2(mx, ls);
       }
     }
-    first_segment = false;
     v = c.u0 + s1;
-    if (v >= v_end) break;
+    if (v >= v_end) {
+      if (threadIdx.x == 0) leave_note<KT>(p, cta, total, n_ranges, RT, c, s0, s1, first_segment);
+      break;
+    }
+    first_segment = false;
     __syncthreads();
     advance<KT>(p, RT, c);
   }
 }
 
-// Joins a unit that several CTAs worked on: block i looks at the boundary
-// between ranges i and i + 1, and takes the unit it cuts if it is the first
-// boundary inside that unit.
-template <int D, bool BF16, int STEP>
+// Joins a unit that several CTAs worked on, by the note of the CTA where it
+// begins (blockIdx.x); a thread takes four columns of a row, a block
+// kThreads * 4 / D rows.
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    paged_join_kernel(const __grid_constant__ PagedParams p, int RT) {
-  __shared__ DivideScratch sc;
+    paged_join_kernel(const __grid_constant__ PagedParams p, int rt) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int n = p.n_ctas, i = static_cast<int>(blockIdx.x);
-  long long total;
-  Cursor c;
-  const long long v = divide<STEP, kThreads>(
-      p, RT, &sc, [&](long long all) { return range_start(all, i + 1, n); }, total, c);
-  if (v < 0) return;
-  // cuts no unit, or an earlier boundary lies inside it too
-  if (v == c.u0 || range_start(total, i, n) > c.u0) return;
-  const long long u1 = c.u0 + unit_steps<STEP>(p, c.s, c.t, RT);
-  const int rows = min(RT, c.s.nq * p.G - c.t * RT);
-  for (int e = static_cast<int>(blockIdx.y * kThreads + threadIdx.x); e < rows * (D / 4);
+  const int i = static_cast<int>(blockIdx.x);
+  const JoinNote note = reinterpret_cast<const JoinNote*>(p.part)[i];
+  if (note.pieces == 0) return;
+  const int64_t step = static_cast<int64_t>(2) * rt * (D + 2);   // the next CTA's first piece
+  // (the grid has rows for the caller's bound on them, which may be too small)
+  for (int e = static_cast<int>(blockIdx.y * kThreads + threadIdx.x); e < note.rows * (D / 4);
        e += static_cast<int>(gridDim.y) * kThreads) {
     const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-    float mx = -INFINITY, ls = 0.0f;
+    const float* row0 = part_rows<D>(p, i, note.slot, rt) + r * (D + 2);
+    const float* row1 = part_rows<D>(p, i + 1, 0, rt) + r * (D + 2);
+    auto piece = [&](int k) { return k == 0 ? row0 : row1 + (k - 1) * step; };
+    float mx = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < note.pieces; ++k) mx = fmaxf(mx, piece(k)[D]);
+    const float base = mx == -INFINITY ? 0.0f : mx;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = i; k < n; ++k) {
-      const long long a = range_start(total, k, n), b = range_start(total, k + 1, n);
-      if (a >= u1) break;
-      if (a == b) continue;
-      const float* row = part_rows<D>(p, k, k == i && c.u0 > a ? 1 : 0, RT) + r * (D + 2);
-      const float2 x0 = __ldg(reinterpret_cast<const float2*>(row + d));
-      const float2 x1 = __ldg(reinterpret_cast<const float2*>(row + d + 2));
-      const float2 y = __ldg(reinterpret_cast<const float2*>(row + D));
-      if (y.x > mx) {
-        const float f = ex2(mx - y.x);
-        sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
-        ls *= f;
-        mx = y.x;
-      }
-      const float f = ex2(y.x - (mx == -INFINITY ? 0.0f : mx));
+    float ls = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < note.pieces; ++k) {
+      const float* row = piece(k);
+      const float2 x0 = *reinterpret_cast<const float2*>(row + d);
+      const float2 x1 = *reinterpret_cast<const float2*>(row + d + 2);
+      const float2 y = *reinterpret_cast<const float2*>(row + D);
+      const float f = ex2(y.x - base);
       sum.x = fmaf(x0.x, f, sum.x);
       sum.y = fmaf(x0.y, f, sum.y);
       sum.z = fmaf(x1.x, f, sum.z);
       sum.w = fmaf(x1.y, f, sum.w);
       ls = fmaf(y.y, f, ls);
     }
-    store_out4<D, BF16>(p, c, c.t * RT + r, d, sum, ls == 0.0f ? 0.0f : 1.0f / ls);
-    if (d == 0 && p.lse != nullptr) store_lse(p, c, c.t * RT + r, mx, ls);
+    Cursor c{};
+    c.s.q0 = note.q0;
+    c.h = note.head0 / p.G;
+    store_out4<D, BF16>(p, c, note.row0 + r, d, sum, ls == 0.0f ? 0.0f : 1.0f / ls);
+    if (d == 0 && p.lse != nullptr) store_lse(p, c, note.row0 + r, mx, ls);
   }
 }
 
@@ -601,11 +614,13 @@ cudaError_t launch_pdl(K kern, dim3 grid, int smem, cudaStream_t stream, const A
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, bool BF16, int STEP>
+template <int D, bool BF16>
 cudaError_t launch_join(const PagedParams& p, int rt, cudaStream_t stream) {
   if (p.n_ctas < 2) return cudaSuccess;
-  return launch_pdl(paged_join_kernel<D, BF16, STEP>, dim3(static_cast<unsigned>(p.n_ctas - 1), rt / 16), 0,
-                    stream, p, rt);
+  const int rows = p.max_rows < rt ? p.max_rows : rt, block_rows = kThreads * 4 / D;
+  return launch_pdl(paged_join_kernel<D, BF16>,
+                    dim3(static_cast<unsigned>(p.n_ctas - 1), static_cast<unsigned>((rows + block_rows - 1) / block_rows)),
+                    0, stream, p, rt);
 }
 
 template <int D, bool E4M3, bool BF16, int MT>
@@ -622,7 +637,7 @@ cudaError_t launch_one(const PagedParams& p, cudaStream_t stream) {
   }
   e = launch_pdl(kern, dim3(static_cast<unsigned>(p.n_ctas)), S::kTotal, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_join<D, BF16, KT>(p, S::RT, stream);
+  return launch_join<D, BF16>(p, S::RT, stream);
 }
 
 template <int D, bool E4M3, bool BF16>
@@ -647,10 +662,10 @@ cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m
                         : launch_dim<128>(p, rt, bf16, e4m3, stream);
 }
 
-cudaError_t launch_paged_join128(const PagedParams& p, int head_dim, bool bf16, int rt, cudaStream_t stream) {
+cudaError_t launch_paged_join(const PagedParams& p, int head_dim, bool bf16, int rt, cudaStream_t stream) {
   if (head_dim == 64)
-    return bf16 ? launch_join<64, true, 128>(p, rt, stream) : launch_join<64, false, 128>(p, rt, stream);
-  return bf16 ? launch_join<128, true, 128>(p, rt, stream) : launch_join<128, false, 128>(p, rt, stream);
+    return bf16 ? launch_join<64, true>(p, rt, stream) : launch_join<64, false>(p, rt, stream);
+  return bf16 ? launch_join<128, true>(p, rt, stream) : launch_join<128, false>(p, rt, stream);
 }
 
 }  // namespace sdpa_impl

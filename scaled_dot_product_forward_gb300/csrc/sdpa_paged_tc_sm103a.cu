@@ -39,14 +39,23 @@ __device__ unsigned int g_sdpa_paged_status = 0;
 
 namespace {
 
-constexpr int kThreads = 384;  // warp 0 loads, 1 products, 2-3 conversion; WG1, WG2 softmax
 constexpr int KT = 128;        // keys a step
 constexpr int RT = 256;        // rows a unit
-// Register split: 128 * 88 + 256 * 208 <= 384 * 168 needs 80 for the first
-// warpgroup.
-constexpr uint32_t kLaunchRegs = 168, kRegsControl = 80, kRegsSoftmax = 208;
-static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kLaunchRegs,
-              "register split exceeds the launch allocation");
+// Warp 0 loads the keys and writes the notes on each step, warp 2 loads the
+// values, warp 1 issues the products; warpgroups 1 and 2 are the softmax; with
+// e4m3 pages warpgroup 3 converts.  The register splits exhaust the launch's
+// 64K.
+template <bool E4M3>
+struct Split {
+  static constexpr int kThreads = E4M3 ? 512 : 384;
+  static constexpr uint32_t kLaunch = E4M3 ? 128 : 168;
+  static constexpr uint32_t kControl = E4M3 ? 64 : 80;   // and conversion
+  static constexpr uint32_t kSoftmax = E4M3 ? 192 : 208;
+  static_assert((kThreads - 256) * kControl + 256 * kSoftmax <= kThreads * kLaunch,
+                "register split exceeds the launch allocation");
+};
+constexpr int kConvertWarps = 4;
+constexpr uint32_t kSuspendNs = 4000;  // a waiting thread may sleep this long between its looks
 constexpr float kRescaleLog2 = 8.0f;
 constexpr uint32_t kTmemCols = 512;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
 constexpr int kGroups = KT / 16;     // 16 keys lie in one page
@@ -88,8 +97,9 @@ struct Bars {
   uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t sums;        // alternating steps: both warpgroups' sums are in tensor memory
   uint64_t fin;
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], raw_full[6], raw_empty[6];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], raw_full[4], raw_empty[4];
   uint64_t note[8];
+  int valid[4];         // a raw tile's rows before the sequence's end
   uint32_t bad[8];      // a step's groups of 16 keys without a page
   uint32_t tmem_base, abort_flag;
 };
@@ -101,8 +111,17 @@ enum Site : unsigned int {
 
 __device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, Bars* bars, uint64_t limit,
                                          unsigned int site, bool honour_abort = true) {
-  return sdpa_sched::wait_phase(bar, parity, &bars->abort_flag, &g_sdpa_paged_status, limit, site,
-                                honour_abort);
+  if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
+    if (honour_abort && *reinterpret_cast<volatile uint32_t*>(&bars->abort_flag) != 0) return false;
+    if (global_timer_ns() - t0 > limit) {
+      *reinterpret_cast<volatile uint32_t*>(&bars->abort_flag) = 1u;
+      atomicOr(&g_sdpa_paged_status, 1u | site);
+      return false;
+    }
+  }
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* bars, uint64_t limit,
                                           unsigned int site) {
@@ -129,6 +148,16 @@ struct Segment {
   int s0, s1, rows;
   bool whole, split, first;
 };
+
+// tma_load_4d to a shared-memory address.
+__device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                               int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      : "memory");
+}
 
 __device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor& c, long long v, long long v_end,
                                               bool first) {
@@ -193,7 +222,7 @@ __device__ __forceinline__ uint2 with_nan(uint2 h, uint32_t w) {
   return h;
 }
 
-// Converter warp w (0, 1): its half of a value tile's 128 rows from codes to
+// Converter warp w: its quarter of a value tile's 128 rows from codes to
 // fp16 in the swizzled layout; rows from `valid` on become zeros.  Eight lanes
 // take two rows at a time, so that both the 16-byte reads and the writes of
 // each eight touch all banks.  TAIL: rows may be past `valid` and codes may be
@@ -203,33 +232,42 @@ template <int D, bool TAIL>
 __device__ __forceinline__ bool convert_rows(const uint8_t* raw, uint8_t* tile, int w, int lane, int valid) {
   constexpr int kUnits = D / 16;  // 16-byte units of a raw row
   constexpr int kChunkBytes = KT * 128;
+  constexpr int kIters = KT / kConvertWarps * kUnits / 32, kBatch = 2;
+  // lane's row and unit in iteration 0; in the odd ones (D = 128) the unit is
+  // the other half's
   const int sub = lane & 7;
+  const int row0 = w * (KT / kConvertWarps) + (lane >> 3) * 2 + (sub >> 2);
+  const int unit0 = D == 128 ? sub : (sub & 3);
   uint32_t nan = 0;
-#pragma unroll(TAIL ? 1 : 4)
-  for (int i = 0; i < 64 * kUnits / 32; ++i) {
-    int row, unit;
-    if constexpr (D == 128) {
-      row = w * 64 + (i >> 1) * 8 + (lane >> 3) * 2 + (sub >> 2);
-      unit = (i & 1) ? sub ^ 4 : sub;
-    } else {
-      row = w * 64 + i * 8 + (lane >> 3) * 2 + (sub >> 2);
-      unit = sub & 3;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kIters; i0 += kBatch) {
+    // a batch's loads first: they may not pass the stores of the one before
+    uint4 x[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k, row = row0 + (D == 128 ? (i >> 1) : i) * 8;
+      const int unit = D == 128 && (i & 1) ? unit0 ^ 4 : unit0;
+      x[k] = *reinterpret_cast<const uint4*>(raw + row * D + unit * 16);
+      if (TAIL && row >= valid) x[k] = make_uint4(0u, 0u, 0u, 0u);
     }
-    uint4 x = *reinterpret_cast<const uint4*>(raw + row * D + unit * 16);
-    if (TAIL && row >= valid) x = make_uint4(0u, 0u, 0u, 0u);
-    uint2 h0 = halves_of(x.x), h1 = halves_of(x.y), h2 = halves_of(x.z), h3 = halves_of(x.w);
-    if constexpr (TAIL) {
-      h0 = with_nan(h0, x.x);
-      h1 = with_nan(h1, x.y);
-      h2 = with_nan(h2, x.z);
-      h3 = with_nan(h3, x.w);
-    } else {
-      nan |= nan_codes(x.x) | nan_codes(x.y) | nan_codes(x.z) | nan_codes(x.w);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k, row = row0 + (D == 128 ? (i >> 1) : i) * 8;
+      const int unit = D == 128 && (i & 1) ? unit0 ^ 4 : unit0;
+      uint2 h0 = halves_of(x[k].x), h1 = halves_of(x[k].y), h2 = halves_of(x[k].z), h3 = halves_of(x[k].w);
+      if constexpr (TAIL) {
+        h0 = with_nan(h0, x[k].x);
+        h1 = with_nan(h1, x[k].y);
+        h2 = with_nan(h2, x[k].z);
+        h3 = with_nan(h3, x[k].w);
+      } else {
+        nan |= nan_codes(x[k].x) | nan_codes(x[k].y) | nan_codes(x[k].z) | nan_codes(x[k].w);
+      }
+      uint8_t* dst = tile + (unit >> 2) * kChunkBytes + row * 128;
+      const int q = (unit & 3) * 2;
+      *reinterpret_cast<uint4*>(dst + ((q ^ (row & 7)) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+      *reinterpret_cast<uint4*>(dst + (((q + 1) ^ (row & 7)) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
     }
-    uint8_t* dst = tile + (unit >> 2) * kChunkBytes + row * 128;
-    const int q = (unit & 3) * 2;
-    *reinterpret_cast<uint4*>(dst + ((q ^ (row & 7)) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
-    *reinterpret_cast<uint4*>(dst + (((q + 1) ^ (row & 7)) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
   }
   return nan != 0;
 }
@@ -326,6 +364,12 @@ __device__ __forceinline__ int swizzled(int r, int c) {
   return ROW_BYTES == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 128 + ((c ^ (r & 7)) << 4);
 }
 
+// Two codes' values (a conversion instruction: not for the inner loops).
+__device__ __forceinline__ float2 codes_value2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // Thread's row of Q to its warpgroup's shared tile (zeros when it has none),
 // negated for a negative scale; returns the (positive) multiplier of the
 // scores, |scale| * log2(e).  For e4m3 keys the row is brought by a power of
@@ -367,16 +411,17 @@ __device__ __forceinline__ float store_query(const PagedParams& p, const uint16_
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float v[4];
-        const float2 a = unpack2<BF16>(x[8 * i + 2 * (k)]), b = unpack2<BF16>(x[8 * i + 2 * k + 1]);
+        const float2 a = unpack2<BF16>(x[8 * i + 2 * k]), b = unpack2<BF16>(x[8 * i + 2 * k + 1]);
         v[0] = a.x * up, v[1] = a.y * up, v[2] = b.x * up, v[3] = b.y * up;
 #pragma unroll
         for (int n = 0; n < q_terms(E4M3, BF16); ++n) {
           const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
           const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
           term[n][k] = lo | (hi << 16);
-          const uint2 h = with_nan(halves_of(term[n][k]), term[n][k]);
-          const float2 g0 = unpack2<false>(h.x), g1 = unpack2<false>(h.y);
-          v[0] -= g0.x, v[1] -= g0.y, v[2] -= g1.x, v[3] -= g1.y;
+          if (n + 1 < q_terms(E4M3, BF16)) {
+            const float2 g0 = codes_value2(lo), g1 = codes_value2(hi);
+            v[0] -= g0.x, v[1] -= g0.y, v[2] -= g1.x, v[3] -= g1.y;
+          }
         }
       }
 #pragma unroll
@@ -388,26 +433,30 @@ __device__ __forceinline__ float store_query(const PagedParams& p, const uint16_
   }
 }
 
-// Four consecutive K-steps (32 codes each) of D[tmem] (+)= A[smem] * B[smem]^T
+// Two consecutive K-steps (32 codes each) of D[tmem] (+)= A[smem] * B[smem]^T
 // with e4m3 operands, in one elected issue; see mma_ss_x4.
-template <uint32_t HI, int STEPS>
-__device__ __forceinline__ void mma_codes(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
-                                          uint32_t acc) {
-#pragma unroll
-  for (int k = 0; k < STEPS; ++k)
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-        "mov.b64 da, {%1, %5};\n\t"
-        "mov.b64 db, {%2, %5};\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo + 2u * k), "r"(b_lo + 2u * k), "r"(idesc), "r"(k > 0 ? 1u : acc), "n"(HI)
-        : "memory");
+template <uint32_t HI>
+__device__ __forceinline__ void mma_codes_x2(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                             uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e, q;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, %4, %4;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t"
+      "add.u32 a, %1, 2;\n\t"
+      "add.u32 b, %2, 2;\n\t"
+      "mov.b64 da, {a, %5};\n\t"
+      "mov.b64 db, {b, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, q;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(HI)
+      : "memory");
 }
 
 template <int D, bool E4M3, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v) {
   using L = Lay<D, E4M3, BF16>;
@@ -438,12 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->k_empty[i], 1);
     }
     for (int i = 0; i < L::kVStages; ++i) {
-      mbar_init(&bars->v_full[i], E4M3 ? 2 : 1);
+      mbar_init(&bars->v_full[i], E4M3 ? kConvertWarps : 1);
       mbar_init(&bars->v_empty[i], 1);
     }
     for (int i = 0; i < L::kRawStages; ++i) {
       mbar_init(&bars->raw_full[i], 1);
-      mbar_init(&bars->raw_empty[i], 2);
+      mbar_init(&bars->raw_empty[i], kConvertWarps);
     }
     for (int i = 0; i < L::kNotes; ++i) mbar_init(&bars->note[i], 1);
     bars->abort_flag = 0;
@@ -468,15 +517,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cta = static_cast<int>(blockIdx.x);
   long long total;
   Cursor c0{};
-  const long long v0 = divide<KT, kThreads>(
+  const long long v0 = divide<KT, Split<E4M3>::kThreads>(
       p, RT, reinterpret_cast<DivideScratch*>(sQ),
-      [&](long long all) { return range_start(all, cta, p.n_ctas); }, total, c0);
-  const long long v1 = v0 < 0 ? v0 : range_start(total, cta + 1, p.n_ctas);
+      [&](long long all) {
+        const int n = range_count(all, p.n_ctas);
+        return cta < n ? range_start(all, cta, n) : all;
+      },
+      total, c0);
+  const int n_ranges = range_count(total, p.n_ctas);
+  const long long v1 = v0 < 0 ? v0 : range_start(total, cta + 1, n_ranges);
+  if (v0 < 0 && threadIdx.x == 0) reinterpret_cast<JoinNote*>(p.part)[cta].pieces = 0;
   __syncthreads();
 
-  if (warp >= 4) {
+  if (warp >= 4 && warp < 12) {
     // -------------------------------------------------------- softmax
-    regs_increase<kRegsSoftmax>();
+    regs_increase<Split<E4M3>::kSoftmax>();
     const int t = (warp - 4) >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -558,8 +613,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int left = seen - s * KT;   // keys of this tile that the row sees
         if (__any_sync(0xffffffffu, left < KT) || bad != 0u) {
+          uint32_t keep[KT / 32];
 #pragma unroll
-          for (int i = 0; i < KT; ++i) x[i] = (i >= left || ((bad >> (i >> 4)) & 1u)) ? -INFINITY : x[i];
+          for (int i = 0; i < KT / 32; ++i) {
+            const int n = min(max(left - 32 * i, 0), 32);
+            keep[i] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+            if ((bad >> (2 * i)) & 1u) keep[i] &= 0xffff0000u;
+            if ((bad >> (2 * i)) & 2u) keep[i] &= 0x0000ffffu;
+          }
+#pragma unroll
+          for (int i = 0; i < KT; ++i) x[i] = ((keep[i >> 5] >> (i & 31)) & 1u) ? x[i] : -INFINITY;
         }
         bool need;
         uint32_t pk[KT / 2];
@@ -671,113 +734,131 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      first = false;
       v = c.u0 + g.s1;
-      if (v >= v_end) break;
+      if (v >= v_end) {
+        if (t == 0 && r == 0) leave_note<KT>(p, blockIdx.x, total, n_ranges, RT, c, g.s0, g.s1, first);
+        break;
+      }
+      first = false;
       advance<KT>(p, RT, c);
       __syncwarp();
       save(c, v);
     }
     tc_fence_before();
   } else {
-    regs_decrease<kRegsControl>();
-    if (warp == 0 || (!E4M3 && warp == 2)) {
+    regs_decrease<Split<E4M3>::kControl>();
+    const int P = 1 << p.page_shift;
+    // A window of 32 of a sequence's page entries in the lanes, the next one
+    // behind it; an entry that is no page becomes n_pages, out of the maps'
+    // bounds.
+    struct Window {
+      const int* row;
+      int n, at, ids, next;
+    };
+    auto entries = [&](const Window& w, int from) {
+      const int id = from + lane < w.n ? __ldg(w.row + from + lane) : -1;
+      return id >= 0 && id < p.n_pages ? id : p.n_pages;
+    };
+    auto open_window = [&](const Cursor& c, int s) {
+      Window w;
+      w.row = p.table + static_cast<int64_t>(c.b) * p.table_st;
+      w.n = (c.s.len + P - 1) >> p.page_shift;
+      w.at = (s * KT) >> p.page_shift;
+      w.ids = entries(w, w.at);
+      w.next = entries(w, w.at + 32);
+      return w;
+    };
+    // (a step's entries lie in one window: their number divides 32)
+    auto reach = [&](Window& w, int s) {
+      const int e = (s * KT) >> p.page_shift;
+      if (e - w.at >= 32) {
+        w.at += 32;
+        w.ids = w.next;
+        w.next = entries(w, w.at + 32);
+      }
+      return e;
+    };
+    if (warp == 0 || warp == 2) {
       // ----------------------------------------------------------- loads
-      // (16-bit pages: warp 0 the keys', warp 2 the values')
-      const bool keys = warp == 0;
-      RingAt<L::kKStages> k_at;
-      RingAt<E4M3 ? L::kRawStages : L::kVStages> v_at;
-      RingAt<L::kNotes> note_at;
-      int k_end = 0, v_end = 0;   // tiles issued
-      const int P = 1 << p.page_shift;
+      constexpr int kVRing = E4M3 ? L::kRawStages : L::kVStages;
+      const bool is_k = warp == 0;
+      const int ring = is_k ? L::kKStages : kVRing;
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+      uint64_t* const full0 = is_k ? bars->k_full : E4M3 ? bars->raw_full : bars->v_full;
+      uint64_t* const empty0 = is_k ? bars->k_empty : E4M3 ? bars->raw_empty : bars->v_empty;
+      const uint32_t dst0 = smem_addr(is_k ? sK : E4M3 ? smem + L::kRaw : sV);
       const int box = P < KT ? P : KT, per_step = KT / box;
+      int at = 0, issued = 0;   // ring slot, tiles issued
+      uint32_t phase = 0;
+      bool lapped = false;
+      RingAt<L::kNotes> note_at;
       for_each_segment(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
-        const int* trow = p.table + static_cast<int64_t>(c.b) * p.table_st;
-        const int n_entries = (c.s.len + P - 1) >> p.page_shift;
-        // a window of 32 page entries in the lanes, the next one behind it; an
-        // entry that is no page becomes n_pages, out of the map's bounds
-        int win0 = (g.s0 * KT) >> p.page_shift;
-        auto entries = [&](int from) {
-          const int id = from + lane < n_entries ? __ldg(trow + from + lane) : -1;
-          return id >= 0 && id < p.n_pages ? id : p.n_pages;
+        Window w = open_window(c, g.s0);
+        // keys' warp: lane i < 8 looks after keys 16 i .. of a step; its page's
+        // scales are asked for a step ahead (the entry may lie in the window
+        // behind)
+        int id = 0;
+        float ks = 1.0f, vs = 1.0f;
+        auto ask = [&](int s) {
+          const int e = ((s * KT + (lane & 7) * 16) >> p.page_shift) - w.at;
+          const int a = __shfl_sync(0xffffffffu, w.ids, e & 31), b = __shfl_sync(0xffffffffu, w.next, e & 31);
+          id = e < 32 ? a : b;
+          if (E4M3 && lane < 8 && id < p.n_pages) {
+            const int64_t at = static_cast<int64_t>(id) * p.n_kv + c.h;
+            ks = __ldg(p.k_scale + at);
+            vs = __ldg(p.v_scale + at);
+          }
         };
-        int ids = entries(win0), ids_next = entries(win0 + 32);
+        if (is_k) ask(g.s0);
         for (int s = g.s0; s < g.s1; ++s) {
-          const int e0 = (s * KT) >> p.page_shift;
-          if (e0 - win0 >= 32) {
-            win0 += 32;
-            ids = ids_next;
-            ids_next = entries(win0 + 32);
+          const int e0 = reach(w, s), row0 = (s * KT) & (P - 1);
+          if (lapped && !warp_wait(empty0 + at, phase ^ 1u, bars, limit, kSiteEmpty)) return false;
+          uint64_t* full = full0 + at;
+          const uint32_t dst = dst0 + static_cast<uint32_t>(at) * (E4M3 ? L::kCodes : L::kTile);
+          // one elected lane issues the tile's boxes
+          const bool leader = elect_one();
+          if (leader) {
+            if (E4M3 && !is_k) *reinterpret_cast<volatile int*>(&bars->valid[at]) = c.s.len - s * KT;
+            mbar_arrive_expect_tx(full, E4M3 ? L::kCodes : L::kTile);
           }
-          const int row0 = (s * KT) & (P - 1);
-          // one elected lane issues a tile's boxes
-          auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full) {
-            int id[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) id[i] = __shfl_sync(0xffffffffu, ids, (e0 - win0 + i) & 31);
-            if (elect_one()) {
-              mbar_arrive_expect_tx(full, E4M3 ? L::kCodes : L::kTile);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (i >= per_step) break;
-                if constexpr (E4M3) {
-                  tma_load_4d(dst + i * box * D, map, full, 0, row0, c.h, id[i]);
-                } else {
-#pragma unroll
-                  for (int ch = 0; ch < L::kChunks; ++ch)
-                    tma_load_4d(dst + ch * L::kChunkBytes + i * box * 128, map, full, ch * 64, row0, c.h, id[i]);
-                }
-              }
-            }
-            __syncwarp();
-          };
-          if (keys) {
-            if (k_at.lapped && !warp_wait(&bars->k_empty[k_at.idx], k_at.phase ^ 1u, bars, limit, kSiteEmpty))
-              return false;
-            load(&tm_k, sK + k_at.idx * L::kKTile, &bars->k_full[k_at.idx]);
-            k_at.next();
-            ++k_end;
-          }
-          if (E4M3 || !keys) {
-            uint64_t* empty = E4M3 ? &bars->raw_empty[v_at.idx] : &bars->v_empty[v_at.idx];
-            if (v_at.lapped && !warp_wait(empty, v_at.phase ^ 1u, bars, limit, kSiteEmpty)) return false;
-            load(&tm_v, E4M3 ? smem + L::kRaw + v_at.idx * L::kCodes : sV + v_at.idx * L::kTile,
-                 E4M3 ? &bars->raw_full[v_at.idx] : &bars->v_full[v_at.idx]);
-            v_at.next();
-            ++v_end;
-          }
-          if (!keys) continue;
-          // notes: lane i < 8 looks after keys 16 i .. of the step
-          {
-            const int e = min((s * KT + (lane & 7) * 16) >> p.page_shift, win0 + 31);
-            const int id = __shfl_sync(0xffffffffu, ids, e - win0);
-            const bool is_page = id < p.n_pages;
-            const uint32_t bad = __ballot_sync(0xffffffffu, !is_page) & 0xffu;
-            if (lane < 8) {
+#pragma unroll 2
+          for (int i = 0; i < per_step; ++i) {
+            const int id = __shfl_sync(0xffffffffu, w.ids, e0 - w.at + i);
+            if (leader) {
               if constexpr (E4M3) {
-                float4 n = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-                if (is_page) {
-                  const int64_t at = static_cast<int64_t>(id) * p.n_kv + c.h;
-                  const float vs = clamp_scale(__ldg(p.v_scale + at));
-                  n = make_float4(clamp_scale(__ldg(p.k_scale + at)), __log2f(vs), 1.0f / vs, 0.0f);
-                }
-                notes[note_at.idx * kGroups + lane] = n;
+                tma_load_4d_at(dst + i * box * D, map, full, 0, row0, c.h, id);
+              } else {
+#pragma unroll
+                for (int ch = 0; ch < L::kChunks; ++ch)
+                  tma_load_4d_at(dst + ch * L::kChunkBytes + i * box * 128, map, full, ch * 64, row0, c.h, id);
               }
-              if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&bars->bad[note_at.idx]) = bad;
             }
+          }
+          __syncwarp();
+          if (is_k) {
+            const uint32_t bad = __ballot_sync(0xffffffffu, id >= p.n_pages) & 0xffu;
+            if (E4M3 && lane < 8) {
+              vs = clamp_scale(vs);
+              notes[note_at.idx * kGroups + lane] = make_float4(clamp_scale(ks), __log2f(vs), 1.0f / vs, 0.0f);
+            }
+            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&bars->bad[note_at.idx]) = bad;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->note[note_at.idx]);
             note_at.next();
+            if (s + 1 < g.s1) ask(s + 1);
+          }
+          ++issued;
+          if (++at == ring) {
+            at = 0;
+            phase ^= 1u;
+            lapped = true;
           }
         }
         return true;
       });
       // what was issued must land before shared memory is released
-      constexpr int kN = E4M3 ? L::kRawStages : L::kVStages;
-      for (int j = max(0, k_end - L::kKStages); j < k_end; ++j)
-        wait_any(&bars->k_full[j % L::kKStages], (j / L::kKStages) & 1, bars, limit, kSiteDrain, false);
-      for (int j = max(0, v_end - kN); j < v_end; ++j)
-        wait_any(E4M3 ? &bars->raw_full[j % kN] : &bars->v_full[j % kN], (j / kN) & 1, bars, limit, kSiteDrain, false);
+      for (int j = max(0, issued - ring); j < issued; ++j)
+        wait_any(full0 + j % ring, (j / ring) & 1, bars, limit, kSiteDrain, false);
     } else if (warp == 1) {
       // -------------------------------------------------------- products
       constexpr uint32_t idS = idesc_f16_f32acc(MBF, false, 128, KT);
@@ -792,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t v_lo = desc_lo_sw128(smem_addr(sV), L::kChunkBytes);
       RingAt<L::kKStages> k_at;
       RingAt<L::kVStages> v_at;
-      uint32_t n_p[2] = {0, 0}, n_seg = 0;
+      uint32_t p_phase = 0, n_seg = 0;   // p_phase: a bit a warpgroup
       bool issued = false;
       auto issue_s = [&](int t) {
         const uint32_t a0 = q_lo + static_cast<uint32_t>(t * (L::kQTile >> 4));
@@ -800,7 +881,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (E4M3) {
 #pragma unroll
           for (int n = 0; n < q_terms(E4M3, BF16); ++n)
-            mma_codes<kHiCodes, D / 32>(tmem + (t ? 128u : 0u), a0 + n * (L::kCodes >> 4), b0, idCodes, n > 0 ? 1u : 0u);
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)
+              mma_codes_x2<kHiCodes>(tmem + (t ? 128u : 0u), a0 + n * (L::kCodes >> 4) + 4 * k, b0 + 4 * k, idCodes,
+                                     n + k > 0 ? 1u : 0u);
         } else {
 #pragma unroll
           for (int ch = 0; ch < L::kChunks; ++ch) {
@@ -843,8 +927,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       auto next_p = [&](int t) {
-        if (!warp_wait(&bars->p_ready[t], n_p[t] & 1, bars, limit, kSiteP)) return false;
-        ++n_p[t];
+        if (!warp_wait(&bars->p_ready[t], (p_phase >> t) & 1u, bars, limit, kSiteP)) return false;
+        p_phase ^= 1u << t;
         tc_fence_after();
         return true;
       };
@@ -854,47 +938,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_seg;
         tc_fence_after();
         const int n = g.s1 - g.s0;
-        if (!next_k()) return false;
         issued = true;
-        if (g.split) {
-          issue_s(0);
-          done_k();
-          if (n > 1) {
-            if (!next_k()) return false;
-            issue_s(1);
-            done_k();
-          }
-          for (int j = 0; j < n; ++j) {
-            const int t = j & 1;
-            if (!next_v(c.s.len - (g.s0 + j) * KT) || !next_p(t)) return false;
-            issue_pv(t, j > 1);
-            mma_commit_elect(&bars->v_empty[v_at.idx]);
-            v_at.next();
-            if (j + 2 < n) {
-              if (!next_k()) return false;
-              issue_s(t);
-              done_k();
+        // One place each for the two products, whatever the mode (the code of
+        // all roles together is what the instruction cache has to hold):
+        // event e is warpgroup t = e & 1's product of its step j and S of its
+        // next one, the first two only the latter.
+        const int events = g.split ? n : 2 * n;
+#pragma unroll 1
+        for (int e = -2; e < events; ++e) {
+          const int t = e & 1, j = g.split ? e : e >> 1;
+          const int ahead = j + (g.split ? 2 : 1);
+          const bool head = g.split || t == 0, tail = g.split || t == 1;   // of the step's events
+          if (e >= 0) {
+            if (head && !next_v(c.s.len - (g.s0 + j) * KT)) return false;
+            if (!next_p(t)) return false;
+            issue_pv(t, j > (g.split ? 1 : 0));
+            if (tail) {
+              mma_commit_elect(&bars->v_empty[v_at.idx]);
+              v_at.next();
             }
           }
-        } else {
-          issue_s(0);
-          issue_s(1);
-          done_k();
-          for (int j = 0; j < n; ++j) {
-            if (!next_v(c.s.len - (g.s0 + j) * KT) || !next_p(0)) return false;
-            issue_pv(0, j > 0);
-            if (j + 1 < n) {
-              if (!next_k()) return false;
-              issue_s(0);
-            }
-            if (!next_p(1)) return false;
-            issue_pv(1, j > 0);
-            mma_commit_elect(&bars->v_empty[v_at.idx]);
-            v_at.next();
-            if (j + 1 < n) {
-              issue_s(1);
-              done_k();
-            }
+          if (ahead < n) {
+            if (head && !next_k()) return false;
+            issue_s(t);
+            if (tail) done_k();
           }
         }
         return true;
@@ -903,28 +970,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit_elect(&bars->fin);
         wait_any(&bars->fin, 0, bars, limit, kSiteDrain, false);
       }
-    } else if constexpr (E4M3) {
+    } else if (E4M3 && warp >= 12) {
       // ------------------------------------------------------ conversion
+     if constexpr (E4M3) {
       RingAt<L::kVStages> v_at;
       RingAt<L::kRawStages> raw_at;
-      for_each_segment(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
-        for (int s = g.s0; s < g.s1; ++s) {
-          if (!warp_wait(&bars->raw_full[raw_at.idx], raw_at.phase, bars, limit, kSiteK)) return false;
-          if (v_at.lapped && !warp_wait(&bars->v_empty[v_at.idx], v_at.phase ^ 1u, bars, limit, kSiteEmpty))
-            return false;
-          convert_tile<D>(smem + L::kRaw + raw_at.idx * L::kCodes, sV + v_at.idx * L::kTile, warp - 2, lane,
-                          c.s.len - s * KT);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars->raw_empty[raw_at.idx]);
-            mbar_arrive(&bars->v_full[v_at.idx]);
-          }
-          raw_at.next();
-          v_at.next();
+      // the CTA's steps, whatever units they belong to
+      for (int left = static_cast<int>(min(v1 - v0, 0x7fffffffLL)); left > 0; --left) {
+        if (!warp_wait(&bars->raw_full[raw_at.idx], raw_at.phase, bars, limit, kSiteK)) break;
+        const int valid = *reinterpret_cast<volatile int*>(&bars->valid[raw_at.idx]);
+        if (v_at.lapped && !warp_wait(&bars->v_empty[v_at.idx], v_at.phase ^ 1u, bars, limit, kSiteEmpty)) break;
+        convert_tile<D>(smem + L::kRaw + raw_at.idx * L::kCodes, sV + v_at.idx * L::kTile, warp - 12, lane, valid);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->raw_empty[raw_at.idx]);
+          mbar_arrive(&bars->v_full[v_at.idx]);
         }
-        return true;
-      });
+        raw_at.next();
+        v_at.next();
+      }
+     }
     }
   }
 
@@ -943,19 +1009,19 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUte
   const uint64_t bit = 1ull << p.device;
   cudaError_t e = cudaSuccess;
   if ((configured.load(std::memory_order_relaxed) & bit) == 0) {
-    // the register split assumes kLaunchRegs a thread at launch: never start a
+    // the register split assumes kLaunch a thread at launch: never start a
     // build where that does not hold (setmaxnreg would wait)
     cudaFuncAttributes fa{};
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs != static_cast<int>(Split<E4M3>::kLaunch)) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, E4M3, BF16>::kTotal);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.n_ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Split<E4M3>::kThreads);
   cfg.dynamicSmemBytes = Lay<D, E4M3, BF16>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -965,7 +1031,7 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUte
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, p, tm_k, tm_v);
   if (e != cudaSuccess) return e;
-  return sdpa_impl::launch_paged_join128(p, D, BF16, RT, stream);
+  return sdpa_impl::launch_paged_join(p, D, BF16, RT, stream);
 }
 
 template <int D>
