@@ -480,8 +480,10 @@ class SdpaPagedCache:
     sdpa_paged_forward; it owns no device memory of its own."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
+        global _torch
         import torch
 
+        _torch = torch
         elem = {torch.bfloat16: SDPA_BF16, torch.float16: SDPA_FP16, torch.float8_e4m3fn: SDPA_CACHE_E4M3}.get(k.dtype)
         if elem is None or v.dtype != k.dtype:
             raise SdpaError(4, "SdpaPagedCache")
@@ -513,33 +515,40 @@ class SdpaPagedCache:
         ptr = [t.data_ptr() if t is not None else None for t in (k, v, k_scale, v_scale)]
         self._struct = _PagedCacheStruct(*ptr, n_pages, page_size, n_kv, dim, k.stride()[:3], v.stride()[:3], elem)
         self._ref = ctypes.byref(self._struct)
+        self._workspace = {}   # bytes that a forward needs, by (query heads, rows)
+
+
+_torch = None      # set by the first SdpaPagedCache (the calls below come after one)
 
 
 def _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, rows):
-    """Checks what append and forward share; (n_seqs, max_pages, int type code)."""
-    import torch
-
-    i32 = torch.int32
-    if page_table.dtype != i32 or kv_lens.dtype != i32 or (cu_seqlens is not None and cu_seqlens.dtype != i32):
+    """Checks what append and forward share; (n_seqs, max_pages, type code)."""
+    i32 = _torch.int32
+    if page_table.dtype is not i32 or kv_lens.dtype is not i32 or \
+            (cu_seqlens is not None and cu_seqlens.dtype is not i32):
         raise SdpaError(4, where)
-    n_seqs = kv_lens.numel()
-    if kv_lens.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != n_seqs or \
-            (cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() != n_seqs + 1)):
+    lens_shape, table_shape = kv_lens.shape, page_table.shape
+    if len(lens_shape) != 1 or len(table_shape) != 2 or table_shape[0] != lens_shape[0] or \
+            (cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != lens_shape[0] + 1)):
         raise SdpaError(3, where)
     if not kv_lens.is_contiguous() or page_table.stride(1) != 1 or \
             (cu_seqlens is not None and not cu_seqlens.is_contiguous()):
         raise SdpaError(5, where)
-    dt = _dtype_code(rows)
-    if cache.elem not in (dt, SDPA_CACHE_E4M3):
+    dtype = rows.dtype
+    dt = SDPA_BF16 if dtype is _torch.bfloat16 else SDPA_FP16 if dtype is _torch.float16 else -1
+    if dt < 0 or cache.elem not in (dt, SDPA_CACHE_E4M3):
         raise SdpaError(4, where)
-    return n_seqs, page_table.shape[1], dt
+    return lens_shape[0], table_shape[1], dt
+
+
+_Two = ctypes.c_int64 * 2
 
 
 def _two_strides(t, where):
     st = t.stride()
     if st[2] != 1:
         raise SdpaError(5, where)
-    return (ctypes.c_int64 * 2)(st[0], st[1])
+    return _Two(st[0], st[1])
 
 
 def _same_device(device, where, *tensors):
@@ -551,20 +560,19 @@ def _same_device(device, where, *tensors):
             raise SdpaError(6, where)
 
 
-def _on_device(device, stream, call):
-    """call(stream handle) with ``device`` current, memory that it allocates
-    belonging to the stream it launches on."""
-    import torch
-
+def _on_device(device, where, stream, call, *args):
+    """call(stream handle, *args) with ``device`` current, memory that it
+    allocates belonging to the stream it launches on."""
+    cuda = _torch.cuda
     if stream is not None:
         if stream.device_index != device:
-            raise SdpaError(6)
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if torch.cuda.current_device() != device:
-        with torch.cuda.device(device):
-            return call(torch.cuda.current_stream(device).cuda_stream)
-    return call(torch.cuda.current_stream(device).cuda_stream)
+            raise SdpaError(6, where)
+        with cuda.stream(stream):
+            return call(stream.cuda_stream, *args)
+    if cuda.current_device() != device:
+        with cuda.device(device):
+            return call(cuda.current_stream(device).cuda_stream, *args)
+    return call(cuda.current_stream(device).cuda_stream, *args)
 
 
 def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=None, sin=None,
@@ -583,42 +591,53 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
 
     where = "sdpa_cache_append"
     n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, k)
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype) or (q_out is not None and q_out.dtype != k.dtype):
+    dtype, shape = k.dtype, k.shape
+    if v.dtype is not dtype or (q is not None and q.dtype is not dtype) or \
+            (q_out is not None and q_out.dtype is not dtype):
         raise SdpaError(4, where)
-    total = k.shape[0]
-    if k.dim() != 3 or k.shape != v.shape or k.shape[1] != cache.n_kv_heads or k.shape[2] != cache.head_dim:
+    total = shape[0]
+    if len(shape) != 3 or v.shape != shape or shape[1] != cache.n_kv_heads or shape[2] != cache.head_dim:
         raise SdpaError(3, where)
     if (cos is None) != (sin is None) or (q is None and q_out is not None):
         raise SdpaError(1, where)
-    if q is not None and (q.dim() != 3 or q.shape[0] != total or q.shape[2] != cache.head_dim or
-                          (q_out is not None and q_out.shape != q.shape)):
-        raise SdpaError(3, where)
+    heads = 0
+    if q is not None:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != total or q_shape[2] != cache.head_dim or \
+                (q_out is not None and q_out.shape != q_shape):
+            raise SdpaError(3, where)
+        heads = q_shape[1]
     n_pos = rot = 0
     if cos is not None:
-        if cos.dtype != torch.float32 or sin.dtype != torch.float32:
+        f32 = _torch.float32
+        if cos.dtype is not f32 or sin.dtype is not f32:
             raise SdpaError(4, where)
+        n_pos, rot = (*cos.shape, 0)[:2]
         if cos.dim() != 2 or cos.shape != sin.shape:
             raise SdpaError(3, where)
         if not cos.is_contiguous() or not sin.is_contiguous():
             raise SdpaError(5, where)
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        rot *= 2
     ks, vs = _two_strides(k, where), _two_strides(v, where)
     _same_device(cache.device, where, k, v, page_table, kv_lens, cu_seqlens, cos, sin, q, q_out)
 
     def call(st):
-        qo = torch.empty_like(q, memory_format=torch.contiguous_format) if q is not None and q_out is None else q_out
+        qo, qs, qos = q_out, None, None
+        if q is not None:
+            if qo is None:
+                qo = _torch.empty(q.shape, dtype=dtype, device=q.device)
+            qs, qos = _two_strides(q, where), _two_strides(qo, where)
         rc = load_library().sdpa_cache_append(
             cache._ref, k.data_ptr(), v.data_ptr(), dt, total, ks, vs, page_table.data_ptr(), page_table.stride(0),
             max_pages, kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None, n_seqs,
             cos.data_ptr() if cos is not None else None, sin.data_ptr() if sin is not None else None, n_pos, rot,
             1 if interleaved else 0, q.data_ptr() if q is not None else None,
-            qo.data_ptr() if q is not None else None, q.shape[1] if q is not None else 0,
-            _two_strides(q, where) if q is not None else None, _two_strides(qo, where) if q is not None else None, st)
+            qo.data_ptr() if q is not None else None, heads, qs, qos, st)
         if rc != 0:
             raise SdpaError(rc, where)
         return qo
 
-    return _on_device(cache.device, stream, call)
+    return _on_device(cache.device, where, stream, call)
 
 
 def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seqlen_q=None, out=None, *,
@@ -638,41 +657,50 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
 
     where = "sdpa_paged_forward"
     n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens_q, q)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.n_kv_heads != 0:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or shape[1] % cache.n_kv_heads != 0:
         raise SdpaError(3, where)
-    total, heads = q.shape[0], q.shape[1]
+    total, heads, _ = shape
     if cu_seqlens_q is None:
         if n_seqs == 0 or total % n_seqs != 0:
             raise SdpaError(3, where)
         max_seqlen_q = total // n_seqs
     elif max_seqlen_q is None:
         raise SdpaError(1, where)
-    if out is not None and (out.dtype != q.dtype or out.shape != q.shape):
+    if out is not None and (out.dtype is not q.dtype or out.shape != shape):
         raise SdpaError(3, where)
-    want_lse = return_lse or lse is not None
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total, heads)):
+    if lse is not None and (lse.dtype is not _torch.float32 or tuple(lse.shape) != (total, heads)):
         raise SdpaError(3, where)
     qs = _two_strides(q, where)
     _same_device(cache.device, where, q, page_table, kv_lens, cu_seqlens_q, out, lse)
-    s = float("nan") if scale is None else float(scale)
 
     def call(st):
         lib = load_library()
-        o = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
-        ls = torch.empty((total, heads), dtype=torch.float32, device=q.device) if want_lse and lse is None else lse
-        size = lib.sdpa_paged_workspace_bytes(cache.head_dim, heads, cache.n_kv_heads, max_seqlen_q)
-        work = torch.empty(size, dtype=torch.uint8, device=q.device)
+        empty, dev = _torch.empty, q.device
+        o, ls = out, lse
+        if o is None:
+            o = empty(shape, dtype=q.dtype, device=dev)
+        if ls is None and return_lse:
+            ls = empty((total, heads), dtype=_torch.float32, device=dev)
+        key = (heads, max_seqlen_q)
+        size = cache._workspace.get(key)
+        if size is None:
+            size = lib.sdpa_paged_workspace_bytes(cache.head_dim, heads, cache.n_kv_heads, max_seqlen_q)
+            if len(cache._workspace) > 1000:
+                cache._workspace.clear()
+            cache._workspace[key] = size
+        work = empty(size, dtype=_torch.uint8, device=dev)
         rc = lib.sdpa_paged_forward(
-            q.data_ptr(), o.data_ptr(), ls.data_ptr() if want_lse else None, dt, cache._ref, total, heads, qs,
-            _two_strides(o, where), _arr(ls.stride()) if want_lse else None, page_table.data_ptr(),
+            q.data_ptr(), o.data_ptr(), ls.data_ptr() if ls is not None else None, dt, cache._ref, total, heads, qs,
+            _two_strides(o, where), _Two(*ls.stride()) if ls is not None else None, page_table.data_ptr(),
             page_table.stride(0), max_pages, kv_lens.data_ptr(),
             cu_seqlens_q.data_ptr() if cu_seqlens_q is not None else None, n_seqs, max_seqlen_q,
-            1 if is_causal else 0, s, work.data_ptr(), size, st)
+            1 if is_causal else 0, math.nan if scale is None else scale, work.data_ptr(), size, st)
         if rc != 0:
             raise SdpaError(rc, where)
-        return (o, ls) if want_lse else o
+        return o if ls is None else (o, ls)
 
-    return _on_device(cache.device, stream, call)
+    return _on_device(cache.device, where, stream, call)
 
 
 def sdpa_last_device_status(stream=None):

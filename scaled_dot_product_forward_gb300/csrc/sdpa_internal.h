@@ -140,11 +140,14 @@ struct PagedParams {
   const int* kv_lens;       // [n_seqs]
   const int* cu;            // [n_seqs + 1], or null: total_q / n_seqs tokens each
   int total_q, n_seqs, n_kv, G, n_pages, max_len;
+  int unit_heads, n_groups; // key/value heads of a unit, groups of them
+  int step_shift;           // keys a step = 1 << step_shift
+  int min_steps;            // of a CTA's range
   int page_shift;           // page size = 1 << page_shift
   int is_causal;
   float scale_log2;
   int max_rows;             // the caller's bound on a sequence's rows a head (>= 1)
-  float* part;              // workspace: n_ctas notes, [n_ctas][2][rows of a unit][D + 2] floats
+  float* part;              // workspace: n_ctas notes, [n_ctas][2][unit_heads][rows of a unit][D + 2] floats
   int n_ctas;               // ranges of the division (grid of the main kernel)
   int device;               // the current device (below 64)
   int debug_withhold_q;     // test hook: 1 = no products are issued, so the waits run out
@@ -180,16 +183,28 @@ cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, 
                                 cudaStream_t stream);
 constexpr int kJoinNoteBytes = 32;  // a CTA's note at the workspace's start
 
-// How a launch is divided: CTAs, rows of a unit, and whether it is the form
-// for many rows (paged_tc).
+// How a launch is divided: CTAs, rows and key/value heads of a unit, keys of
+// a step, and whether it is the form for many rows (paged_tc).
 struct PagedForm {
-  int ctas, rows;
+  int ctas, rows, heads, step_shift, min_steps;
   bool tc;
 };
-inline PagedForm paged_form(int64_t max_rows, int sms) {
-  if (max_rows <= 16) return {2 * sms, 16, false};
-  if (max_rows <= 32) return {2 * sms, 32, false};
-  return {sms, 256, true};
+// CTAs an SM of the form for few rows.  They hide each other's latencies (a
+// step is a chain of loads, conversions, two products and an exponential), as
+// many as the registers and the rings leave room for.
+constexpr int paged_per_sm(int head_dim, bool e4m3, int rows) {
+  return head_dim == 64 ? (rows == 16 ? 4 : 3) : (e4m3 && rows == 16 ? 3 : 2);
+}
+// The form for few rows has four warps, for up to four heads of a unit (as
+// many as divide the heads; tokens' rows of neighbouring heads lie together,
+// so reading them together keeps DRAM pages open), which share a head's keys
+// when there are fewer: 16 keys of a head each a step.
+inline PagedForm paged_form(int64_t max_rows, int head_dim, bool e4m3, int64_t n_kv, int sms) {
+  if (max_rows > 32) return {sms, 256, 1, 7, 2, true};
+  const int rows = max_rows <= 16 ? 16 : 32;
+  const int heads = n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1;
+  return {paged_per_sm(head_dim, e4m3, rows) * sms, rows, heads, heads == 4 ? 4 : heads == 2 ? 5 : 6,
+          heads == 4 ? 4 : 2, false};
 }
 cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile_rows,
                          cudaStream_t stream);

@@ -2,12 +2,12 @@
 // the division of a batch of uneven sequences into equal shares of key
 // tiles, and small conversions.
 //
-// A unit is (sequence, key/value head, tile of query rows); row r of a
-// sequence's nq * G rows for one key/value head is token r / G, query head
+// A unit is (sequence, group of key/value heads, tile of query rows); row r of
+// a sequence's nq * G rows for one key/value head is token r / G, query head
 // h * G + r % G, so the G query heads that share the head's keys sit in one
 // tile and its pages are read once for all of them.  A unit costs as many
-// steps as its rows see tiles of kt keys (at least one, which writes the
-// rows).  The units' steps, laid end to end, are cut into n equal ranges, one
+// steps as its rows see runs of 2^step_shift keys (at least one, which writes
+// the rows).  The units' steps, laid end to end, are cut into n equal ranges, one
 // a CTA, whatever the lengths are: the host knows none of them, they stay on
 // the device.  A range begins and ends inside a unit, so each CTA leaves at
 // most two partial units (its first and its last), kept in the workspace as
@@ -77,12 +77,12 @@ __device__ __forceinline__ int unit_keys(const PagedParams& p, const Seq& s, int
   const int last = (min((t + 1) * rt, s.nq * p.G) - 1) / p.G;
   return min(max(s.len - s.nq + last + 1, 0), s.len);
 }
-template <int KT>
 __device__ __forceinline__ int unit_steps(const PagedParams& p, const Seq& s, int t, int rt) {
-  return max((unit_keys(p, s, t, rt) + KT - 1) / KT, 1);
+  return max((unit_keys(p, s, t, rt) + (1 << p.step_shift) - 1) >> p.step_shift, 1);
 }
 
-// A position in the division: unit (b, h, t), whose steps begin at u0.
+// A position in the division: unit (b, h, t) (h: the group of heads), whose
+// steps begin at u0.
 struct Cursor {
   int b, h, t;
   long long u0;
@@ -94,11 +94,14 @@ struct DivideScratch {
   long long warp_sum[16];
   int found_b;
   long long found_u0, found_steps;
+  Seq found;
 };
 
-// Ranges of a division into at most n: never an empty one.
-__device__ __forceinline__ int range_count(long long total, int n) {
-  return total < n ? static_cast<int>(total) : n;
+// Ranges of a division: at most one a CTA, and of at least p.min_steps steps
+// (joining many short pieces costs more than it saves; never an empty range).
+__device__ __forceinline__ int range_count(const PagedParams& p, long long total) {
+  const long long n = (total + p.min_steps - 1) / p.min_steps;
+  return n < p.n_ctas ? static_cast<int>(n) : p.n_ctas;
 }
 // First step of range i of the n equal ones of `total` steps.
 __device__ __forceinline__ long long range_start(long long total, int i, int n) {
@@ -111,7 +114,7 @@ __device__ __forceinline__ long long range_start(long long total, int i, int n) 
 // block calls it.  A group of W lanes adds up a sequence's units, as many
 // sequences at a time as the block has groups; a batch of at most that many is
 // read once.
-template <int KT, int NT, class At>
+template <int NT, class At>
 __device__ __forceinline__ long long divide(const PagedParams& p, int rt, DivideScratch* sc, At&& at,
                                             long long& total, Cursor& c) {
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -122,18 +125,19 @@ __device__ __forceinline__ long long divide(const PagedParams& p, int rt, Divide
   // this thread's part of sequence b0 + tid / w; inclusive sum over the block
   // of the sequences' steps, at each group's first lane
   long long mine, incl, all;
+  Seq seq{};
   auto chunk = [&](int b0) {
     const int b = b0 + tid / w;
     mine = 0;
     if (b < p.n_seqs) {
-      const Seq s = load_seq(p, b, rt);
+      seq = load_seq(p, b, rt);
       if (!p.is_causal)
-        mine = s.nt == 0 ? 0 : static_cast<long long>(s.nt) * unit_steps<KT>(p, s, 0, rt);
+        mine = seq.nt == 0 ? 0 : static_cast<long long>(seq.nt) * unit_steps(p, seq, 0, rt);
       else
-        for (int t = sub; t < s.nt; t += w) mine += unit_steps<KT>(p, s, t, rt);
+        for (int t = sub; t < seq.nt; t += w) mine += unit_steps(p, seq, t, rt);
     }
     for (int o = 1; o < w; o <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    incl = sub == 0 ? mine * p.n_kv : 0;
+    incl = sub == 0 ? mine * p.n_groups : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -162,24 +166,25 @@ __device__ __forceinline__ long long divide(const PagedParams& p, int rt, Divide
   long long base = 0;
   for (int k = 0; k < chunks; ++k) {
     if (chunks > 1) chunk(k * per);
-    const long long u1 = base + incl, u0 = u1 - mine * p.n_kv;
+    const long long u1 = base + incl, u0 = u1 - mine * p.n_groups;
     if (sub == 0 && mine > 0 && v >= u0 && v < u1) {
       sc->found_b = k * per + tid / w;
       sc->found_u0 = u0;
       sc->found_steps = mine;
+      sc->found = seq;
     }
     base += all;
     if (v < base) break;
   }
   __syncthreads();
   c.b = sc->found_b;
-  c.s = load_seq(p, c.b, rt);
+  c.s = sc->found;
   const long long off = v - sc->found_u0;
   c.h = static_cast<int>(off < (1ll << 31) ? static_cast<int>(off) / static_cast<int>(min(sc->found_steps, 0x7fffffffll))
                                            : off / sc->found_steps);
   c.u0 = sc->found_u0 + c.h * sc->found_steps;
   for (int t0 = 0;; t0 += 32) {
-    const long long n = t0 + lane < c.s.nt ? unit_steps<KT>(p, c.s, t0 + lane, rt) : 0;
+    const long long n = t0 + lane < c.s.nt ? unit_steps(p, c.s, t0 + lane, rt) : 0;
     long long sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -199,12 +204,11 @@ __device__ __forceinline__ long long divide(const PagedParams& p, int rt, Divide
 }
 
 // The next unit (its steps begin where this one's end).
-template <int KT>
 __device__ __forceinline__ void advance(const PagedParams& p, int rt, Cursor& c) {
-  c.u0 += unit_steps<KT>(p, c.s, c.t, rt);
+  c.u0 += unit_steps(p, c.s, c.t, rt);
   if (++c.t < c.s.nt) return;
   c.t = 0;
-  if (++c.h < p.n_kv) return;
+  if (++c.h < p.n_groups) return;
   c.h = 0;
   do {
     ++c.b;
@@ -214,29 +218,29 @@ __device__ __forceinline__ void advance(const PagedParams& p, int rt, Cursor& c)
 }
 
 // The workspace: what to join, a note of each CTA's, then the partial units,
-// two a CTA of rt rows of D sums and their maximum and sum.
+// two a CTA of rt rows a head of D sums and their maximum and sum.
 struct JoinNote {
   int pieces;        // 0: no unit begins in this CTA's range and ends behind it
   int slot;          // of its piece here; the following CTAs' pieces are their first
-  int rows, row0;    // the unit's rows, the first one's number in the sequence
-  int q0, head0;     // the sequence's first row of q, the unit's first query head
-  int unused[2];
+  int rows, row0;    // the unit's rows a head, the first one's number in the sequence
+  int q0, kv_head0;  // the sequence's first row of q, the unit's first key/value head
+  int heads;         // key/value heads of a unit
+  int unused;
 };
 static_assert(sizeof(JoinNote) == sdpa_impl::kJoinNoteBytes, "workspace layout");
 
 template <int D>
 __device__ __forceinline__ float* part_rows(const PagedParams& p, int i, int slot, int rt) {
   return p.part + static_cast<int64_t>(p.n_ctas) * (sizeof(JoinNote) / 4) +
-         (static_cast<int64_t>(i) * 2 + slot) * rt * (D + 2);
+         (static_cast<int64_t>(i) * 2 + slot) * p.unit_heads * rt * (D + 2);
 }
 
 // CTA i's note: its last unit, if that begins here (with its first or a later
 // segment) and goes on behind its range.
-template <int KT>
 __device__ __forceinline__ void leave_note(const PagedParams& p, int i, long long total, int n, int rt,
                                            const Cursor& c, int s0, int s1, bool first) {
   JoinNote j{};
-  const int steps = unit_steps<KT>(p, c.s, c.t, rt);
+  const int steps = unit_steps(p, c.s, c.t, rt);
   if (s0 == 0 && s1 < steps) {
     // the range that holds the unit's last step
     const long long last = ((c.u0 + steps) * n - 1) / total;
@@ -245,7 +249,8 @@ __device__ __forceinline__ void leave_note(const PagedParams& p, int i, long lon
     j.rows = min(rt, c.s.nq * p.G - c.t * rt);
     j.row0 = c.t * rt;
     j.q0 = c.s.q0;
-    j.head0 = c.h * p.G;
+    j.kv_head0 = c.h * p.unit_heads;
+    j.heads = p.unit_heads;
   }
   reinterpret_cast<JoinNote*>(p.part)[i] = j;
 }

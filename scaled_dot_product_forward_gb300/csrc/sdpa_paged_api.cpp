@@ -122,7 +122,7 @@ void byte_strides(const sdpa_paged_cache* c, const int64_t* st, int64_t* sp, int
 
 uint64_t workspace_bytes(const sdpa_impl::PagedForm& f, int64_t head_dim) {
   return static_cast<uint64_t>(f.ctas) *
-         (sdpa_impl::kJoinNoteBytes + 2u * static_cast<uint64_t>(f.rows) * static_cast<uint64_t>(head_dim + 2) * 4u);
+         (sdpa_impl::kJoinNoteBytes + 2u * static_cast<uint64_t>(f.heads) * static_cast<uint64_t>(f.rows) * static_cast<uint64_t>(head_dim + 2) * 4u);
 }
 
 }  // namespace
@@ -236,7 +236,14 @@ uint64_t sdpa_paged_workspace_bytes(int64_t head_dim, int64_t n_heads, int64_t n
     return 0;
   int dev = 0, sms = 0;
   if (sdpa_impl::current_device(&dev, &sms) != SDPA_OK) return 0;
-  return workspace_bytes(sdpa_impl::paged_form(max_seqlen_q * (n_heads / n_kv_heads), sms), head_dim);
+  // enough for a cache of either kind
+  const int64_t rows = max_seqlen_q * (n_heads / n_kv_heads);
+  uint64_t most = 0;
+  for (const bool e4m3 : {false, true}) {
+    const uint64_t n = workspace_bytes(sdpa_impl::paged_form(rows, static_cast<int>(head_dim), e4m3, n_kv_heads, sms), head_dim);
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype dtype,
@@ -291,7 +298,7 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   s = static_cast<sdpa_status>(sdpa_impl::current_device(&dev, &sms));
   if (s != SDPA_OK) return s;
   const int64_t max_rows = (max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
-  const sdpa_impl::PagedForm form = sdpa_impl::paged_form(max_rows, sms);
+  const sdpa_impl::PagedForm form = sdpa_impl::paged_form(max_rows, static_cast<int>(D), e4m3, hkv, sms);
   if (workspace_size < workspace_bytes(form, D)) return SDPA_ERR_ARG;
   sdpa_impl::PagedParams p;
   std::memset(&p, 0, sizeof(p));
@@ -324,6 +331,10 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   p.part = static_cast<float*>(workspace);
   p.n_ctas = form.ctas;
   p.max_rows = static_cast<int>(max_rows);
+  p.unit_heads = form.heads;
+  p.n_groups = static_cast<int>(hkv) / form.heads;
+  p.step_shift = form.step_shift;
+  p.min_steps = form.min_steps;
   p.device = dev;
   cudaError_t e;
   if (form.tc) {

@@ -15,11 +15,13 @@
 // for elements down to 2^-29 of it; the factor goes into the score's).
 //
 // Bound by memory while few rows share the keys: 2 D bytes (e4m3) a key and
-// head against 4 G D operations.  Each of a CTA's four warps reads its own 16
-// keys of every 64 (16 keys lie in one page, whose entry and scales the warp
+// head against 4 G D operations.  Each of a CTA's four warps has a key/value
+// head of its own (with fewer than four heads, a share of one's keys) and reads
+// 16 keys of it a step (they lie in one page, whose entry and scales the warp
 // needs once) into its own ring of stages with asynchronous 16-byte copies and
-// multiplies from there: no block barrier and no exchange between warps until
-// the unit ends, when their sums are joined.  The tensor work is one 16 x 16
+// multiplies from there: no block barrier, and no exchange between warps but
+// for a shared head's sums at the end.  The next unit's first stages are asked
+// for before this one's rows are written.  The tensor work is one 16 x 16
 // tile a step (mma.sync; the rows of one head seldom fill it): a tcgen05 tile
 // of 128 rows would be 7/8 padding here.  The order of D inside both products
 // is free, so each thread takes 16 consecutive bytes of a key's row as they
@@ -36,14 +38,13 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kWarpKeys = 16;
-constexpr int KT = kWarps * kWarpKeys;  // keys a step
 constexpr float kRescaleLog2 = 8.0f;
 
 template <int D, bool E4M3>
 struct Ring {
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kTile = kWarpKeys * kRowBytes;  // 16 keys of K or of V
-  static constexpr int kStages = kTile == 4096 ? 3 : 4;
+  static constexpr int kStages = kTile == 1024 ? 6 : E4M3 ? 4 : 3;
   static constexpr int kWarpBytes = kStages * 2 * kTile;
 };
 
@@ -65,6 +66,9 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(full ? 16 : 0)
                : "memory");
+}
+__device__ __forceinline__ void cp_async_16_at(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -109,9 +113,15 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 struct WarpScratch {      // a warp's notes on its stages
-  float k_scale[4], v_scale[4];
-  int ok[4];              // 0: the stage's page is not one of the cache's
+  float k_scale[6], v_scale[6];
+  int ok[6];              // 0: the stage's page is not one of the cache's
 };
 
 template <int D, bool E4M3, bool BF16, int MT>
@@ -125,34 +135,35 @@ struct Smem {
   static constexpr int kNotes = kBulk;
   static constexpr int kMl = kNotes + static_cast<int>(sizeof(WarpScratch)) * kWarps;
   static constexpr int kDivide = (kMl + kWarps * RT * 8 + 15) / 16 * 16;
-  // Not below 80 KB: two CTAs an SM and never three, or the kernel's equal
-  // shares land on some SMs three at a time and on others one.
+  // Exactly kPerSm CTAs an SM: with room for more, the kernel's equal shares
+  // would land on some SMs one more at a time and on others one fewer.
+  static constexpr int kPerSm = sdpa_impl::paged_per_sm(D, E4M3, RT);
   static constexpr int kNeed = kDivide + static_cast<int>(sizeof(DivideScratch));
-  static constexpr int kTotal = kNeed > 80 * 1024 ? kNeed : 80 * 1024;
-  static_assert(2 * (kTotal + 1024) <= 227 * 1024, "two CTAs an SM");
+  static constexpr int kLeast = 227 * 1024 / (kPerSm + 1);
+  static constexpr int kTotal = kNeed > kLeast ? kNeed : kLeast;
+  static_assert(kPerSm * (kTotal + 1024) <= 228 * 1024, "CTAs an SM");
 };
 
-// Writes a finished element group (4 values of row r from column d) of a unit.
-template <int D, bool BF16>
-__device__ __forceinline__ void store_out4(const PagedParams& p, const Cursor& c, int row, int d,
-                                           const float4& o, float inv) {
-  const int i = row / p.G, g = row - i * p.G;
-  uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (static_cast<int64_t>(c.s.q0) + i) * p.o_st +
-                  (static_cast<int64_t>(c.h) * p.G + g) * p.o_sh + d;
-  *reinterpret_cast<uint2*>(dst) =
-      make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+// Row r of a sequence's rows for key/value head h: its place in out, and its
+// log-sum-exp.
+__device__ __forceinline__ uint16_t* out_row(const PagedParams& p, int q0, int h, int r) {
+  const int i = r / p.G, g = r - i * p.G;
+  return reinterpret_cast<uint16_t*>(p.out) + (static_cast<int64_t>(q0) + i) * p.o_st +
+         (static_cast<int64_t>(h) * p.G + g) * p.o_sh;
 }
-__device__ __forceinline__ void store_lse(const PagedParams& p, const Cursor& c, int row, float m,
-                                          float l) {
-  const int i = row / p.G, g = row - i * p.G;
+__device__ __forceinline__ void store_lse(const PagedParams& p, int q0, int h, int r, float m, float l) {
+  const int i = r / p.G, g = r - i * p.G;
   constexpr float kLn2 = 0.693147180559945309f;
-  p.lse[(static_cast<int64_t>(c.s.q0) + i) * p.lse_st +
-        (static_cast<int64_t>(c.h) * p.G + g) * p.lse_sh] =
+  p.lse[(static_cast<int64_t>(q0) + i) * p.lse_st + (static_cast<int64_t>(h) * p.G + g) * p.lse_sh] =
       l == 0.0f ? -INFINITY : (log2f(l) + m) * kLn2;
+}
+template <int D, bool BF16>
+__device__ __forceinline__ void store_out4(uint16_t* at, const float4& o, float inv) {
+  *reinterpret_cast<uint2*>(at) = make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
 }
 
 template <int D, bool E4M3, bool BF16, int MT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 * MT))
     paged_kernel(const __grid_constant__ PagedParams p) {
   using S = Smem<D, E4M3, BF16, MT>;
   using R = Ring<D, E4M3>;
@@ -164,40 +175,131 @@ __global__ void __launch_bounds__(kThreads)
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
-  uint8_t* ring = smem + warp * R::kWarpBytes;
+  uint8_t* const ring = smem + warp * R::kWarpBytes;
   const uint32_t ring_addr = smem_addr(ring);
   WarpScratch* notes = reinterpret_cast<WarpScratch*>(smem + S::kNotes) + warp;
   float* ml = reinterpret_cast<float*>(smem + S::kMl);  // [warp][RT][2]
   DivideScratch* sc = reinterpret_cast<DivideScratch*>(smem + S::kDivide);
 
   grid_dependency_wait();
-  grid_launch_dependents();
 
   const int cta = static_cast<int>(blockIdx.x);
   long long total;
   Cursor c;
-  long long v = divide<KT, kThreads>(
+  long long v = divide<kThreads>(
       p, RT, sc,
       [&](long long all) {
-        const int n = range_count(all, p.n_ctas);
+        const int n = range_count(p, all);
         return cta < n ? range_start(all, cta, n) : all;
       },
       total, c);
-  const int n_ranges = range_count(total, p.n_ctas);
+  const int n_ranges = range_count(p, total);
   if (v < 0) {
     // more CTAs than steps
     if (threadIdx.x == 0) reinterpret_cast<JoinNote*>(p.part)[cta].pieces = 0;
     return;
   }
   const long long v_end = range_start(total, cta + 1, n_ranges);
-  bool first_segment = true;
+  // this warp's head of a unit's, and its share of the head's keys
+  const int hsub = warp % p.unit_heads, slice = warp / p.unit_heads;
+  const int slices = kWarps / p.unit_heads;
+  const int page_mask = (1 << p.page_shift) - 1;
 
+  // a lane's share of a 16-row tile: piece cc of rows r0, r0 + kRowsAtOnce, ..
+  constexpr int kPieces = RB / 16;
+  constexpr int kRowsAtOnce = 32 / kPieces;
+  const int r0 = lane / kPieces, cc = lane % kPieces;
+  const int64_t k_step = kRowsAtOnce * p.k_st, v_step = kRowsAtOnce * p.v_st;
+
+  // The warp's loads: a segment's steps [s0, s1) of a unit's keys.
+  struct Loads {
+    const int* trow;
+    const uint8_t *kh, *vh;
+    int64_t scale_at;
+    int s0, s1, keys, len;
+    int ids_at, ids, ids_next;   // lane i: the page entry of step ids_at + i
+  };
+  auto key_of = [&](int s) { return (s << p.step_shift) + slice * kWarpKeys; };
+  auto load_ids = [&](const Loads& a, int s) {
+    const int key0 = key_of(s + lane);
+    return (s + lane < a.s1 && key0 < a.keys) ? __ldg(a.trow + (key0 >> p.page_shift)) : -1;
+  };
+  auto issue = [&](Loads& a, int s, int stage) {
+    if (s < a.s1) {
+      if (s - a.ids_at == 32) {
+        a.ids = a.ids_next;
+        a.ids_at += 32;
+        a.ids_next = load_ids(a, a.ids_at + 32);
+      }
+      const int page = __shfl_sync(0xffffffffu, a.ids, s - a.ids_at);
+      const int key0 = key_of(s);
+      const bool ok = page >= 0 && page < p.n_pages;
+      const int64_t pg = ok ? page : 0;
+      const int tok = key0 & page_mask;
+      if (key0 < a.keys) {
+        const uint8_t* ks = a.kh + (pg * p.k_sp + tok * p.k_st);
+        const uint8_t* vs = a.vh + (pg * p.v_sp + tok * p.v_st);
+        const uint32_t dst = ring_addr + stage * 2 * R::kTile;
+        if (ok && key0 + kWarpKeys <= a.len) {
+#pragma unroll
+          for (int i = 0; i < kWarpKeys / kRowsAtOnce; ++i) {
+            cp_async_16_at(dst + piece_at<RB, false>(r0 + i * kRowsAtOnce, cc), ks);
+            cp_async_16_at(dst + R::kTile + piece_at<RB, true>(r0 + i * kRowsAtOnce, cc), vs);
+            ks += k_step;
+            vs += v_step;
+          }
+        } else {
+          // rows past the sequence's end, and a page that is none, read as
+          // zeros: their weights are zero, and a stale NaN there must not
+          // meet them
+#pragma unroll
+          for (int i = 0; i < kWarpKeys / kRowsAtOnce; ++i) {
+            const int r = r0 + i * kRowsAtOnce;
+            const bool in = ok && key0 + r < a.len;
+            cp16(dst + piece_at<RB, false>(r, cc), ks, in);
+            cp16(dst + R::kTile + piece_at<RB, true>(r, cc), vs, in);
+            ks += k_step;
+            vs += v_step;
+          }
+        }
+        if (lane < 2) {
+          if constexpr (E4M3) {
+            const float* src = (lane == 0 ? p.k_scale : p.v_scale) + pg * p.n_kv + a.scale_at;
+            cp4(smem_addr(lane == 0 ? &notes->k_scale[stage] : &notes->v_scale[stage]), src);
+          }
+          if (lane == 0) notes->ok[stage] = ok ? 1 : 0;
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  auto open = [&](const Cursor& cu, long long from) {
+    Loads a;
+    const int h = cu.h * p.unit_heads + hsub;
+    a.trow = p.table + static_cast<int64_t>(cu.b) * p.table_st;
+    a.kh = p.k + h * p.k_sh + r0 * p.k_st + cc * 16;   // this lane's piece
+    a.vh = p.v + h * p.v_sh + r0 * p.v_st + cc * 16;
+    a.scale_at = h;
+    a.keys = unit_keys(p, cu.s, cu.t, RT);
+    a.len = cu.s.len;
+    a.s0 = static_cast<int>(from - cu.u0);
+    a.s1 = static_cast<int>(min(static_cast<long long>(unit_steps(p, cu.s, cu.t, RT)), v_end - cu.u0));
+    a.ids_at = a.s0;
+    a.ids = load_ids(a, a.s0);
+    a.ids_next = load_ids(a, a.s0 + 32);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < R::kStages - 1; ++i) issue(a, a.s0 + i, i);
+    return a;
+  };
+
+  Loads ld = open(c, v);
+  bool first_segment = true;
   while (true) {
-    const int steps = unit_steps<KT>(p, c.s, c.t, RT);
-    const int s0 = static_cast<int>(v - c.u0);
-    const int s1 = static_cast<int>(min(static_cast<long long>(steps), v_end - c.u0));
+    const int s0 = ld.s0, s1 = ld.s1, keys = ld.keys;
+    const bool whole = s0 == 0 && s1 == unit_steps(p, c.s, c.t, RT);
     const int rows = min(RT, c.s.nq * p.G - c.t * RT);
-    const int keys = unit_keys(p, c.s, c.t, RT);
+    const int head = c.h * p.unit_heads + hsub;
 
     // the rows' queries as operand fragments, and how many keys each sees
     uint32_t qf[MT][NK][4];
@@ -216,7 +318,7 @@ __global__ void __launch_bounds__(kThreads)
         if (live) lim_min = min(lim_min, lim[mt][hf]);
         const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) +
                               (static_cast<int64_t>(c.s.q0) + i) * p.q_st +
-                              (static_cast<int64_t>(c.h) * p.G + g) * p.q_sh;
+                              (static_cast<int64_t>(head) * p.G + g) * p.q_sh;
         uint2 w[NK];
 #pragma unroll
         for (int ks = 0; ks < NK; ++ks) {
@@ -266,69 +368,12 @@ __global__ void __launch_bounds__(kThreads)
       l[mt][0] = l[mt][1] = 0.0f;
     }
 
-    // Page entries: lane i holds the entry of step `ids_at + i`'s 16 keys.
-    const int* trow = p.table + static_cast<int64_t>(c.b) * p.table_st;
-    auto load_ids = [&](int s) {
-      const int key0 = (s + lane) * KT + warp * kWarpKeys;
-      return (s + lane < s1 && key0 < keys) ? __ldg(trow + (key0 >> p.page_shift)) : -1;
-    };
-    int ids_at = s0;
-    int ids = load_ids(s0), ids_next = load_ids(s0 + 32);
-    const int page_mask = (1 << p.page_shift) - 1;
-    const uint8_t* kh = p.k + c.h * p.k_sh;
-    const uint8_t* vh = p.v + c.h * p.v_sh;
-
-    auto issue = [&](int s, int stage) {
-      if (s < s1) {
-        if (s - ids_at == 32) {
-          ids = ids_next;
-          ids_at += 32;
-          ids_next = load_ids(ids_at + 32);
-        }
-        const int page = __shfl_sync(0xffffffffu, ids, s - ids_at);
-        const int key0 = s * KT + warp * kWarpKeys;
-        const bool ok = page >= 0 && page < p.n_pages;
-        const int64_t pg = ok ? page : 0;
-        const int tok = key0 & page_mask;
-        if (key0 < keys) {
-          constexpr int kPieces = RB / 16;
-          constexpr int kRowsAtOnce = 32 / kPieces;
-          const int r0 = lane / kPieces, cc = lane % kPieces;
-          const uint8_t* ks = kh + pg * p.k_sp + (tok + r0) * p.k_st + cc * 16;
-          const uint8_t* vs = vh + pg * p.v_sp + (tok + r0) * p.v_st + cc * 16;
-          const uint32_t dst = ring_addr + stage * 2 * R::kTile;
-#pragma unroll
-          for (int i = 0; i < kWarpKeys / kRowsAtOnce; ++i) {
-            const int r = r0 + i * kRowsAtOnce;
-            // rows past the sequence's end read as zeros: their weights are
-            // zero, and a stale NaN there must not meet them
-            const bool in = ok && key0 + r < c.s.len;
-            cp16(dst + piece_at<RB, false>(r, cc), ks + i * kRowsAtOnce * p.k_st, in);
-            cp16(dst + R::kTile + piece_at<RB, true>(r, cc), vs + i * kRowsAtOnce * p.v_st, in);
-          }
-          if (lane < 2) {
-            if constexpr (E4M3) {
-              const float* src = (lane == 0 ? p.k_scale : p.v_scale) + pg * p.n_kv + c.h;
-              cp4(smem_addr(lane == 0 ? &notes->k_scale[stage] : &notes->v_scale[stage]), src);
-            }
-            if (lane == 0) notes->ok[stage] = ok ? 1 : 0;
-          }
-        }
-      }
-      cp_async_commit();
-    };
-
-#pragma unroll
-    for (int i = 0; i < R::kStages - 1; ++i) issue(s0 + i, i);
     int stage = 0;
     for (int s = s0; s < s1; ++s) {
       cp_async_wait<R::kStages - 2>();
       __syncwarp();
-      {
-        const int ahead = stage == 0 ? R::kStages - 1 : stage - 1;
-        issue(s + R::kStages - 1, ahead);
-      }
-      const int key0 = s * KT + warp * kWarpKeys;
+      issue(ld, s + R::kStages - 1, stage == 0 ? R::kStages - 1 : stage - 1);
+      const int key0 = key_of(s);
       if (key0 < keys && notes->ok[stage] != 0) {
         const uint8_t* kt = ring + stage * 2 * R::kTile;
         const uint8_t* vt = kt + R::kTile;
@@ -368,25 +413,37 @@ __global__ void __launch_bounds__(kThreads)
           ksc = clamp_scale(notes->k_scale[stage]);
           const float vsc = clamp_scale(notes->v_scale[stage]);
           lv = lg2(vsc);
-          ivs = 1.0f / vsc;
+          ivs = rcp(vsc);
         }
-        const bool all_seen = key0 + kWarpKeys <= lim_min;
         bool grow = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float f = mul[mt][hf] * ksc;
+            float* x = acc[mt][0] + 2 * hf;
+            float* y = acc[mt][1] + 2 * hf;
+            x[0] = fmaf(x[0], f, lv);
+            x[1] = fmaf(x[1], f, lv);
+            y[0] = fmaf(y[0], f, lv);
+            y[1] = fmaf(y[1], f, lv);
+          }
+        if (key0 + kWarpKeys > lim_min) {
+          // some row does not see some of these keys
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& x = acc[mt][n][2 * hf + e];
-                x = fmaf(x, f, lv);
-                if (!all_seen && key0 + n * 8 + t4 * 2 + e >= lim[mt][hf]) x = -INFINITY;
-                grow |= x > m[mt][hf] + kRescaleLog2;
-              }
-          }
+              for (int e = 0; e < 4; ++e)
+                if (key0 + n * 8 + t4 * 2 + (e & 1) >= lim[mt][e >> 1]) acc[mt][n][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            grow |= fmaxf(max3f(acc[mt][0][2 * hf], acc[mt][0][2 * hf + 1], acc[mt][1][2 * hf]),
+                          acc[mt][1][2 * hf + 1]) > m[mt][hf] + kRescaleLog2;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -477,125 +534,180 @@ __global__ void __launch_bounds__(kThreads)
       stage = stage + 1 == R::kStages ? 0 : stage + 1;
     }
 
-    // Join the warps: each leaves its rows' maximum, sum and O (over its own
-    // ring, which holds no copies in flight any more).
-    cp_async_wait<0>();
-    __syncthreads();
+    // the next unit
+    const long long v_next = c.u0 + s1;
+    const bool more = v_next < v_end;
+    // The join may start only now: its blocks, waiting early, would take the
+    // place of CTAs of the next call's kernel on some SMs and leave those
+    // behind (64 sequences up to 4096 tokens: 110 us a call, so 72).
+    if (!more) grid_launch_dependents();
+    Cursor next = c;
+    if (more) {
+      advance(p, RT, next);
+      if (slices == 1) ld = open(next, v_next);
+    } else if (threadIdx.x == 0) {
+      leave_note(p, cta, total, n_ranges, RT, c, s0, s1, first_segment);
+    }
+
+    // Accumulator columns 2 t4 and 2 t4 + 1 of group j are elements j of the
+    // runs 2 t4 and 2 t4 + 1; column of element j of run n:
+    auto column = [](int n, int j) {
+      return (E4M3 || D == 64) ? n * NV + j : (j < 8 ? 8 * n + j : 64 + 8 * n + j - 8);
+    };
+    float* part = part_rows<D>(p, cta, first_segment ? 0 : 1, RT) + hsub * RT * (D + 2);
+    if (slices > 1) {
+      // join the head's warps: each leaves its rows' maximum, sum and O (over
+      // its own ring, which holds no copies in flight any more)
+      cp_async_wait<0>();
+      __syncthreads();
+    }
     float* join = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float x = l[mt][hf];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        float ls = l[mt][hf];
+        ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+        const float mx = m[mt][hf];
         const int r = mt * 16 + hf * 8 + g8;
-        if (t4 == 0) {
-          ml[(warp * RT + r) * 2] = m[mt][hf];
-          ml[(warp * RT + r) * 2 + 1] = x;
-        }
-        if (r < rows) {
-          float* row = join + (warp * RT + r) * S::kJoinRow;
-          // accumulator columns 2 t4 and 2 t4 + 1 of group j are elements j of
-          // the runs g8 = 2 t4 and 2 t4 + 1
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int run = 2 * t4 + e;
-#pragma unroll
-            for (int j = 0; j < NV; j += 4) {
-              const int d = (E4M3 || D == 64) ? run * NV + j : (j < 8 ? 8 * run + j : 64 + 8 * run + j - 8);
-              *reinterpret_cast<float4*>(row + d) =
-                  make_float4(o[mt][j][2 * hf + e], o[mt][j + 1][2 * hf + e],
-                              o[mt][j + 2][2 * hf + e], o[mt][j + 3][2 * hf + e]);
-            }
+        if (slices > 1) {
+          if (t4 == 0) {
+            ml[(warp * RT + r) * 2] = mx;
+            ml[(warp * RT + r) * 2 + 1] = ls;
           }
         }
-      }
-    __syncthreads();
-    const bool whole = s0 == 0 && s1 == steps;
-    float* part = part_rows<D>(p, blockIdx.x, first_segment ? 0 : 1, RT);
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-      float mx = ml[r * 2];
+        if (r >= rows) continue;
+        if (slices > 1 || !whole) {
+          float* row = slices > 1 ? join + (warp * RT + r) * S::kJoinRow : part + r * (D + 2);
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, ml[(w * RT + r) * 2]);
-      const float base = mx == -INFINITY ? 0.0f : mx;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      float ls = 0.0f;
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float a = ex2(ml[(w * RT + r) * 2] - base);
-        const float4 x = *reinterpret_cast<const float4*>(join + (w * RT + r) * S::kJoinRow + d);
-        sum.x = fmaf(x.x, a, sum.x);
-        sum.y = fmaf(x.y, a, sum.y);
-        sum.z = fmaf(x.z, a, sum.z);
-        sum.w = fmaf(x.w, a, sum.w);
-        ls = fmaf(ml[(w * RT + r) * 2 + 1], a, ls);
+            for (int j = 0; j < NV; j += 2)
+              *reinterpret_cast<float2*>(row + column(2 * t4 + e, j)) =
+                  make_float2(o[mt][j][2 * hf + e], o[mt][j + 1][2 * hf + e]);
+          if (slices == 1 && t4 == 0) *reinterpret_cast<float2*>(row + D) = make_float2(mx, ls);
+        } else {
+          const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < NV; j += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2<BF16>(o[mt][j + 2 * k][2 * hf + e] * inv, o[mt][j + 2 * k + 1][2 * hf + e] * inv);
+              *reinterpret_cast<uint4*>(out_row(p, c.s.q0, head, c.t * RT + r) + column(2 * t4 + e, j)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          if (t4 == 0 && p.lse != nullptr) store_lse(p, c.s.q0, head, c.t * RT + r, mx, ls);
+        }
       }
-      if (whole) {
-        store_out4<D, BF16>(p, c, c.t * RT + r, d, sum, ls == 0.0f ? 0.0f : 1.0f / ls);
-        if (d == 0 && p.lse != nullptr) store_lse(p, c, c.t * RT + r, mx, ls);
-      } else {
-        float* row = part + r * (D + 2);
-        *reinterpret_cast<float2*>(row + d) = make_float2(sum.x, sum.y);
-        *reinterpret_cast<float2*>(row + d + 2) = make_float2(sum.z, sum.w);
-        if (d == 0) *reinterpret_cast<float2*>(row + D) = make_float2(mx, ls);
+    if (slices > 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < p.unit_heads * rows * (D / 4); i += kThreads) {
+        const int d = (i % (D / 4)) * 4, hr = i / (D / 4);
+        const int hs = hr / rows, r = hr - hs * rows;
+        float mx = -INFINITY;
+        for (int w = hs; w < kWarps; w += p.unit_heads) mx = fmaxf(mx, ml[(w * RT + r) * 2]);
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float ls = 0.0f;
+        for (int w = hs; w < kWarps; w += p.unit_heads) {
+          const float a = ex2(ml[(w * RT + r) * 2] - base);
+          const float4 x = *reinterpret_cast<const float4*>(join + (w * RT + r) * S::kJoinRow + d);
+          sum.x = fmaf(x.x, a, sum.x);
+          sum.y = fmaf(x.y, a, sum.y);
+          sum.z = fmaf(x.z, a, sum.z);
+          sum.w = fmaf(x.w, a, sum.w);
+          ls = fmaf(ml[(w * RT + r) * 2 + 1], a, ls);
+        }
+        const int hd = c.h * p.unit_heads + hs;
+        if (whole) {
+          store_out4<D, BF16>(out_row(p, c.s.q0, hd, c.t * RT + r) + d, sum, ls == 0.0f ? 0.0f : 1.0f / ls);
+          if (d == 0 && p.lse != nullptr) store_lse(p, c.s.q0, hd, c.t * RT + r, mx, ls);
+        } else {
+          float* row = part_rows<D>(p, cta, first_segment ? 0 : 1, RT) + (hs * RT + r) * (D + 2);
+          *reinterpret_cast<float2*>(row + d) = make_float2(sum.x, sum.y);
+          *reinterpret_cast<float2*>(row + d + 2) = make_float2(sum.z, sum.w);
+          if (d == 0) *reinterpret_cast<float2*>(row + D) = make_float2(mx, ls);
+        }
       }
+      __syncthreads();
     }
-    v = c.u0 + s1;
-    if (v >= v_end) {
-      if (threadIdx.x == 0) leave_note<KT>(p, cta, total, n_ranges, RT, c, s0, s1, first_segment);
-      break;
-    }
+    if (!more) break;
     first_segment = false;
-    __syncthreads();
-    advance<KT>(p, RT, c);
+    c = next;
+    v = v_next;
+    if (slices > 1) ld = open(c, v);
   }
 }
 
 // Joins a unit that several CTAs worked on, by the note of the CTA where it
-// begins (blockIdx.x); a thread takes four columns of a row, a block
-// kThreads * 4 / D rows.
+// begins (blockIdx.x).  A warp takes a row: lane k reads piece k's maximum and
+// sum, then each lane four columns of one piece after the other (head size 64:
+// half the lanes every second piece).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
     paged_join_kernel(const __grid_constant__ PagedParams p, int rt) {
   grid_dependency_wait();
-  grid_launch_dependents();
   const int i = static_cast<int>(blockIdx.x);
   const JoinNote note = reinterpret_cast<const JoinNote*>(p.part)[i];
   if (note.pieces == 0) return;
-  const int64_t step = static_cast<int64_t>(2) * rt * (D + 2);   // the next CTA's first piece
+  constexpr int kCols = D / 4, kSplit = 32 / kCols;
+  const int lane = threadIdx.x & 31, d = (lane % kCols) * 4, first = lane / kCols;
+  const int64_t step = static_cast<int64_t>(2) * note.heads * rt * (D + 2);   // the next CTA's first piece
   // (the grid has rows for the caller's bound on them, which may be too small)
-  for (int e = static_cast<int>(blockIdx.y * kThreads + threadIdx.x); e < note.rows * (D / 4);
-       e += static_cast<int>(gridDim.y) * kThreads) {
-    const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-    const float* row0 = part_rows<D>(p, i, note.slot, rt) + r * (D + 2);
-    const float* row1 = part_rows<D>(p, i + 1, 0, rt) + r * (D + 2);
+  for (int hr = static_cast<int>(blockIdx.y * kWarps + (threadIdx.x >> 5)); hr < note.heads * note.rows;
+       hr += static_cast<int>(gridDim.y) * kWarps) {
+    const int hs = hr / note.rows, r = hr - hs * note.rows;
+    const float* row0 = part_rows<D>(p, i, note.slot, rt) + (hs * rt + r) * (D + 2);
+    const float* row1 = part_rows<D>(p, i + 1, 0, rt) + (hs * rt + r) * (D + 2);
     auto piece = [&](int k) { return k == 0 ? row0 : row1 + (k - 1) * step; };
-    float mx = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < note.pieces; ++k) mx = fmaxf(mx, piece(k)[D]);
-    const float base = mx == -INFINITY ? 0.0f : mx;
+    float mx = -INFINITY, ls = 0.0f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ls = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k < note.pieces; ++k) {
-      const float* row = piece(k);
-      const float2 x0 = *reinterpret_cast<const float2*>(row + d);
-      const float2 x1 = *reinterpret_cast<const float2*>(row + d + 2);
-      const float2 y = *reinterpret_cast<const float2*>(row + D);
-      const float f = ex2(y.x - base);
-      sum.x = fmaf(x0.x, f, sum.x);
-      sum.y = fmaf(x0.y, f, sum.y);
-      sum.z = fmaf(x1.x, f, sum.z);
-      sum.w = fmaf(x1.y, f, sum.w);
-      ls = fmaf(y.y, f, ls);
+    for (int k0 = 0; k0 < note.pieces; k0 += 32) {
+      const int n = min(note.pieces - k0, 32);
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (lane < n) ml = *reinterpret_cast<const float2*>(piece(k0 + lane) + D);
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (top > mx) {
+        const float f = ex2(mx - top);   // 0 for the first pieces
+        sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
+        ls *= f;
+        mx = top;
+      }
+      const float f = ex2(ml.x - (mx == -INFINITY ? 0.0f : mx));
+      float l = ml.y * f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      ls += l;
+#pragma unroll 8
+      for (int k = 0; k < n; k += kSplit) {
+        const float fk = __shfl_sync(0xffffffffu, f, (k + first) & 31);
+        if (kSplit == 1 || k + first < n) {
+          const float* row = piece(k0 + k + first) + d;
+          const float2 x0 = *reinterpret_cast<const float2*>(row);
+          const float2 x1 = *reinterpret_cast<const float2*>(row + 2);
+          sum.x = fmaf(x0.x, fk, sum.x);
+          sum.y = fmaf(x0.y, fk, sum.y);
+          sum.z = fmaf(x1.x, fk, sum.z);
+          sum.w = fmaf(x1.y, fk, sum.w);
+        }
+      }
     }
-    Cursor c{};
-    c.s.q0 = note.q0;
-    c.h = note.head0 / p.G;
-    store_out4<D, BF16>(p, c, note.row0 + r, d, sum, ls == 0.0f ? 0.0f : 1.0f / ls);
-    if (d == 0 && p.lse != nullptr) store_lse(p, c, note.row0 + r, mx, ls);
+    if (kSplit == 2) {
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, 16);
+      sum.y += __shfl_xor_sync(0xffffffffu, sum.y, 16);
+      sum.z += __shfl_xor_sync(0xffffffffu, sum.z, 16);
+      sum.w += __shfl_xor_sync(0xffffffffu, sum.w, 16);
+    }
+    const int h = note.kv_head0 + hs;
+    if (first == 0)
+      store_out4<D, BF16>(out_row(p, note.q0, h, note.row0 + r) + d, sum, ls == 0.0f ? 0.0f : 1.0f / ls);
+    if (lane == 0 && p.lse != nullptr) store_lse(p, note.q0, h, note.row0 + r, mx, ls);
   }
 }
 
@@ -617,7 +729,9 @@ cudaError_t launch_pdl(K kern, dim3 grid, int smem, cudaStream_t stream, const A
 template <int D, bool BF16>
 cudaError_t launch_join(const PagedParams& p, int rt, cudaStream_t stream) {
   if (p.n_ctas < 2) return cudaSuccess;
-  const int rows = p.max_rows < rt ? p.max_rows : rt, block_rows = kThreads * 4 / D;
+  // a row a warp, or four when there are many
+  const int rows = (p.max_rows < rt ? p.max_rows : rt) * p.unit_heads;
+  const int block_rows = rows <= 64 ? kWarps : 4 * kWarps;
   return launch_pdl(paged_join_kernel<D, BF16>,
                     dim3(static_cast<unsigned>(p.n_ctas - 1), static_cast<unsigned>((rows + block_rows - 1) / block_rows)),
                     0, stream, p, rt);

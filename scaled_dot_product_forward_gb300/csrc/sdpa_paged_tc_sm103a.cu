@@ -161,7 +161,7 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* 
 
 __device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor& c, long long v, long long v_end,
                                               bool first) {
-  const int steps = unit_steps<KT>(p, c.s, c.t, RT);
+  const int steps = unit_steps(p, c.s, c.t, RT);
   Segment g;
   g.s0 = static_cast<int>(v - c.u0);
   g.s1 = static_cast<int>(min(static_cast<long long>(steps), v_end - c.u0));
@@ -183,7 +183,7 @@ __device__ __forceinline__ void for_each_segment(const PagedParams& p, Cursor c,
     if (!f(c, g)) return;
     first = false;
     v = c.u0 + g.s1;
-    if (v < v_end) advance<KT>(p, RT, c);
+    if (v < v_end) advance(p, RT, c);
   }
 }
 
@@ -510,21 +510,20 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   grid_dependency_wait();
-  grid_launch_dependents();
   const uint32_t tmem = bars->tmem_base;
 
   // the division, in the scratch of the Q tiles
   const int cta = static_cast<int>(blockIdx.x);
   long long total;
   Cursor c0{};
-  const long long v0 = divide<KT, Split<E4M3>::kThreads>(
+  const long long v0 = divide<Split<E4M3>::kThreads>(
       p, RT, reinterpret_cast<DivideScratch*>(sQ),
       [&](long long all) {
-        const int n = range_count(all, p.n_ctas);
+        const int n = range_count(p, all);
         return cta < n ? range_start(all, cta, n) : all;
       },
       total, c0);
-  const int n_ranges = range_count(total, p.n_ctas);
+  const int n_ranges = range_count(p, total);
   const long long v1 = v0 < 0 ? v0 : range_start(total, cta + 1, n_ranges);
   if (v0 < 0 && threadIdx.x == 0) reinterpret_cast<JoinNote*>(p.part)[cta].pieces = 0;
   __syncthreads();
@@ -736,11 +735,12 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       tc_fence_before();
       v = c.u0 + g.s1;
       if (v >= v_end) {
-        if (t == 0 && r == 0) leave_note<KT>(p, blockIdx.x, total, n_ranges, RT, c, g.s0, g.s1, first);
+        grid_launch_dependents();
+        if (t == 0 && r == 0) leave_note(p, blockIdx.x, total, n_ranges, RT, c, g.s0, g.s1, first);
         break;
       }
       first = false;
-      advance<KT>(p, RT, c);
+      advance(p, RT, c);
       __syncwarp();
       save(c, v);
     }
