@@ -15,11 +15,17 @@
 // type's least normal: when a token arrives that does not fit, the page's
 // earlier codes are multiplied by old / new in place.
 //
-// Bound by memory: each new row is read once and written once.  A block takes
-// one page's new tokens (one sequence) and a share of the heads, so the
-// scale of a (page, head) has one owner, a warp, and needs no atomics; lane
-// j of a row's D / 8 holds pairs 4j .. 4j + 3, both halves of each, so the
-// rotation needs no exchange either.
+// Bound by memory: each new row is read once and written once.  Two kinds of
+// work share one launch:
+//   * rows without a scale (the queries; 16-bit keys and values): a warp takes a
+//     token's heads, or a share of them when tokens are few, eight rows a lane
+//     at a time, with the token's angles read once;
+//   * 8-bit pages: one page's new rows of one head are one unit, of a warp (few
+//     rows) or of four, so the scale of a (page, head) has one owner and needs
+//     no atomics.  The rows wait in registers, eight a lane, while their
+//     largest value is found.
+// Lane j of a row's D / 8 holds pairs 4j .. 4j + 3, both halves of each, so the
+// rotation needs no exchange.
 #include <cuda_fp8.h>
 
 #include "sdpa_paged.cuh"
@@ -104,7 +110,6 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const float4& c, const fl
 // The page's new tokens: positions [lo, hi), the first being row t0 of k, v, q.
 struct PageTokens {
   int lo, hi, t0;
-  int page;       // -1: the table has no page here (its rows are not written)
 };
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
@@ -133,45 +138,94 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __int_as_float((e + 127) << 23);
 }
 
-// One warp: the page's new rows of one head, quantised under the page's scale.
+// Rows [r, r + kBatch * stride) of a unit, rotated (ROT), in registers; rows
+// from n on are zeros.
+constexpr int kBatch = 8;
 template <int D, bool BF16, bool ROT>
+__device__ __forceinline__ void load_rows(const sdpa_impl::AppendParams& p, const PageTokens& pt,
+                                          const uint16_t* src, int64_t src_st, const Lane& at, int j, int r,
+                                          int stride, int n, float (&x)[kBatch][8]) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int row = r + k * stride;
+    if (row < n) {
+      load8<BF16>(src + static_cast<int64_t>(pt.t0 + row) * src_st, at, x[k]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[k][e] = 0.0f;
+    }
+  }
+  if (ROT && at.rotated) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int row = r + k * stride;
+      if (row < n) {
+        const int64_t o = static_cast<int64_t>(pt.lo + row) * (p.rot / 2) + 4 * j;
+        const float4 c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
+        rotate8(x[k], c, s, p.interleaved);
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_codes(uint8_t* dst, int64_t dst_st, const Lane& at, int r, int stride, int n,
+                                            float inv, const float (&x)[kBatch][8]) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int row = r + k * stride;
+    if (row >= n) break;
+    uint8_t* to = dst + row * dst_st;
+    *reinterpret_cast<uint32_t*>(to + at.ea) =
+        codes4(x[k][0] * inv, x[k][1] * inv, x[k][2] * inv, x[k][3] * inv);
+    *reinterpret_cast<uint32_t*>(to + at.eb) =
+        codes4(x[k][4] * inv, x[k][5] * inv, x[k][6] * inv, x[k][7] * inv);
+  }
+}
+
+// A unit: the page's new rows of one head, quantised under the page's scale, by
+// WARPS warps (part: this one's number, red: their shared scratch).
+template <int D, bool BF16, bool ROT, int WARPS>
 __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, const PageTokens& pt,
                                              const uint16_t* src, int64_t src_st, uint8_t* dst,
-                                             int64_t dst_st, float* scale_at) {
-  constexpr int kLanes = D / 8;       // lanes a row
-  constexpr int kRows = 32 / kLanes;  // rows a step
+                                             int64_t dst_st, float* scale_at, int part, float* red) {
+  constexpr int kLanes = D / 8;                  // lanes a row
+  constexpr int kStride = WARPS * 32 / kLanes;   // rows a step
   const int lane = threadIdx.x & 31;
-  const int j = lane % kLanes, sub = lane / kLanes;
-  const int rot = ROT ? p.rot : 0;
-  const Lane at = lane_of(j, rot, p.interleaved);
+  const int j = lane % kLanes, first = part * (32 / kLanes) + lane / kLanes;
+  const Lane at = lane_of(j, ROT ? p.rot : 0, p.interleaved);
   const int n = pt.hi - pt.lo;
-  auto row_values = [&](int r, float (&x)[8]) {
-    load8<BF16>(src + static_cast<int64_t>(pt.t0 + r) * src_st, at, x);
-    if (ROT && at.rotated) {
-      const int64_t o = static_cast<int64_t>(pt.lo + r) * (rot / 2) + 4 * j;
-      const float4 c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
-      rotate8(x, c, s, p.interleaved);
-    }
-  };
+  const int row0 = pt.lo & ((1 << p.page_shift) - 1);
+  // the page's scale, if earlier rows have made one
+  float old = 0.0f;
+  if (row0 > 0) old = clamp_scale(*scale_at);
+  float x[kBatch][8];
   float amax = 0.0f;
-#pragma unroll 4
-  for (int r = sub; r < n; r += kRows) {
-    float x[8];
-    row_values(r, x);
+  // (more rows than the registers hold are read again below)
+  for (int r = first; r - first < n; r += kBatch * kStride) {
+    load_rows<D, BF16, ROT>(p, pt, src, src_st, at, j, r, kStride, n, x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(x[k][e]));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const int row0 = pt.lo & ((1 << p.page_shift) - 1);
+  if constexpr (WARPS > 1) {
+    if (lane == 0) red[part] = amax;
+    __syncthreads();   // (also: every warp has read the old scale)
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, red[w]);
+  } else {
+    __syncwarp();
+  }
   float scale = scale_for(amax);
   if (row0 > 0) {
-    const float old = clamp_scale(*scale_at);
     if (scale > old) {
       // raise the scale: the page's earlier codes of this head
       const float ratio = old / scale;
-      for (int i = lane; i < row0 * (D / 16); i += 32) {
+      for (int i = part * 32 + lane; i < row0 * (D / 16); i += WARPS * 32) {
         uint4* at16 = reinterpret_cast<uint4*>(dst + (i / (D / 16)) * dst_st + (i % (D / 16)) * 16);
         const uint4 w = *at16;
         uint32_t in[4] = {w.x, w.y, w.z, w.w}, res[4];
@@ -186,149 +240,162 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
       scale = old;
     }
   }
-  __syncwarp();
-  if (lane == 0) *scale_at = scale;
+  if (part == 0 && lane == 0) *scale_at = scale;
   const float inv = 1.0f / scale;
-#pragma unroll 4
-  for (int r = sub; r < n; r += kRows) {
-    float x[8];
-    row_values(r, x);
-    uint8_t* row = dst + (row0 + r) * dst_st;
-    *reinterpret_cast<uint32_t*>(row + at.ea) =
-        codes4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    *reinterpret_cast<uint32_t*>(row + at.eb) =
-        codes4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+  uint8_t* to = dst + row0 * dst_st;
+  if (n <= kBatch * kStride) {
+    store_codes<D>(to, dst_st, at, first, kStride, n, inv, x);
+    return;
+  }
+  for (int r = first; r - first < n; r += kBatch * kStride) {
+    load_rows<D, BF16, ROT>(p, pt, src, src_st, at, j, r, kStride, n, x);
+    store_codes<D>(to, dst_st, at, r, kStride, n, inv, x);
   }
 }
 
-// One warp: heads [h0, h1) of one token, rotated (ROT) or copied, in steps of
-// four rows a lane group so that the token's angles are read once for them.
+// One warp: heads [h0, h1) of one token, rotated (ROT) or copied, eight rows a
+// lane at a time.  (c, s): the lane's angles.
 template <int D, bool BF16, bool ROT>
-__device__ __forceinline__ void token_rows(const sdpa_impl::AppendParams& p, int pos,
-                                           const uint16_t* src, int64_t src_sh, uint8_t* dst,
+__device__ __forceinline__ void token_rows(const sdpa_impl::AppendParams& p, const Lane& at, const float4& c,
+                                           const float4& s, const uint16_t* src, int64_t src_sh, uint8_t* dst,
                                            int64_t dst_sh_bytes, int h0, int h1) {
   constexpr int kLanes = D / 8;
   constexpr int kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31;
-  const int j = lane % kLanes, sub = lane / kLanes;
-  const int rot = ROT ? p.rot : 0;
-  const Lane at = lane_of(j, rot, p.interleaved);
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ROT && at.rotated) {
-    const int64_t o = static_cast<int64_t>(pos) * (rot / 2) + 4 * j;
-    c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
-    s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
-  }
-  float x[4][8];
+  const int sub = (threadIdx.x & 31) / kLanes;
+  for (int h8 = h0; h8 < h1; h8 += kBatch * kRows) {
+    float x[kBatch][8];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int h = h0 + sub + u * kRows;
-    if (h < h1) load8<BF16>(src + h * src_sh, at, x[u]);
-  }
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = h8 + sub + u * kRows;
+      if (h < h1) load8<BF16>(src + h * src_sh, at, x[u]);
+    }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int h = h0 + sub + u * kRows;
-    if (h < h1) {
-      if (ROT && at.rotated) rotate8(x[u], c, s, p.interleaved);
-      store8<BF16>(reinterpret_cast<uint16_t*>(dst + h * dst_sh_bytes), at, x[u]);
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = h8 + sub + u * kRows;
+      if (h < h1) {
+        if (ROT && at.rotated) rotate8(x[u], c, s, p.interleaved);
+        store8<BF16>(reinterpret_cast<uint16_t*>(dst + h * dst_sh_bytes), at, x[u]);
+      }
     }
   }
 }
 
-// grid.x: slots of (sequence, page with new tokens); sequence b has the slots
-// [f(b), f(b+1)), f(b) = cu[b] / P + 2 b, which is at least the pages its new
+// The last of n values, f(0) <= f(1) <= .., that is at most x (-1: none); the
+// whole warp calls it.
+template <class F>
+__device__ __forceinline__ int last_at_most(int n, int x, F&& f) {
+  int count = 0;
+#pragma unroll 4
+  for (int b0 = 0; b0 < n; b0 += 32) {
+    const int i = b0 + static_cast<int>(threadIdx.x & 31);
+    count += __popc(__ballot_sync(0xffffffffu, i < n && f(i) <= x));
+  }
+  return count - 1;
+}
+
+// Blocks [0, kv_blocks): units of 8-bit pages, UNIT_WARPS warps each.  A slot
+// stands for a (sequence, page with new tokens): sequence b has the slots
+// [f(b), f(b+1)), f(b) = cu[b] / P + 2 b, at least as many as the pages its new
 // tokens can touch, so a slot finds its sequence without a prefix sum over
-// lengths.  grid.y: shares of the heads.
-template <int D, bool BF16, bool E4M3, bool ROT>
+// lengths; a slot's units are its value and key heads.  The other blocks: a
+// warp takes a share (1 / parts) of one token's rows.
+template <int D, bool BF16, bool E4M3, bool ROT, int UNIT_WARPS>
 __global__ void __launch_bounds__(kThreads)
-    append_kernel(const __grid_constant__ sdpa_impl::AppendParams p) {
+    append_kernel(const __grid_constant__ sdpa_impl::AppendParams p, int kv_blocks, int parts) {
+  __shared__ float red[kWarps];
   grid_dependency_wait();
   grid_launch_dependents();
   const int P = 1 << p.page_shift;
-  const int slot = static_cast<int>(blockIdx.x);
   const int uniform = p.total / p.n_seqs;
+  const int warp = threadIdx.x >> 5;
   auto first_token = [&](int b) {
     return p.cu != nullptr ? min(max(__ldg(p.cu + b), 0), p.total) : b * uniform;
   };
-  auto first_slot = [&](int b) { return (first_token(b) >> p.page_shift) + 2 * b; };
-  int b = -1;
-  for (int b0 = 0; b0 < p.n_seqs; b0 += kThreads) {
-    const int i = b0 + static_cast<int>(threadIdx.x);
-    const int c = __syncthreads_count(i < p.n_seqs && first_slot(i) <= slot);
-    b += c;
-    if (c < kThreads) break;
-  }
-  if (b < 0) return;
-  const int q0 = first_token(b), q1 = max(first_token(b + 1), q0);
-  const int len = __ldg(p.kv_lens + b), n = q1 - q0;
-  const int p0 = max(len - n, 0);          // position of the first token that has one
-  const int page_i = (p0 >> p.page_shift) + (slot - first_slot(b));
-  PageTokens pt;
-  pt.lo = max(p0, page_i << p.page_shift);
-  // a position past the table's pages or the angles' table is left out
-  pt.hi = min(min(len, p.max_len), (page_i << p.page_shift) + P);
-  if (p.cos != nullptr) pt.hi = min(pt.hi, p.n_pos);
-  if (pt.lo >= pt.hi) return;
-  pt.t0 = q0 + (pt.lo - (len - n));
-  pt.page = __ldg(p.table + b * p.table_st + page_i);
-  if (pt.page < 0 || pt.page >= p.n_pages) pt.page = -1;
-
-  const int y = static_cast<int>(blockIdx.y), Y = static_cast<int>(gridDim.y);
-  const int kv0 = p.n_kv * y / Y, kv1 = p.n_kv * (y + 1) / Y, n_kv = kv1 - kv0;
-  const int hq0 = p.q != nullptr ? p.H * y / Y : 0, hq1 = p.q != nullptr ? p.H * (y + 1) / Y : 0;
-  const int tokens = pt.hi - pt.lo;
-  const int row0 = pt.lo & (P - 1);
-  const int warp = threadIdx.x >> 5;
-  constexpr int kGroup = 4 * (32 / (D / 8));  // heads a warp takes of a token
-  const int q_units = ((hq1 - hq0 + kGroup - 1) / kGroup) * tokens;
-  const int kv_groups = (n_kv + kGroup - 1) / kGroup;
-  const int kv_units = pt.page < 0 ? 0 : (E4M3 ? 2 * n_kv : 2 * kv_groups * tokens);
-  for (int u = warp; u < kv_units + q_units; u += kWarps) {
-    if (u < kv_units) {
-      if constexpr (E4M3) {
-        const int h = kv0 + (u >> 1);
-        float* scale_at = ((u & 1) ? p.v_scale : p.k_scale) + static_cast<int64_t>(pt.page) * p.n_kv + h;
-        if (u & 1)
-          append_codes<D, BF16, false>(p, pt, reinterpret_cast<const uint16_t*>(p.v) + h * p.v_sh,
-                                       p.v_st, p.cv + pt.page * p.cv_sp + h * p.cv_sh, p.cv_st,
-                                       scale_at);
-        else
-          append_codes<D, BF16, ROT>(p, pt, reinterpret_cast<const uint16_t*>(p.k) + h * p.k_sh,
-                                     p.k_st, p.ck + pt.page * p.ck_sp + h * p.ck_sh, p.ck_st,
-                                     scale_at);
-      } else {
-        const int r = u / (2 * kv_groups), g = u - r * 2 * kv_groups;
-        const int64_t tok = pt.t0 + r;
-        const int h0 = kv0 + (g >> 1) * kGroup, h1 = min(h0 + kGroup, kv1);
-        if (g & 1)
-          token_rows<D, BF16, false>(p, pt.lo + r, reinterpret_cast<const uint16_t*>(p.v) + tok * p.v_st,
-                                     p.v_sh, p.cv + pt.page * p.cv_sp + (row0 + r) * p.cv_st, p.cv_sh,
-                                     h0, h1);
-        else
-          token_rows<D, BF16, ROT>(p, pt.lo + r, reinterpret_cast<const uint16_t*>(p.k) + tok * p.k_st,
-                                   p.k_sh, p.ck + pt.page * p.ck_sp + (row0 + r) * p.ck_st, p.ck_sh,
-                                   h0, h1);
-      }
-    } else {
-      const int groups = (hq1 - hq0 + kGroup - 1) / kGroup;
-      const int w = u - kv_units, r = w / groups, g = w - r * groups;
-      const int64_t tok = pt.t0 + r;
-      const int h0 = hq0 + g * kGroup, h1 = min(h0 + kGroup, hq1);
-      token_rows<D, BF16, ROT>(p, pt.lo + r, reinterpret_cast<const uint16_t*>(p.q) + tok * p.q_st, p.q_sh,
-                               reinterpret_cast<uint8_t*>(p.q_out) + tok * p.qo_st * 2, p.qo_sh * 2, h0,
-                               h1);
+  if constexpr (E4M3) {
+    if (static_cast<int>(blockIdx.x) < kv_blocks) {
+      const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kWarps / UNIT_WARPS) + warp / UNIT_WARPS;
+      const int slot = static_cast<int>(unit / (2 * p.n_kv));
+      const int hv = static_cast<int>(unit - static_cast<int64_t>(slot) * 2 * p.n_kv);
+      auto first_slot = [&](int b) { return (first_token(b) >> p.page_shift) + 2 * b; };
+      const int b = last_at_most(p.n_seqs, slot, first_slot);
+      if (b < 0) return;
+      const int q0 = first_token(b), q1 = max(first_token(b + 1), q0);
+      const int len = __ldg(p.kv_lens + b), n = q1 - q0;
+      const int p0 = max(len - n, 0);          // position of the first token that has one
+      const int page_i = (p0 >> p.page_shift) + (slot - first_slot(b));
+      PageTokens pt;
+      pt.lo = max(p0, page_i << p.page_shift);
+      // a position past the table's pages or the angles' table is left out
+      pt.hi = min(min(len, p.max_len), (page_i << p.page_shift) + P);
+      if (p.cos != nullptr) pt.hi = min(pt.hi, p.n_pos);
+      if (pt.lo >= pt.hi) return;
+      pt.t0 = q0 + (pt.lo - (len - n));
+      const int page = __ldg(p.table + b * p.table_st + page_i);
+      if (page < 0 || page >= p.n_pages) return;
+      const int h = hv < p.n_kv ? hv : hv - p.n_kv;
+      const int64_t at = static_cast<int64_t>(page) * p.n_kv + h;
+      const int part = warp % UNIT_WARPS;
+      if (hv < p.n_kv)
+        append_codes<D, BF16, false, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.v) + h * p.v_sh, p.v_st,
+                                                 p.cv + page * p.cv_sp + h * p.cv_sh, p.cv_st, p.v_scale + at, part, red);
+      else
+        append_codes<D, BF16, ROT, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.k) + h * p.k_sh, p.k_st,
+                                               p.ck + page * p.ck_sp + h * p.ck_sh, p.ck_st, p.k_scale + at, part, red);
+      return;
     }
+  }
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) - kv_blocks) * kWarps + warp;
+  const int64_t tok = w / parts;
+  const int share = static_cast<int>(w - tok * parts);
+  if (tok >= p.total) return;
+  const int b = last_at_most(p.n_seqs, static_cast<int>(tok), first_token);
+  if (b < 0) return;
+  const int q0 = first_token(b), q1 = first_token(b + 1);
+  if (tok >= q1) return;   // behind the last sequence
+  const int pos = __ldg(p.kv_lens + b) - (q1 - q0) + (static_cast<int>(tok) - q0);
+  if (pos < 0 || pos >= p.max_len || (p.cos != nullptr && pos >= p.n_pos)) return;
+  const int j = (threadIdx.x & 31) % (D / 8);
+  const Lane at = lane_of(j, ROT ? p.rot : 0, p.interleaved);
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (ROT && at.rotated) {
+    const int64_t o = static_cast<int64_t>(pos) * (p.rot / 2) + 4 * j;
+    c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
+    s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
+  }
+  if (p.q != nullptr)
+    token_rows<D, BF16, ROT>(p, at, c, s, reinterpret_cast<const uint16_t*>(p.q) + tok * p.q_st, p.q_sh,
+                             reinterpret_cast<uint8_t*>(p.q_out) + tok * p.qo_st * 2, p.qo_sh * 2, p.H * share / parts,
+                             p.H * (share + 1) / parts);
+  if constexpr (!E4M3) {
+    const int page = __ldg(p.table + b * p.table_st + (pos >> p.page_shift));
+    if (page < 0 || page >= p.n_pages) return;
+    const int row = pos & (P - 1), h0 = p.n_kv * share / parts, h1 = p.n_kv * (share + 1) / parts;
+    token_rows<D, BF16, ROT>(p, at, c, s, reinterpret_cast<const uint16_t*>(p.k) + tok * p.k_st, p.k_sh,
+                             p.ck + page * p.ck_sp + row * p.ck_st, p.ck_sh, h0, h1);
+    // (plain copies: every lane takes eight elements that lie together)
+    token_rows<D, BF16, false>(p, lane_of(j, 0, 0), c, s, reinterpret_cast<const uint16_t*>(p.v) + tok * p.v_st, p.v_sh,
+                               p.cv + page * p.cv_sp + row * p.cv_st, p.cv_sh, h0, h1);
   }
 }
 
-template <int D, bool BF16, bool E4M3, bool ROT>
+template <int D, bool BF16, bool E4M3, bool ROT, int UNIT_WARPS>
 cudaError_t launch_one(const sdpa_impl::AppendParams& p, int sms, cudaStream_t stream) {
-  const long long slots = (p.total >> p.page_shift) + 2LL * p.n_seqs;
-  // enough blocks for about twelve an SM, by sharing out the heads
-  long long y = (12LL * sms + slots - 1) / slots;
-  y = y < p.n_kv ? y : p.n_kv;
+  long long kv_blocks = 0;
+  if (E4M3) {
+    const long long units = ((p.total >> p.page_shift) + 2LL * p.n_seqs) * 2 * p.n_kv;
+    kv_blocks = (units + kWarps / UNIT_WARPS - 1) / (kWarps / UNIT_WARPS);
+  }
+  // Tokens' rows: a warp a token, or a share of its heads each where that
+  // leaves SMs without work.
+  int parts = 1;
+  const int heads = p.H > p.n_kv ? p.H : p.n_kv;
+  while (parts < 16 && static_cast<long long>(p.total) * parts < 16LL * sms && parts * 2 <= heads) parts *= 2;
+  const bool rows = !E4M3 || p.q != nullptr;
+  const long long row_blocks = rows ? (static_cast<long long>(p.total) * parts + kWarps - 1) / kWarps : 0;
+  const long long blocks = kv_blocks + row_blocks;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(slots), static_cast<unsigned>(y));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -336,14 +403,16 @@ cudaError_t launch_one(const sdpa_impl::AppendParams& p, int sms, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<D, BF16, E4M3, ROT>, p);
+  return cudaLaunchKernelEx(&cfg, append_kernel<D, BF16, E4M3, ROT, UNIT_WARPS>, p, static_cast<int>(kv_blocks), parts);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool ROT>
 cudaError_t launch_typed(const sdpa_impl::AppendParams& p, bool e4m3, int sms, cudaStream_t s) {
-  if (e4m3)
-    return p.cos ? launch_one<D, BF16, true, true>(p, sms, s) : launch_one<D, BF16, true, false>(p, sms, s);
-  return p.cos ? launch_one<D, BF16, false, true>(p, sms, s) : launch_one<D, BF16, false, false>(p, sms, s);
+  if (!e4m3) return launch_one<D, BF16, false, ROT, 1>(p, sms, s);
+  // a unit's rows fit one warp's registers (decoding, or small pages), or not
+  const int rows = kBatch * 32 / (D / 8);
+  return (1 << p.page_shift) <= rows || p.total / p.n_seqs <= rows ? launch_one<D, BF16, true, ROT, 1>(p, sms, s)
+                                                                   : launch_one<D, BF16, true, ROT, 4>(p, sms, s);
 }
 
 }  // namespace
@@ -352,9 +421,12 @@ namespace sdpa_impl {
 
 cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, bool e4m3, int sms,
                                 cudaStream_t stream) {
-  if (head_dim == 64)
-    return bf16 ? launch_typed<64, true>(p, e4m3, sms, stream) : launch_typed<64, false>(p, e4m3, sms, stream);
-  return bf16 ? launch_typed<128, true>(p, e4m3, sms, stream) : launch_typed<128, false>(p, e4m3, sms, stream);
+  if (head_dim == 64) {
+    if (p.cos) return bf16 ? launch_typed<64, true, true>(p, e4m3, sms, stream) : launch_typed<64, false, true>(p, e4m3, sms, stream);
+    return bf16 ? launch_typed<64, true, false>(p, e4m3, sms, stream) : launch_typed<64, false, false>(p, e4m3, sms, stream);
+  }
+  if (p.cos) return bf16 ? launch_typed<128, true, true>(p, e4m3, sms, stream) : launch_typed<128, false, true>(p, e4m3, sms, stream);
+  return bf16 ? launch_typed<128, true, false>(p, e4m3, sms, stream) : launch_typed<128, false, false>(p, e4m3, sms, stream);
 }
 
 }  // namespace sdpa_impl
