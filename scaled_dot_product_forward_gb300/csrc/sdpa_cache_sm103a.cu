@@ -18,11 +18,11 @@
 // Bound by memory: each new row is read once and written once.  Two kinds of
 // work share one launch:
 //   * rows without a scale (the queries; 16-bit keys and values): a warp takes a
-//     token's heads, or a share of them when tokens are few, eight rows a lane
+//     token's heads, or a share of them when tokens are few, four rows a lane
 //     at a time, with the token's angles read once;
 //   * 8-bit pages: one page's new rows of one head are one unit, of a warp (few
-//     rows) or of four, so the scale of a (page, head) has one owner and needs
-//     no atomics.  The rows wait in registers, eight a lane, while their
+//     rows) or of several, so the scale of a (page, head) has one owner and needs
+//     no atomics.  The rows wait in registers, four a lane, while their
 //     largest value is found.
 // Lane j of a row's D / 8 holds pairs 4j .. 4j + 3, both halves of each, so the
 // rotation needs no exchange.
@@ -35,8 +35,9 @@ using namespace sdpa_paged;
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPerSm = 4;   // blocks an SM: the loads' latency is hidden by warps, not by registers
 
 // Where lane j of a row keeps its eight elements: a[0..3] from `ea`, b[0..3]
 // from `eb`; pairs (a[e], b[e]) in the half-split form, (a0,a1), (a2,a3),
@@ -85,25 +86,43 @@ __device__ __forceinline__ void store8(uint16_t* row, const Lane& l, const float
       make_uint2(pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
 }
 
-__device__ __forceinline__ void turn(float& x1, float& x2, float c, float s) {
-  const float y1 = __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
-  const float y2 = __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
-  x1 = y1;
-  x2 = y2;
+// Two fp32 values an instruction, each product and each sum rounded on its own.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// (x1, x2) of two pairs turned by (c, s): x1 c - x2 s, x2 c + x1 s.
+__device__ __forceinline__ void turn2(float& a1, float& b1, float& a2, float& b2, float c0, float c1, float s0,
+                                      float s1) {
+  const uint64_t x1 = pair(a1, b1), x2 = pair(a2, b2), c = pair(c0, c1), s = pair(s0, s1);
+  // (adding the product by -s is subtracting the product by s)
+  unpair(add2(mul2(x1, c), mul2(x2, pair(-s0, -s1))), a1, b1);
+  unpair(add2(mul2(x2, c), mul2(x1, s)), a2, b2);
 }
 
 __device__ __forceinline__ void rotate8(float (&x)[8], const float4& c, const float4& s,
                                         int interleaved) {
   if (interleaved) {
-    turn(x[0], x[1], c.x, s.x);
-    turn(x[2], x[3], c.y, s.y);
-    turn(x[4], x[5], c.z, s.z);
-    turn(x[6], x[7], c.w, s.w);
+    turn2(x[0], x[2], x[1], x[3], c.x, c.y, s.x, s.y);
+    turn2(x[4], x[6], x[5], x[7], c.z, c.w, s.z, s.w);
   } else {
-    turn(x[0], x[4], c.x, s.x);
-    turn(x[1], x[5], c.y, s.y);
-    turn(x[2], x[6], c.z, s.z);
-    turn(x[3], x[7], c.w, s.w);
+    turn2(x[0], x[1], x[4], x[5], c.x, c.y, s.x, s.y);
+    turn2(x[2], x[3], x[6], x[7], c.z, c.w, s.z, s.w);
   }
 }
 
@@ -123,11 +142,14 @@ __device__ __forceinline__ float2 values2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The largest |x| that a scale has to cover: infinities and NaN are left out
-// (an infinity is stored as +-448 codes, a NaN as NaN).
+// What a scale has to cover: infinities and NaN are left out (an infinity is
+// stored as +-448 codes, a NaN as NaN).
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
   return a < INFINITY ? a : 0.0f;
+}
+__device__ __forceinline__ float abs_max(float m, float a, float b) {   // drops NaN, keeps infinities
+  return max3f(m, fabsf(a), fabsf(b));
 }
 
 // The least power of two s with amax <= 448 s = 1.75 * 2^8 s, in range.
@@ -138,49 +160,48 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __int_as_float((e + 127) << 23);
 }
 
-// Rows [r, r + kBatch * stride) of a unit, rotated (ROT), in registers; rows
-// from n on are zeros.
-constexpr int kBatch = 8;
-template <int D, bool BF16, bool ROT>
-__device__ __forceinline__ void load_rows(const sdpa_impl::AppendParams& p, const PageTokens& pt,
-                                          const uint16_t* src, int64_t src_st, const Lane& at, int j, int r,
-                                          int stride, int n, float (&x)[kBatch][8]) {
+// Rows r, r + stride, .. (kBatch of them) of a unit of n rows, rotated (ROT), in
+// registers; rows from n on are zeros.  src, cos, sin: this lane's part of row
+// r; steps in elements.
+constexpr int kBatch = 4;
+template <bool BF16, bool ROT>
+__device__ __forceinline__ void load_rows(const uint16_t* src, int64_t src_step, const float* cos, const float* sin,
+                                          int64_t angle_step, const Lane& at, int interleaved, int r, int stride, int n,
+                                          float (&x)[kBatch][8]) {
 #pragma unroll
   for (int k = 0; k < kBatch; ++k) {
-    const int row = r + k * stride;
-    if (row < n) {
-      load8<BF16>(src + static_cast<int64_t>(pt.t0 + row) * src_st, at, x[k]);
+    if (r + k * stride < n) {
+      load8<BF16>(src, at, x[k]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[k][e] = 0.0f;
     }
+    src += src_step;
   }
   if (ROT && at.rotated) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int row = r + k * stride;
-      if (row < n) {
-        const int64_t o = static_cast<int64_t>(pt.lo + row) * (p.rot / 2) + 4 * j;
-        const float4 c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
-        rotate8(x[k], c, s, p.interleaved);
-      }
+      if (r + k * stride < n)
+        rotate8(x[k], __ldg(reinterpret_cast<const float4*>(cos)), __ldg(reinterpret_cast<const float4*>(sin)), interleaved);
+      cos += angle_step;
+      sin += angle_step;
     }
   }
 }
 
-template <int D>
-__device__ __forceinline__ void store_codes(uint8_t* dst, int64_t dst_st, const Lane& at, int r, int stride, int n,
-                                            float inv, const float (&x)[kBatch][8]) {
+__device__ __forceinline__ void store_codes(uint8_t* to, int64_t step, const Lane& at, int r, int stride, int n, float inv,
+                                            const float (&x)[kBatch][8]) {
+  const uint64_t f = pair(inv, inv);
 #pragma unroll
   for (int k = 0; k < kBatch; ++k) {
-    const int row = r + k * stride;
-    if (row >= n) break;
-    uint8_t* to = dst + row * dst_st;
-    *reinterpret_cast<uint32_t*>(to + at.ea) =
-        codes4(x[k][0] * inv, x[k][1] * inv, x[k][2] * inv, x[k][3] * inv);
-    *reinterpret_cast<uint32_t*>(to + at.eb) =
-        codes4(x[k][4] * inv, x[k][5] * inv, x[k][6] * inv, x[k][7] * inv);
+    if (r + k * stride < n) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) unpair(mul2(pair(x[k][e], x[k][e + 1]), f), y[e], y[e + 1]);
+      *reinterpret_cast<uint32_t*>(to + at.ea) = codes4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint32_t*>(to + at.eb) = codes4(y[4], y[5], y[6], y[7]);
+    }
+    to += step;
   }
 }
 
@@ -200,21 +221,44 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
   // the page's scale, if earlier rows have made one
   float old = 0.0f;
   if (row0 > 0) old = clamp_scale(*scale_at);
+  // this lane's part of its first row, and from one of its rows to the next
+  const uint16_t* const rows = src + (static_cast<int64_t>(pt.t0) + first) * src_st;
+  const int64_t row_step = kStride * src_st, angle_step = static_cast<int64_t>(kStride) * (p.rot / 2);
+  const int64_t angle = (static_cast<int64_t>(pt.lo) + first) * (p.rot / 2) + 4 * j;
+  const float* const cos = ROT ? p.cos + angle : nullptr;
+  const float* const sin = ROT ? p.sin + angle : nullptr;
+  auto load = [&](int batch, float (&x)[kBatch][8]) {
+    load_rows<BF16, ROT>(rows + batch * (kBatch * row_step), row_step, cos + batch * (kBatch * angle_step),
+                         sin + batch * (kBatch * angle_step), angle_step, at, p.interleaved,
+                         first + batch * kBatch * kStride, kStride, n, x);
+  };
   float x[kBatch][8];
   float amax = 0.0f;
   // (more rows than the registers hold are read again below)
-  for (int r = first; r - first < n; r += kBatch * kStride) {
-    load_rows<D, BF16, ROT>(p, pt, src, src_st, at, j, r, kStride, n, x);
+  const int batches = (n + kBatch * kStride - 1) / (kBatch * kStride);
+#pragma unroll 1
+  for (int i = 0; i < batches; ++i) {
+    load(i, x);
+    float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(x[k][e]));
+      for (int e = 0; e < 8; e += 2) top = abs_max(top, x[k][e], x[k][e + 1]);
+    if (top == INFINITY) {
+      top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(x[k][e]));
+    }
+    amax = fmaxf(amax, top);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if constexpr (WARPS > 1) {
     if (lane == 0) red[part] = amax;
-    __syncthreads();   // (also: every warp has read the old scale)
+    // the unit's warps (also: all have read the old scale)
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / (WARPS * 32)), "n"(WARPS * 32) : "memory");
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, red[w]);
   } else {
@@ -242,18 +286,16 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
   }
   if (part == 0 && lane == 0) *scale_at = scale;
   const float inv = 1.0f / scale;
-  uint8_t* to = dst + row0 * dst_st;
-  if (n <= kBatch * kStride) {
-    store_codes<D>(to, dst_st, at, first, kStride, n, inv, x);
-    return;
-  }
-  for (int r = first; r - first < n; r += kBatch * kStride) {
-    load_rows<D, BF16, ROT>(p, pt, src, src_st, at, j, r, kStride, n, x);
-    store_codes<D>(to, dst_st, at, r, kStride, n, inv, x);
+  uint8_t* const to = dst + (row0 + first) * dst_st;
+  const int64_t to_step = kStride * dst_st;
+#pragma unroll 1
+  for (int i = 0; i < batches; ++i) {
+    if (batches > 1) load(i, x);
+    store_codes(to + i * (kBatch * to_step), to_step, at, first + i * kBatch * kStride, kStride, n, inv, x);
   }
 }
 
-// One warp: heads [h0, h1) of one token, rotated (ROT) or copied, eight rows a
+// One warp: heads [h0, h1) of one token, rotated (ROT) or copied, four rows a
 // lane at a time.  (c, s): the lane's angles.
 template <int D, bool BF16, bool ROT>
 __device__ __forceinline__ void token_rows(const sdpa_impl::AppendParams& p, const Lane& at, const float4& c,
@@ -261,21 +303,25 @@ __device__ __forceinline__ void token_rows(const sdpa_impl::AppendParams& p, con
                                            int64_t dst_sh_bytes, int h0, int h1) {
   constexpr int kLanes = D / 8;
   constexpr int kRows = 32 / kLanes;
-  const int sub = (threadIdx.x & 31) / kLanes;
-  for (int h8 = h0; h8 < h1; h8 += kBatch * kRows) {
+  int h = h0 + static_cast<int>(threadIdx.x & 31) / kLanes;
+  src += h * src_sh;
+  dst += h * dst_sh_bytes;
+  const int64_t src_step = kRows * src_sh, dst_step = kRows * dst_sh_bytes;
+#pragma unroll 1
+  for (; h < h1; h += kBatch * kRows) {
     float x[kBatch][8];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int h = h8 + sub + u * kRows;
-      if (h < h1) load8<BF16>(src + h * src_sh, at, x[u]);
+      if (h + u * kRows < h1) load8<BF16>(src, at, x[u]);
+      src += src_step;
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int h = h8 + sub + u * kRows;
-      if (h < h1) {
+      if (h + u * kRows < h1) {
         if (ROT && at.rotated) rotate8(x[u], c, s, p.interleaved);
-        store8<BF16>(reinterpret_cast<uint16_t*>(dst + h * dst_sh_bytes), at, x[u]);
+        store8<BF16>(reinterpret_cast<uint16_t*>(dst), at, x[u]);
       }
+      dst += dst_step;
     }
   }
 }
@@ -300,7 +346,7 @@ __device__ __forceinline__ int last_at_most(int n, int x, F&& f) {
 // lengths; a slot's units are its value and key heads.  The other blocks: a
 // warp takes a share (1 / parts) of one token's rows.
 template <int D, bool BF16, bool E4M3, bool ROT, int UNIT_WARPS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kPerSm)
     append_kernel(const __grid_constant__ sdpa_impl::AppendParams p, int kv_blocks, int parts) {
   __shared__ float red[kWarps];
   grid_dependency_wait();
@@ -313,9 +359,9 @@ __global__ void __launch_bounds__(kThreads)
   };
   if constexpr (E4M3) {
     if (static_cast<int>(blockIdx.x) < kv_blocks) {
-      const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kWarps / UNIT_WARPS) + warp / UNIT_WARPS;
-      const int slot = static_cast<int>(unit / (2 * p.n_kv));
-      const int hv = static_cast<int>(unit - static_cast<int64_t>(slot) * 2 * p.n_kv);
+      const unsigned unit = blockIdx.x * (kWarps / UNIT_WARPS) + warp / UNIT_WARPS;
+      const int slot = static_cast<int>(unit / (2u * p.n_kv));
+      const int hv = static_cast<int>(unit - slot * 2u * p.n_kv);
       auto first_slot = [&](int b) { return (first_token(b) >> p.page_shift) + 2 * b; };
       const int b = last_at_most(p.n_seqs, slot, first_slot);
       if (b < 0) return;
@@ -337,16 +383,16 @@ __global__ void __launch_bounds__(kThreads)
       const int part = warp % UNIT_WARPS;
       if (hv < p.n_kv)
         append_codes<D, BF16, false, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.v) + h * p.v_sh, p.v_st,
-                                                 p.cv + page * p.cv_sp + h * p.cv_sh, p.cv_st, p.v_scale + at, part, red);
+                                                 p.cv + page * p.cv_sp + h * p.cv_sh, p.cv_st, p.v_scale + at, part, red + warp - part);
       else
         append_codes<D, BF16, ROT, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.k) + h * p.k_sh, p.k_st,
-                                               p.ck + page * p.ck_sp + h * p.ck_sh, p.ck_st, p.k_scale + at, part, red);
+                                               p.ck + page * p.ck_sp + h * p.ck_sh, p.ck_st, p.k_scale + at, part, red + warp - part);
       return;
     }
   }
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) - kv_blocks) * kWarps + warp;
-  const int64_t tok = w / parts;
-  const int share = static_cast<int>(w - tok * parts);
+  const unsigned w = (blockIdx.x - kv_blocks) * kWarps + warp;
+  const int64_t tok = w / static_cast<unsigned>(parts);
+  const int share = static_cast<int>(w % static_cast<unsigned>(parts));
   if (tok >= p.total) return;
   const int b = last_at_most(p.n_seqs, static_cast<int>(tok), first_token);
   if (b < 0) return;
@@ -393,7 +439,7 @@ cudaError_t launch_one(const sdpa_impl::AppendParams& p, int sms, cudaStream_t s
   const bool rows = !E4M3 || p.q != nullptr;
   const long long row_blocks = rows ? (static_cast<long long>(p.total) * parts + kWarps - 1) / kWarps : 0;
   const long long blocks = kv_blocks + row_blocks;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (blocks > 0x7fffffffLL / kWarps) return cudaErrorInvalidValue;   // (units and warps are counted in 32 bits)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kThreads);
@@ -409,10 +455,14 @@ cudaError_t launch_one(const sdpa_impl::AppendParams& p, int sms, cudaStream_t s
 template <int D, bool BF16, bool ROT>
 cudaError_t launch_typed(const sdpa_impl::AppendParams& p, bool e4m3, int sms, cudaStream_t s) {
   if (!e4m3) return launch_one<D, BF16, false, ROT, 1>(p, sms, s);
-  // a unit's rows fit one warp's registers (decoding, or small pages), or not
-  const int rows = kBatch * 32 / (D / 8);
-  return (1 << p.page_shift) <= rows || p.total / p.n_seqs <= rows ? launch_one<D, BF16, true, ROT, 1>(p, sms, s)
-                                                                   : launch_one<D, BF16, true, ROT, 4>(p, sms, s);
+  // as many warps a unit as hold its rows in registers (the most it can have:
+  // a page's, or about a sequence's when those are fewer)
+  const int P = 1 << p.page_shift, n = p.total / p.n_seqs, rows = P < n ? P : n;
+  const int warp_rows = kBatch * 32 / (D / 8);
+  if (rows <= warp_rows) return launch_one<D, BF16, true, ROT, 1>(p, sms, s);
+  if (rows <= 2 * warp_rows) return launch_one<D, BF16, true, ROT, 2>(p, sms, s);
+  if (rows <= 4 * warp_rows) return launch_one<D, BF16, true, ROT, 4>(p, sms, s);
+  return launch_one<D, BF16, true, ROT, 8>(p, sms, s);
 }
 
 }  // namespace
