@@ -142,7 +142,7 @@ struct PagedParams {
   int total_q, n_seqs, n_kv, G, n_pages, max_len;
   int unit_heads, n_groups; // key/value heads of a unit, groups of them
   int step_shift;           // keys a step = 1 << step_shift
-  int min_steps;            // of a CTA's range
+  int min_steps, min_steps_shift;  // of a CTA's range, a power of two
   int page_shift;           // page size = 1 << page_shift
   int is_causal;
   float scale_log2;

@@ -82,31 +82,28 @@ __device__ __forceinline__ int unit_steps(const PagedParams& p, const Seq& s, in
 }
 
 // A position in the division: unit (b, h, t) (h: the group of heads), whose
-// steps begin at u0.
+// steps begin at u0.  (The host has checked that all steps fit 31 bits.)
 struct Cursor {
-  int b, h, t;
-  long long u0;
+  int b, h, t, u0;
   Seq s;
 };
 
 // Shared scratch of divide().
 struct DivideScratch {
-  long long warp_sum[16];
-  int found_b;
-  long long found_u0, found_steps;
+  int warp_sum[16];
+  int found_b, found_u0, found_steps;
   Seq found;
 };
 
 // Ranges of a division: at most one a CTA, and of at least p.min_steps steps
 // (joining many short pieces costs more than it saves; never an empty range).
-__device__ __forceinline__ int range_count(const PagedParams& p, long long total) {
-  const long long n = (total + p.min_steps - 1) / p.min_steps;
-  return n < p.n_ctas ? static_cast<int>(n) : p.n_ctas;
+__device__ __forceinline__ int range_count(const PagedParams& p, int total) {
+  return min((total + p.min_steps - 1) >> p.min_steps_shift, p.n_ctas);
 }
 // First step of range i of the n equal ones of `total` steps.
-__device__ __forceinline__ long long range_start(long long total, int i, int n) {
-  const long long q = total < (1ll << 31) ? static_cast<int>(total) / n : total / n;
-  return q * i + static_cast<int>(total - q * n) * i / n;   // both factors below n
+__device__ __forceinline__ int range_start(int total, int i, int n) {
+  const int q = total / n;
+  return q * i + (total - q * n) * i / n;   // (both factors below n)
 }
 
 // The batch's total of steps, and the unit that holds step `at(total)` when
@@ -115,45 +112,42 @@ __device__ __forceinline__ long long range_start(long long total, int i, int n) 
 // sequences at a time as the block has groups; a batch of at most that many is
 // read once.
 template <int NT, class At>
-__device__ __forceinline__ long long divide(const PagedParams& p, int rt, DivideScratch* sc, At&& at,
-                                            long long& total, Cursor& c) {
+__device__ __forceinline__ int divide(const PagedParams& p, int rt, DivideScratch* sc, At&& at, int& total,
+                                      Cursor& c) {
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  int w = 1;
-  if (p.is_causal)
-    while (w < 32 && p.n_seqs * w * 2 <= NT) w *= 2;
-  const int per = NT / w, sub = tid % w;
+  int w_shift = 0;
+  if (p.is_causal && p.max_rows > rt)   // (else a sequence has one unit a group)
+    while (w_shift < 5 && p.n_seqs * (2 << w_shift) <= NT) ++w_shift;
+  const int w = 1 << w_shift, per = NT >> w_shift, sub = tid & (w - 1);
   // this thread's part of sequence b0 + tid / w; inclusive sum over the block
   // of the sequences' steps, at each group's first lane
-  long long mine, incl, all;
+  int mine, incl, all;
   Seq seq{};
   auto chunk = [&](int b0) {
-    const int b = b0 + tid / w;
+    const int b = b0 + (tid >> w_shift);
     mine = 0;
     if (b < p.n_seqs) {
       seq = load_seq(p, b, rt);
       if (!p.is_causal)
-        mine = seq.nt == 0 ? 0 : static_cast<long long>(seq.nt) * unit_steps(p, seq, 0, rt);
+        mine = seq.nt == 0 ? 0 : seq.nt * unit_steps(p, seq, 0, rt);
       else
+#pragma unroll 1
         for (int t = sub; t < seq.nt; t += w) mine += unit_steps(p, seq, t, rt);
     }
     for (int o = 1; o < w; o <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     incl = sub == 0 ? mine * p.n_groups : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
     __syncthreads();
     if (lane == 31) sc->warp_sum[warp] = incl;
     __syncthreads();
-    all = 0;
-    long long before = 0;
-#pragma unroll
-    for (int k = 0; k < NT / 32; ++k) {
-      if (k < warp) before += sc->warp_sum[k];
-      all += sc->warp_sum[k];
-    }
-    incl += before;
+    // each lane one warp's sum
+    const int ws = lane < NT / 32 ? sc->warp_sum[lane] : 0;
+    all = __reduce_add_sync(0xffffffffu, ws);
+    incl += __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
   };
   total = 0;
   const int chunks = (p.n_seqs + per - 1) / per;
@@ -161,14 +155,14 @@ __device__ __forceinline__ long long divide(const PagedParams& p, int rt, Divide
     chunk(k * per);
     total += all;
   }
-  const long long v = at(total);
+  const int v = at(total);
   if (v >= total) return -1;
-  long long base = 0;
+  int base = 0;
   for (int k = 0; k < chunks; ++k) {
     if (chunks > 1) chunk(k * per);
-    const long long u1 = base + incl, u0 = u1 - mine * p.n_groups;
+    const int u1 = base + incl, u0 = u1 - mine * p.n_groups;
     if (sub == 0 && mine > 0 && v >= u0 && v < u1) {
-      sc->found_b = k * per + tid / w;
+      sc->found_b = k * per + (tid >> w_shift);
       sc->found_u0 = u0;
       sc->found_steps = mine;
       sc->found = seq;
@@ -179,25 +173,26 @@ __device__ __forceinline__ long long divide(const PagedParams& p, int rt, Divide
   __syncthreads();
   c.b = sc->found_b;
   c.s = sc->found;
-  const long long off = v - sc->found_u0;
-  c.h = static_cast<int>(off < (1ll << 31) ? static_cast<int>(off) / static_cast<int>(min(sc->found_steps, 0x7fffffffll))
-                                           : off / sc->found_steps);
+  c.h = (v - sc->found_u0) / sc->found_steps;
   c.u0 = sc->found_u0 + c.h * sc->found_steps;
-  for (int t0 = 0;; t0 += 32) {
-    const long long n = t0 + lane < c.s.nt ? unit_steps(p, c.s, t0 + lane, rt) : 0;
-    long long sum = n;
+  c.t = 0;
+#pragma unroll 1
+  while (c.s.nt > 1) {
+    const int n = c.t + lane < c.s.nt ? unit_steps(p, c.s, c.t + lane, rt) : 0;
+    int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+      const int x = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += x;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, v < c.u0 + sum);
-    if (hit != 0 || t0 + 32 >= c.s.nt) {
+    if (hit != 0 || c.t + 32 >= c.s.nt) {
       const int k = hit != 0 ? __ffs(static_cast<int>(hit)) - 1 : 31;
-      c.t = t0 + k;
+      c.t += k;
       c.u0 += __shfl_sync(0xffffffffu, sum - n, k);
       break;
     }
+    c.t += 32;
     c.u0 += __shfl_sync(0xffffffffu, sum, 31);
   }
   return v;
@@ -237,13 +232,13 @@ __device__ __forceinline__ float* part_rows(const PagedParams& p, int i, int slo
 
 // CTA i's note: its last unit, if that begins here (with its first or a later
 // segment) and goes on behind its range.
-__device__ __forceinline__ void leave_note(const PagedParams& p, int i, long long total, int n, int rt,
+__device__ __forceinline__ void leave_note(const PagedParams& p, int i, int total, int n, int rt,
                                            const Cursor& c, int s0, int s1, bool first) {
   JoinNote j{};
   const int steps = unit_steps(p, c.s, c.t, rt);
   if (s0 == 0 && s1 < steps) {
     // the range that holds the unit's last step
-    const long long last = ((c.u0 + steps) * n - 1) / total;
+    const long long last = (static_cast<long long>(c.u0 + steps) * n - 1) / total;
     j.pieces = static_cast<int>(last) - i + 1;
     j.slot = first ? 0 : 1;
     j.rows = min(rt, c.s.nq * p.G - c.t * rt);

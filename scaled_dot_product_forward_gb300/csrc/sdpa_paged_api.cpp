@@ -299,6 +299,12 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   if (s != SDPA_OK) return s;
   const int64_t max_rows = (max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
   const sdpa_impl::PagedForm form = sdpa_impl::paged_form(max_rows, static_cast<int>(D), e4m3, hkv, sms);
+  {
+    // the kernels count their steps in 31 bits
+    const double units = static_cast<double>(total_q) * static_cast<double>(G) / form.rows + static_cast<double>(n_seqs);
+    const double steps = static_cast<double>((max_pages * cache->page_size) >> form.step_shift) + 1.0;
+    if (units * static_cast<double>(hkv / form.heads) * steps > 2.0e9) return SDPA_ERR_SHAPE;
+  }
   if (workspace_size < workspace_bytes(form, D)) return SDPA_ERR_ARG;
   sdpa_impl::PagedParams p;
   std::memset(&p, 0, sizeof(p));
@@ -335,6 +341,7 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   p.n_groups = static_cast<int>(hkv) / form.heads;
   p.step_shift = form.step_shift;
   p.min_steps = form.min_steps;
+  p.min_steps_shift = log2_of(form.min_steps);
   p.device = dev;
   cudaError_t e;
   if (form.tc) {

@@ -184,11 +184,11 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
   grid_dependency_wait();
 
   const int cta = static_cast<int>(blockIdx.x);
-  long long total;
+  int total;
   Cursor c;
-  long long v = divide<kThreads>(
+  int v = divide<kThreads>(
       p, RT, sc,
-      [&](long long all) {
+      [&](int all) {
         const int n = range_count(p, all);
         return cta < n ? range_start(all, cta, n) : all;
       },
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
     if (threadIdx.x == 0) reinterpret_cast<JoinNote*>(p.part)[cta].pieces = 0;
     return;
   }
-  const long long v_end = range_start(total, cta + 1, n_ranges);
+  const int v_end = range_start(total, cta + 1, n_ranges);
   // this warp's head of a unit's, and its share of the head's keys
   const int hsub = warp % p.unit_heads, slice = warp / p.unit_heads;
   const int slices = kWarps / p.unit_heads;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
     }
     cp_async_commit();
   };
-  auto open = [&](const Cursor& cu, long long from) {
+  auto open = [&](const Cursor& cu, int from) {
     Loads a;
     const int h = cu.h * p.unit_heads + hsub;
     a.trow = p.table + static_cast<int64_t>(cu.b) * p.table_st;
@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
     a.scale_at = h;
     a.keys = unit_keys(p, cu.s, cu.t, RT);
     a.len = cu.s.len;
-    a.s0 = static_cast<int>(from - cu.u0);
-    a.s1 = static_cast<int>(min(static_cast<long long>(unit_steps(p, cu.s, cu.t, RT)), v_end - cu.u0));
+    a.s0 = from - cu.u0;
+    a.s1 = min(unit_steps(p, cu.s, cu.t, RT), v_end - cu.u0);
     a.ids_at = a.s0;
     a.ids = load_ids(a, a.s0);
     a.ids_next = load_ids(a, a.s0 + 32);
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
     }
 
     // the next unit
-    const long long v_next = c.u0 + s1;
+    const int v_next = c.u0 + s1;
     const bool more = v_next < v_end;
     // The join may start only now: its blocks, waiting early, would take the
     // place of CTAs of the next call's kernel on some SMs and leave those

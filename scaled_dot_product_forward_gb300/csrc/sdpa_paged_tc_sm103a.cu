@@ -159,12 +159,12 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
-__device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor& c, long long v, long long v_end,
+__device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor& c, int v, int v_end,
                                               bool first) {
   const int steps = unit_steps(p, c.s, c.t, RT);
   Segment g;
-  g.s0 = static_cast<int>(v - c.u0);
-  g.s1 = static_cast<int>(min(static_cast<long long>(steps), v_end - c.u0));
+  g.s0 = v - c.u0;
+  g.s1 = min(steps, v_end - c.u0);
   g.rows = min(RT, c.s.nq * p.G - c.t * RT);
   g.whole = g.s0 == 0 && g.s1 == steps;
   g.split = g.rows <= 128;
@@ -175,8 +175,8 @@ __device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor
 // Calls f(cursor, segment) for the CTA's segments in order until it returns
 // false.
 template <class F>
-__device__ __forceinline__ void for_each_segment(const PagedParams& p, Cursor c, long long v,
-                                                 long long v_end, F&& f) {
+__device__ __forceinline__ void for_each_segment(const PagedParams& p, Cursor c, int v,
+                                                 int v_end, F&& f) {
   bool first = true;
   while (v < v_end) {
     const Segment g = segment_of(p, c, v, v_end, first);
@@ -191,7 +191,7 @@ __device__ __forceinline__ void for_each_segment(const PagedParams& p, Cursor c,
 // hold a row of scores.
 struct Place {
   Cursor c;
-  long long v, v_end;
+  int v, v_end;
 };
 static_assert(sizeof(Place) <= 64, "place");
 
@@ -370,20 +370,27 @@ __device__ __forceinline__ float2 codes_value2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Thread's row of Q to its warpgroup's shared tile (zeros when it has none),
-// negated for a negative scale; returns the (positive) multiplier of the
-// scores, |scale| * log2(e).  For e4m3 keys the row is brought by a power of
-// two to a largest element in [2^7, 2^8) (the factor goes into the
-// multiplier) and split into e4m3 terms, each what the earlier ones leave: a
-// bf16 value is exact in two, an fp16 one in three, down to 2^-10 in that
-// scale, 2^-17 of the row's largest element.
-template <int D, bool E4M3, bool BF16>
-__device__ __forceinline__ float store_query(const PagedParams& p, const uint16_t* src, bool live, uint8_t* tile,
-                                             int r) {
+// Thread's row of Q (zeros when it has none).
+template <int D>
+struct QueryRow {
   uint4 w[D / 8];
+};
+template <int D>
+__device__ __forceinline__ void load_query(const uint16_t* src, bool live, QueryRow<D>& q) {
 #pragma unroll
   for (int i = 0; i < D / 8; ++i)
-    w[i] = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+    q.w[i] = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// The row to its warpgroup's shared tile, negated for a negative scale; returns
+// the (positive) multiplier of the scores, |scale| * log2(e).  For e4m3 keys
+// the row is brought by a power of two to a largest element in [2^7, 2^8) (the
+// factor goes into the multiplier) and split into e4m3 terms, each what the
+// earlier ones leave: a bf16 value is exact in two, an fp16 one in three, down
+// to 2^-10 in that scale, 2^-17 of the row's largest element.
+template <int D, bool E4M3, bool BF16>
+__device__ __forceinline__ float put_query(const PagedParams& p, QueryRow<D>& q, uint8_t* tile, int r) {
+  uint4* w = q.w;
   uint32_t* x = reinterpret_cast<uint32_t*>(w);
   const float f = fabsf(p.scale_log2);
   if (p.scale_log2 < 0.0f) {
@@ -514,17 +521,17 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
 
   // the division, in the scratch of the Q tiles
   const int cta = static_cast<int>(blockIdx.x);
-  long long total;
+  int total;
   Cursor c0{};
-  const long long v0 = divide<Split<E4M3>::kThreads>(
+  const int v0 = divide<Split<E4M3>::kThreads>(
       p, RT, reinterpret_cast<DivideScratch*>(sQ),
-      [&](long long all) {
+      [&](int all) {
         const int n = range_count(p, all);
         return cta < n ? range_start(all, cta, n) : all;
       },
       total, c0);
   const int n_ranges = range_count(p, total);
-  const long long v1 = v0 < 0 ? v0 : range_start(total, cta + 1, n_ranges);
+  const int v1 = v0 < 0 ? v0 : range_start(total, cta + 1, n_ranges);
   if (v0 < 0 && threadIdx.x == 0) reinterpret_cast<JoinNote*>(p.part)[cta].pieces = 0;
   __syncthreads();
 
@@ -539,7 +546,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     uint32_t n_s = 0, n_sums = 0;   // completions consumed
     RingAt<L::kNotes> note_at;
     volatile Place* vplace = reinterpret_cast<volatile Place*>(smem + L::kCursors) + (warp - 4);
-    auto save = [&](const Cursor& c, long long v) {
+    auto save = [&](const Cursor& c, int v) {
       if (lane == 0) {
         vplace->c.b = c.b, vplace->c.h = c.h, vplace->c.t = c.t, vplace->c.u0 = c.u0;
         vplace->c.s.q0 = c.s.q0, vplace->c.s.nq = c.s.nq, vplace->c.s.len = c.s.len, vplace->c.s.nt = c.s.nt;
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       }
       __syncwarp();
     };
-    auto load = [&](Cursor& c, long long& v, long long& v_end) {
+    auto load = [&](Cursor& c, int& v, int& v_end) {
       c.b = vplace->c.b, c.h = vplace->c.h, c.t = vplace->c.t, c.u0 = vplace->c.u0;
       c.s.q0 = vplace->c.s.q0, c.s.nq = vplace->c.s.nq, c.s.len = vplace->c.s.len, c.s.nt = vplace->c.s.nt;
       v = vplace->v, v_end = vplace->v_end;
@@ -559,25 +566,38 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       head = static_cast<int64_t>(c.h) * p.G + (rr - tok * p.G);
       return tok;
     };
+    // the row of a segment's unit, and its query
+    auto row_of = [&](const Segment& g) { return g.split ? r : t * 128 + r; };
+    auto ask = [&](const Cursor& c, const Segment& g, QueryRow<D>& q) {
+      int64_t token, head;
+      const int ru = row_of(g);
+      place(c, ru, token, head);
+      load_query<D>(reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh, ru < g.rows, q);
+    };
     save(c0, v0);
     bool first = true;
     for (bool ok = v0 < v1; ok;) {
-      float f;
+      float f = 0.0f;
       int seen, s0, s1;
-      bool split;
+      bool split, idle;
       {
         Cursor c;
-        long long v, v_end;
+        int v, v_end;
         load(c, v, v_end);
         const Segment g = segment_of(p, c, v, v_end, first);
         s0 = g.s0, s1 = g.s1, split = g.split;
-        const int ru = split ? r : t * 128 + r;   // row of the unit
+        const int ru = row_of(g);
         int64_t token, head;
         const int tok = place(c, ru, token, head);
-        const bool live = ru < g.rows;
-        seen = !live ? 0 : p.is_causal ? min(max(c.s.len - c.s.nq + tok + 1, 0), c.s.len) : c.s.len;
-        f = store_query<D, E4M3, BF16>(
-            p, reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh, live, sQ + t * L::kQTile, r);
+        // rows that the unit has not: nothing of theirs is removed (a removed
+        // key costs the whole warp), and a warp of them alone only keeps step
+        idle = ru - lane >= g.rows;
+        seen = ru >= g.rows ? 0x7fffffff : p.is_causal ? min(max(c.s.len - c.s.nq + tok + 1, 0), c.s.len) : c.s.len;
+        if (!idle) {
+          QueryRow<D> q;
+          ask(c, g, q);
+          f = put_query<D, E4M3, BF16>(p, q, sQ + t * L::kQTile, r);
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -600,6 +620,12 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
           break;
         }
         ++n_s;
+        if (idle) {
+          // (its rows of P are whatever is there: their products are not read)
+          if (lane == 0) mbar_arrive(&bars->p_ready[t]);
+          ++mine;
+          continue;
+        }
         tc_fence_after();
         float x[KT];
         {
@@ -648,8 +674,18 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->p_ready[t]);
         ++mine;
       }
+      if (!ok) break;
+      Cursor c;
+      int v, v_end;
+      load(c, v, v_end);
+      const Segment g = segment_of(p, c, v, v_end, first);
+      Cursor next = c;
+      const int v_next = c.u0 + g.s1;
+      if (v_next < v_end) {
+        advance(p, RT, next);
+      }
       // n_s completions of s_full[t] so far, as many of o_done[t]
-      if (!ok || (mine > 0 && !warp_wait(&bars->o_done[t], (n_s - 1) & 1, bars, limit, kSiteO))) break;
+      if (mine > 0 && !warp_wait(&bars->o_done[t], (n_s - 1) & 1, bars, limit, kSiteO)) break;
       tc_fence_after();
       float fa = 1.0f, fb = 0.0f;
       if (split) {
@@ -680,11 +716,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         l = l * fa + lo * fb;
         m = mx;
       }
-      Cursor c;
-      long long v, v_end;
-      load(c, v, v_end);
-      const Segment g = segment_of(p, c, v, v_end, first);
-      const int ru = g.split ? r : t * 128 + r;
+      const int ru = row_of(g);
       const bool live = ru < g.rows;
       int64_t token, head;
       place(c, ru, token, head);
@@ -696,7 +728,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       uint16_t* orow = reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh;
       float* prow = part_rows<D>(p, blockIdx.x, g.first ? 0 : 1, RT) + static_cast<int64_t>(ru) * (D + 2);
       const int i0 = g.split ? t * (D / 64) : 0, i1 = g.split ? i0 + D / 64 : D / 32;
-      for (int i = i0; i < i1; ++i) {
+      for (int i = i0; i < i1 && !idle; ++i) {
         uint32_t o[32];
         tmem_ld32(tO + i * 32, o);
         tmem_ld_wait();
@@ -733,16 +765,14 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         }
       }
       tc_fence_before();
-      v = c.u0 + g.s1;
-      if (v >= v_end) {
+      if (v_next >= v_end) {
         grid_launch_dependents();
         if (t == 0 && r == 0) leave_note(p, blockIdx.x, total, n_ranges, RT, c, g.s0, g.s1, first);
         break;
       }
       first = false;
-      advance(p, RT, c);
       __syncwarp();
-      save(c, v);
+      save(next, v_next);
     }
     tc_fence_before();
   } else {
@@ -976,7 +1006,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       RingAt<L::kVStages> v_at;
       RingAt<L::kRawStages> raw_at;
       // the CTA's steps, whatever units they belong to
-      for (int left = static_cast<int>(min(v1 - v0, 0x7fffffffLL)); left > 0; --left) {
+      for (int left = v1 - v0; left > 0; --left) {
         if (!warp_wait(&bars->raw_full[raw_at.idx], raw_at.phase, bars, limit, kSiteK)) break;
         const int valid = *reinterpret_cast<volatile int*>(&bars->valid[raw_at.idx]);
         if (v_at.lapped && !warp_wait(&bars->v_empty[v_at.idx], v_at.phase ^ 1u, bars, limit, kSiteEmpty)) break;
