@@ -448,8 +448,11 @@ SDPA_API sdpa_status sdpa_cache_append(
  * may be anything, NaN too).  Products on tensor cores with fp32 sums, softmax
  * in fp32; each key's weight, times its value's scale, is rounded to 16 bits
  * (bf16 for a bf16 cache, else fp16) before the second product.  Results do
- * not depend on timing.  Asynchronous on `stream`.  Errors as above, and ARG
- * for an infinite scale or too small a workspace.
+ * not depend on timing.  Asynchronous on `stream`; two kernel launches.  The
+ * kernel for many rows a head waits on barriers, each for a bounded time
+ * (sdpa_last_device_status).  Errors as above; ARG for an infinite scale or too
+ * small a workspace, SHAPE also when (total_q * n_heads / n_kv_heads / 16 +
+ * n_seqs) * n_kv_heads * max_pages * page_size / 16 exceeds about 2^31.
  */
 SDPA_API sdpa_status sdpa_paged_forward(
     const void* q, void* out, float* lse, sdpa_dtype dtype, const sdpa_paged_cache* cache,

@@ -686,6 +686,8 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
         size = cache._workspace.get(key)
         if size is None:
             size = lib.sdpa_paged_workspace_bytes(cache.head_dim, heads, cache.n_kv_heads, max_seqlen_q)
+            if size == 0:
+                raise SdpaError(9, where)
             if len(cache._workspace) > 1000:
                 cache._workspace.clear()
             cache._workspace[key] = size

@@ -86,7 +86,7 @@ __device__ __forceinline__ void store8(uint16_t* row, const Lane& l, const float
       make_uint2(pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
 }
 
-// Two fp32 values an instruction, each product and each sum rounded on its own.
+// Two fp32 values an instruction.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -100,19 +100,21 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// (x1, x2) of two pairs turned by (c, s): x1 c - x2 s, x2 c + x1 s.
+// (x1, x2) of two pairs turned by (c, s): x1 c - x2 s, x2 c + x1 s.  (The sums
+// one by one: a packed sum behind a packed product is made one operation,
+// without the product's rounding.)
 __device__ __forceinline__ void turn2(float& a1, float& b1, float& a2, float& b2, float c0, float c1, float s0,
                                       float s1) {
   const uint64_t x1 = pair(a1, b1), x2 = pair(a2, b2), c = pair(c0, c1), s = pair(s0, s1);
-  // (adding the product by -s is subtracting the product by s)
-  unpair(add2(mul2(x1, c), mul2(x2, pair(-s0, -s1))), a1, b1);
-  unpair(add2(mul2(x2, c), mul2(x1, s)), a2, b2);
+  float p0, p1, q0, q1, r0, r1, t0, t1;
+  unpair(mul2(x1, c), p0, p1);
+  unpair(mul2(x2, s), q0, q1);
+  unpair(mul2(x2, c), r0, r1);
+  unpair(mul2(x1, s), t0, t1);
+  a1 = __fsub_rn(p0, q0);
+  b1 = __fsub_rn(p1, q1);
+  a2 = __fadd_rn(r0, t0);
+  b2 = __fadd_rn(r1, t1);
 }
 
 __device__ __forceinline__ void rotate8(float (&x)[8], const float4& c, const float4& s,

@@ -236,13 +236,15 @@ uint64_t sdpa_paged_workspace_bytes(int64_t head_dim, int64_t n_heads, int64_t n
     return 0;
   int dev = 0, sms = 0;
   if (sdpa_impl::current_device(&dev, &sms) != SDPA_OK) return 0;
-  // enough for a cache of either kind
+  // enough for a cache of either kind, and for the forms that fewer rows take
   const int64_t rows = max_seqlen_q * (n_heads / n_kv_heads);
   uint64_t most = 0;
-  for (const bool e4m3 : {false, true}) {
-    const uint64_t n = workspace_bytes(sdpa_impl::paged_form(rows, static_cast<int>(head_dim), e4m3, n_kv_heads, sms), head_dim);
-    most = n > most ? n : most;
-  }
+  for (const bool e4m3 : {false, true})
+    for (const int64_t r : {rows < 16 ? rows : 16, rows < 32 ? rows : 32, rows}) {
+      const uint64_t n =
+          workspace_bytes(sdpa_impl::paged_form(r, static_cast<int>(head_dim), e4m3, n_kv_heads, sms), head_dim);
+      most = n > most ? n : most;
+    }
   return most;
 }
 

@@ -88,6 +88,13 @@ ATTEND = [  # D, cache, dtype, page, kv heads, G, memory order, causal, counts, 
     (64, "16", torch.float16, 128, 1, 4, "tokens", True, [77, 5], [300, 64]),
     (64, "e4m3", torch.bfloat16, 16, 1, 64, "tokens", True, [5, 1], [129, 200]),
     (128, "e4m3", torch.float16, 16, 1, 33, "padded", False, [6, 2], [129, 640]),
+    (64, "e4m3", torch.float16, 32, 2, 8, "heads", True, [20, 1, 260], [20, 700, 300]),
+    (128, "16", torch.float16, 64, 1, 16, "heads", False, [9, 33], [513, 128]),
+    (64, "16", torch.bfloat16, 16, 4, 4, "padded", True, [70, 11], [200, 11]),
+    (128, "e4m3", torch.bfloat16, 16, 8, 4, "tokens", True, [1, 3, 1, 0], [130, 3, 77, 12]),
+    (64, "e4m3", torch.float16, 256, 4, 8, "tokens", True, [4, 2], [600, 31]),
+    (128, "16", torch.bfloat16, 1024, 4, 2, "tokens", True, [1, 16], [1500, 16]),
+    (64, "16", torch.float16, 512, 6, 1, "heads", False, [1, 2], [515, 40]),
 ]
 
 
@@ -117,6 +124,86 @@ def test_attend_many_ctas_a_sequence(sdpa_lib, cache, rows):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     run_attend(sdpa_lib, c, q, t, lens, [rows], True, max_q=1)
     run_attend(sdpa_lib, c, q, t, lens, [rows], True, max_q=5000)
+
+
+@gpu
+@pytest.mark.parametrize("hkv,G", [(4, 2), (8, 1), (2, 3)])
+def test_attend_many_ctas_and_heads(sdpa_lib, hkv, G):
+    """Units of several heads, cut between CTAs; any bound on the rows gives the results, with
+    what sdpa_paged_workspace_bytes says for it."""
+    lens = [2500, 1, 700]
+    c = make_cache(sdpa_lib, 170, 32, hkv, 64, "e4m3", torch.bfloat16, 9)
+    q = torch.randn(3, hkv * G, 64, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    t = tables(3, 79, 3 * 79, 3) % 170
+    for max_q in (1, 7, 30, 4000):
+        run_attend(sdpa_lib, c, q, t, lens, [1, 1, 1], True, max_q=max_q)
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 40])
+def test_shared_pages_and_lengths_out_of_range(sdpa_lib, rows):
+    """Sequences with pages in common; lengths below zero and past the table are clamped."""
+    c = make_cache(sdpa_lib, 9, 16, 2, 128, "e4m3", torch.bfloat16, 30)
+    table = torch.tensor([[3, 5, 7, 1], [3, 5, 2, 0], [3, 5, 7, 8]], dtype=torch.int32)
+    q = torch.randn(3 * rows, 8, 128, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    lens = torch.tensor([50, -7, 1 << 30], dtype=torch.int32).cuda()
+    out, lse = sdpa_lib.sdpa_paged_forward(q, c, table.cuda(), lens, is_causal=True, return_lse=True)
+    k, v = ref.values(c.k, c.k_scale), ref.values(c.v, c.v_scale)
+    want = ref.attend(q, k, v, table, [50, 0, 64], [rows] * 3, None, True)
+    tol, _ = ref.attend_bounds(want, 64, 128, torch.bfloat16, torch.float16)
+    check(out, want[0], tol, "out")
+    assert torch.isinf(lse[rows:2 * rows]).all() and (out[rows:2 * rows] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("rows_max", [1, 60])
+def test_bad_offsets_stay_inside(sdpa_lib, rows_max):
+    """Offsets out of order and out of range: rows of one sequence only are right, nothing else is
+    touched."""
+    c = make_cache(sdpa_lib, 9, 16, 1, 64, "e4m3", torch.float16, 31)
+    buf = torch.full((10, 2, 64), 5.0, dtype=torch.float16, device="cuda")
+    q = torch.randn(6, 2, 64, generator=torch.Generator().manual_seed(3)).half().cuda()
+    table = tables(3, 2, 9, 1)
+    cu = torch.tensor([-4, 4, 2, 99], dtype=torch.int32).cuda()   # rows 0-3, none, 2-5
+    lens = torch.tensor([20, 20, 30], dtype=torch.int32).cuda()
+    sdpa_lib.sdpa_paged_forward(q, c, table.cuda(), lens, cu, rows_max, buf[2:8])
+    assert sdpa_lib.sdpa_last_device_status()[0] == 0
+    k, v = ref.values(c.k, c.k_scale), ref.values(c.v, c.v_scale)
+    for b, r in ((0, slice(0, 2)), (2, slice(4, 6))):
+        want = ref.attend(q[r], k, v, table[b:b + 1], [int(lens[b])], [2])
+        tol, _ = ref.attend_bounds(want, 30, 64, torch.float16, torch.float16)
+        check(buf[2:8][r], want[0], tol, "out")
+    assert (buf[:2] == 5).all() and (buf[8:] == 5).all()
+    before = [x.clone() for x in (c.k.view(torch.uint8), c.v.view(torch.uint8))]
+    kn = torch.randn(6, 1, 64, generator=torch.Generator().manual_seed(3)).half().cuda()
+    sdpa_lib.sdpa_cache_append(c, kn, kn, table[:, :1].contiguous().cuda(), torch.tensor([4, 0, 4], dtype=torch.int32).cuda(), cu)
+    torch.cuda.synchronize()
+    touched = [int(table[0, 0]), int(table[2, 0])]
+    rest = [p for p in range(9) if p not in touched]
+    for x, y in zip(before, (c.k.view(torch.uint8), c.v.view(torch.uint8))):
+        assert torch.equal(x[rest], y[rest]) and torch.equal(x[touched, 4:], y[touched, 4:])
+
+
+@gpu
+def test_waits_run_out(sdpa_lib):
+    """The many-row kernel's waits are bounded: with its products withheld it returns, says so, and
+    the next call is right."""
+    c = make_cache(sdpa_lib, 20, 16, 1, 128, "e4m3", torch.bfloat16, 8)
+    q = torch.randn(50, 2, 128, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    t = tables(1, 9, 20, 3)
+    lens = torch.tensor([140], dtype=torch.int32).cuda()
+    assert sdpa_lib.sdpa_last_device_status()[0] == 0
+    sdpa_lib.sdpa_debug_set_wait_limit_ns(20_000_000)
+    sdpa_lib.sdpa_debug_withhold_q_load(True)
+    try:
+        sdpa_lib.sdpa_paged_forward(q, c, t.cuda(), lens)
+        rc, bits = sdpa_lib.sdpa_last_device_status()
+    finally:
+        sdpa_lib.sdpa_debug_withhold_q_load(False)
+        sdpa_lib.sdpa_debug_set_wait_limit_ns(0)
+    assert rc == 8 and bits & 1
+    run_attend(sdpa_lib, c, q, t, [140], [50], True)
+    assert sdpa_lib.sdpa_last_device_status()[0] == 0
 
 
 @gpu
