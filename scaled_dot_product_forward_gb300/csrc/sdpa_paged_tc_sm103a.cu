@@ -93,9 +93,9 @@ struct Lay {
 };
 
 struct Bars {
-  uint64_t q_full;      // both warpgroups: Q written, the last unit's rows read out
+  uint64_t q_full[2];   // a warpgroup's Q is written, its last unit's rows are read out
   uint64_t s_full[2], p_ready[2], o_done[2];
-  uint64_t sums;        // alternating steps: both warpgroups' sums are in tensor memory
+  uint64_t sums, read;  // alternating steps: both warpgroups' sums are in tensor memory; are read
   uint64_t fin;
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], raw_full[4], raw_empty[4];
   uint64_t note[8];
@@ -370,27 +370,37 @@ __device__ __forceinline__ float2 codes_value2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Thread's row of Q (zeros when it has none).
-template <int D>
-struct QueryRow {
-  uint4 w[D / 8];
-};
-template <int D>
-__device__ __forceinline__ void load_query(const uint16_t* src, bool live, QueryRow<D>& q) {
+// Where 16-byte piece i of thread r's query row (as it lies in memory) waits in
+// its tile: in the places that put_query gives the same row (16-bit: its own
+// piece; e4m3 terms: the row's of the first two), so it needs no other room and
+// no other thread's consent.
+template <int D, bool E4M3>
+__device__ __forceinline__ int query_piece(int r, int i) {
+  if constexpr (!E4M3) return (i >> 3) * (KT * 128) + swizzled<128>(r, i & 7);
+  return (i / (D / 16)) * (KT * D) + r * D + (i % (D / 16)) * 16;
+}
+// Asks for the row; finished by cp_async_wait<0>().
+template <int D, bool E4M3>
+__device__ __forceinline__ void ask_query(const uint16_t* src, uint8_t* tile, int r) {
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-    q.w[i] = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < D / 8; ++i) cp_async_16(tile + query_piece<D, E4M3>(r, i), src + i * 8);
+  cp_async_commit();
 }
 
-// The row to its warpgroup's shared tile, negated for a negative scale; returns
-// the (positive) multiplier of the scores, |scale| * log2(e).  For e4m3 keys
-// the row is brought by a power of two to a largest element in [2^7, 2^8) (the
-// factor goes into the multiplier) and split into e4m3 terms, each what the
-// earlier ones leave: a bf16 value is exact in two, an fp16 one in three, down
-// to 2^-10 in that scale, 2^-17 of the row's largest element.
+// The row (none: zeros) to the tile as the products read it, negated for a
+// negative scale; returns the (positive) multiplier of the scores, |scale| *
+// log2(e).  For e4m3 keys the row is brought by a power of two to a largest
+// element in [2^7, 2^8) (the factor goes into the multiplier) and split into
+// e4m3 terms, each what the earlier ones leave: a bf16 value is exact in two,
+// an fp16 one in three, down to 2^-10 in that scale, 2^-17 of the row's largest
+// element.
 template <int D, bool E4M3, bool BF16>
-__device__ __forceinline__ float put_query(const PagedParams& p, QueryRow<D>& q, uint8_t* tile, int r) {
-  uint4* w = q.w;
+__device__ __forceinline__ float put_query(const PagedParams& p, bool live, uint8_t* tile, int r) {
+  if (!E4M3 && live && p.scale_log2 >= 0.0f) return p.scale_log2;   // it lies there already
+  uint4 w[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+    w[i] = live ? *reinterpret_cast<const uint4*>(tile + query_piece<D, E4M3>(r, i)) : make_uint4(0u, 0u, 0u, 0u);
   uint32_t* x = reinterpret_cast<uint32_t*>(w);
   const float f = fabsf(p.scale_log2);
   if (p.scale_log2 < 0.0f) {
@@ -481,13 +491,14 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
   const uint64_t limit = p.wait_limit_ns;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 8);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 4);
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_ready[t], 4);
       mbar_init(&bars->o_done[t], 1);
     }
     mbar_init(&bars->sums, 8);
+    mbar_init(&bars->read, 8);
     mbar_init(&bars->fin, 1);
     for (int i = 0; i < L::kKStages; ++i) {
       mbar_init(&bars->k_full[i], 1);
@@ -568,14 +579,16 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     };
     // the row of a segment's unit, and its query
     auto row_of = [&](const Segment& g) { return g.split ? r : t * 128 + r; };
-    auto ask = [&](const Cursor& c, const Segment& g, QueryRow<D>& q) {
+    auto ask = [&](const Cursor& c, const Segment& g) {
       int64_t token, head;
       const int ru = row_of(g);
       place(c, ru, token, head);
-      load_query<D>(reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh, ru < g.rows, q);
+      if (ru < g.rows)
+        ask_query<D, E4M3>(reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh, sQ + t * L::kQTile, r);
     };
     save(c0, v0);
     bool first = true;
+    if (v0 < v1) ask(c0, segment_of(p, c0, v0, v1, true));
     for (bool ok = v0 < v1; ok;) {
       float f = 0.0f;
       int seen, s0, s1;
@@ -593,16 +606,13 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         // key costs the whole warp), and a warp of them alone only keeps step
         idle = ru - lane >= g.rows;
         seen = ru >= g.rows ? 0x7fffffff : p.is_causal ? min(max(c.s.len - c.s.nq + tok + 1, 0), c.s.len) : c.s.len;
-        if (!idle) {
-          QueryRow<D> q;
-          ask(c, g, q);
-          f = put_query<D, E4M3, BF16>(p, q, sQ + t * L::kQTile, r);
-        }
+        cp_async_wait<0>();
+        if (!idle) f = put_query<D, E4M3, BF16>(p, ru < g.rows, sQ + t * L::kQTile, r);
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->q_full);
+      if (lane == 0) mbar_arrive(&bars->q_full[t]);
       float m = -INFINITY, l = 0.0f;
       int mine = 0;
       for (int s = s0; s < s1; ++s) {
@@ -683,6 +693,8 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       const int v_next = c.u0 + g.s1;
       if (v_next < v_end) {
         advance(p, RT, next);
+        // its query, while this one's rows are written (S of this tile is complete)
+        ask(next, segment_of(p, next, v_next, v_end, false));
       }
       // n_s completions of s_full[t] so far, as many of o_done[t]
       if (mine > 0 && !warp_wait(&bars->o_done[t], (n_s - 1) & 1, bars, limit, kSiteO)) break;
@@ -756,6 +768,13 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
           }
         }
       }
+      if (split) {
+        // this warpgroup's sums stay until the other has read them
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->read);
+        if (!warp_wait(&bars->read, (n_sums - 1) & 1, bars, limit, kSiteSums)) break;
+      }
       if (live && (!g.split || t == 0)) {
         if (!g.whole) {
           *reinterpret_cast<float2*>(prow + D) = make_float2(m, l);
@@ -774,6 +793,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       __syncwarp();
       save(next, v_next);
     }
+    cp_async_wait<0>();
     tc_fence_before();
   } else {
     regs_decrease<Split<E4M3>::kControl>();
@@ -964,9 +984,6 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       };
       for_each_segment(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
         if (p.debug_withhold_q) return false;
-        if (!warp_wait(&bars->q_full, n_seg & 1, bars, limit, kSiteQ)) return false;
-        ++n_seg;
-        tc_fence_after();
         const int n = g.s1 - g.s0;
         issued = true;
         // One place each for the two products, whatever the mode (the code of
@@ -988,12 +1005,19 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
               v_at.next();
             }
           }
+          if (e < 0) {
+            // each warpgroup's Q on its own: one may still be writing the last
+            // unit's rows
+            if (!warp_wait(&bars->q_full[t], n_seg & 1, bars, limit, kSiteQ)) return false;
+            tc_fence_after();
+          }
           if (ahead < n) {
             if (head && !next_k()) return false;
             issue_s(t);
             if (tail) done_k();
           }
         }
+        ++n_seg;
         return true;
       });
       if (issued) {
