@@ -200,7 +200,7 @@ constexpr int paged_per_sm(int head_dim, bool e4m3, int rows) {
 // so reading them together keeps DRAM pages open), which share a head's keys
 // when there are fewer: 16 keys of a head each a step.
 inline PagedForm paged_form(int64_t max_rows, int head_dim, bool e4m3, int64_t n_kv, int sms) {
-  if (max_rows > 32) return {sms, 256, 1, 7, 2, true};
+  if (max_rows > 32) return {sms, max_rows <= 64 ? 64 : 256, 1, 7, 2, true};
   const int rows = max_rows <= 16 ? 16 : 32;
   const int heads = n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1;
   return {paged_per_sm(head_dim, e4m3, rows) * sms, rows, heads, heads == 4 ? 4 : heads == 2 ? 5 : 6,
@@ -212,8 +212,8 @@ cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m
 // page), box min(page size, 128) tokens by 64 16-bit elements with the 128-byte
 // swizzle, or by D codes, the keys' with the swizzle of D bytes, the values'
 // without.
-cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, bool bf16, bool e4m3, const CUtensorMap& tm_k,
-                            const CUtensorMap& tm_v, cudaStream_t stream);
+cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile_rows,
+                            const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream);
 // Joins the units that the division cut.
 cudaError_t launch_paged_join(const PagedParams& p, int head_dim, bool bf16, int tile_rows,
                                  cudaStream_t stream);

@@ -14,6 +14,10 @@
 //     or by the softmax's latency, still keeps both at work; their sums are
 //     joined at the end through tensor memory, each thread of one reading the
 //     other's lane.
+// When no sequence has more than 64 rows a head, units have 64 and take the
+// second way with M = 64 products, which put row h in lane 32 (h / 16) + h % 16;
+// two threads share a row, each half of a step's keys and of the columns
+// (HALF; five tokens of 16 sequences, 40 rows a head: 119 -> 97 us).
 // Pages arrive by TMA (one box a page and 128-byte column chunk; an entry that
 // is no page lies out of the map's bounds and reads as zeros).  16-bit pages
 // land in the 128-byte-swizzled layout that the products read.  e4m3 pages
@@ -40,7 +44,9 @@ __device__ unsigned int g_sdpa_paged_status = 0;
 namespace {
 
 constexpr int KT = 128;        // keys a step
-constexpr int RT = 256;        // rows a unit
+// Rows of a unit, and of a softmax warpgroup's tile.  HALF: see below.
+__host__ __device__ constexpr int unit_rows(bool half) { return half ? 64 : 256; }
+__host__ __device__ constexpr int tile_rows(bool half) { return half ? 64 : 128; }
 // Warp 0 loads the keys and writes the notes on each step, warp 2 loads the
 // values, warp 1 issues the products; warpgroups 1 and 2 are the softmax; with
 // e4m3 pages warpgroup 3 converts.  The register splits exhaust the launch's
@@ -64,17 +70,19 @@ constexpr int kGroups = KT / 16;     // 16 keys lie in one page
 // bits each, so two carry a bf16 value and three an fp16 one.
 __host__ __device__ constexpr int q_terms(bool e4m3, bool bf16) { return !e4m3 ? 1 : bf16 ? 2 : 3; }
 
-template <int D, bool E4M3, bool BF16>
+template <int D, bool E4M3, bool BF16, bool HALF>
 struct Lay {
   static constexpr int kChunks = D / 64;
   static constexpr int kChunkBytes = KT * 128;
   static constexpr int kTile = kChunks * kChunkBytes;      // 128 rows of 16-bit elements
   static constexpr int kCodes = KT * D;                    // 128 rows of codes
-  static constexpr int kQTile = q_terms(E4M3, BF16) * (E4M3 ? kCodes : kTile);
+  static constexpr int kQRows = tile_rows(HALF);
+  static constexpr int kQChunk = kQRows * (E4M3 ? D : 128);   // a term, or 64 columns
+  static constexpr int kQTile = (E4M3 ? q_terms(E4M3, BF16) : kChunks) * kQChunk;
   static constexpr int kKTile = E4M3 ? kCodes : kTile;
-  static constexpr int kKStages = E4M3 ? (D == 128 ? (BF16 ? 3 : 2) : 4) : (D == 128 ? 3 : 4);
-  static constexpr int kVStages = D == 128 ? 2 : (E4M3 ? 3 : 4);
-  static constexpr int kRawStages = !E4M3 ? 0 : (D == 128 ? (BF16 ? 3 : 2) : 4);  // V's codes
+  static constexpr int kKStages = D == 64 ? 4 : !E4M3 ? 3 : (BF16 ? 3 : 2) + (HALF ? 1 : 0);
+  static constexpr int kVStages = D == 64 ? (E4M3 ? 3 : 4) : !E4M3 && HALF ? 3 : 2;
+  static constexpr int kRawStages = !E4M3 ? 0 : D == 64 || HALF ? 4 : BF16 ? 3 : 2;  // V's codes
   // Notes on a step (its pages' scales), written when step x's keys have been
   // asked for: S of step x - K stages is complete then, and so (S is issued
   // behind the product that needs the weights of two steps before, at most)
@@ -159,6 +167,7 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
+template <int RT>
 __device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor& c, int v, int v_end,
                                               bool first) {
   const int steps = unit_steps(p, c.s, c.t, RT);
@@ -174,12 +183,12 @@ __device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor
 
 // Calls f(cursor, segment) for the CTA's segments in order until it returns
 // false.
-template <class F>
+template <int RT, class F>
 __device__ __forceinline__ void for_each_segment(const PagedParams& p, Cursor c, int v,
                                                  int v_end, F&& f) {
   bool first = true;
   while (v < v_end) {
-    const Segment g = segment_of(p, c, v, v_end, first);
+    const Segment g = segment_of<RT>(p, c, v, v_end, first);
     if (!f(c, g)) return;
     first = false;
     v = c.u0 + g.s1;
@@ -281,15 +290,17 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* tile, 
 // with groups of 16 keys that have scales of their own 2^(f ks s + log2 vs -
 // m).  f >= 0.  Returns the factor that the earlier sums have to take (need:
 // it is not 1).
-template <bool E4M3, bool MBF>
-__device__ __forceinline__ float weights(float (&s)[KT], float f, const float4* note, float& m, float& l,
-                                         bool& need, uint32_t (&pk)[KT / 2]) {
+// With N = 64 a row's other half is the partner thread's (lane ^ 16): both take
+// the same maximum, and l is this half's sum.
+template <bool E4M3, bool MBF, int N>
+__device__ __forceinline__ float weights(float (&s)[N], float f, const float4* note, float& m, float& l,
+                                         bool& need, uint32_t (&pk)[N / 2]) {
   float top = -INFINITY;
   // never zero: a removed score, an infinity, has to stay one
   auto mul = [&](int g) { return fmaxf(f * note[g].x, 1.17549435e-38f); };
   if constexpr (E4M3) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < N / 16; ++g) {
       const float* x = s + g * 16;
       const float a = max3f(x[0], x[1], x[2]), b = max3f(x[3], x[4], x[5]), c = max3f(x[6], x[7], x[8]);
       const float d = max3f(x[9], x[10], x[11]), e = max3f(x[12], x[13], x[14]);
@@ -300,12 +311,13 @@ __device__ __forceinline__ float weights(float (&s)[KT], float f, const float4* 
 #pragma unroll
     for (int i = 0; i < 8; ++i) e8[i] = s[i];
 #pragma unroll
-    for (int c = 8; c < KT; c += 16)
+    for (int c = 8; c < N; c += 16)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e8[i] = max3f(e8[i], s[c + i], s[c + 8 + i < KT ? c + 8 + i : c + i]);
+      for (int i = 0; i < 8; ++i) e8[i] = max3f(e8[i], s[c + i], s[c + 8 + i < N ? c + 8 + i : c + i]);
     e8[0] = fmaxf(max3f(e8[0], e8[1], e8[2]), max3f(e8[3], e8[4], e8[5]));
     top = max3f(e8[0], e8[6], e8[7]) * f;
   }
+  if constexpr (N < KT) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
   need = top > m + kRescaleLog2;
   float alpha = 1.0f;
   if (need) {
@@ -316,20 +328,20 @@ __device__ __forceinline__ float weights(float (&s)[KT], float f, const float4* 
   const float neg_m = m == -INFINITY ? 0.0f : -m;
   if constexpr (E4M3) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < N / 16; ++g) {
       const float a = mul(g), b = note[g].y + neg_m;
 #pragma unroll
       for (int c = 16 * g; c < 16 * g + 16; c += 2) fma2_bcast(s[c], s[c + 1], s[c], s[c + 1], a, b);
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < KT; c += 2) fma2_bcast(s[c], s[c + 1], s[c], s[c + 1], f, neg_m);
+    for (int c = 0; c < N; c += 2) fma2_bcast(s[c], s[c + 1], s[c], s[c + 1], f, neg_m);
   }
 #pragma unroll
-  for (int c = 0; c < KT; ++c) s[c] = ex2(s[c]);
+  for (int c = 0; c < N; ++c) s[c] = ex2(s[c]);
   if constexpr (E4M3) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < N / 16; ++g) {
       float r[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -345,7 +357,7 @@ __device__ __forceinline__ float weights(float (&s)[KT], float f, const float4* 
 #pragma unroll
     for (int i = 0; i < 8; ++i) rs[i] = 0.0f;
 #pragma unroll
-    for (int c = 0; c < KT / 2; ++c) {
+    for (int c = 0; c < N / 2; ++c) {
       add2_acc(rs[2 * (c & 3)], rs[2 * (c & 3) + 1], s[2 * c], s[2 * c + 1]);
       pk[c] = pack2<MBF>(s[2 * c], s[2 * c + 1]);
     }
@@ -370,60 +382,72 @@ __device__ __forceinline__ float2 codes_value2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Where 16-byte piece i of thread r's query row (as it lies in memory) waits in
-// its tile: in the places that put_query gives the same row (16-bit: its own
-// piece; e4m3 terms: the row's of the first two), so it needs no other room and
-// no other thread's consent.
-template <int D, bool E4M3>
+// Where 16-byte piece i of row r of a query tile waits as it lies in memory: in
+// the places that put_query gives the same row (16-bit: its own piece; e4m3
+// terms: the row's of the first two), so it needs no other room and no other
+// row's consent.
+template <int D, bool E4M3, int QCHUNK>
 __device__ __forceinline__ int query_piece(int r, int i) {
-  if constexpr (!E4M3) return (i >> 3) * (KT * 128) + swizzled<128>(r, i & 7);
-  return (i / (D / 16)) * (KT * D) + r * D + (i % (D / 16)) * 16;
+  if constexpr (!E4M3) return (i >> 3) * QCHUNK + swizzled<128>(r, i & 7);
+  return (i / (D / 16)) * QCHUNK + r * D + (i % (D / 16)) * 16;
 }
-// Asks for the row; finished by cp_async_wait<0>().
-template <int D, bool E4M3>
-__device__ __forceinline__ void ask_query(const uint16_t* src, uint8_t* tile, int r) {
+// A thread's share of a row: all of it, or half (0, 1) of it.
+template <int D, bool HALF>
+struct RowShare {
+  static constexpr int kPieces = D / 8 / (HALF ? 2 : 1);   // 16-byte pieces of 16-bit elements
+};
+// Asks for the row's share; finished by cp_async_wait<0>().
+template <int D, bool E4M3, bool HALF, int QCHUNK>
+__device__ __forceinline__ void ask_query(const uint16_t* src, uint8_t* tile, int r, int half) {
+  constexpr int kN = RowShare<D, HALF>::kPieces;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) cp_async_16(tile + query_piece<D, E4M3>(r, i), src + i * 8);
+  for (int k = 0; k < kN; ++k) {
+    const int i = half * kN + k;
+    cp_async_16(tile + query_piece<D, E4M3, QCHUNK>(r, i), src + i * 8);
+  }
   cp_async_commit();
 }
 
-// The row (none: zeros) to the tile as the products read it, negated for a
-// negative scale; returns the (positive) multiplier of the scores, |scale| *
-// log2(e).  For e4m3 keys the row is brought by a power of two to a largest
-// element in [2^7, 2^8) (the factor goes into the multiplier) and split into
-// e4m3 terms, each what the earlier ones leave: a bf16 value is exact in two,
-// an fp16 one in three, down to 2^-10 in that scale, 2^-17 of the row's largest
-// element.
-template <int D, bool E4M3, bool BF16>
-__device__ __forceinline__ float put_query(const PagedParams& p, bool live, uint8_t* tile, int r) {
-  if (!E4M3 && live && p.scale_log2 >= 0.0f) return p.scale_log2;   // it lies there already
-  uint4 w[D / 8];
+// The row's share (none: zeros) to the tile as the products read it, negated
+// for a negative scale; returns the (positive) multiplier of the scores,
+// |scale| * log2(e).  For e4m3 keys the row is brought by a power of two to a
+// largest element in [2^7, 2^8) (the factor goes into the multiplier) and split
+// into e4m3 terms, each what the earlier ones leave: a bf16 value is exact in
+// two, an fp16 one in three, down to 2^-10 in that scale, 2^-17 of the row's
+// largest element.  The whole warp calls it.
+template <int D, bool E4M3, bool BF16, bool HALF, int QCHUNK>
+__device__ __forceinline__ float put_query(const PagedParams& p, bool live, uint8_t* tile, int r, int half) {
+  constexpr int kN = RowShare<D, HALF>::kPieces;
+  uint4 w[kN];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-    w[i] = live ? *reinterpret_cast<const uint4*>(tile + query_piece<D, E4M3>(r, i)) : make_uint4(0u, 0u, 0u, 0u);
+  for (int k = 0; k < kN; ++k)
+    w[k] = live ? *reinterpret_cast<const uint4*>(tile + query_piece<D, E4M3, QCHUNK>(r, half * kN + k))
+                : make_uint4(0u, 0u, 0u, 0u);
   uint32_t* x = reinterpret_cast<uint32_t*>(w);
   const float f = fabsf(p.scale_log2);
   if (p.scale_log2 < 0.0f) {
 #pragma unroll
-    for (int i = 0; i < D / 2; ++i) x[i] ^= 0x80008000u;
+    for (int i = 0; i < 4 * kN; ++i) x[i] ^= 0x80008000u;
   }
+  __syncwarp();   // (a partner's pieces lie where this thread's terms go)
   if constexpr (!E4M3) {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-      *reinterpret_cast<uint4*>(tile + (i >> 3) * (KT * 128) + swizzled<128>(r, i & 7)) = w[i];
+    for (int k = 0; k < kN; ++k)
+      *reinterpret_cast<uint4*>(tile + query_piece<D, E4M3, QCHUNK>(r, half * kN + k)) = w[k];
     return f;
   } else {
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < D / 2; ++i) {
+    for (int i = 0; i < 4 * kN; ++i) {
       const float2 a = unpack2<BF16>(x[i]);
       top = max3f(top, fabsf(a.x), fabsf(a.y));
     }
+    if (HALF) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
     const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
     // (an infinite element makes the row NaN)
     const float up = top < INFINITY ? __int_as_float((127 + 7 - e) << 23) : NAN;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
+    for (int i = 0; i < kN / 2; ++i) {
       uint32_t term[3][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -443,11 +467,28 @@ __device__ __forceinline__ float put_query(const PagedParams& p, bool live, uint
       }
 #pragma unroll
       for (int n = 0; n < q_terms(E4M3, BF16); ++n)
-        *reinterpret_cast<uint4*>(tile + n * (KT * D) + swizzled<D>(r, i)) =
+        *reinterpret_cast<uint4*>(tile + n * QCHUNK + swizzled<D>(r, half * (kN / 2) + i)) =
             make_uint4(term[n][0], term[n][1], term[n][2], term[n][3]);
     }
     return f * __int_as_float((127 - 7 + e) << 23);
   }
+}
+
+// A thread's part of 32 (HALF: two times 32, SPLIT columns apart) accumulator
+// columns.
+template <bool HALF, int SPLIT>
+__device__ __forceinline__ void acc_load(uint32_t at, uint32_t* r) {
+  if constexpr (HALF)
+    tmem_ld16x2_32<SPLIT>(at, r);
+  else
+    tmem_ld32(at, r);
+}
+template <bool HALF, int SPLIT>
+__device__ __forceinline__ void acc_store(uint32_t at, const uint32_t* r) {
+  if constexpr (HALF)
+    tmem_st16x2_32<SPLIT>(at, r);
+  else
+    tmem_st32(at, r);
 }
 
 // Two consecutive K-steps (32 codes each) of D[tmem] (+)= A[smem] * B[smem]^T
@@ -472,12 +513,14 @@ __device__ __forceinline__ void mma_codes_x2(uint32_t d_tmem, uint32_t a_lo, uin
       : "memory");
 }
 
-template <int D, bool E4M3, bool BF16>
+template <int D, bool E4M3, bool BF16, bool HALF>
 __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v) {
-  using L = Lay<D, E4M3, BF16>;
+  using L = Lay<D, E4M3, BF16, HALF>;
   constexpr bool MBF = BF16 && !E4M3;
+  constexpr int RT = unit_rows(HALF);
+  constexpr int kPer = HALF ? KT / 2 : KT;   // a step's keys a softmax thread takes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -550,7 +593,9 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     // -------------------------------------------------------- softmax
     regs_increase<Split<E4M3>::kSoftmax>();
     const int t = (warp - 4) >> 2, wq = warp & 3;
-    const int r = wq * 32 + lane;
+    // row of the tile, and which half of it
+    const int half = HALF ? lane >> 4 : 0;
+    const int r = HALF ? wq * 16 + (lane & 15) : wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + (t ? 128u : 0u) + lane_off;
     const uint32_t tO = tmem + (t ? 384u : 256u) + lane_off;
@@ -578,17 +623,18 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       return tok;
     };
     // the row of a segment's unit, and its query
-    auto row_of = [&](const Segment& g) { return g.split ? r : t * 128 + r; };
+    auto row_of = [&](const Segment& g) { return HALF || g.split ? r : t * 128 + r; };
     auto ask = [&](const Cursor& c, const Segment& g) {
       int64_t token, head;
       const int ru = row_of(g);
       place(c, ru, token, head);
       if (ru < g.rows)
-        ask_query<D, E4M3>(reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh, sQ + t * L::kQTile, r);
+        ask_query<D, E4M3, HALF, L::kQChunk>(reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh,
+                                             sQ + t * L::kQTile, r, half);
     };
     save(c0, v0);
     bool first = true;
-    if (v0 < v1) ask(c0, segment_of(p, c0, v0, v1, true));
+    if (v0 < v1) ask(c0, segment_of<RT>(p, c0, v0, v1, true));
     for (bool ok = v0 < v1; ok;) {
       float f = 0.0f;
       int seen, s0, s1;
@@ -597,17 +643,20 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         Cursor c;
         int v, v_end;
         load(c, v, v_end);
-        const Segment g = segment_of(p, c, v, v_end, first);
-        s0 = g.s0, s1 = g.s1, split = g.split;
+        const Segment g = segment_of<RT>(p, c, v, v_end, first);
+        s0 = g.s0, s1 = g.s1, split = HALF || g.split;
         const int ru = row_of(g);
         int64_t token, head;
         const int tok = place(c, ru, token, head);
         // rows that the unit has not: nothing of theirs is removed (a removed
         // key costs the whole warp), and a warp of them alone only keeps step
-        idle = ru - lane >= g.rows;
+        idle = ru - (HALF ? lane & 15 : lane) >= g.rows;
         seen = ru >= g.rows ? 0x7fffffff : p.is_causal ? min(max(c.s.len - c.s.nq + tok + 1, 0), c.s.len) : c.s.len;
         cp_async_wait<0>();
-        if (!idle) f = put_query<D, E4M3, BF16>(p, ru < g.rows, sQ + t * L::kQTile, r);
+        if (!idle) {
+          __syncwarp();
+          f = put_query<D, E4M3, BF16, HALF, L::kQChunk>(p, ru < g.rows, sQ + t * L::kQTile, r, half);
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -637,47 +686,49 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
           continue;
         }
         tc_fence_after();
-        float x[KT];
+        float x[kPer];
         {
-          uint32_t u[KT];
+          uint32_t u[kPer];
 #pragma unroll
-          for (int i = 0; i < KT / 32; ++i) tmem_ld32(tS + i * 32, u + i * 32);
+          for (int i = 0; i < kPer / 32; ++i) acc_load<HALF, KT / 2>(tS + i * 32, u + i * 32);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < KT; ++i) x[i] = __uint_as_float(u[i]);
+          for (int i = 0; i < kPer; ++i) x[i] = __uint_as_float(u[i]);
         }
         const int left = seen - s * KT;   // keys of this tile that the row sees
         if (__any_sync(0xffffffffu, left < KT) || bad != 0u) {
-          uint32_t keep[KT / 32];
+          const int mine_left = left - half * kPer;
+          const uint32_t mine_bad = bad >> (half * (kPer / 16));
+          uint32_t keep[kPer / 32];
 #pragma unroll
-          for (int i = 0; i < KT / 32; ++i) {
-            const int n = min(max(left - 32 * i, 0), 32);
+          for (int i = 0; i < kPer / 32; ++i) {
+            const int n = min(max(mine_left - 32 * i, 0), 32);
             keep[i] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
-            if ((bad >> (2 * i)) & 1u) keep[i] &= 0xffff0000u;
-            if ((bad >> (2 * i)) & 2u) keep[i] &= 0x0000ffffu;
+            if ((mine_bad >> (2 * i)) & 1u) keep[i] &= 0xffff0000u;
+            if ((mine_bad >> (2 * i)) & 2u) keep[i] &= 0x0000ffffu;
           }
 #pragma unroll
-          for (int i = 0; i < KT; ++i) x[i] = ((keep[i >> 5] >> (i & 31)) & 1u) ? x[i] : -INFINITY;
+          for (int i = 0; i < kPer; ++i) x[i] = ((keep[i >> 5] >> (i & 31)) & 1u) ? x[i] : -INFINITY;
         }
         bool need;
-        uint32_t pk[KT / 2];
-        const float alpha = weights<E4M3, MBF>(x, f, notes + slot * kGroups, m, l, need, pk);
+        uint32_t pk[kPer / 2];
+        const float alpha = weights<E4M3, MBF, kPer>(x, f, notes + slot * kGroups + half * (kPer / 16), m, l, need, pk);
         if (mine > 0 && __any_sync(0xffffffffu, need)) {
           // the earlier products of this tile are complete: S of this step was
           // issued behind them
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
+          for (int i = 0; i < D / (HALF ? 64 : 32); ++i) {
             uint32_t o[32];
-            tmem_ld32(tO + i * 32, o);
+            acc_load<HALF, D / 2>(tO + i * 32, o);
             tmem_ld_wait();
             float* of = reinterpret_cast<float*>(o);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) mul2_bcast(of[e], of[e + 1], alpha);
-            tmem_st32(tO + i * 32, o);
+            acc_store<HALF, D / 2>(tO + i * 32, o);
           }
         }
-        tmem_st32(tS, pk);
-        tmem_st32(tS + 32, pk + 32);
+#pragma unroll
+        for (int i = 0; i < kPer / 64; ++i) acc_store<HALF, KT / 4>(tS + i * 32, pk + i * 32);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -688,18 +739,19 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       Cursor c;
       int v, v_end;
       load(c, v, v_end);
-      const Segment g = segment_of(p, c, v, v_end, first);
+      const Segment g = segment_of<RT>(p, c, v, v_end, first);
       Cursor next = c;
       const int v_next = c.u0 + g.s1;
       if (v_next < v_end) {
         advance(p, RT, next);
         // its query, while this one's rows are written (S of this tile is complete)
-        ask(next, segment_of(p, next, v_next, v_end, false));
+        ask(next, segment_of<RT>(p, next, v_next, v_end, false));
       }
       // n_s completions of s_full[t] so far, as many of o_done[t]
       if (mine > 0 && !warp_wait(&bars->o_done[t], (n_s - 1) & 1, bars, limit, kSiteO)) break;
       tc_fence_after();
       float fa = 1.0f, fb = 0.0f;
+      if (HALF) l += __shfl_xor_sync(0xffffffffu, l, 16);   // the row's sum
       if (split) {
         // join the two warpgroups' sums: each leaves (m, l) behind its P and
         // writes half of the columns
@@ -708,7 +760,8 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         for (int i = 0; i < 32; ++i) ml[i] = 0u;
         ml[0] = __float_as_uint(m);
         ml[1] = __float_as_uint(l);
-        tmem_st32(tS + 96, ml);
+        // (HALF: a copy for each of a row's threads)
+        acc_store<HALF, 32>(tS + (HALF ? 64 : 96), ml);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -719,7 +772,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         }
         ++n_sums;
         tc_fence_after();
-        tmem_ld32(tmem + (t ? 0u : 128u) + lane_off + 96, ml);
+        acc_load<HALF, 32>(tmem + (t ? 0u : 128u) + lane_off + (HALF ? 64 : 96), ml);
         tmem_ld_wait();
         const float mo = __uint_as_float(ml[0]), lo = __uint_as_float(ml[1]);
         const float mx = fmaxf(m, mo), base = mx == -INFINITY ? 0.0f : mx;
@@ -733,23 +786,28 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       int64_t token, head;
       place(c, ru, token, head);
       // O is undefined where no step was taken; otherwise (no key seen) zeros
-      const bool own = mine > 0, other = g.split && (t == 0 ? g.s1 - g.s0 > 1 : true);
+      const bool own = mine > 0, other = split && (t == 0 ? g.s1 - g.s0 > 1 : true);
       const float inv = !g.whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
       fa *= inv;
       fb *= inv;
       uint16_t* orow = reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh;
       float* prow = part_rows<D>(p, blockIdx.x, g.first ? 0 : 1, RT) + static_cast<int64_t>(ru) * (D + 2);
-      const int i0 = g.split ? t * (D / 64) : 0, i1 = g.split ? i0 + D / 64 : D / 32;
+      // this thread's runs of 32 columns: all, or half of them (HALF: of its
+      // half row's; where that is one run, the first warpgroup's)
+      constexpr int kRuns = HALF ? D / 64 : D / 32;
+      const int i0 = split ? t * (kRuns / 2) : 0;
+      const int i1 = !split ? kRuns : kRuns == 1 ? 1 - t : i0 + kRuns / 2;
+      const int col0 = half * (D / 2);
       for (int i = i0; i < i1 && !idle; ++i) {
         uint32_t o[32];
-        tmem_ld32(tO + i * 32, o);
+        acc_load<HALF, D / 2>(tO + i * 32, o);
         tmem_ld_wait();
         float* of = reinterpret_cast<float*>(o);
 #pragma unroll
         for (int e = 0; e < 32; ++e) of[e] = own ? of[e] * fa : 0.0f;
         if (other) {
           uint32_t o2[32];
-          tmem_ld32(tmem + (t ? 256u : 384u) + lane_off + i * 32, o2);
+          acc_load<HALF, D / 2>(tmem + (t ? 256u : 384u) + lane_off + i * 32, o2);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) of[e] = fmaf(__uint_as_float(o2[e]), fb, of[e]);
@@ -758,13 +816,13 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
           if (g.whole) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(orow + i * 32 + e * 8) =
+              *reinterpret_cast<uint4*>(orow + col0 + i * 32 + e * 8) =
                   make_uint4(pack2<BF16>(of[8 * e], of[8 * e + 1]), pack2<BF16>(of[8 * e + 2], of[8 * e + 3]),
                              pack2<BF16>(of[8 * e + 4], of[8 * e + 5]), pack2<BF16>(of[8 * e + 6], of[8 * e + 7]));
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
-              *reinterpret_cast<float2*>(prow + i * 32 + e) = make_float2(of[e], of[e + 1]);
+              *reinterpret_cast<float2*>(prow + col0 + i * 32 + e) = make_float2(of[e], of[e + 1]);
           }
         }
       }
@@ -775,7 +833,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->read);
         if (!warp_wait(&bars->read, (n_sums - 1) & 1, bars, limit, kSiteSums)) break;
       }
-      if (live && (!g.split || t == 0)) {
+      if (live && half == 0 && (!split || t == 0)) {
         if (!g.whole) {
           *reinterpret_cast<float2*>(prow + D) = make_float2(m, l);
         } else if (p.lse != nullptr) {
@@ -842,7 +900,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       uint32_t phase = 0;
       bool lapped = false;
       RingAt<L::kNotes> note_at;
-      for_each_segment(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
+      for_each_segment<RT>(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
         Window w = open_window(c, g.s0);
         // keys' warp: lane i < 8 looks after keys 16 i .. of a step; its page's
         // scales are asked for a step ahead (the entry may lie in the window
@@ -911,12 +969,13 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         wait_any(full0 + j % ring, (j / ring) & 1, bars, limit, kSiteDrain, false);
     } else if (warp == 1) {
       // -------------------------------------------------------- products
-      constexpr uint32_t idS = idesc_f16_f32acc(MBF, false, 128, KT);
-      constexpr uint32_t idPV = idesc_f16_f32acc(MBF, true, 128, D);
+      constexpr uint32_t kM = tile_rows(HALF);
+      constexpr uint32_t idS = idesc_f16_f32acc(MBF, false, kM, KT);
+      constexpr uint32_t idPV = idesc_f16_f32acc(MBF, true, kM, D);
       constexpr uint32_t kHi = desc_hi_sw128(1024);
       // e4m3 operands (type 0 in the descriptor's fields, D = fp32), rows of D
       // bytes: the 128-byte swizzle, or the 64-byte one (mode 4)
-      constexpr uint32_t idCodes = (1u << 4) | ((KT >> 3) << 17) | ((128 >> 4) << 24);
+      constexpr uint32_t idCodes = (1u << 4) | ((KT >> 3) << 17) | ((kM >> 4) << 24);
       constexpr uint32_t kHiCodes = D == 128 ? kHi : ((512u >> 4) | (1u << 14) | (4u << 29));
       const uint32_t q_lo = desc_lo_sw128(smem_addr(sQ), 16);
       const uint32_t k_lo = desc_lo_sw128(smem_addr(sK), 16);
@@ -933,13 +992,13 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
           for (int n = 0; n < q_terms(E4M3, BF16); ++n)
 #pragma unroll
             for (int k = 0; k < D / 64; ++k)
-              mma_codes_x2<kHiCodes>(tmem + (t ? 128u : 0u), a0 + n * (L::kCodes >> 4) + 4 * k, b0 + 4 * k, idCodes,
+              mma_codes_x2<kHiCodes>(tmem + (t ? 128u : 0u), a0 + n * (L::kQChunk >> 4) + 4 * k, b0 + 4 * k, idCodes,
                                      n + k > 0 ? 1u : 0u);
         } else {
 #pragma unroll
           for (int ch = 0; ch < L::kChunks; ++ch) {
             const uint32_t off = static_cast<uint32_t>(ch * L::kChunkBytes) >> 4;
-            mma_ss_x4<kHi, kHi>(tmem + (t ? 128u : 0u), a0 + off, b0 + off, 2u, 2u, idS, ch > 0 ? 1u : 0u);
+            mma_ss_x4<kHi, kHi>(tmem + (t ? 128u : 0u), a0 + ((ch * L::kQChunk) >> 4), b0 + off, 2u, 2u, idS, ch > 0 ? 1u : 0u);
           }
         }
         mma_commit_elect(&bars->s_full[t]);
@@ -982,7 +1041,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         tc_fence_after();
         return true;
       };
-      for_each_segment(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
+      for_each_segment<RT>(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
         if (p.debug_withhold_q) return false;
         const int n = g.s1 - g.s0;
         issued = true;
@@ -990,16 +1049,17 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         // all roles together is what the instruction cache has to hold):
         // event e is warpgroup t = e & 1's product of its step j and S of its
         // next one, the first two only the latter.
-        const int events = g.split ? n : 2 * n;
+        const int events = HALF || g.split ? n : 2 * n;
 #pragma unroll 1
         for (int e = -2; e < events; ++e) {
-          const int t = e & 1, j = g.split ? e : e >> 1;
-          const int ahead = j + (g.split ? 2 : 1);
-          const bool head = g.split || t == 0, tail = g.split || t == 1;   // of the step's events
+          const bool split = HALF || g.split;
+          const int t = e & 1, j = split ? e : e >> 1;
+          const int ahead = j + (split ? 2 : 1);
+          const bool head = split || t == 0, tail = split || t == 1;   // of the step's events
           if (e >= 0) {
             if (head && !next_v(c.s.len - (g.s0 + j) * KT)) return false;
             if (!next_p(t)) return false;
-            issue_pv(t, j > (g.split ? 1 : 0));
+            issue_pv(t, j > (split ? 1 : 0));
             if (tail) {
               mma_commit_elect(&bars->v_empty[v_at.idx]);
               v_at.next();
@@ -1056,9 +1116,9 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
   }
 }
 
-template <int D, bool E4M3, bool BF16>
+template <int D, bool E4M3, bool BF16, bool HALF>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
-  auto kern = paged_tc_kernel<D, E4M3, BF16>;
+  auto kern = paged_tc_kernel<D, E4M3, BF16, HALF>;
   static std::atomic<uint64_t> configured{0};  // a bit a device
   const uint64_t bit = 1ull << p.device;
   cudaError_t e = cudaSuccess;
@@ -1069,14 +1129,14 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUte
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != static_cast<int>(Split<E4M3>::kLaunch)) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, E4M3, BF16>::kTotal);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, E4M3, BF16, HALF>::kTotal);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.n_ctas));
   cfg.blockDim = dim3(Split<E4M3>::kThreads);
-  cfg.dynamicSmemBytes = Lay<D, E4M3, BF16>::kTotal;
+  cfg.dynamicSmemBytes = Lay<D, E4M3, BF16, HALF>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1085,24 +1145,27 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUte
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, p, tm_k, tm_v);
   if (e != cudaSuccess) return e;
-  return sdpa_impl::launch_paged_join(p, D, BF16, RT, stream);
+  return sdpa_impl::launch_paged_join(p, D, BF16, unit_rows(HALF), stream);
 }
 
-template <int D>
+template <int D, bool HALF>
 cudaError_t launch_dim(const PagedParams& p, bool bf16, bool e4m3, const CUtensorMap& k, const CUtensorMap& v,
                        cudaStream_t s) {
-  if (e4m3) return bf16 ? launch_one<D, true, true>(p, k, v, s) : launch_one<D, true, false>(p, k, v, s);
-  return bf16 ? launch_one<D, false, true>(p, k, v, s) : launch_one<D, false, false>(p, k, v, s);
+  if (e4m3) return bf16 ? launch_one<D, true, true, HALF>(p, k, v, s) : launch_one<D, true, false, HALF>(p, k, v, s);
+  return bf16 ? launch_one<D, false, true, HALF>(p, k, v, s) : launch_one<D, false, false, HALF>(p, k, v, s);
 }
 
 }  // namespace
 
 namespace sdpa_impl {
 
-cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, bool bf16, bool e4m3, const CUtensorMap& tm_k,
+cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile, const CUtensorMap& tm_k,
                             const CUtensorMap& tm_v, cudaStream_t stream) {
-  return head_dim == 64 ? launch_dim<64>(p, bf16, e4m3, tm_k, tm_v, stream)
-                        : launch_dim<128>(p, bf16, e4m3, tm_k, tm_v, stream);
+  if (tile == unit_rows(true))
+    return head_dim == 64 ? launch_dim<64, true>(p, bf16, e4m3, tm_k, tm_v, stream)
+                          : launch_dim<128, true>(p, bf16, e4m3, tm_k, tm_v, stream);
+  return head_dim == 64 ? launch_dim<64, false>(p, bf16, e4m3, tm_k, tm_v, stream)
+                        : launch_dim<128, false>(p, bf16, e4m3, tm_k, tm_v, stream);
 }
 
 cudaError_t read_and_clear_paged_status(unsigned int* status) {

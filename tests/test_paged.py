@@ -95,6 +95,9 @@ ATTEND = [  # D, cache, dtype, page, kv heads, G, memory order, causal, counts, 
     (64, "e4m3", torch.float16, 256, 4, 8, "tokens", True, [4, 2], [600, 31]),
     (128, "16", torch.bfloat16, 1024, 4, 2, "tokens", True, [1, 16], [1500, 16]),
     (64, "16", torch.float16, 512, 6, 1, "heads", False, [1, 2], [515, 40]),
+    (128, "e4m3", torch.float16, 32, 2, 8, "heads", True, [5, 8, 1, 0], [300, 8, 129, 4]),
+    (128, "16", torch.bfloat16, 64, 3, 16, "tokens", True, [4, 3, 1], [1000, 3, 128]),
+    (64, "16", torch.float16, 16, 1, 48, "padded", False, [1, 1], [257, 40]),
 ]
 
 
