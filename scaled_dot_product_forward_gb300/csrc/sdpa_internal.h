@@ -192,22 +192,23 @@ struct PagedForm {
 // CTAs an SM of the form for few rows.  They hide each other's latencies (a
 // step is a chain of loads, conversions, two products and an exponential), as
 // many as the registers and the rings leave room for.
-constexpr int paged_per_sm(int head_dim, bool e4m3, int rows) {
-  return head_dim == 64 ? (rows == 16 ? 4 : 3) : (e4m3 && rows == 16 ? 3 : 2);
-}
+constexpr int paged_per_sm(int head_dim, bool e4m3) { return head_dim == 64 ? 4 : e4m3 ? 3 : 2; }
+// Up to 16 rows a head go to the form for few rows (sdpa_paged_sm103a.cu), up
+// to 64 to the half-tile form of the other (sdpa_paged_tc_sm103a.cu), more to
+// its full tiles.  16 sequences of 8192 tokens, 8 heads of 128, e4m3 / heads of
+// 64, e4m3: 8 rows 72 / 41 us in the first form, 75 / 58 in the second; 16 rows
+// 81 / 45 and 76 / 58; 24 rows (two tiles, in the first form) 103 / 66 and 79 /
+// 59; 64 rows 85 / 63 in half tiles, 72 rows 101 / 87 in full ones.
 // The form for few rows has four warps, for up to four heads of a unit (as
 // many as divide the heads; tokens' rows of neighbouring heads lie together,
 // so reading them together keeps DRAM pages open), which share a head's keys
 // when there are fewer: 16 keys of a head each a step.
 inline PagedForm paged_form(int64_t max_rows, int head_dim, bool e4m3, int64_t n_kv, int sms) {
-  if (max_rows > 32) return {sms, max_rows <= 64 ? 64 : 256, 1, 7, 2, true};
-  const int rows = max_rows <= 16 ? 16 : 32;
+  if (max_rows > 16) return {sms, max_rows <= 64 ? 64 : 256, 1, 7, 2, true};
   const int heads = n_kv % 4 == 0 ? 4 : n_kv % 2 == 0 ? 2 : 1;
-  return {paged_per_sm(head_dim, e4m3, rows) * sms, rows, heads, heads == 4 ? 4 : heads == 2 ? 5 : 6,
-          heads == 4 ? 4 : 2, false};
+  return {paged_per_sm(head_dim, e4m3) * sms, 16, heads, heads == 4 ? 4 : heads == 2 ? 5 : 6, heads == 4 ? 4 : 2, false};
 }
-cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile_rows,
-                         cudaStream_t stream);
+cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, cudaStream_t stream);
 // The form for many rows; tm_k, tm_v: 4-D maps of the pages (D, token, head,
 // page), box min(page size, 128) tokens by 64 16-bit elements with the 128-byte
 // swizzle, or by D codes, the keys' with the swizzle of D bytes, the values'

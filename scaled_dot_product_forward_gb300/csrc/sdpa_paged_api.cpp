@@ -240,7 +240,7 @@ uint64_t sdpa_paged_workspace_bytes(int64_t head_dim, int64_t n_heads, int64_t n
   const int64_t rows = max_seqlen_q * (n_heads / n_kv_heads);
   uint64_t most = 0;
   for (const bool e4m3 : {false, true})
-    for (const int64_t r : {rows < 16 ? rows : 16, rows < 32 ? rows : 32, rows < 64 ? rows : 64, rows}) {
+    for (const int64_t r : {rows < 16 ? rows : 16, rows < 64 ? rows : 64, rows}) {
       const uint64_t n =
           workspace_bytes(sdpa_impl::paged_form(r, static_cast<int>(head_dim), e4m3, n_kv_heads, sms), head_dim);
       most = n > most ? n : most;
@@ -365,8 +365,7 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
     e = sdpa_impl::launch_paged_tc(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, form.rows, tm_k, tm_v,
                                    static_cast<cudaStream_t>(stream));
   } else {
-    e = sdpa_impl::launch_paged(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, form.rows,
-                                static_cast<cudaStream_t>(stream));
+    e = sdpa_impl::launch_paged(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, static_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }

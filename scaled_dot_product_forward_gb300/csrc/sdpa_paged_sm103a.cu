@@ -38,6 +38,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kWarpKeys = 16;
+constexpr int RT = 16;                 // rows a unit: one tile of the products
 constexpr float kRescaleLog2 = 8.0f;
 
 template <int D, bool E4M3>
@@ -124,9 +125,8 @@ struct WarpScratch {      // a warp's notes on its stages
   int ok[6];              // 0: the stage's page is not one of the cache's
 };
 
-template <int D, bool E4M3, bool BF16, int MT>
+template <int D, bool E4M3>
 struct Smem {
-  static constexpr int RT = 16 * MT;
   using R = Ring<D, E4M3>;
   static constexpr int kJoinRow = D + 4;                        // floats
   static constexpr int kJoin = kWarps * RT * kJoinRow * 4;      // over the rings
@@ -137,7 +137,7 @@ struct Smem {
   static constexpr int kDivide = (kMl + kWarps * RT * 8 + 15) / 16 * 16;
   // Exactly kPerSm CTAs an SM: with room for more, the kernel's equal shares
   // would land on some SMs one more at a time and on others one fewer.
-  static constexpr int kPerSm = sdpa_impl::paged_per_sm(D, E4M3, RT);
+  static constexpr int kPerSm = sdpa_impl::paged_per_sm(D, E4M3);
   static constexpr int kNeed = kDivide + static_cast<int>(sizeof(DivideScratch));
   static constexpr int kLeast = 227 * 1024 / (kPerSm + 1);
   static constexpr int kTotal = kNeed > kLeast ? kNeed : kLeast;
@@ -162,12 +162,11 @@ __device__ __forceinline__ void store_out4(uint16_t* at, const float4& o, float 
   *reinterpret_cast<uint2*>(at) = make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
 }
 
-template <int D, bool E4M3, bool BF16, int MT>
-__global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 * MT))
+template <int D, bool E4M3, bool BF16>
+__global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
     paged_kernel(const __grid_constant__ PagedParams p) {
-  using S = Smem<D, E4M3, BF16, MT>;
+  using S = Smem<D, E4M3>;
   using R = Ring<D, E4M3>;
-  constexpr int RT = 16 * MT;
   constexpr int NK = D / 16;              // k-steps of S
   constexpr int NV = D / 8;               // column groups of O
   constexpr int RB = R::kRowBytes;
@@ -302,71 +301,64 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
     const int head = c.h * p.unit_heads + hsub;
 
     // the rows' queries as operand fragments, and how many keys each sees
-    uint32_t qf[MT][NK][4];
-    float mul[MT][2];
-    int lim[MT][2];
+    uint32_t qf[NK][4];
+    float mul[2];
+    int lim[2];
     int lim_min = keys;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = hf * 8 + g8;
+      const bool live = r < rows;
+      const int rr = c.t * RT + r;
+      const int i = rr / p.G, g = rr - i * p.G;
+      lim[hf] = live ? (p.is_causal ? min(max(c.s.len - c.s.nq + i + 1, 0), c.s.len) : c.s.len) : 0;
+      if (live) lim_min = min(lim_min, lim[hf]);
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) +
+                            (static_cast<int64_t>(c.s.q0) + i) * p.q_st +
+                            (static_cast<int64_t>(head) * p.G + g) * p.q_sh;
+      uint2 w[NK];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = mt * 16 + hf * 8 + g8;
-        const bool live = r < rows;
-        const int rr = c.t * RT + r;
-        const int i = rr / p.G, g = rr - i * p.G;
-        lim[mt][hf] = live ? (p.is_causal ? min(max(c.s.len - c.s.nq + i + 1, 0), c.s.len) : c.s.len) : 0;
-        if (live) lim_min = min(lim_min, lim[mt][hf]);
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) +
-                              (static_cast<int64_t>(c.s.q0) + i) * p.q_st +
-                              (static_cast<int64_t>(head) * p.G + g) * p.q_sh;
-        uint2 w[NK];
-#pragma unroll
-        for (int ks = 0; ks < NK; ++ks) {
-          const int d = E4M3 ? 16 * (t4 + 4 * (ks / 4)) + 4 * (ks % 4)
-                             : 8 * (t4 + 4 * (ks / 2)) + 4 * (ks % 2);
-          w[ks] = live ? __ldg(reinterpret_cast<const uint2*>(src + d)) : make_uint2(0u, 0u);
-        }
-        float f = p.scale_log2;
-        if constexpr (E4M3 && BF16) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int ks = 0; ks < NK; ++ks) {
-            top = max(top, max(w[ks].x & 0x7fffu, (w[ks].x >> 16) & 0x7fffu));
-            top = max(top, max(w[ks].y & 0x7fffu, (w[ks].y >> 16) & 0x7fffu));
-          }
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^(14 - exponent of the row's largest element), itself within fp32
-          const int e = max(static_cast<int>(top >> 7) - 127, -110);
-          const float up = __int_as_float((127 + 14 - e) << 23);
-          f *= __int_as_float((127 - 14 + e) << 23);
-#pragma unroll
-          for (int ks = 0; ks < NK; ++ks) {
-            const float2 a = unpack2<true>(w[ks].x), b = unpack2<true>(w[ks].y);
-            w[ks].x = pack2<false>(a.x * up, a.y * up);
-            w[ks].y = pack2<false>(b.x * up, b.y * up);
-          }
-        }
-        mul[mt][hf] = f;
+      for (int ks = 0; ks < NK; ++ks) {
+        const int d = E4M3 ? 16 * (t4 + 4 * (ks / 4)) + 4 * (ks % 4)
+                           : 8 * (t4 + 4 * (ks / 2)) + 4 * (ks % 2);
+        w[ks] = live ? __ldg(reinterpret_cast<const uint2*>(src + d)) : make_uint2(0u, 0u);
+      }
+      float f = p.scale_log2;
+      if constexpr (E4M3 && BF16) {
+        uint32_t top = 0;
 #pragma unroll
         for (int ks = 0; ks < NK; ++ks) {
-          qf[mt][ks][hf] = w[ks].x;
-          qf[mt][ks][2 + hf] = w[ks].y;
+          top = max(top, max(w[ks].x & 0x7fffu, (w[ks].x >> 16) & 0x7fffu));
+          top = max(top, max(w[ks].y & 0x7fffu, (w[ks].y >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(14 - exponent of the row's largest element), itself within fp32
+        const int e = max(static_cast<int>(top >> 7) - 127, -110);
+        const float up = __int_as_float((127 + 14 - e) << 23);
+        f *= __int_as_float((127 - 14 + e) << 23);
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) {
+          const float2 a = unpack2<true>(w[ks].x), b = unpack2<true>(w[ks].y);
+          w[ks].x = pack2<false>(a.x * up, a.y * up);
+          w[ks].y = pack2<false>(b.x * up, b.y * up);
         }
       }
+      mul[hf] = f;
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        qf[ks][hf] = w[ks].x;
+        qf[ks][2 + hf] = w[ks].y;
+      }
+    }
     lim_min = __reduce_min_sync(0xffffffffu, lim_min);
 
-    float o[MT][NV][4];
-    float m[MT][2], l[MT][2];
+    float o[NV][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.0f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.0f;
-    }
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
 
     int stage = 0;
     for (int s = s0; s < s1; ++s) {
@@ -379,13 +371,11 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
         const uint8_t* vt = kt + R::kTile;
         // S = Q K^T: thread (g8, t4) reads pieces t4, t4 + 4, .. of keys g8
         // and 8 + g8
-        float acc[MT][2][4];
+        float acc[2][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -397,15 +387,12 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const uint32_t b0 = codes_to_half2(w[e]), b1 = codes_to_half2_hi(w[e]);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma16816<MBF>(acc[mt][n], qf[mt][cc * 4 + e], b0, b1);
+                mma16816<MBF>(acc[n], qf[cc * 4 + e], b0, b1);
               }
             } else {
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                  mma16816<MBF>(acc[mt][n], qf[mt][cc * 2 + e], w[2 * e], w[2 * e + 1]);
+                mma16816<MBF>(acc[n], qf[cc * 2 + e], w[2 * e], w[2 * e + 1]);
             }
           }
         float ksc = 1.0f, lv = 0.0f, ivs = 1.0f;
@@ -417,69 +404,59 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
         }
         bool grow = false;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float f = mul[mt][hf] * ksc;
-            float* x = acc[mt][0] + 2 * hf;
-            float* y = acc[mt][1] + 2 * hf;
-            x[0] = fmaf(x[0], f, lv);
-            x[1] = fmaf(x[1], f, lv);
-            y[0] = fmaf(y[0], f, lv);
-            y[1] = fmaf(y[1], f, lv);
-          }
+        for (int hf = 0; hf < 2; ++hf) {
+          const float f = mul[hf] * ksc;
+          float* x = acc[0] + 2 * hf;
+          float* y = acc[1] + 2 * hf;
+          x[0] = fmaf(x[0], f, lv);
+          x[1] = fmaf(x[1], f, lv);
+          y[0] = fmaf(y[0], f, lv);
+          y[1] = fmaf(y[1], f, lv);
+        }
         if (key0 + kWarpKeys > lim_min) {
           // some row does not see some of these keys
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (key0 + n * 8 + t4 * 2 + (e & 1) >= lim[mt][e >> 1]) acc[mt][n][e] = -INFINITY;
+            for (int e = 0; e < 4; ++e)
+              if (key0 + n * 8 + t4 * 2 + (e & 1) >= lim[e >> 1]) acc[n][e] = -INFINITY;
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            grow |= fmaxf(max3f(acc[mt][0][2 * hf], acc[mt][0][2 * hf + 1], acc[mt][1][2 * hf]),
-                          acc[mt][1][2 * hf + 1]) > m[mt][hf] + kRescaleLog2;
+        for (int hf = 0; hf < 2; ++hf)
+          grow |= fmaxf(max3f(acc[0][2 * hf], acc[0][2 * hf + 1], acc[1][2 * hf]),
+                        acc[1][2 * hf + 1]) > m[hf] + kRescaleLog2;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int hf = 0; hf < 2; ++hf) {
+            float x = fmaxf(fmaxf(acc[0][2 * hf], acc[0][2 * hf + 1]),
+                            fmaxf(acc[1][2 * hf], acc[1][2 * hf + 1]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            if (x > m[hf]) {
+              const float alpha = ex2(m[hf] - x);
+              m[hf] = x;
+              l[hf] *= alpha;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              float x = fmaxf(fmaxf(acc[mt][0][2 * hf], acc[mt][0][2 * hf + 1]),
-                              fmaxf(acc[mt][1][2 * hf], acc[mt][1][2 * hf + 1]));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-              if (x > m[mt][hf]) {
-                const float alpha = ex2(m[mt][hf] - x);
-                m[mt][hf] = x;
-                l[mt][hf] *= alpha;
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                  o[mt][j][2 * hf] *= alpha;
-                  o[mt][j][2 * hf + 1] *= alpha;
-                }
+              for (int j = 0; j < NV; ++j) {
+                o[j][2 * hf] *= alpha;
+                o[j][2 * hf + 1] *= alpha;
               }
             }
+          }
         }
         // weights, rounded to 16 bits for the second product (the sum keeps
         // them in fp32)
-        uint32_t pf[MT][4];
+        uint32_t pf[4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int hf = 0; hf < 2; ++hf) {
+          const float mm = m[hf] == -INFINITY ? 0.0f : m[hf];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float mm = m[mt][hf] == -INFINITY ? 0.0f : m[mt][hf];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const float w0 = ex2(acc[mt][n][2 * hf] - mm), w1 = ex2(acc[mt][n][2 * hf + 1] - mm);
-              l[mt][hf] = fmaf(w0 + w1, ivs, l[mt][hf]);
-              pf[mt][2 * n + hf] = pack2<MBF>(w0, w1);
-            }
+          for (int n = 0; n < 2; ++n) {
+            const float w0 = ex2(acc[n][2 * hf] - mm), w1 = ex2(acc[n][2 * hf + 1] - mm);
+            l[hf] = fmaf(w0 + w1, ivs, l[hf]);
+            pf[2 * n + hf] = pack2<MBF>(w0, w1);
           }
+        }
         // O += P V: thread (g8, t4) reads its run of columns of keys 2 t4,
         // 2 t4 + 1, 8 + 2 t4, 9 + 2 t4, and pairs neighbouring keys' elements
         auto columns = [&](int piece, int sub, int j0) {
@@ -505,20 +482,14 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
                 const uint32_t hi = __byte_perm(cw, d, hh ? 0x7362 : 0x5140);
                 const uint32_t l0 = codes_to_half2(lo), l1 = codes_to_half2_hi(lo);
                 const uint32_t h0 = codes_to_half2(hi), h1 = codes_to_half2_hi(hi);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  mma16816<MBF>(o[mt][j0 + e * 4 + hh * 2], pf[mt], l0, h0);
-                  mma16816<MBF>(o[mt][j0 + e * 4 + hh * 2 + 1], pf[mt], l1, h1);
-                }
+                mma16816<MBF>(o[j0 + e * 4 + hh * 2], pf, l0, h0);
+                mma16816<MBF>(o[j0 + e * 4 + hh * 2 + 1], pf, l1, h1);
               }
             } else {
               const uint32_t l0 = __byte_perm(a, b, 0x5410), l1 = __byte_perm(a, b, 0x7632);
               const uint32_t h0 = __byte_perm(cw, d, 0x5410), h1 = __byte_perm(cw, d, 0x7632);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<MBF>(o[mt][j0 + e * 2], pf[mt], l0, h0);
-                mma16816<MBF>(o[mt][j0 + e * 2 + 1], pf[mt], l1, h1);
-              }
+              mma16816<MBF>(o[j0 + e * 2], pf, l0, h0);
+              mma16816<MBF>(o[j0 + e * 2 + 1], pf, l1, h1);
             }
           }
         };
@@ -563,46 +534,44 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3, 16 
     }
     float* join = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float ls = l[mt][hf];
-        ls += __shfl_xor_sync(0xffffffffu, ls, 1);
-        ls += __shfl_xor_sync(0xffffffffu, ls, 2);
-        const float mx = m[mt][hf];
-        const int r = mt * 16 + hf * 8 + g8;
-        if (slices > 1) {
-          if (t4 == 0) {
-            ml[(warp * RT + r) * 2] = mx;
-            ml[(warp * RT + r) * 2 + 1] = ls;
-          }
-        }
-        if (r >= rows) continue;
-        if (slices > 1 || !whole) {
-          float* row = slices > 1 ? join + (warp * RT + r) * S::kJoinRow : part + r * (D + 2);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int j = 0; j < NV; j += 2)
-              *reinterpret_cast<float2*>(row + column(2 * t4 + e, j)) =
-                  make_float2(o[mt][j][2 * hf + e], o[mt][j + 1][2 * hf + e]);
-          if (slices == 1 && t4 == 0) *reinterpret_cast<float2*>(row + D) = make_float2(mx, ls);
-        } else {
-          const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int j = 0; j < NV; j += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack2<BF16>(o[mt][j + 2 * k][2 * hf + e] * inv, o[mt][j + 2 * k + 1][2 * hf + e] * inv);
-              *reinterpret_cast<uint4*>(out_row(p, c.s.q0, head, c.t * RT + r) + column(2 * t4 + e, j)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          if (t4 == 0 && p.lse != nullptr) store_lse(p, c.s.q0, head, c.t * RT + r, mx, ls);
+    for (int hf = 0; hf < 2; ++hf) {
+      float ls = l[hf];
+      ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+      ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+      const float mx = m[hf];
+      const int r = hf * 8 + g8;
+      if (slices > 1) {
+        if (t4 == 0) {
+          ml[(warp * RT + r) * 2] = mx;
+          ml[(warp * RT + r) * 2 + 1] = ls;
         }
       }
+      if (r >= rows) continue;
+      if (slices > 1 || !whole) {
+        float* row = slices > 1 ? join + (warp * RT + r) * S::kJoinRow : part + r * (D + 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < NV; j += 2)
+            *reinterpret_cast<float2*>(row + column(2 * t4 + e, j)) =
+                make_float2(o[j][2 * hf + e], o[j + 1][2 * hf + e]);
+        if (slices == 1 && t4 == 0) *reinterpret_cast<float2*>(row + D) = make_float2(mx, ls);
+      } else {
+        const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < NV; j += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack2<BF16>(o[j + 2 * k][2 * hf + e] * inv, o[j + 2 * k + 1][2 * hf + e] * inv);
+            *reinterpret_cast<uint4*>(out_row(p, c.s.q0, head, c.t * RT + r) + column(2 * t4 + e, j)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        if (t4 == 0 && p.lse != nullptr) store_lse(p, c.s.q0, head, c.t * RT + r, mx, ls);
+      }
+    }
     if (slices > 1) {
       __syncthreads();
       for (int i = threadIdx.x; i < p.unit_heads * rows * (D / 4); i += kThreads) {
@@ -737,10 +706,10 @@ cudaError_t launch_join(const PagedParams& p, int rt, cudaStream_t stream) {
                     0, stream, p, rt);
 }
 
-template <int D, bool E4M3, bool BF16, int MT>
+template <int D, bool E4M3, bool BF16>
 cudaError_t launch_one(const PagedParams& p, cudaStream_t stream) {
-  using S = Smem<D, E4M3, BF16, MT>;
-  auto kern = paged_kernel<D, E4M3, BF16, MT>;
+  using S = Smem<D, E4M3>;
+  auto kern = paged_kernel<D, E4M3, BF16>;
   static std::atomic<uint64_t> configured{0};  // a bit a device
   const uint64_t bit = 1ull << p.device;
   cudaError_t e = cudaSuccess;
@@ -751,29 +720,21 @@ cudaError_t launch_one(const PagedParams& p, cudaStream_t stream) {
   }
   e = launch_pdl(kern, dim3(static_cast<unsigned>(p.n_ctas)), S::kTotal, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_join<D, BF16>(p, S::RT, stream);
-}
-
-template <int D, bool E4M3, bool BF16>
-cudaError_t launch_rows(const PagedParams& p, int rt, cudaStream_t stream) {
-  return rt == 16 ? launch_one<D, E4M3, BF16, 1>(p, stream) : launch_one<D, E4M3, BF16, 2>(p, stream);
+  return launch_join<D, BF16>(p, RT, stream);
 }
 
 template <int D>
-cudaError_t launch_dim(const PagedParams& p, int rt, bool bf16, bool e4m3, cudaStream_t s) {
-  if (e4m3)
-    return bf16 ? launch_rows<D, true, true>(p, rt, s) : launch_rows<D, true, false>(p, rt, s);
-  return bf16 ? launch_rows<D, false, true>(p, rt, s) : launch_rows<D, false, false>(p, rt, s);
+cudaError_t launch_dim(const PagedParams& p, bool bf16, bool e4m3, cudaStream_t s) {
+  if (e4m3) return bf16 ? launch_one<D, true, true>(p, s) : launch_one<D, true, false>(p, s);
+  return bf16 ? launch_one<D, false, true>(p, s) : launch_one<D, false, false>(p, s);
 }
 
 }  // namespace
 
 namespace sdpa_impl {
 
-cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int rt,
-                         cudaStream_t stream) {
-  return head_dim == 64 ? launch_dim<64>(p, rt, bf16, e4m3, stream)
-                        : launch_dim<128>(p, rt, bf16, e4m3, stream);
+cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
+  return head_dim == 64 ? launch_dim<64>(p, bf16, e4m3, stream) : launch_dim<128>(p, bf16, e4m3, stream);
 }
 
 cudaError_t launch_paged_join(const PagedParams& p, int head_dim, bool bf16, int rt, cudaStream_t stream) {
