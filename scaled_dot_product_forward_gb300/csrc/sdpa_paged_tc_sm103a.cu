@@ -586,7 +586,9 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       total, c0);
   const int n_ranges = range_count(p, total);
   const int v1 = v0 < 0 ? v0 : range_start(total, cta + 1, n_ranges);
-  if (v0 < 0 && threadIdx.x == 0) reinterpret_cast<JoinNote*>(p.part)[cta].pieces = 0;
+  // nothing to join, until the last segment says otherwise: a CTA that stops
+  // early leaves no note that the join would follow out of the workspace
+  if (threadIdx.x == 0) reinterpret_cast<JoinNote*>(p.part)[cta].pieces = 0;
   __syncthreads();
 
   if (warp >= 4 && warp < 12) {

@@ -210,6 +210,35 @@ def test_waits_run_out(sdpa_lib):
 
 
 @gpu
+@pytest.mark.parametrize("rows", [50, 300])
+def test_waits_run_out_over_a_used_workspace(sdpa_lib, monkeypatch, rows):
+    """A workspace may hold anything: what it says of units to join is not followed when a call
+    gives up."""
+    c = make_cache(sdpa_lib, 20, 16, 1, 128, "e4m3", torch.bfloat16, 8)
+    q = torch.randn(rows, 2, 128, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    t = tables(1, 19, 20, 3)
+    lens = torch.tensor([300], dtype=torch.int32).cuda()
+    plain = torch.empty
+
+    def used(*a, **kw):
+        x = plain(*a, **kw)
+        return x.fill_(0x7f) if x.dtype == torch.uint8 else x
+
+    monkeypatch.setattr(torch, "empty", used)
+    sdpa_lib.sdpa_debug_set_wait_limit_ns(20_000_000)
+    sdpa_lib.sdpa_debug_withhold_q_load(True)
+    try:
+        sdpa_lib.sdpa_paged_forward(q, c, t.cuda(), lens)
+        rc, bits = sdpa_lib.sdpa_last_device_status()
+    finally:
+        sdpa_lib.sdpa_debug_withhold_q_load(False)
+        sdpa_lib.sdpa_debug_set_wait_limit_ns(0)
+    assert rc == 8 and bits & 1
+    run_attend(sdpa_lib, c, q, t, [300], [rows], True)
+    assert sdpa_lib.sdpa_last_device_status()[0] == 0
+
+
+@gpu
 @pytest.mark.parametrize("batch", [129, 300])
 def test_attend_large_batches(sdpa_lib, batch):
     g = torch.Generator().manual_seed(batch)
