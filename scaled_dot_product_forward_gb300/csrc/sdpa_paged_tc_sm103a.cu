@@ -21,9 +21,10 @@
 // Pages arrive by TMA (one box a page and 128-byte column chunk; an entry that
 // is no page lies out of the map's bounds and reads as zeros).  16-bit pages
 // land in the 128-byte-swizzled layout that the products read.  e4m3 pages
-// land as they are in a small ring, and two warps turn them into fp16 tiles
-// (exact); a key's weight carries its page's value scale, so the scales touch
-// eight constants a row and step, not the elements.
+// land as they are in a small ring; the keys' are multiplied as they are, with
+// the queries split into e4m3 terms, and a warpgroup turns the values' into
+// fp16 tiles (exact); a key's weight carries its page's value scale, so the
+// scales touch eight constants a row and step, not the elements.
 //
 // The steps of all units are divided equally over the CTAs (one an SM), the
 // two cut units of a CTA joined by a second kernel (sdpa_paged.cuh).  Every
@@ -116,6 +117,19 @@ enum Site : unsigned int {
   kSiteQ = 1u << 1, kSiteK = 1u << 2, kSiteEmpty = 1u << 3, kSiteS = 1u << 4, kSiteP = 1u << 5,
   kSiteO = 1u << 6, kSiteDrain = 1u << 7, kSiteV = 1u << 8, kSiteNote = 1u << 9, kSiteSums = 1u << 10,
 };
+
+// mbar_try_wait with a hint how long (ns) the thread may be suspended meanwhile.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return done != 0;
+}
 
 __device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, Bars* bars, uint64_t limit,
                                          unsigned int site, bool honour_abort = true) {
