@@ -661,12 +661,16 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
     if len(shape) != 3 or shape[2] != cache.head_dim or shape[1] % cache.n_kv_heads != 0:
         raise SdpaError(3, where)
     total, heads, _ = shape
+    if n_seqs < 1:
+        raise SdpaError(3, where)
     if cu_seqlens_q is None:
-        if n_seqs == 0 or total % n_seqs != 0:
+        if total % n_seqs != 0:
             raise SdpaError(3, where)
         max_seqlen_q = total // n_seqs
     elif max_seqlen_q is None:
         raise SdpaError(1, where)
+    if total < 1 or heads < 1 or max_pages < 1 or max_seqlen_q < 1:
+        raise SdpaError(3, where)
     if out is not None and (out.dtype is not q.dtype or out.shape != shape):
         raise SdpaError(3, where)
     if lse is not None and (lse.dtype is not _torch.float32 or tuple(lse.shape) != (total, heads)):

@@ -94,6 +94,22 @@ def test_forward_arguments():
     assert status(f, q, c, t, lens) == ARG
 
 
+def test_forward_of_nothing():
+    """Extents below one are a wrong shape, not a device without a workspace size."""
+    c = cache()
+    t, lens = batch()
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    cu = torch.zeros(3, dtype=torch.int32)
+    f = sdpa.sdpa_paged_forward
+    assert status(f, q[:0], c, t, lens) == SHAPE
+    assert status(f, q[:, :0], c, t, lens) == SHAPE
+    assert status(f, q, c, t, lens, cu, 0) == SHAPE
+    assert status(f, q, c, t, lens, cu, -1) == SHAPE
+    assert status(f, q, c, t[:, :0], lens) == SHAPE
+    assert status(f, q, c, t[:0], lens[:0]) == SHAPE
+    assert status(f, q, c, t[:0], lens[:0], cu[:1], 1) == SHAPE
+
+
 class Raw:
     """The C entry points with made-up addresses far apart: every call here is refused before
     any of them is used."""
