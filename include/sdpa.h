@@ -385,8 +385,8 @@ typedef struct sdpa_paged_cache {
  * kv_lens      : DEVICE int32 [n_seqs], the sequences' lengths WITH the new
  *                tokens: token i of n has position kv_lens[b] - n + i.
  * page_table   : DEVICE int32 [n_seqs, max_pages], row stride
- *                page_table_stride >= max_pages.  No two sequences may append
- *                to one page.
+ *                page_table_stride >= max_pages.  No two entries with new
+ *                tokens may name one page, in one sequence or in two.
  * cos, sin     : both NULL (no rotation), or DEVICE fp32 [n_pos, rot_dim / 2]
  *                contiguous, 16-byte aligned: entry (pos, j) turns pair j of
  *                every key (and query) head: (x1, x2) -> (x1 cos - x2 sin,
@@ -398,7 +398,7 @@ typedef struct sdpa_paged_cache {
  *                may be q with q's strides (in place).
  *
  * A token whose position is negative or not below max_pages * page_size or
- * n_pos is left out: none of its rows is written.  A page entry outside [0,
+ * n_pos is left out: none of its rows is written, in q_out neither.  A page entry outside [0,
  * n_pages) leaves the token's key and value out.  Rows of tokens beyond the
  * last sequence are not touched.
  *
@@ -445,14 +445,19 @@ SDPA_API sdpa_status sdpa_cache_append(
  * A row that sees no key gives zeros and lse = -inf; rows of q outside every
  * sequence are not written.  A page entry outside [0, n_pages) removes its
  * tokens' keys.  What pages hold beyond a sequence's length is not used (it
- * may be anything, NaN too).  Products on tensor cores with fp32 sums, softmax
- * in fp32; each key's weight, times its value's scale, is rounded to 16 bits
- * (bf16 for a bf16 cache, else fp16) before the second product.  Results do
- * not depend on timing.  Asynchronous on `stream`; two kernel launches.  The
- * kernel for many rows a head waits on barriers, each for a bounded time
- * (sdpa_last_device_status).  Errors as above; ARG for an infinite scale or too
- * small a workspace, SHAPE also when (total_q * n_heads / n_kv_heads / 16 +
- * n_seqs) * n_kv_heads * max_pages * page_size / 16 exceeds about 2^31.
+ * may be anything, NaN too).  A key within the length that a causal row does
+ * not see has the weight zero in that row, times its value, which therefore
+ * has to be finite for the row to be.  Products on tensor cores with fp32
+ * sums, softmax in fp32; each key's weight, times its value's scale, is
+ * rounded to 16 bits (bf16 for a bf16 cache, else fp16) before the second
+ * product.  With an 8-bit cache, elements of a query row down to 2^-9 (bf16)
+ * or 2^-6 (fp16) of the row's largest are exact, smaller ones are taken to
+ * within 2^-17 of it.  Results do not depend on timing.  Asynchronous on
+ * `stream`; two kernel launches.  The kernel for many rows a head waits on
+ * barriers, each for a bounded time (sdpa_last_device_status).  Errors as
+ * above; ARG for an infinite scale or too small a workspace, SHAPE also when
+ * (total_q * n_heads / n_kv_heads / 16 + n_seqs) * n_kv_heads * max_pages *
+ * page_size / 16 exceeds about 2^31.
  */
 SDPA_API sdpa_status sdpa_paged_forward(
     const void* q, void* out, float* lse, sdpa_dtype dtype, const sdpa_paged_cache* cache,

@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       const int len = __ldg(p.kv_lens + b), n = q1 - q0;
       const int p0 = max(len - n, 0);          // position of the first token that has one
       const int page_i = (p0 >> p.page_shift) + (slot - first_slot(b));
+      if (page_i < 0 || page_i > (p.max_len - 1) >> p.page_shift) return;
       PageTokens pt;
       pt.lo = max(p0, page_i << p.page_shift);
       // a position past the table's pages or the angles' table is left out

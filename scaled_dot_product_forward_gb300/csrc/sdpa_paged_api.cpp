@@ -150,9 +150,9 @@ sdpa_status sdpa_cache_append(const sdpa_paged_cache* cache, const void* k, cons
   const int64_t D = cache->head_dim, hkv = cache->n_kv_heads;
   if (cos && (rot_dim < 8 || rot_dim > D || rot_dim % 8 != 0 || n_pos < 1)) return SDPA_ERR_SHAPE;
   if (q && (n_heads < 1 || n_heads > kIntMax)) return SDPA_ERR_SHAPE;
-  // blocks: (total / page_size + 2 n_seqs) by at most the heads
-  if (total > kIntMax / 2 || n_seqs > kIntMax / 8 || hkv > 65535 ||
-      hkv * cache->page_size > kIntMax / 4 || (q && n_heads * cache->page_size > kIntMax / 4))
+  // (the kernel counts page slots, total / page_size + 2 n_seqs, and shares of
+  // heads in 32 bits)
+  if (total > kIntMax / 2 || n_seqs > kIntMax / 8 || hkv > 65535 || (q && n_heads > kIntMax / 32))
     return SDPA_ERR_SHAPE;
   if (cos && (!aligned(cos, 16) || !aligned(sin, 16))) return SDPA_ERR_LAYOUT;
   Rows rk, rv, rq{}, ro{};
