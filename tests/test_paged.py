@@ -598,3 +598,191 @@ def test_two_streams_at_once(sdpa_lib):
     for i in range(2):
         for x in got[i]:
             assert torch.equal(x, want[i])
+
+
+@gpu
+@pytest.mark.parametrize("size", [1e-30, 1e30])
+@pytest.mark.parametrize("rows", [12, 40, 100])
+def test_small_and_large_queries_of_many_rows(sdpa_lib, size, rows):
+    """The tensor-core form splits a query row into 8-bit terms under a power of two of its own.
+    (Elements below 2^-9 of the row's largest are off by up to 2^-17 of it: four of them by 2^-17 * 4
+    * 4 against a key of 4 each change a score by 5e-5, inside (D + 16) 2^-24 sum |q| |k| = 7e-5.)"""
+    c = make_cache(sdpa_lib, 16, 16, 1, 128, "e4m3", torch.bfloat16, 14)
+    q = (torch.randn(2 * rows, 3, 128, generator=torch.Generator().manual_seed(4)) * size).bfloat16().cuda()
+    run_attend(sdpa_lib, c, q, tables(2, 8, 16, 1), [110, 128], [rows] * 2, True, scale=0.1 / size)
+
+
+@gpu
+@pytest.mark.parametrize("scale", [0.0, 1e-42, -0.3])
+@pytest.mark.parametrize("cache", ["e4m3", "16"])
+@pytest.mark.parametrize("rows", [12, 100])
+def test_scales_of_the_scores_of_many_rows(sdpa_lib, cache, scale, rows):
+    c = make_cache(sdpa_lib, 20, 32, 2, 64, cache, torch.float16, 8, spread=0.5)
+    q = torch.randn(2 * rows, 6, 64, generator=torch.Generator().manual_seed(2)).half().cuda()
+    run_attend(sdpa_lib, c, q, tables(2, 6, 20, 2), [150, rows - 3], [rows] * 2, True, scale=scale)
+
+
+@gpu
+@pytest.mark.parametrize("where", [3, 129, 256, 299])
+@pytest.mark.parametrize("cache", ["e4m3", "16"])
+@pytest.mark.parametrize("rows", [1, 12, 100])
+def test_nan_inside_the_length(sdpa_lib, cache, rows, where):
+    """A NaN that the rows see reaches them: in a value one column of its head, in a key the rows
+    of its head; and nothing else."""
+    P, D, lens = 16, 128, [300, 290]
+    c = make_cache(sdpa_lib, 40, P, 2, D, cache, torch.bfloat16, 6)
+    table = tables(2, 19, 40, 11)
+    q = torch.randn(2 * rows, 8, D, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    for t, head in ((c.v, 1), (c.k, 0)):
+        page, row = int(table[0, where // P]), where % P
+        x = t[page, row, head].float()
+        x[70] = math.nan
+        t[page, row, head].copy_(x.to(t.dtype))
+    cu = torch.tensor([0, rows, 2 * rows], dtype=torch.int32, device="cuda")
+    out, lse = sdpa_lib.sdpa_paged_forward(q, c, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), cu, rows,
+                                           return_lse=True)
+    want = ref.attend(q, ref.values(c.k, c.k_scale), ref.values(c.v, c.v_scale), table, lens, [rows] * 2)
+    nan = torch.zeros(2 * rows, 8, D, dtype=torch.bool)
+    nan[:rows, 4:, 70] = True
+    nan[:rows, :4] = True
+    assert torch.equal(torch.isnan(out.cpu()), nan) and torch.equal(torch.isnan(want[0]), nan)
+    assert torch.equal(torch.isnan(lse.cpu()), nan[..., 0])
+    tol, _ = ref.attend_bounds(want, 300, D, torch.bfloat16, torch.bfloat16 if cache == "16" else torch.float16)
+    check(out.cpu()[~nan], want[0][~nan], tol[~nan], "out")
+
+
+@gpu
+@pytest.mark.parametrize("cache", ["e4m3", "16"])
+@pytest.mark.parametrize("rows", [6, 80])
+def test_captured_many_rows(sdpa_lib, cache, rows):
+    """The tensor-core form captured once and replayed with other lengths, tables and queries, an
+    append before it."""
+    B, H, hkv, D, P, mp = 2, 8, 2, 64, 32, 12
+    g = torch.Generator().manual_seed(rows)
+    c = make_cache(sdpa_lib, B * mp, P, hkv, D, cache, torch.float16, 4)
+    q, k, v = (torch.randn(B * rows, n, D, generator=g).half().cuda() for n in (H, hkv, hkv))
+    tab, lens = tables(B, mp, B * mp, 1).cuda(), torch.tensor([rows, 200], dtype=torch.int32, device="cuda")
+    sdpa_lib.sdpa_cache_append(c, k, v, tab, lens)
+    sdpa_lib.sdpa_paged_forward(q, c, tab, lens, is_causal=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sdpa_lib.sdpa_cache_append(c, k, v, tab, lens)
+        out, lse = sdpa_lib.sdpa_paged_forward(q, c, tab, lens, is_causal=True, return_lse=True)
+    for seed, n in ((2, [rows, 384]), (3, [331, rows + 1])):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        tab.copy_(tables(B, mp, B * mp, seed))
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g).half())
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = sdpa_lib.sdpa_paged_forward(q, c, tab, lens, is_causal=True, return_lse=True)
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+        run_attend(sdpa_lib, c, q, tab.cpu(), n, [rows] * B, True, use_cu=False)
+
+
+@gpu
+def test_calls_on_another_stream(sdpa_lib):
+    """stream= of both calls, with the work before them still running on it."""
+    c = make_cache(sdpa_lib, 24, 32, 2, 128, "e4m3", torch.bfloat16, 4)
+    d = sdpa_lib.SdpaPagedCache(c.k.clone(), c.v.clone(), c.k_scale.clone(), c.v_scale.clone())
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(50, n, 128, generator=g).bfloat16().cuda() for n in (8, 2, 2))
+    tab, lens = tables(1, 20, 24, 1).cuda(), torch.tensor([600], dtype=torch.int32, device="cuda")
+    a = (torch.arange(640)[:, None] * torch.exp2(-torch.arange(64) / 8.0))
+    cos, sin = a.cos().cuda(), a.sin().cuda()
+    qr = sdpa_lib.sdpa_cache_append(c, k, v, tab, lens, cos=cos, sin=sin, q=q)
+    want = sdpa_lib.sdpa_paged_forward(qr, c, tab, lens, is_causal=True)
+    late = [torch.zeros_like(x) for x in (q, k, v)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        busy = torch.randn(4096, 4096, device="cuda")
+        for _ in range(10):
+            busy = busy @ busy * 1e-2
+        for x, y in zip(late, (q, k, v)):
+            x.copy_(y)
+    qr2 = sdpa_lib.sdpa_cache_append(d, late[1], late[2], tab, lens, cos=cos, sin=sin, q=late[0], stream=s)
+    got = sdpa_lib.sdpa_paged_forward(qr2, d, tab, lens, is_causal=True, stream=s)
+    s.synchronize()
+    assert torch.equal(qr, qr2) and torch.equal(want, got) and torch.equal(c.k_scale, d.k_scale)
+    assert torch.equal(c.k.view(torch.uint8), d.k.view(torch.uint8)) and torch.equal(c.v.view(torch.uint8), d.v.view(torch.uint8))
+
+
+@gpu
+@pytest.mark.parametrize("cache", ["e4m3", "16"])
+@pytest.mark.parametrize("rows", [1, 7, 900])
+def test_one_page_of_1024(sdpa_lib, cache, rows):
+    """The largest pages, a cache of one page, appended to from its first row and attended to."""
+    c = make_cache(sdpa_lib, 1, 1024, 1, 64, cache, torch.bfloat16, 4)
+    g = torch.Generator().manual_seed(rows)
+    table = torch.zeros(1, 1, dtype=torch.int32)
+    n = 1024 - rows
+    for count, length in ((n, n), (rows, 1024)):
+        k, v = (torch.randn(count, 1, 64, generator=g).bfloat16().cuda() for _ in range(2))
+        sdpa_lib.sdpa_cache_append(c, k, v, table.cuda(), torch.tensor([length], dtype=torch.int32, device="cuda"))
+        x = ref.values(c.v, c.v_scale)[0, length - count:length]
+        w = v.cpu().double()
+        if cache == "16":
+            assert torch.equal(x, w)
+        else:   # one rounding: half a step, or half of the least subnormal 2^-9 under the page's scale
+            check(x, w, ref.half_step(E4M3) * w.abs() + c.v_scale.item() * 2.0 ** -10, "v")
+    q = torch.randn(rows, 4, 64, generator=g).bfloat16().cuda()
+    run_attend(sdpa_lib, c, q, table, [1024], [rows], True, use_cu=False)
+
+
+@gpu
+@pytest.mark.parametrize("rot", [0, 64])
+def test_scale_grows_token_by_token(sdpa_lib, rot):
+    """Tokens that grow, one call each: codes and scales as the same steps give in plain tensors,
+    bit for bit (values and ratios are such that each step is one rounding)."""
+    c = make_cache(sdpa_lib, 3, 16, 2, 64, "e4m3", torch.bfloat16, 4)
+    g = torch.Generator().manual_seed(9)
+    codes, scale = torch.zeros(16, 2, 64, dtype=E4M3), None
+    table = torch.tensor([[2]], dtype=torch.int32, device="cuda")
+    cos, sin = (torch.ones(16, 32, device="cuda"), torch.zeros(16, 32, device="cuda")) if rot else (None, None)
+    for i in range(16):
+        x = (torch.randn(1, 2, 64, generator=g) * 2.0 ** (1.5 * i - 20 if i % 5 else -20)).bfloat16()
+        sdpa_lib.sdpa_cache_append(c, x.cuda(), x.cuda(), table, torch.tensor([i + 1], dtype=torch.int32, device="cuda"),
+                                   cos=cos, sin=sin)
+        need = torch.tensor([ref.scale_for(float(x[0, h].float().abs().max())) for h in range(2)])
+        new = need if i == 0 else torch.maximum(need, scale)
+        if i:
+            codes[:i] = (codes[:i].float() * (scale / new)[:, None]).to(E4M3)
+        scale = new
+        codes[i] = (x[0].float() / scale[:, None]).to(E4M3)
+        for t, s in ((c.k, c.k_scale), (c.v, c.v_scale)):
+            assert torch.equal(s[2].cpu(), scale), i
+            assert torch.equal(t[2, :i + 1].cpu().float(), codes[:i + 1].float()), i
+
+
+@gpu
+def test_append_beyond_the_tables(sdpa_lib):
+    """Lengths past the page table and past the angles: tokens that have a place are written, the
+    others are left out, and so are their queries."""
+    for cache in ("e4m3", "16"):
+        for n_pos, last in ((100, 32), (20, 20)):
+            c = make_cache(sdpa_lib, 6, 16, 1, 64, cache, torch.bfloat16, 4)
+            k, v, q = (torch.randn(40, n, 64, generator=torch.Generator().manual_seed(n_pos)).bfloat16().cuda() for n in (1, 1, 3))
+            table = torch.tensor([[4, 1]], dtype=torch.int32, device="cuda")
+            was = [t.clone().view(torch.uint8) for t in (c.k, c.v)]
+            out = torch.full_like(q, 7.0)
+            one, zero = torch.ones(n_pos, 32, device="cuda"), torch.zeros(n_pos, 32, device="cuda")
+            # 40 tokens at positions 5 .. 44
+            sdpa_lib.sdpa_cache_append(c, k, v, table, torch.tensor([45], dtype=torch.int32, device="cuda"), cos=one, sin=zero,
+                                       q=q, q_out=out)
+            kept = last - 5
+            assert torch.equal(out[:kept], q[:kept]) and (out[kept:] == 7).all()
+            for t, w, x in ((c.k, was[0], k), (c.v, was[1], v)):
+                s = None if cache == "16" else (c.k_scale if t is c.k else c.v_scale)
+                got = ref.values(t, s)[[4, 1]].reshape(32, 64)[5:last]
+                want = x[:kept, 0].cpu().double()
+                if cache == "16":
+                    assert torch.equal(got, want)
+                    assert torch.equal(t.view(torch.uint8)[4, :5], w[4, :5])
+                else:
+                    # one rounding: half a step, or half of the least subnormal 2^-9 under the pages' scales
+                    check(got, want, ref.half_step(E4M3) * want.abs() + s[[4, 1]].max().item() * 2.0 ** -10, "codes")
+                rest = torch.tensor([0, 2, 3, 5], device="cuda")
+                assert torch.equal(t.view(torch.uint8)[rest], w[rest])
+                if last == 20:
+                    assert torch.equal(t.view(torch.uint8)[1, 4:], w[1, 4:])
