@@ -140,6 +140,9 @@ struct PagedParams {
   const int* kv_lens;       // [n_seqs]
   const int* cu;            // [n_seqs + 1], or null: total_q / n_seqs tokens each
   int total_q, n_seqs, n_kv, G, n_pages, max_len;
+  unsigned int g_mul;       // n / G = n g_mul >> g_shift, for 31-bit n (by_G)
+  int g_shift;
+  int seq_q;                // total_q / n_seqs
   int unit_heads, n_groups; // key/value heads of a unit, groups of them
   int step_shift;           // keys a step = 1 << step_shift
   int min_steps, min_steps_shift;  // of a CTA's range, a power of two

@@ -50,6 +50,12 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
+// n / G for 0 <= n < 2^31 (the quotients of a unit's rows are wanted in many
+// places, whose code would be a division's each).
+__device__ __forceinline__ int by_G(const PagedParams& p, int n) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * p.g_mul) >> p.g_shift);
+}
+
 struct Seq {
   int q0, nq, len, nt;
 };
@@ -61,9 +67,8 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, int rt) {
     s.q0 = min(max(__ldg(p.cu + b), 0), p.total_q);
     q1 = min(max(__ldg(p.cu + b + 1), s.q0), p.total_q);
   } else {
-    const int n = p.total_q / p.n_seqs;
-    s.q0 = b * n;
-    q1 = s.q0 + n;
+    s.q0 = b * p.seq_q;
+    q1 = s.q0 + p.seq_q;
   }
   s.nq = q1 - s.q0;
   s.len = min(max(__ldg(p.kv_lens + b), 0), p.max_len);
@@ -74,7 +79,7 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, int rt) {
 // Keys that the rows of tile t see (the last row sees the most).
 __device__ __forceinline__ int unit_keys(const PagedParams& p, const Seq& s, int t, int rt) {
   if (!p.is_causal) return s.len;
-  const int last = (min((t + 1) * rt, s.nq * p.G) - 1) / p.G;
+  const int last = by_G(p, min((t + 1) * rt, s.nq * p.G) - 1);
   return min(max(s.len - s.nq + last + 1, 0), s.len);
 }
 __device__ __forceinline__ int unit_steps(const PagedParams& p, const Seq& s, int t, int rt) {

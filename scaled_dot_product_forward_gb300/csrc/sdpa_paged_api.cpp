@@ -330,6 +330,12 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   p.n_seqs = static_cast<int>(n_seqs);
   p.n_kv = static_cast<int>(hkv);
   p.G = static_cast<int>(G);
+  // m = floor(2^(31+s) / G) + 1 with 2^s >= G: n m is off from n 2^(31+s) / G by
+  // at most n < 2^31 parts of G <= 2^s, too little to reach the next multiple
+  p.g_shift = 31;
+  while ((int64_t(1) << (p.g_shift - 31)) < G) ++p.g_shift;
+  p.g_mul = static_cast<unsigned int>((uint64_t(1) << p.g_shift) / static_cast<uint64_t>(G) + 1);
+  p.seq_q = static_cast<int>(total_q / n_seqs);
   p.n_pages = static_cast<int>(cache->n_pages);
   p.max_len = static_cast<int>(max_pages * cache->page_size);
   p.page_shift = log2_of(cache->page_size);

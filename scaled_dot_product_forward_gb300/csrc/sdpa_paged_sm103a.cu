@@ -147,12 +147,12 @@ struct Smem {
 // Row r of a sequence's rows for key/value head h: its place in out, and its
 // log-sum-exp.
 __device__ __forceinline__ uint16_t* out_row(const PagedParams& p, int q0, int h, int r) {
-  const int i = r / p.G, g = r - i * p.G;
+  const int i = by_G(p, r), g = r - i * p.G;
   return reinterpret_cast<uint16_t*>(p.out) + (static_cast<int64_t>(q0) + i) * p.o_st +
          (static_cast<int64_t>(h) * p.G + g) * p.o_sh;
 }
 __device__ __forceinline__ void store_lse(const PagedParams& p, int q0, int h, int r, float m, float l) {
-  const int i = r / p.G, g = r - i * p.G;
+  const int i = by_G(p, r), g = r - i * p.G;
   constexpr float kLn2 = 0.693147180559945309f;
   p.lse[(static_cast<int64_t>(q0) + i) * p.lse_st + (static_cast<int64_t>(h) * p.G + g) * p.lse_sh] =
       l == 0.0f ? -INFINITY : (log2f(l) + m) * kLn2;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
       const int r = hf * 8 + g8;
       const bool live = r < rows;
       const int rr = c.t * RT + r;
-      const int i = rr / p.G, g = rr - i * p.G;
+      const int i = by_G(p, rr), g = rr - i * p.G;
       lim[hf] = live ? (p.is_causal ? min(max(c.s.len - c.s.nq + i + 1, 0), c.s.len) : c.s.len) : 0;
       if (live) lim_min = min(lim_min, lim[hf]);
       const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) +

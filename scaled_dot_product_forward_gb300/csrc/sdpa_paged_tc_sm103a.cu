@@ -131,19 +131,26 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity
   return done != 0;
 }
 
+// All roles' loops together have to fit the instruction cache, and this stands in
+// each of them at every wait: a wait that gives up only raises the flag, which
+// thread 0 reports at the end (with that, rolled loops where little runs, and
+// divisions by multiplication, 106 -> 96 KB of code with e4m3 pages: a chunk of
+// 2048 tokens behind 14336 445 -> 441 us, with 16-bit pages 424 -> 392; uneven
+// prompts, 16-bit 597 -> 541, e4m3 742 -> 661).
 __device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, Bars* bars, uint64_t limit,
                                          unsigned int site, bool honour_abort = true) {
-  if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
-    if (honour_abort && *reinterpret_cast<volatile uint32_t*>(&bars->abort_flag) != 0) return false;
-    if (global_timer_ns() - t0 > limit) {
-      *reinterpret_cast<volatile uint32_t*>(&bars->abort_flag) = 1u;
-      atomicOr(&g_sdpa_paged_status, 1u | site);
+  uint64_t t0 = 0;
+  while (!mbar_try_wait_for(bar, parity, kSuspendNs)) {
+    volatile uint32_t* const flag = &bars->abort_flag;
+    if (honour_abort && *flag != 0) return false;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit) {
+      *flag = 1u | site;
       return false;
     }
   }
+  return true;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* bars, uint64_t limit,
                                           unsigned int site) {
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     };
     // the row's token and query head
     auto place = [&](const Cursor& c, int ru, int64_t& token, int64_t& head) {
-      const int rr = c.t * RT + ru, tok = rr / p.G;
+      const int rr = c.t * RT + ru, tok = by_G(p, rr);
       token = static_cast<int64_t>(c.s.q0) + tok;
       head = static_cast<int64_t>(c.h) * p.G + (rr - tok * p.G);
       return tok;
@@ -731,8 +738,8 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         const float alpha = weights<E4M3, MBF, kPer>(x, f, notes + slot * kGroups + half * (kPer / 16), m, l, need, pk);
         if (mine > 0 && __any_sync(0xffffffffu, need)) {
           // the earlier products of this tile are complete: S of this step was
-          // issued behind them
-#pragma unroll
+          // issued behind them (rolled, as whatever seldom runs)
+#pragma unroll 1
           for (int i = 0; i < D / (HALF ? 64 : 32); ++i) {
             uint32_t o[32];
             acc_load<HALF, D / 2>(tO + i * 32, o);
@@ -814,6 +821,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       const int i0 = split ? t * (kRuns / 2) : 0;
       const int i1 = !split ? kRuns : kRuns == 1 ? 1 - t : i0 + kRuns / 2;
       const int col0 = half * (D / 2);
+#pragma unroll 1
       for (int i = i0; i < i1 && !idle; ++i) {
         uint32_t o[32];
         acc_load<HALF, D / 2>(tO + i * 32, o);
@@ -963,7 +971,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
             const uint32_t bad = __ballot_sync(0xffffffffu, id >= p.n_pages) & 0xffu;
             if (E4M3 && lane < 8) {
               vs = clamp_scale(vs);
-              notes[note_at.idx * kGroups + lane] = make_float4(clamp_scale(ks), __log2f(vs), 1.0f / vs, 0.0f);
+              notes[note_at.idx * kGroups + lane] = make_float4(clamp_scale(ks), __log2f(vs), __fdividef(1.0f, vs), 0.0f);
             }
             if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&bars->bad[note_at.idx]) = bad;
             __syncwarp();
@@ -1042,6 +1050,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         if (!warp_wait(&bars->v_full[v_at.idx], v_at.phase, bars, limit, kSiteV)) return false;
         if (!E4M3 && valid < KT) {
           uint8_t* tile = sV + v_at.idx * L::kTile;
+#pragma unroll 1
           for (int i = max(valid, 0) * 8 + lane; i < KT * 8; i += 32)
 #pragma unroll
             for (int ch = 0; ch < L::kChunks; ++ch)
@@ -1125,6 +1134,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
   }
 
   __syncthreads();
+  if (threadIdx.x == 0 && bars->abort_flag != 0) atomicOr(&g_sdpa_paged_status, bars->abort_flag);
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
