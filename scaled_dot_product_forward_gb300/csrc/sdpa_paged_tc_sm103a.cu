@@ -403,78 +403,74 @@ __device__ __forceinline__ float2 codes_value2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Where 16-byte piece i of row r of a query tile waits as it lies in memory: in
-// the places that put_query gives the same row (16-bit: its own piece; e4m3
-// terms: the row's of the first two), so it needs no other room and no other
-// row's consent.
+// Where 16-byte piece i of row r of a query tile waits as it lies in memory.
+// 16-bit: its own place.  e4m3 terms: pieces 2u and 2u + 1 become piece u of
+// every term, and wait in that piece's places of the first two.
 template <int D, bool E4M3, int QCHUNK>
 __device__ __forceinline__ int query_piece(int r, int i) {
   if constexpr (!E4M3) return (i >> 3) * QCHUNK + swizzled<128>(r, i & 7);
-  return (i / (D / 16)) * QCHUNK + r * D + (i % (D / 16)) * 16;
+  return (i & 1) * QCHUNK + swizzled<D>(r, i >> 1);
 }
-// A thread's share of a row: all of it, or half (0, 1) of it.
-template <int D, bool HALF>
-struct RowShare {
-  static constexpr int kPieces = D / 8 / (HALF ? 2 : 1);   // 16-byte pieces of 16-bit elements
-};
-// Asks for the row's share; finished by cp_async_wait<0>().
-template <int D, bool E4M3, bool HALF, int QCHUNK>
-__device__ __forceinline__ void ask_query(const uint16_t* src, uint8_t* tile, int r, int half) {
-  constexpr int kN = RowShare<D, HALF>::kPieces;
+// Asks for the row's pieces [i0, i1); finished by cp_async_wait<0>().
+template <int D, bool E4M3, int N, int QCHUNK>
+__device__ __forceinline__ void ask_query(const uint16_t* src, uint8_t* tile, int r, int i0) {
 #pragma unroll
-  for (int k = 0; k < kN; ++k) {
-    const int i = half * kN + k;
-    cp_async_16(tile + query_piece<D, E4M3, QCHUNK>(r, i), src + i * 8);
-  }
+  for (int k = 0; k < N; ++k)
+    cp_async_16(tile + query_piece<D, E4M3, QCHUNK>(r, i0 + k), src + (i0 + k) * 8);
   cp_async_commit();
 }
 
-// The row's share (none: zeros) to the tile as the products read it, negated
-// for a negative scale; returns the (positive) multiplier of the scores,
-// |scale| * log2(e).  For e4m3 keys the row is brought by a power of two to a
-// largest element in [2^7, 2^8) (the factor goes into the multiplier) and split
-// into e4m3 terms, each what the earlier ones leave: a bf16 value is exact in
-// two, an fp16 one in three, down to 2^-10 in that scale, 2^-17 of the row's
-// largest element.  The whole warp calls it.
-template <int D, bool E4M3, bool BF16, bool HALF, int QCHUNK>
-__device__ __forceinline__ float put_query(const PagedParams& p, bool live, uint8_t* tile, int r, int half) {
-  constexpr int kN = RowShare<D, HALF>::kPieces;
-  uint4 w[kN];
-#pragma unroll
-  for (int k = 0; k < kN; ++k)
-    w[k] = live ? *reinterpret_cast<const uint4*>(tile + query_piece<D, E4M3, QCHUNK>(r, half * kN + k))
-                : make_uint4(0u, 0u, 0u, 0u);
-  uint32_t* x = reinterpret_cast<uint32_t*>(w);
+// N pieces of the row from i0 on (not live: zeros) to the tile as the products
+// read it, negated for a negative scale; returns the (positive) multiplier of
+// the scores, |scale| * log2(e).  For e4m3 keys the row is brought by a power of
+// two to a largest element in [2^7, 2^8) (the factor goes into the multiplier)
+// and split into e4m3 terms, each what the earlier ones leave: a bf16 value is
+// exact in two, an fp16 one in three, down to 2^-10 in that scale, 2^-17 of the
+// row's largest element.  HALF: a row is two threads' (lane ^ 16).  The whole
+// warp calls it.  (Rolled loops over pieces that are rewritten in place: with
+// the row in registers this was 16 to 24 KB of code between the softmax's loops;
+// uneven prompts with e4m3 pages 660 -> 625 us.)
+template <int D, bool E4M3, bool BF16, bool HALF, int N, int QCHUNK>
+__device__ __forceinline__ float put_query(const PagedParams& p, bool live, uint8_t* tile, int r, int i0) {
   const float f = fabsf(p.scale_log2);
-  if (p.scale_log2 < 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 4 * kN; ++i) x[i] ^= 0x80008000u;
-  }
-  __syncwarp();   // (a partner's pieces lie where this thread's terms go)
+  const uint32_t sign = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
+  auto at = [&](int i) { return reinterpret_cast<uint4*>(tile + query_piece<D, E4M3, QCHUNK>(r, i)); };
   if constexpr (!E4M3) {
-#pragma unroll
-    for (int k = 0; k < kN; ++k)
-      *reinterpret_cast<uint4*>(tile + query_piece<D, E4M3, QCHUNK>(r, half * kN + k)) = w[k];
+    if (live && sign == 0u) return f;
+#pragma unroll 1
+    for (int i = i0; i < i0 + N; ++i) {
+      const uint4 w = *at(i);
+      *at(i) = live ? make_uint4(w.x ^ sign, w.y ^ sign, w.z ^ sign, w.w ^ sign) : make_uint4(0u, 0u, 0u, 0u);
+    }
     return f;
   } else {
+    const uint32_t keep = live ? 0xffffffffu : 0u;
     float top = 0.0f;
+#pragma unroll 2
+    for (int i = i0; i < i0 + N; ++i) {
+      const uint4 w = *at(i);
+      const uint32_t x[4] = {w.x & keep, w.y & keep, w.z & keep, w.w & keep};
 #pragma unroll
-    for (int i = 0; i < 4 * kN; ++i) {
-      const float2 a = unpack2<BF16>(x[i]);
-      top = max3f(top, fabsf(a.x), fabsf(a.y));
+      for (int k = 0; k < 4; ++k) {
+        const float2 a = unpack2<BF16>(x[k]);
+        top = max3f(top, fabsf(a.x), fabsf(a.y));
+      }
     }
     if (HALF) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
     const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
     // (an infinite element makes the row NaN)
-    const float up = top < INFINITY ? __int_as_float((127 + 7 - e) << 23) : NAN;
-#pragma unroll
-    for (int i = 0; i < kN / 2; ++i) {
+    float up = top < INFINITY ? __int_as_float((127 + 7 - e) << 23) : NAN;
+    if (sign != 0u) up = -up;
+#pragma unroll 1
+    for (int i = i0; i < i0 + N; i += 2) {
+      const uint4 w0 = *at(i), w1 = *at(i + 1);
+      const uint32_t x[8] = {w0.x & keep, w0.y & keep, w0.z & keep, w0.w & keep,
+                             w1.x & keep, w1.y & keep, w1.z & keep, w1.w & keep};
       uint32_t term[3][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float v[4];
-        const float2 a = unpack2<BF16>(x[8 * i + 2 * k]), b = unpack2<BF16>(x[8 * i + 2 * k + 1]);
-        v[0] = a.x * up, v[1] = a.y * up, v[2] = b.x * up, v[3] = b.y * up;
+        const float2 a = unpack2<BF16>(x[2 * k]), b = unpack2<BF16>(x[2 * k + 1]);
+        float v[4] = {a.x * up, a.y * up, b.x * up, b.y * up};
 #pragma unroll
         for (int n = 0; n < q_terms(E4M3, BF16); ++n) {
           const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
@@ -488,7 +484,7 @@ __device__ __forceinline__ float put_query(const PagedParams& p, bool live, uint
       }
 #pragma unroll
       for (int n = 0; n < q_terms(E4M3, BF16); ++n)
-        *reinterpret_cast<uint4*>(tile + n * QCHUNK + swizzled<D>(r, half * (kN / 2) + i)) =
+        *reinterpret_cast<uint4*>(tile + n * QCHUNK + swizzled<D>(r, i >> 1)) =
             make_uint4(term[n][0], term[n][1], term[n][2], term[n][3]);
     }
     return f * __int_as_float((127 - 7 + e) << 23);
@@ -542,6 +538,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
   constexpr bool MBF = BF16 && !E4M3;
   constexpr int RT = unit_rows(HALF);
   constexpr int kPer = HALF ? KT / 2 : KT;   // a step's keys a softmax thread takes
+  constexpr int kQPieces = D / 8 / (HALF ? 2 : 1);   // 16-byte pieces of the queries
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -652,8 +649,8 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       const int ru = row_of(g);
       place(c, ru, token, head);
       if (ru < g.rows)
-        ask_query<D, E4M3, HALF, L::kQChunk>(reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh,
-                                             sQ + t * L::kQTile, r, half);
+        ask_query<D, E4M3, kQPieces, L::kQChunk>(reinterpret_cast<const uint16_t*>(p.q) + token * p.q_st + head * p.q_sh,
+                                             sQ + t * L::kQTile, r, half * kQPieces);
     };
     save(c0, v0);
     bool first = true;
@@ -678,7 +675,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         cp_async_wait<0>();
         if (!idle) {
           __syncwarp();
-          f = put_query<D, E4M3, BF16, HALF, L::kQChunk>(p, ru < g.rows, sQ + t * L::kQTile, r, half);
+          f = put_query<D, E4M3, BF16, HALF, kQPieces, L::kQChunk>(p, ru < g.rows, sQ + t * L::kQTile, r, half * kQPieces);
         }
       }
       fence_proxy_async_smem();
