@@ -149,6 +149,7 @@ struct PagedParams {
   int page_shift;           // page size = 1 << page_shift
   int is_causal;
   float scale_log2;
+  int out_sectors;          // rows of out begin on 32-byte boundaries
   int max_rows;             // the caller's bound on a sequence's rows a head (>= 1)
   float* part;              // workspace: n_ctas notes, [n_ctas][2][unit_heads][rows of a unit][D + 2] floats
   int n_ctas;               // ranges of the division (grid of the main kernel)

@@ -314,6 +314,7 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   p.q_st = rq.st, p.q_sh = rq.sh;
   p.out = out;
   p.o_st = ro.st, p.o_sh = ro.sh;
+  p.out_sectors = aligned(out, 32) && ro.st % 16 == 0 && ro.sh % 16 == 0;
   p.lse = lse;
   p.lse_st = lt, p.lse_sh = lh;
   p.k = static_cast<const uint8_t*>(cache->k);

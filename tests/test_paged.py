@@ -786,3 +786,18 @@ def test_append_beyond_the_tables(sdpa_lib):
                 assert torch.equal(t.view(torch.uint8)[rest], w[rest])
                 if last == 20:
                     assert torch.equal(t.view(torch.uint8)[1, 4:], w[1, 4:])
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 12, 100])
+@pytest.mark.parametrize("shift,width", [(8, 152), (16, 152), (16, 160), (0, 128)])
+def test_rows_of_out_on_any_16_bytes(sdpa_lib, rows, shift, width):
+    """Output rows that begin on 16-byte boundaries and not on 32-byte ones, and on both."""
+    c = make_cache(sdpa_lib, 16, 32, 2, 128, "16", torch.bfloat16, 4)
+    q = torch.randn(rows, 6, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    wide = torch.full((rows * 6 * width + 64,), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = wide[shift:shift + rows * 6 * width].view(rows, 6, width)[..., :128]
+    run_attend(sdpa_lib, c, q, tables(1, 10, 16, 1), [300], [rows], True, use_cu=False, out=out)
+    untouched = torch.ones_like(wide, dtype=torch.bool)
+    untouched[shift:shift + rows * 6 * width].view(rows, 6, width)[..., :128] = False
+    assert (wide[untouched] == 9).all()
