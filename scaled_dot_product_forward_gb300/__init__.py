@@ -114,11 +114,12 @@ def load_library(path: str | None = None):
     lib.sdpa_forward_masked_noalloc.argtypes = [vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, i64p,
                                                 i64p, i64p, i64p, i64p, vp, ctypes.c_float, vp]
     lib.sdpa_forward_masked_noalloc.restype = ctypes.c_int
-    i64, cp = ctypes.c_int64, ctypes.POINTER(_PagedCacheStruct)
-    lib.sdpa_cache_append.argtypes = [cp, vp, vp, ctypes.c_int, i64, i64p, i64p, vp, i64, i64, vp, vp, i64, vp, vp,
-                                      i64, i64, ctypes.c_int, vp, vp, i64, i64p, i64p, vp]
+    # (addresses of the cache and of the strides: a decoding step's call is bound by the host)
+    i64 = ctypes.c_int64
+    lib.sdpa_cache_append.argtypes = [vp, vp, vp, ctypes.c_int, i64, vp, vp, vp, i64, i64, vp, vp, i64, vp, vp,
+                                      i64, i64, ctypes.c_int, vp, vp, i64, vp, vp, vp]
     lib.sdpa_cache_append.restype = ctypes.c_int
-    lib.sdpa_paged_forward.argtypes = [vp, vp, vp, ctypes.c_int, cp, i64, i64, i64p, i64p, i64p, vp, i64, i64, vp, vp,
+    lib.sdpa_paged_forward.argtypes = [vp, vp, vp, ctypes.c_int, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp,
                                        i64, i64, ctypes.c_int, ctypes.c_float, vp, ctypes.c_uint64, vp]
     lib.sdpa_paged_forward.restype = ctypes.c_int
     lib.sdpa_paged_workspace_bytes.argtypes = [i64, i64, i64, i64]
@@ -514,7 +515,7 @@ class SdpaPagedCache:
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv, dim
         ptr = [t.data_ptr() if t is not None else None for t in (k, v, k_scale, v_scale)]
         self._struct = _PagedCacheStruct(*ptr, n_pages, page_size, n_kv, dim, k.stride()[:3], v.stride()[:3], elem)
-        self._ref = ctypes.byref(self._struct)
+        self._ref = ctypes.addressof(self._struct)
         self._workspace = {}   # bytes that a forward needs, by (query heads, rows)
 
 
@@ -541,38 +542,31 @@ def _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, rows):
     return lens_shape[0], table_shape[1], dt
 
 
-_Two = ctypes.c_int64 * 2
+_Strides = ctypes.c_int64 * 8
+_address = ctypes.addressof
 
 
 def _two_strides(t, where):
-    st = t.stride()
-    if st[2] != 1:
+    a, b, last = t.stride()
+    if last != 1:
         raise SdpaError(5, where)
-    return _Two(st[0], st[1])
+    return a, b
 
 
-def _same_device(device, where, *tensors):
-    """All tensors on the cache's CUDA device (a host pointer would fault)."""
-    if device < 0:
-        raise SdpaError(6, where)
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise SdpaError(6, where)
-
-
-def _on_device(device, where, stream, call, *args):
-    """call(stream handle, *args) with ``device`` current, memory that it
-    allocates belonging to the stream it launches on."""
+def _on_device(device, where, stream, call):
+    """call(stream handle) with ``device`` current, memory that it allocates
+    belonging to the stream it launches on."""
     cuda = _torch.cuda
     if stream is not None:
         if stream.device_index != device:
             raise SdpaError(6, where)
         with cuda.stream(stream):
-            return call(stream.cuda_stream, *args)
-    if cuda.current_device() != device:
+            return call(stream.cuda_stream)
+    c = _torch._C
+    if c._cuda_getDevice() != device:
         with cuda.device(device):
-            return call(cuda.current_stream(device).cuda_stream, *args)
-    return call(cuda.current_stream(device).cuda_stream, *args)
+            return call(c._cuda_getCurrentRawStream(device))
+    return call(c._cuda_getCurrentRawStream(device))
 
 
 def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=None, sin=None,
@@ -587,8 +581,6 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
     2), or neighbours when ``interleaved``.  q: the tokens' queries [total,
     n_heads, head_dim], rotated too, into ``q_out`` (allocated if None; may be
     ``q``).  Returns ``q_out`` (None without q)."""
-    import torch
-
     where = "sdpa_cache_append"
     n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, k)
     dtype, shape = k.dtype, k.shape
@@ -619,25 +611,33 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
             raise SdpaError(5, where)
         rot *= 2
     ks, vs = _two_strides(k, where), _two_strides(v, where)
-    _same_device(cache.device, where, k, v, page_table, kv_lens, cu_seqlens, cos, sin, q, q_out)
+    device = cache.device
+    # all on the cache's CUDA device (a host pointer would fault)
+    if device < 0 or k.get_device() != device or v.get_device() != device or page_table.get_device() != device or \
+            kv_lens.get_device() != device or (cu_seqlens is not None and cu_seqlens.get_device() != device) or \
+            (cos is not None and (cos.get_device() != device or sin.get_device() != device)) or \
+            (q is not None and q.get_device() != device) or (q_out is not None and q_out.get_device() != device):
+        raise SdpaError(6, where)
 
     def call(st):
-        qo, qs, qos = q_out, None, None
+        qo, qs, qos = q_out, (0, 0), (0, 0)
         if q is not None:
             if qo is None:
-                qo = _torch.empty(q.shape, dtype=dtype, device=q.device)
+                qo = _torch.empty(q_shape, dtype=dtype, device=q.device)
             qs, qos = _two_strides(q, where), _two_strides(qo, where)
+        strides = _Strides(*ks, *vs, *qs, *qos)
+        at = _address(strides)
         rc = load_library().sdpa_cache_append(
-            cache._ref, k.data_ptr(), v.data_ptr(), dt, total, ks, vs, page_table.data_ptr(), page_table.stride(0),
+            cache._ref, k.data_ptr(), v.data_ptr(), dt, total, at, at + 16, page_table.data_ptr(), page_table.stride(0),
             max_pages, kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None, n_seqs,
-            cos.data_ptr() if cos is not None else None, sin.data_ptr() if sin is not None else None, n_pos, rot,
+            cos.data_ptr() if cos is not None else None, sin.data_ptr() if cos is not None else None, n_pos, rot,
             1 if interleaved else 0, q.data_ptr() if q is not None else None,
-            qo.data_ptr() if q is not None else None, heads, qs, qos, st)
+            qo.data_ptr() if q is not None else None, heads, at + 32, at + 48, st)
         if rc != 0:
             raise SdpaError(rc, where)
         return qo
 
-    return _on_device(cache.device, where, stream, call)
+    return _on_device(device, where, stream, call)
 
 
 def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seqlen_q=None, out=None, *,
@@ -653,8 +653,6 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
     i.  Returns ``out`` [total_q, n_heads, head_dim], or ``(out, lse)`` with
     lse fp32 [total_q, n_heads].  The workspace is allocated from torch's
     pool for this call and stream."""
-    import torch
-
     where = "sdpa_paged_forward"
     n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens_q, q)
     shape = q.shape
@@ -676,7 +674,12 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
     if lse is not None and (lse.dtype is not _torch.float32 or tuple(lse.shape) != (total, heads)):
         raise SdpaError(3, where)
     qs = _two_strides(q, where)
-    _same_device(cache.device, where, q, page_table, kv_lens, cu_seqlens_q, out, lse)
+    device = cache.device
+    # all on the cache's CUDA device (a host pointer would fault)
+    if device < 0 or q.get_device() != device or page_table.get_device() != device or \
+            kv_lens.get_device() != device or (cu_seqlens_q is not None and cu_seqlens_q.get_device() != device) or \
+            (out is not None and out.get_device() != device) or (lse is not None and lse.get_device() != device):
+        raise SdpaError(6, where)
 
     def call(st):
         lib = load_library()
@@ -696,17 +699,18 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
                 cache._workspace.clear()
             cache._workspace[key] = size
         work = empty(size, dtype=_torch.uint8, device=dev)
+        strides = _Strides(*qs, *_two_strides(o, where), *(ls.stride() if ls is not None else ()))
+        at = _address(strides)
         rc = lib.sdpa_paged_forward(
-            q.data_ptr(), o.data_ptr(), ls.data_ptr() if ls is not None else None, dt, cache._ref, total, heads, qs,
-            _two_strides(o, where), _Two(*ls.stride()) if ls is not None else None, page_table.data_ptr(),
-            page_table.stride(0), max_pages, kv_lens.data_ptr(),
+            q.data_ptr(), o.data_ptr(), ls.data_ptr() if ls is not None else None, dt, cache._ref, total, heads, at,
+            at + 16, at + 32, page_table.data_ptr(), page_table.stride(0), max_pages, kv_lens.data_ptr(),
             cu_seqlens_q.data_ptr() if cu_seqlens_q is not None else None, n_seqs, max_seqlen_q,
             1 if is_causal else 0, math.nan if scale is None else scale, work.data_ptr(), size, st)
         if rc != 0:
             raise SdpaError(rc, where)
         return o if ls is None else (o, ls)
 
-    return _on_device(cache.device, where, stream, call)
+    return _on_device(device, where, stream, call)
 
 
 def sdpa_last_device_status(stream=None):
