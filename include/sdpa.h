@@ -449,8 +449,8 @@ SDPA_API sdpa_status sdpa_cache_append(
  * not see has the weight zero in that row, times its value, which therefore
  * has to be finite for the row to be.  Products on tensor cores with fp32
  * sums, softmax in fp32; each key's weight, times its value's scale, is
- * rounded to 16 bits (bf16 for a bf16 cache, else fp16) before the second
- * product.  With an 8-bit cache, elements of a query row down to 2^-9 (bf16)
+ * rounded to 16 bits (bf16 for a bf16 cache, else fp16, an fp16 one to within
+ * 2^-36 of the row's largest) before the second product.  With an 8-bit cache, elements of a query row down to 2^-9 (bf16)
  * or 2^-6 (fp16) of the row's largest are exact, smaller ones are taken to
  * within 2^-17 of it.  Results do not depend on timing.  Asynchronous on
  * `stream`; two kernel launches.  The kernel for many rows a head waits on

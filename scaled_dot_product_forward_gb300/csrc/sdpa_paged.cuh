@@ -50,6 +50,19 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
+// Where a row's weights 2^(exponent - base) lie.  The base follows the running
+// maximum of the exponents: it is moved when one exceeds it by kRoom, to kTop
+// below that one.  bf16 weights reach from 1 (or, until the next move, 2^8) down
+// to 2^-126.  fp16 ones end at 2^-24: a base kTop below the maximum leaves each
+// weight an error of at most 2^-(25 + kTop) of the row's largest, whatever that
+// one's value is (many small weights beside one large one, whose value may be
+// zero, add up), and kRoom keeps the largest at 2^15.
+template <bool BF16>
+struct WeightRange {
+  static constexpr float kTop = BF16 ? 0.0f : 11.0f;
+  static constexpr float kRoom = BF16 ? 8.0f : 15.0f;
+};
+
 // n / G for 0 <= n < 2^31 (the quotients of a unit's rows are wanted in many
 // places, whose code would be a division's each).
 __device__ __forceinline__ int by_G(const PagedParams& p, int n) {

@@ -7,7 +7,8 @@
 // sum_j p_j.  One pass over the pages, online: with a = scale * log2(e), each
 // key's weight is w_j = 2^(a ks_j q.kcode_j + log2 vs_j - m), m the running
 // maximum of that exponent, so that the value's scale is inside the weight
-// before it is rounded to 16 bits (w <= 2^8 whatever the scales are), and
+// before it is rounded to 16 bits (w <= 2^15 whatever the scales are: m is the
+// maximum less a constant, see WeightRange), and
 //     out = sum_j w_j vcode_j / sum_j w_j / vs_j,
 // the sums in fp32.  e4m3 codes are exact in fp16, so products of an 8-bit
 // cache run in fp16 whatever the query's type: a bf16 query row is brought to
@@ -39,7 +40,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kWarpKeys = 16;
 constexpr int RT = 16;                 // rows a unit: one tile of the products
-constexpr float kRescaleLog2 = 8.0f;
 
 template <int D, bool E4M3>
 struct Ring {
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
   constexpr int NV = D / 8;               // column groups of O
   constexpr int RB = R::kRowBytes;
   constexpr bool MBF = BF16 && !E4M3;     // type of the products
+  using W = WeightRange<MBF>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
           grow |= fmaxf(max3f(acc[0][2 * hf], acc[0][2 * hf + 1], acc[1][2 * hf]),
-                        acc[1][2 * hf + 1]) > m[hf] + kRescaleLog2;
+                        acc[1][2 * hf + 1]) > m[hf] + W::kRoom;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -432,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
                             fmaxf(acc[1][2 * hf], acc[1][2 * hf + 1]));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            x -= W::kTop;
             if (x > m[hf]) {
               const float alpha = ex2(m[hf] - x);
               m[hf] = x;

@@ -63,7 +63,6 @@ struct Split {
 };
 constexpr int kConvertWarps = 4;
 constexpr uint32_t kSuspendNs = 4000;  // a waiting thread may sleep this long between its looks
-constexpr float kRescaleLog2 = 8.0f;
 constexpr uint32_t kTmemCols = 512;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
 constexpr int kGroups = KT / 16;     // 16 keys lie in one page
 
@@ -339,11 +338,12 @@ __device__ __forceinline__ float weights(float (&s)[N], float f, const float4* n
     top = max3f(e8[0], e8[6], e8[7]) * f;
   }
   if constexpr (N < KT) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-  need = top > m + kRescaleLog2;
+  need = top > m + WeightRange<MBF>::kRoom;
   float alpha = 1.0f;
   if (need) {
-    alpha = ex2(m - top);
-    m = top;
+    const float base = top - WeightRange<MBF>::kTop;
+    alpha = ex2(m - base);
+    m = base;
     l *= alpha;
   }
   const float neg_m = m == -INFINITY ? 0.0f : -m;
