@@ -436,7 +436,8 @@ SDPA_API sdpa_status sdpa_cache_append(
  *                the new tokens are the sequence's last ones; zero: all keys.
  * lse          : NULL or DEVICE fp32 [total_q, n_heads] (2 strides).
  * max_seqlen_q : an upper bound on the sequences' rows, used to choose a
- *                kernel; a smaller value costs time, never results.
+ *                kernel; a smaller value costs time, and results differ by
+ *                roundings only.
  * scale        : multiplier of q.k; NaN selects 1/sqrt(head_dim).
  * workspace    : DEVICE scratch, 16-byte aligned, of at least
  *                sdpa_paged_workspace_bytes(...) bytes, whatever it holds.
@@ -450,9 +451,11 @@ SDPA_API sdpa_status sdpa_cache_append(
  * has to be finite for the row to be.  Products on tensor cores with fp32
  * sums, softmax in fp32; each key's weight, times its value's scale, is
  * rounded to 16 bits (bf16 for a bf16 cache, else fp16, an fp16 one to within
- * 2^-36 of the row's largest) before the second product.  With an 8-bit cache, elements of a query row down to 2^-9 (bf16)
- * or 2^-6 (fp16) of the row's largest are exact, smaller ones are taken to
- * within 2^-17 of it.  Results do not depend on timing.  Asynchronous on
+ * 2^-36 of the row's largest) before the second product.  With an
+ * 8-bit cache, elements of a query row down to 2^-13 of the row's largest are
+ * exact; with more than 16 rows a key/value head (max_seqlen_q * n_heads /
+ * n_kv_heads) smaller ones are taken to within 2^-21 (bf16) or 2^-24 (fp16) of
+ * it, with fewer bf16 ones to within 2^-39 and fp16 ones are all exact.  Results do not depend on timing.  Asynchronous on
  * `stream`; two kernel launches.  The kernel for many rows a head waits on
  * barriers, each for a bounded time (sdpa_last_device_status).  Errors as
  * above; ARG for an infinite scale or too small a workspace, SHAPE also when

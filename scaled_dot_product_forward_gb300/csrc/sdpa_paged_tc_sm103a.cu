@@ -22,7 +22,7 @@
 // is no page lies out of the map's bounds and reads as zeros).  16-bit pages
 // land in the 128-byte-swizzled layout that the products read.  e4m3 pages
 // land as they are in a small ring; the keys' are multiplied as they are, with
-// the queries split into e4m3 terms, and a warpgroup turns the values' into
+// the queries split into 8-bit terms, and a warpgroup turns the values' into
 // fp16 tiles (exact); a key's weight carries its page's value scale, so the
 // scales touch eight constants a row and step, not the elements.
 //
@@ -66,8 +66,9 @@ constexpr uint32_t kSuspendNs = 4000;  // a waiting thread may sleep this long b
 constexpr uint32_t kTmemCols = 512;  // S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512)
 constexpr int kGroups = KT / 16;     // 16 keys lie in one page
 
-// Terms of a query row in e4m3 for products with e4m3 keys: four significant
-// bits each, so two carry a bf16 value and three an fp16 one.
+// Terms of a query row for products with e4m3 keys, the first in e4m3 (four
+// significant bits), the others in e5m2 (three, and the sign of what is left is
+// one more): two carry a bf16 value, three an fp16 one.
 __host__ __device__ constexpr int q_terms(bool e4m3, bool bf16) { return !e4m3 ? 1 : bf16 ? 2 : 3; }
 
 template <int D, bool E4M3, bool BF16, bool HALF>
@@ -398,13 +399,25 @@ __device__ __forceinline__ int swizzled(int r, int c) {
 }
 
 // Two codes' values (a conversion instruction: not for the inner loops).
+template <__nv_fp8_interpretation_t TYPE>
 __device__ __forceinline__ float2 codes_value2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), TYPE);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// v to codes of one term, and what they leave.
+template <__nv_fp8_interpretation_t TYPE, bool LAST>
+__device__ __forceinline__ uint32_t take_term(float (&v)[4]) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, TYPE);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, TYPE);
+  if constexpr (!LAST) {
+    const float2 g0 = codes_value2<TYPE>(lo), g1 = codes_value2<TYPE>(hi);
+    v[0] -= g0.x, v[1] -= g0.y, v[2] -= g1.x, v[3] -= g1.y;
+  }
+  return lo | (hi << 16);
 }
 
 // Where 16-byte piece i of row r of a query tile waits as it lies in memory.
-// 16-bit: its own place.  e4m3 terms: pieces 2u and 2u + 1 become piece u of
+// 16-bit: its own place.  8-bit terms: pieces 2u and 2u + 1 become piece u of
 // every term, and wait in that piece's places of the first two.
 template <int D, bool E4M3, int QCHUNK>
 __device__ __forceinline__ int query_piece(int r, int i) {
@@ -424,9 +437,13 @@ __device__ __forceinline__ void ask_query(const uint16_t* src, uint8_t* tile, in
 // read it, negated for a negative scale; returns the (positive) multiplier of
 // the scores, |scale| * log2(e).  For e4m3 keys the row is brought by a power of
 // two to a largest element in [2^7, 2^8) (the factor goes into the multiplier)
-// and split into e4m3 terms, each what the earlier ones leave: a bf16 value is
-// exact in two, an fp16 one in three, down to 2^-10 in that scale, 2^-17 of the
-// row's largest element.  HALF: a row is two threads' (lane ^ 16).  The whole
+// and split into terms, each what the earlier ones leave.  Where the first term
+// is a normal e4m3 (from 2^-6, 2^-13 of the row's largest element) all of a bf16
+// value is in two, of an fp16 one in three: the first leaves a multiple of the
+// value's last place, at most 8 of them (fp16: 64, of which the next leaves at
+// most 4), and an e5m2 holds any of these, its least step being 2^-16.  Below,
+// the first leaves up to 2^-10, and the last is off by half a step of e5m2: 2^-14
+// (fp16: 2^-17), 2^-21 (2^-24) of the row's largest.  HALF: a row is two threads' (lane ^ 16).  The whole
 // warp calls it.  (Rolled loops over pieces that are rewritten in place: with
 // the row in registers this was 16 to 24 KB of code between the softmax's loops;
 // uneven prompts with e4m3 pages 660 -> 625 us.)
@@ -471,16 +488,9 @@ __device__ __forceinline__ float put_query(const PagedParams& p, bool live, uint
       for (int k = 0; k < 4; ++k) {
         const float2 a = unpack2<BF16>(x[2 * k]), b = unpack2<BF16>(x[2 * k + 1]);
         float v[4] = {a.x * up, a.y * up, b.x * up, b.y * up};
-#pragma unroll
-        for (int n = 0; n < q_terms(E4M3, BF16); ++n) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
-          term[n][k] = lo | (hi << 16);
-          if (n + 1 < q_terms(E4M3, BF16)) {
-            const float2 g0 = codes_value2(lo), g1 = codes_value2(hi);
-            v[0] -= g0.x, v[1] -= g0.y, v[2] -= g1.x, v[3] -= g1.y;
-          }
-        }
+        term[0][k] = take_term<__NV_E4M3, false>(v);
+        if constexpr (q_terms(E4M3, BF16) == 3) term[1][k] = take_term<__NV_E5M2, false>(v);
+        term[q_terms(E4M3, BF16) - 1][k] = take_term<__NV_E5M2, true>(v);
       }
 #pragma unroll
       for (int n = 0; n < q_terms(E4M3, BF16); ++n)
@@ -518,7 +528,8 @@ __device__ __forceinline__ void acc_store(uint32_t at, const uint32_t* r) {
 }
 
 // Two consecutive K-steps (32 codes each) of D[tmem] (+)= A[smem] * B[smem]^T
-// with e4m3 operands, in one elected issue; see mma_ss_x4.
+// with 8-bit operands (each of a type of its own), in one elected issue; see
+// mma_ss_x4.
 template <uint32_t HI>
 __device__ __forceinline__ void mma_codes_x2(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                              uint32_t acc) {
@@ -1013,6 +1024,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       // e4m3 operands (type 0 in the descriptor's fields, D = fp32), rows of D
       // bytes: the 128-byte swizzle, or the 64-byte one (mode 4)
       constexpr uint32_t idCodes = (1u << 4) | ((KT >> 3) << 17) | ((kM >> 4) << 24);
+      constexpr uint32_t kQueryE5m2 = 1u << 7;   // the later terms' type
       constexpr uint32_t kHiCodes = D == 128 ? kHi : ((512u >> 4) | (1u << 14) | (4u << 29));
       const uint32_t q_lo = desc_lo_sw128(smem_addr(sQ), 16);
       const uint32_t k_lo = desc_lo_sw128(smem_addr(sK), 16);
@@ -1029,8 +1041,8 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
           for (int n = 0; n < q_terms(E4M3, BF16); ++n)
 #pragma unroll
             for (int k = 0; k < D / 64; ++k)
-              mma_codes_x2<kHiCodes>(tmem + (t ? 128u : 0u), a0 + n * (L::kQChunk >> 4) + 4 * k, b0 + 4 * k, idCodes,
-                                     n + k > 0 ? 1u : 0u);
+              mma_codes_x2<kHiCodes>(tmem + (t ? 128u : 0u), a0 + n * (L::kQChunk >> 4) + 4 * k, b0 + 4 * k,
+                                     n > 0 ? idCodes | kQueryE5m2 : idCodes, n + k > 0 ? 1u : 0u);
         } else {
 #pragma unroll
           for (int ch = 0; ch < L::kChunks; ++ch) {

@@ -1,5 +1,5 @@
 """Precision of the attention over a paged cache where it is easily lost: small
-weights beside a large one."""
+weights beside a large one, small query elements beside a large one."""
 import math
 
 import pytest
@@ -93,3 +93,58 @@ def test_a_key_far_above_the_rest(sdpa_lib, rows, copies, cache, dtype, D, above
     assert worst <= 1, f"worst by {worst:.3g}, relative to the output's size {size:.3g}"
     want_lse = torch.logsumexp(s, 1)
     assert ((lse.double() - want_lse).abs() <= e[:, 0] + n * 2.0 ** -23 + 2.0 ** -22 * (1 + want_lse.abs())).all()
+
+
+def query_error(D, rows, G, dtype):
+    """What of its row's largest element a query element may be off by over an 8-bit cache: none down
+    to 2^-13 of it; below, with more than 16 rows a head, half a step of the last of the e4m3 and
+    e5m2 terms that carry it (two for bf16, three for fp16); with fewer, a bf16 row is fp16 under a
+    power of two that takes the largest element to 2^14 or more."""
+    if rows * G > 16:
+        return 2.0 ** -21 if dtype is torch.bfloat16 else 2.0 ** -24
+    return 2.0 ** -39 if dtype is torch.bfloat16 else 0.0
+
+
+@gpu
+@pytest.mark.parametrize("rows", [4, 5, 12, 30, 70])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ratio,exact", [(2 ** 8, False), (2 ** 11, True), (2 ** 12, False)])
+def test_a_query_channel_far_above_the_rest(sdpa_lib, rows, dtype, D, ratio, exact):
+    """One channel of the queries is 2^8 to 2^12 times the others, where the keys are small: the
+    others decide the scores.  exact: no element is below 2^-13 of its row's largest, so none is
+    off.  (Otherwise a score is off by that error times the sum of |k|.)  Other terms as above."""
+    n, G, P = 300, 4, 32
+    g = torch.Generator().manual_seed(D + rows)
+    q = torch.randn(rows, G, D, generator=g)
+    q[..., 5] = ratio * (1 + torch.rand(rows, G, generator=g)) / 2
+    if exact:
+        q = torch.where(q.abs() < 0.25, torch.copysign(torch.tensor(0.25), q), q)
+    q = q.to(dtype).cuda()
+    k, v = torch.randn(n, 1, D, generator=g), torch.randn(n, 1, D, generator=g)
+    k[..., 5] = torch.randn(n, 1, generator=g) / ratio
+    c, table = paged(sdpa_lib, k, v, P, E4M3, 2.0 ** -6, 3)
+    out, lse = call(sdpa_lib, q, c, table, n, True)
+    kk, vv = held(c.k, table, 2.0 ** -6, n)[:, 0], held(c.v, table, 2.0 ** -6, n)[:, 0]
+    qd = q.double().flatten(0, 1)
+    top = qd.abs().amax(1)
+    if exact:
+        assert (qd.abs().amin(1) >= 2.0 ** -13 * top).all()
+    s = qd @ kk.T / math.sqrt(D)
+    last = torch.arange(rows, device="cuda").repeat_interleave(G) + n - rows
+    s = s.masked_fill(torch.arange(n, device="cuda")[None] > last[:, None], -math.inf)
+    reach = (qd.abs() @ kk.T.abs() / math.sqrt(D)).amax(1)
+    e = (D + 16) * 2.0 ** -24 * reach + 2.0 ** -21 * (1 + reach)
+    if not exact:
+        e = e + query_error(D, rows, G, dtype) * top * kk.abs().sum(1).max() / math.sqrt(D)
+    p = torch.softmax(s, 1)
+    want, spread = p @ vv, p @ vv.abs()
+    tol = ref.half_step(dtype) * want.abs() + (ref.half_step(torch.float16) + 2 * e + 2 * n * 2.0 ** -23)[:, None] * spread * (1 + 2.0 ** -6)
+    tol = tol + 2.0 ** -36 * vv.abs().sum(0)
+    if dtype is torch.float16:
+        tol = tol + 2.0 ** -25
+    want_lse = torch.logsumexp(s, 1)
+    off = (lse[0].double() - want_lse).abs() / (e + n * 2.0 ** -23 + 2.0 ** -22 * (1 + want_lse.abs()))
+    assert off.max() <= 1, f"log-sum-exp: worst by {off.max().item():.3g}"
+    bad = (out[0].double() - want).abs() / tol
+    assert bad.max() <= 1, f"worst by {bad.max().item():.3g}"
