@@ -5,6 +5,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "sdpa_internal.h"
 
@@ -14,16 +15,68 @@ constexpr int64_t kIntMax = 0x7fffffffLL;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Bytes [lo, lo + bytes) of one operand.
-struct Span {
-  uintptr_t lo;
-  uint64_t bytes;
+// An operand's memory: runs of `run` bytes at every combination of up to three
+// steps (in bytes, positive).  `bytes`: from its first byte to behind its last one,
+// 0 for an operand that is not there.
+struct Block {
+  uintptr_t p = 0;
+  uint64_t run = 0, bytes = 0;
+  int n = 0;
+  int64_t extent[3], step[3];
+
+  void add(int64_t ext, int64_t st) {
+    if (ext <= 1) return;
+    extent[n] = ext, step[n++] = st;
+    bytes += static_cast<uint64_t>(ext - 1) * static_cast<uint64_t>(st);
+  }
+  void sort() {   // the largest step first
+    for (int i = 1; i < n; ++i)
+      for (int j = i; j > 0 && step[j - 1] < step[j]; --j) {
+        std::swap(step[j - 1], step[j]);
+        std::swap(extent[j - 1], extent[j]);
+      }
+  }
 };
 
-Span span_of(const void* p, uint64_t bytes) { return {reinterpret_cast<uintptr_t>(p), p ? bytes : 0}; }
+Block block_of(const void* p, uint64_t bytes) {
+  Block b;
+  b.p = reinterpret_cast<uintptr_t>(p);
+  b.run = b.bytes = p ? bytes : 0;
+  return b;
+}
 
-bool overlap(const Span& a, const Span& b) {
-  return a.bytes != 0 && b.bytes != 0 && a.lo < b.lo + b.bytes && b.lo < a.lo + a.bytes;
+// Whether a's steps from ia on and b's from ib on reach a byte in common, b's
+// beginning `shift` bytes behind a's; span_a, span_b: the bytes that they span.
+// Operands cut from one buffer (queries, keys and values side by side) interleave
+// without sharing: with s the larger step, places i s + x of a and shift + j s + y
+// of b (x, y: below s) meet only where shift + (j - i) s is one of the two
+// remainders between -s and s.  Taken for shared where a step's inner part is
+// longer than the step.
+bool shares(const Block& a, int ia, int64_t span_a, const Block& b, int ib, int64_t span_b, int64_t shift) {
+  if (shift >= span_a || -shift >= span_b) return false;
+  if (ia == a.n && ib == b.n) return true;
+  const int64_t sa = ia < a.n ? a.step[ia] : 0, sb = ib < b.n ? b.step[ib] : 0, s = sa > sb ? sa : sb;
+  const int64_t na = sa == s ? a.extent[ia++] : 1, nb = sb == s ? b.extent[ib++] : 1;
+  span_a -= (na - 1) * s;
+  span_b -= (nb - 1) * s;
+  if (span_a > s || span_b > s) return true;
+  int64_t k = shift / s, r = shift % s;
+  if (r < 0) r += s, --k;
+  // j - i = -k, or -k - 1
+  const auto possible = [&](int64_t d) { return d > -na && d < nb; };
+  return (possible(-k) && shares(a, ia, span_a, b, ib, span_b, r)) ||
+         (possible(-k - 1) && shares(a, ia, span_a, b, ib, span_b, r - s));
+}
+bool shares(Block a, Block b) {
+  // (no operand of a program spans 2^62 bytes)
+  if ((a.bytes | b.bytes) >> 62) return true;
+  a.sort();
+  b.sort();
+  return shares(a, 0, static_cast<int64_t>(a.bytes), b, 0, static_cast<int64_t>(b.bytes),
+                static_cast<int64_t>(b.p) - static_cast<int64_t>(a.p));
+}
+inline bool overlap(const Block& a, const Block& b) {
+  return a.bytes != 0 && b.bytes != 0 && a.p < b.p + b.bytes && b.p < a.p + a.bytes && shares(a, b);
 }
 
 // [tokens, heads, D] of 16-bit elements with (token, head) strides.
@@ -31,8 +84,11 @@ struct Rows {
   const void* p;
   int64_t tokens, heads, dim, st, sh;
 
-  uint64_t row_bytes() const { return 2ull * static_cast<uint64_t>((heads - 1) * sh + dim); }
-  Span span() const { return span_of(p, 2ull * static_cast<uint64_t>((tokens - 1) * st) + row_bytes()); }
+  Block block() const {
+    Block b = block_of(p, 2ull * static_cast<uint64_t>(dim));
+    if (p) b.add(tokens, 2 * st), b.add(heads, 2 * sh);
+    return b;
+  }
 };
 
 sdpa_status check_rows(const void* p, int64_t tokens, int64_t heads, int64_t dim,
@@ -43,21 +99,6 @@ sdpa_status check_rows(const void* p, int64_t tokens, int64_t heads, int64_t dim
   if (heads > 1 && (r->sh <= 0 || r->sh % 8 != 0)) return SDPA_ERR_LAYOUT;
   if (r->st >= (int64_t(1) << 38) || r->sh >= (int64_t(1) << 38)) return SDPA_ERR_LAYOUT;
   return SDPA_OK;
-}
-
-// Whether two operands share an element.  Operands cut from one buffer of
-// rows (queries, keys and values side by side) interleave without sharing:
-// with equal token strides the rows are compared around the stride.
-bool rows_overlap(const Rows& a, const Rows& b) {
-  if (!overlap(a.span(), b.span())) return false;
-  if (a.tokens > 1 && a.st == b.st) {
-    const uint64_t period = 2ull * static_cast<uint64_t>(a.st);
-    const uint64_t d = (reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % period;
-    const uint64_t neg = (period - d) % period;
-    if (a.row_bytes() <= period && b.row_bytes() <= period && d >= a.row_bytes() && neg >= b.row_bytes())
-      return false;
-  }
-  return true;
 }
 
 bool in_16_to_1024(int64_t page_size) {
@@ -84,13 +125,12 @@ sdpa_status check_cache(const sdpa_paged_cache* c, sdpa_dtype dtype) {
   return SDPA_OK;
 }
 
-Span cache_span(const sdpa_paged_cache* c, const void* p, const int64_t* st) {
+Block cache_block(const sdpa_paged_cache* c, const void* p, const int64_t* st) {
   const int64_t ext[3] = {c->n_pages, c->page_size, c->n_kv_heads};
-  uint64_t last = 0;
-  for (int i = 0; i < 3; ++i)
-    if (ext[i] > 1) last += static_cast<uint64_t>(ext[i] - 1) * static_cast<uint64_t>(st[i]);
-  const uint64_t bytes = c->elem == SDPA_CACHE_E4M3 ? 1 : 2;
-  return span_of(p, (last + static_cast<uint64_t>(c->head_dim)) * bytes);
+  const int64_t bytes = c->elem == SDPA_CACHE_E4M3 ? 1 : 2;
+  Block b = block_of(p, static_cast<uint64_t>(c->head_dim * bytes));
+  for (int i = 0; i < 3; ++i) b.add(ext[i], st[i] * bytes);
+  return b;
 }
 
 // The batch's index arrays.
@@ -165,28 +205,28 @@ sdpa_status sdpa_cache_append(const sdpa_paged_cache* cache, const void* k, cons
   {
     const bool e4m3 = cache->elem == SDPA_CACHE_E4M3;
     const uint64_t sb = 4ull * static_cast<uint64_t>(cache->n_pages) * static_cast<uint64_t>(hkv);
-    const Span outs[4] = {cache_span(cache, cache->k, cache->k_stride), cache_span(cache, cache->v, cache->v_stride),
-                          span_of(e4m3 ? cache->k_scale : nullptr, sb), span_of(e4m3 ? cache->v_scale : nullptr, sb)};
+    const Block outs[4] = {cache_block(cache, cache->k, cache->k_stride), cache_block(cache, cache->v, cache->v_stride),
+                           block_of(e4m3 ? cache->k_scale : nullptr, sb), block_of(e4m3 ? cache->v_scale : nullptr, sb)};
     const uint64_t tb = cos ? 4ull * static_cast<uint64_t>(n_pos) * static_cast<uint64_t>(rot_dim / 2) : 0;
-    const Span ins[5] = {span_of(page_table, 4ull * static_cast<uint64_t>((n_seqs - 1) * page_table_stride + max_pages)),
-                         span_of(kv_lens, 4ull * static_cast<uint64_t>(n_seqs)),
-                         span_of(cu_seqlens, 4ull * static_cast<uint64_t>(n_seqs + 1)), span_of(cos, tb), span_of(sin, tb)};
-    const Rows* rows[4] = {&rk, &rv, q ? &rq : nullptr, q ? &ro : nullptr};
-    for (const Span& o : outs) {
-      for (const Span& i : ins)
+    const Block ins[5] = {block_of(page_table, 4ull * static_cast<uint64_t>((n_seqs - 1) * page_table_stride + max_pages)),
+                          block_of(kv_lens, 4ull * static_cast<uint64_t>(n_seqs)),
+                          block_of(cu_seqlens, 4ull * static_cast<uint64_t>(n_seqs + 1)), block_of(cos, tb), block_of(sin, tb)};
+    const Block bk = rk.block(), bv = rv.block(), bq = rq.block(), bo = ro.block();
+    for (const Block& o : outs) {
+      for (const Block& i : ins)
         if (overlap(o, i)) return SDPA_ERR_ARG;
-      for (const Rows* r : rows)
-        if (r && overlap(o, r->span())) return SDPA_ERR_ARG;
+      for (const Block* r : {&bk, &bv, &bq, &bo})
+        if (overlap(o, *r)) return SDPA_ERR_ARG;
     }
     // scales apart from the codes and from each other
     if (overlap(outs[0], outs[2]) || overlap(outs[0], outs[3]) || overlap(outs[1], outs[2]) ||
         overlap(outs[1], outs[3]) || overlap(outs[2], outs[3]))
       return SDPA_ERR_ARG;
     if (q) {
-      for (const Span& i : ins)
-        if (overlap(ro.span(), i)) return SDPA_ERR_ARG;
+      for (const Block& i : ins)
+        if (overlap(bo, i)) return SDPA_ERR_ARG;
       const bool in_place = q == q_out && rq.st == ro.st && rq.sh == ro.sh;
-      if ((!in_place && rows_overlap(ro, rq)) || rows_overlap(ro, rk) || rows_overlap(ro, rv)) return SDPA_ERR_ARG;
+      if ((!in_place && overlap(bo, bq)) || overlap(bo, bk) || overlap(bo, bv)) return SDPA_ERR_ARG;
     }
   }
   int dev = 0, sms = 0;
@@ -270,29 +310,31 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
   if ((s = check_rows(q, total_q, n_heads, D, q_stride, &rq)) != SDPA_OK) return s;
   if ((s = check_rows(out, total_q, n_heads, D, o_stride, &ro)) != SDPA_OK) return s;
   if (!aligned(workspace, 16)) return SDPA_ERR_LAYOUT;
-  Span ls = {0, 0};
+  Block ls;
   int64_t lt = 0, lh = 0;
   if (lse) {
     lt = total_q > 1 ? lse_stride[0] : 0;
     lh = n_heads > 1 ? lse_stride[1] : 0;
     if (!aligned(lse, 4) || (total_q > 1 && lt <= 0) || (n_heads > 1 && lh <= 0)) return SDPA_ERR_LAYOUT;
-    ls = span_of(lse, 4ull * static_cast<uint64_t>((total_q - 1) * lt + (n_heads - 1) * lh + 1));
+    if (lt >= (int64_t(1) << 38) || lh >= (int64_t(1) << 38)) return SDPA_ERR_LAYOUT;
+    ls = block_of(lse, 4);
+    ls.add(total_q, 4 * lt), ls.add(n_heads, 4 * lh);
   }
   if (std::isinf(scale)) return SDPA_ERR_ARG;
   const bool e4m3 = cache->elem == SDPA_CACHE_E4M3;
   {
     const uint64_t sb = 4ull * static_cast<uint64_t>(cache->n_pages) * static_cast<uint64_t>(hkv);
-    const Span ins[8] = {rq.span(),
-                         cache_span(cache, cache->k, cache->k_stride),
-                         cache_span(cache, cache->v, cache->v_stride),
-                         span_of(e4m3 ? cache->k_scale : nullptr, sb),
-                         span_of(e4m3 ? cache->v_scale : nullptr, sb),
-                         span_of(page_table, 4ull * static_cast<uint64_t>((n_seqs - 1) * page_table_stride + max_pages)),
-                         span_of(kv_lens, 4ull * static_cast<uint64_t>(n_seqs)),
-                         span_of(cu_seqlens_q, 4ull * static_cast<uint64_t>(n_seqs + 1))};
-    const Span outs[3] = {ro.span(), ls, span_of(workspace, workspace_size)};
-    for (const Span& o : outs)
-      for (const Span& i : ins)
+    const Block ins[8] = {rq.block(),
+                          cache_block(cache, cache->k, cache->k_stride),
+                          cache_block(cache, cache->v, cache->v_stride),
+                          block_of(e4m3 ? cache->k_scale : nullptr, sb),
+                          block_of(e4m3 ? cache->v_scale : nullptr, sb),
+                          block_of(page_table, 4ull * static_cast<uint64_t>((n_seqs - 1) * page_table_stride + max_pages)),
+                          block_of(kv_lens, 4ull * static_cast<uint64_t>(n_seqs)),
+                          block_of(cu_seqlens_q, 4ull * static_cast<uint64_t>(n_seqs + 1))};
+    const Block outs[3] = {ro.block(), ls, block_of(workspace, workspace_size)};
+    for (const Block& o : outs)
+      for (const Block& i : ins)
         if (overlap(o, i)) return SDPA_ERR_ARG;
     if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2])) return SDPA_ERR_ARG;
   }
