@@ -411,7 +411,9 @@ typedef struct sdpa_paged_cache {
  *
  * Errors: NULL; DTYPE (elem of a 16-bit cache is not dtype); SHAPE (an extent
  * < 1 or too large, page_size, head_dim, rot_dim, total not divisible);
- * LAYOUT; ARG (an output overlaps an input or the cache); CUDA; DEVICE.
+ * LAYOUT; ARG (an output overlaps an input or the cache; pages of keys are pages
+ * of values, which attention may read but an append would write twice); CUDA;
+ * DEVICE.
  */
 SDPA_API sdpa_status sdpa_cache_append(
     const sdpa_paged_cache* cache, const void* k, const void* v, sdpa_dtype dtype, int64_t total,

@@ -47,36 +47,36 @@ Block block_of(const void* p, uint64_t bytes) {
 
 // Whether a's steps from ia on and b's from ib on reach a byte in common, b's
 // beginning `shift` bytes behind a's; span_a, span_b: the bytes that they span.
-// Operands cut from one buffer (queries, keys and values side by side) interleave
-// without sharing: with s the larger step, places i s + x of a and shift + j s + y
-// of b (x, y: below s) meet only where shift + (j - i) s is one of the two
-// remainders between -s and s.  Taken for shared where a step's inner part is
-// longer than the step.
-bool shares(const Block& a, int ia, int64_t span_a, const Block& b, int ib, int64_t span_b, int64_t shift) {
+// Operands cut from one buffer (queries, keys and values side by side, key and
+// value pages of one pool) interleave without sharing: with s the larger step,
+// places i s + x of a and shift + j s + y of b (x, y: below s) meet only where
+// shift + (j - i) s is one of the two remainders between -s and s.  unknown: the
+// answer where a step's inner part is longer than the step.
+bool shares(const Block& a, int ia, int64_t span_a, const Block& b, int ib, int64_t span_b, int64_t shift, bool unknown) {
   if (shift >= span_a || -shift >= span_b) return false;
   if (ia == a.n && ib == b.n) return true;
   const int64_t sa = ia < a.n ? a.step[ia] : 0, sb = ib < b.n ? b.step[ib] : 0, s = sa > sb ? sa : sb;
   const int64_t na = sa == s ? a.extent[ia++] : 1, nb = sb == s ? b.extent[ib++] : 1;
   span_a -= (na - 1) * s;
   span_b -= (nb - 1) * s;
-  if (span_a > s || span_b > s) return true;
+  if (span_a > s || span_b > s) return unknown;
   int64_t k = shift / s, r = shift % s;
   if (r < 0) r += s, --k;
   // j - i = -k, or -k - 1
   const auto possible = [&](int64_t d) { return d > -na && d < nb; };
-  return (possible(-k) && shares(a, ia, span_a, b, ib, span_b, r)) ||
-         (possible(-k - 1) && shares(a, ia, span_a, b, ib, span_b, r - s));
+  return (possible(-k) && shares(a, ia, span_a, b, ib, span_b, r, unknown)) ||
+         (possible(-k - 1) && shares(a, ia, span_a, b, ib, span_b, r - s, unknown));
 }
-bool shares(Block a, Block b) {
+bool shares(Block a, Block b, bool unknown) {
   // (no operand of a program spans 2^62 bytes)
-  if ((a.bytes | b.bytes) >> 62) return true;
+  if ((a.bytes | b.bytes) >> 62) return unknown;
   a.sort();
   b.sort();
   return shares(a, 0, static_cast<int64_t>(a.bytes), b, 0, static_cast<int64_t>(b.bytes),
-                static_cast<int64_t>(b.p) - static_cast<int64_t>(a.p));
+                static_cast<int64_t>(b.p) - static_cast<int64_t>(a.p), unknown);
 }
-inline bool overlap(const Block& a, const Block& b) {
-  return a.bytes != 0 && b.bytes != 0 && a.p < b.p + b.bytes && b.p < a.p + a.bytes && shares(a, b);
+inline bool overlap(const Block& a, const Block& b, bool unknown = true) {
+  return a.bytes != 0 && b.bytes != 0 && a.p < b.p + b.bytes && b.p < a.p + a.bytes && shares(a, b, unknown);
 }
 
 // [tokens, heads, D] of 16-bit elements with (token, head) strides.
@@ -218,8 +218,9 @@ sdpa_status sdpa_cache_append(const sdpa_paged_cache* cache, const void* k, cons
       for (const Block* r : {&bk, &bv, &bq, &bo})
         if (overlap(o, *r)) return SDPA_ERR_ARG;
     }
-    // scales apart from the codes and from each other
-    if (overlap(outs[0], outs[2]) || overlap(outs[0], outs[3]) || overlap(outs[1], outs[2]) ||
+    // keys' pages apart from the values' (refused where that is certain), scales
+    // from the codes and from each other
+    if (overlap(outs[0], outs[1], false) || overlap(outs[0], outs[2]) || overlap(outs[0], outs[3]) || overlap(outs[1], outs[2]) ||
         overlap(outs[1], outs[3]) || overlap(outs[2], outs[3]))
       return SDPA_ERR_ARG;
     if (q) {

@@ -64,6 +64,27 @@ def test_operands_that_share_elements_are_refused(lib, out):
     assert r.append(q=B, q_stride=(768, 192), qo=at(out), qo_stride=out[1:]) == ARG
 
 
+@cpu
+@pytest.mark.parametrize("v", [0, 32, 2048, 2048 * 3, 2048 + 128])
+def test_keys_pages_that_are_values_pages_are_not_appended_to(lib, v):
+    """Both would be written; attention may read one tensor as both."""
+    r = Raw(lib)
+    c = r.struct(v=r.a["k"] + 2 * v)
+    assert r.append(c) == ARG
+    assert r.forward(c, size=1 << 40) in NO_DEVICE
+
+
+@cpu
+@pytest.mark.parametrize("v,strides", [(2048, (4096, 128, 64)), (128, (4096, 256, 64)), (64, (4096, 256, 128)), (8192, (2048, 128, 64)),
+                                       (2048, (4096, 64, 1024)), (512, (4096, 64, 1024))])
+def test_pages_of_one_pool_are_appended_to(lib, v, strides):
+    """Keys' and values' pages, rows or heads in turn, or one after the other."""
+    r = Raw(lib)
+    c = r.struct(v=r.a["k"] + 2 * v, k_stride=strides, v_stride=strides)
+    want = (ARG,) if (v, strides) == (512, (4096, 64, 1024)) else NO_DEVICE
+    assert r.append(c) in want
+
+
 @gpu
 @pytest.mark.parametrize("rows", [1, 5, 40, 80])
 @pytest.mark.parametrize("total_first", [True, False])
@@ -90,3 +111,22 @@ def test_queries_keys_and_values_by_head(sdpa_lib, rows, total_first):
         assert torch.equal(getattr(caches[0], name).view(torch.uint8), getattr(caches[1], name).view(torch.uint8))
     assert torch.equal(sdpa_lib.sdpa_paged_forward(q, caches[1], table.cuda(), lens, out=k, is_causal=True), want)
     assert torch.equal(k, want) and torch.equal(q, apart) and torch.equal(v, values)
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("dtype", [E4M3, torch.float16])
+def test_one_tensor_as_keys_and_values(sdpa_lib, dtype, rows):
+    """Attention reads it; it is not appended to."""
+    k = torch.randn(10, 32, 1, 64, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    s = torch.full((10, 1), 0.5, device="cuda") if dtype is E4M3 else None
+    c = sdpa_lib.SdpaPagedCache(k, k, s, s)
+    q = torch.randn(rows, 4, 64, generator=torch.Generator().manual_seed(4)).half().cuda()
+    run_attend(sdpa_lib, c, q, tables(1, 9, 10, 1), [270], [rows], True, use_cu=False)
+    before = k.clone()
+    with pytest.raises(sdpa.SdpaError) as e:
+        sdpa_lib.sdpa_cache_append(c, q[:, :1], q[:, 1:2], tables(1, 9, 10, 1).cuda(),
+                                   torch.tensor([270], dtype=torch.int32, device="cuda"))
+    assert e.value.status == ARG
+    torch.cuda.synchronize()
+    assert torch.equal(k.view(torch.uint8), before.view(torch.uint8))
