@@ -532,7 +532,7 @@ def _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, rows):
     if len(lens_shape) != 1 or len(table_shape) != 2 or table_shape[0] != lens_shape[0] or \
             (cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != lens_shape[0] + 1)):
         raise SdpaError(3, where)
-    if not kv_lens.is_contiguous() or page_table.stride(1) != 1 or \
+    if not kv_lens.is_contiguous() or (page_table.stride(1) != 1 and table_shape[1] != 1) or \
             (cu_seqlens is not None and not cu_seqlens.is_contiguous()):
         raise SdpaError(5, where)
     dtype = rows.dtype
