@@ -587,9 +587,9 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
     if v.dtype is not dtype or (q is not None and q.dtype is not dtype) or \
             (q_out is not None and q_out.dtype is not dtype):
         raise SdpaError(4, where)
-    total = shape[0]
     if len(shape) != 3 or v.shape != shape or shape[1] != cache.n_kv_heads or shape[2] != cache.head_dim:
         raise SdpaError(3, where)
+    total = shape[0]
     if (cos is None) != (sin is None) or (q is None and q_out is not None):
         raise SdpaError(1, where)
     heads = 0
@@ -604,9 +604,9 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
         f32 = _torch.float32
         if cos.dtype is not f32 or sin.dtype is not f32:
             raise SdpaError(4, where)
-        n_pos, rot = (*cos.shape, 0)[:2]
         if cos.dim() != 2 or cos.shape != sin.shape:
             raise SdpaError(3, where)
+        n_pos, rot = cos.shape
         if not cos.is_contiguous() or not sin.is_contiguous():
             raise SdpaError(5, where)
         rot *= 2

@@ -47,3 +47,27 @@ def test_a_page_table_of_one_column_on_the_device(sdpa_lib):
     wide = torch.full((3, 5), -1, dtype=torch.int32, device="cuda")
     wide[:, 2] = t[:, 0]
     assert torch.equal(sdpa_lib.sdpa_paged_forward(q, c, wide.as_strided((3, 1), (5, 3), 2), lens), want)
+
+
+def test_ranks(lib):
+    """A wrong number of dimensions is a wrong shape, also where there is none."""
+    c, lens, t = cache(), torch.ones(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
+    k, v, q = (torch.zeros(2, n, 64, dtype=torch.bfloat16) for n in (2, 2, 4))
+    angles = torch.zeros(9, 32)
+    f = sdpa.sdpa_cache_append
+    for x in (k[0, 0, 0], k[0, 0], k[0], k[None]):
+        assert status(f, c, x, x, t, lens) == SHAPE
+        assert status(f, c, k, x, t, lens) == SHAPE
+        assert status(f, c, k, v, t, lens, q=x) == SHAPE
+        assert status(f, c, k, v, t, lens, q=q, q_out=x) == SHAPE
+        assert status(sdpa.sdpa_paged_forward, x, c, t, lens) == SHAPE
+        assert status(sdpa.sdpa_paged_forward, q, c, t, lens, out=x) == SHAPE
+    for x in (angles[0, 0], angles[0], angles[None]):
+        assert status(f, c, k, v, t, lens, cos=x, sin=x) == SHAPE
+        assert status(f, c, k, v, t, lens, cos=angles, sin=x) == SHAPE
+        assert status(sdpa.sdpa_paged_forward, q, c, t, lens, lse=x) == SHAPE
+    for x in (t[0], t[None], t[0, 0]):
+        assert status(f, c, k, v, x, lens) == SHAPE
+    for x in (lens[0], lens[None]):
+        assert status(f, c, k, v, t, x) == SHAPE
+        assert status(f, c, k, v, t, lens, x) == SHAPE
