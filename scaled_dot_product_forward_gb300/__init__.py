@@ -669,6 +669,8 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
         raise SdpaError(1, where)
     if total < 1 or heads < 1 or max_pages < 1 or max_seqlen_q < 1:
         raise SdpaError(3, where)
+    if max_seqlen_q > total:
+        max_seqlen_q = total
     if out is not None and (out.dtype is not q.dtype or out.shape != shape):
         raise SdpaError(3, where)
     if lse is not None and (lse.dtype is not _torch.float32 or tuple(lse.shape) != (total, heads)):

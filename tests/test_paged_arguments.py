@@ -71,3 +71,17 @@ def test_ranks(lib):
     for x in (lens[0], lens[None]):
         assert status(f, c, k, v, t, x) == SHAPE
         assert status(f, c, k, v, t, lens, x) == SHAPE
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 30])
+def test_any_bound_on_the_rows(sdpa_lib, rows):
+    """max_seqlen_q is an upper bound: however large, it gives the results."""
+    c = make_cache(sdpa_lib, 9, 32, 2, 64, "e4m3", torch.bfloat16, 3)
+    q = torch.randn(2 * rows, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    lens = torch.tensor([40, 96], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, rows, 2 * rows], dtype=torch.int32, device="cuda")
+    t = tables(2, 3, 9, 2).cuda()
+    want = sdpa_lib.sdpa_paged_forward(q, c, t, lens, cu, 2 * rows, is_causal=True)
+    for most in (10 ** 6, 2 ** 31 - 1, 2 ** 31, 2 ** 40):
+        assert torch.equal(sdpa_lib.sdpa_paged_forward(q, c, t, lens, cu, most, is_causal=True), want)
