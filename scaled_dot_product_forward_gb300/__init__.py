@@ -580,7 +580,13 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
     rot_dim / 2] rotation tables (None: no rotation), pairs (j, j + rot_dim /
     2), or neighbours when ``interleaved``.  q: the tokens' queries [total,
     n_heads, head_dim], rotated too, into ``q_out`` (allocated if None; may be
-    ``q``).  Returns ``q_out`` (None without q)."""
+    ``q``).  Returns ``q_out`` (None without q).
+
+    A token whose position is negative, past the page table or past the angles
+    is left out, and so are rows behind the last sequence: their rows of
+    ``q_out`` are not written.  They hold whatever the memory held (NaN,
+    perhaps) if it is allocated here, the queries as they were with
+    ``q_out=q``."""
     where = "sdpa_cache_append"
     n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, k)
     dtype, shape = k.dtype, k.shape
@@ -651,8 +657,11 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
     [n_seqs] cached tokens, the new ones among them; page_table: int32
     [n_seqs, max_pages].  is_causal: row i of n sees keys up to kv_lens - n +
     i.  Returns ``out`` [total_q, n_heads, head_dim], or ``(out, lse)`` with
-    lse fp32 [total_q, n_heads].  The workspace is allocated from torch's
-    pool for this call and stream."""
+    lse fp32 [total_q, n_heads].  Rows of q outside every sequence are not
+    written: they hold whatever the memory held where ``out`` and ``lse`` are
+    allocated here.  (A sequence's own rows are all read and written, those that
+    an append left out too.)  The workspace is allocated from torch's pool for
+    this call and stream."""
     where = "sdpa_paged_forward"
     n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens_q, q)
     shape = q.shape

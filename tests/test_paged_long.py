@@ -272,3 +272,29 @@ def test_append_for_many_sequences(sdpa_lib, cache, dtype, B, most):
     counts[B // 2] = most
     lens = [n + int(x) for n, x in zip(counts, torch.randint(0, 50, (B,), generator=g))]
     same_append(sdpa_lib, 64, cache, dtype, 16, 2, 4, 64, False, lens, counts, B)
+
+
+@gpu
+@pytest.mark.parametrize("cache", ["e4m3", "16"])
+def test_append_allocates_the_queries(sdpa_lib, cache):
+    """q_out allocated by the call: rows of tokens that have a place are the rotated queries (the
+    others are left as allocated); in place the others keep their queries."""
+    from tests.test_paged import make_cache
+    c = make_cache(sdpa_lib, 6, 16, 1, 64, cache, torch.bfloat16, 4)
+    g = torch.Generator().manual_seed(1)
+    k, v, q = (torch.randn(23, n, 64, generator=g).bfloat16().cuda() for n in (1, 1, 3))
+    a = torch.rand(30, 32, generator=g)
+    cos, sin = a.cos().cuda(), a.sin().cuda()
+    table = torch.tensor([[4, 1], [2, 77]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([3, 35], dtype=torch.int32, device="cuda")           # positions -2 .. 2, 20 .. 34
+    cu = torch.tensor([0, 5, 20], dtype=torch.int32, device="cuda")
+    placed = list(range(2, 5)) + list(range(5, 15))                          # 30 is past the angles; a bad page has a place
+    at = torch.tensor([0, 1, 2] + list(range(20, 30)))
+    want = turned(q.float().cpu()[placed], a.cos()[at], a.sin()[at], False).bfloat16()
+    got = sdpa_lib.sdpa_cache_append(c, k, v, table, lens, cu, cos=cos, sin=sin, q=q)
+    assert torch.equal(got.cpu()[placed], want)
+    before = q.clone()
+    assert sdpa_lib.sdpa_cache_append(c, k, v, table, lens, cu, cos=cos, sin=sin, q=q, q_out=q) is q
+    assert torch.equal(q.cpu()[placed], want)
+    rest = [i for i in range(23) if i not in placed]
+    assert torch.equal(q[rest], before[rest])
