@@ -145,7 +145,7 @@ struct PagedParams {
   int seq_q;                // total_q / n_seqs
   int unit_heads, n_groups; // key/value heads of a unit, groups of them
   int step_shift;           // keys a step = 1 << step_shift
-  int min_steps, min_steps_shift;  // of a CTA's range, a power of two
+  int min_steps, min_steps_shift;  // at most one range for as many steps; a power of two
   int page_shift;           // page size = 1 << page_shift
   int is_causal;
   float scale_log2;
@@ -199,10 +199,17 @@ struct PagedForm {
 constexpr int paged_per_sm(int head_dim, bool e4m3) { return head_dim == 64 ? 4 : e4m3 ? 3 : 2; }
 // Up to 16 rows a head go to the form for few rows (sdpa_paged_sm103a.cu), up
 // to 64 to the half-tile form of the other (sdpa_paged_tc_sm103a.cu), more to
-// its full tiles.  16 sequences of 8192 tokens, 8 heads of 128, e4m3 / heads of
-// 64, e4m3: 8 rows 72 / 41 us in the first form, 75 / 58 in the second; 16 rows
-// 81 / 45 and 76 / 58; 24 rows (two tiles, in the first form) 103 / 66 and 79 /
-// 59; 64 rows 85 / 63 in half tiles, 72 rows 101 / 87 in full ones.
+// its full tiles.  16 sequences of 8192 tokens, 8 heads, us in the first form and
+// in the second:
+//                          8 rows      16 rows     24 rows
+//   D 128, e4m3, bf16      72, 77      80, 78      103, 80
+//   D 128, e4m3, fp16      67, 79      76, 80
+//   D 128, 16-bit pages    91, 94      94, 95
+//   D 64, e4m3             41, 60      45, 59      66, 60
+//   D 64, 16-bit pages     55, 58      60, 58
+// (24 rows are two tiles in the first form).  At 16 rows neither form is ahead
+// throughout; one limit serves all of them, and is off by 2 us at most.
+// 64 rows take 85 / 63 us in half tiles, 72 rows 101 / 87 in full ones (e4m3).
 // The form for few rows has four warps, for up to four heads of a unit (as
 // many as divide the heads; tokens' rows of neighbouring heads lie together,
 // so reading them together keeps DRAM pages open), which share a head's keys

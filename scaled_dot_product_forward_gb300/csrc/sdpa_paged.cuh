@@ -113,8 +113,9 @@ struct DivideScratch {
   Seq found;
 };
 
-// Ranges of a division: at most one a CTA, and of at least p.min_steps steps
-// (joining many short pieces costs more than it saves; never an empty range).
+// Ranges of a division: at most one a CTA, and at most one for p.min_steps steps
+// or what is left of them (joining many short pieces costs more than it saves;
+// being equal, ranges of a few steps in all may have fewer, never none).
 __device__ __forceinline__ int range_count(const PagedParams& p, int total) {
   return min((total + p.min_steps - 1) >> p.min_steps_shift, p.n_ctas);
 }
