@@ -472,6 +472,29 @@ SDPA_API sdpa_status sdpa_paged_forward(
     int64_t max_seqlen_q, int is_causal, float scale, void* workspace, uint64_t workspace_bytes,
     void* stream);
 
+/*
+ * sdpa_paged_forward_window -- sdpa_paged_forward, causal, where a token sees a
+ * sliding window of its sequence and the sequence's first tokens: the one at
+ * position p sees keys j <= p with j > p - window or j < sinks.
+ *
+ * window       : tokens of the window, the row's own among them; at least 1.
+ * sinks        : first tokens that stay visible; 0 for none.
+ *
+ * A page none of whose tokens is seen by any of the sequence's rows is not used:
+ * its entry may be anything (the page may be free, or another sequence's).  What
+ * sdpa_paged_forward says of a key that a row does not see holds for the others.
+ * Everything else as sdpa_paged_forward (a window of max_pages * page_size or
+ * more gives its results bit for bit); SDPA_ERR_ARG for a window below 1 or a
+ * negative number of sinks.
+ */
+SDPA_API sdpa_status sdpa_paged_forward_window(
+    const void* q, void* out, float* lse, sdpa_dtype dtype, const sdpa_paged_cache* cache,
+    int64_t total_q, int64_t n_heads, const int64_t* q_stride, const int64_t* o_stride,
+    const int64_t* lse_stride, const int32_t* page_table, int64_t page_table_stride,
+    int64_t max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens_q, int64_t n_seqs,
+    int64_t max_seqlen_q, int64_t window, int64_t sinks, float scale, void* workspace,
+    uint64_t workspace_bytes, void* stream);
+
 /* Bytes of workspace that sdpa_paged_forward needs on the current device (a
  * bound that depends on the device and these arguments alone, not on lengths
  * or batch); 0 when there is no sm_103 device or an argument is out of range. */

@@ -122,6 +122,9 @@ def load_library(path: str | None = None):
     lib.sdpa_paged_forward.argtypes = [vp, vp, vp, ctypes.c_int, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp,
                                        i64, i64, ctypes.c_int, ctypes.c_float, vp, ctypes.c_uint64, vp]
     lib.sdpa_paged_forward.restype = ctypes.c_int
+    lib.sdpa_paged_forward_window.argtypes = [vp, vp, vp, ctypes.c_int, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp,
+                                              i64, i64, i64, i64, ctypes.c_float, vp, ctypes.c_uint64, vp]
+    lib.sdpa_paged_forward_window.restype = ctypes.c_int
     lib.sdpa_paged_workspace_bytes.argtypes = [i64, i64, i64, i64]
     lib.sdpa_paged_workspace_bytes.restype = ctypes.c_uint64
     if path is None:
@@ -542,6 +545,7 @@ def _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, rows):
     return lens_shape[0], table_shape[1], dt
 
 
+_I64_MAX = (1 << 63) - 1
 _Strides = ctypes.c_int64 * 8
 _address = ctypes.addressof
 
@@ -647,7 +651,8 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
 
 
 def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seqlen_q=None, out=None, *,
-                       is_causal: bool = False, scale=None, stream=None, return_lse: bool = False, lse=None):
+                       is_causal: bool = False, window=None, sinks: int = 0, scale=None, stream=None,
+                       return_lse: bool = False, lse=None):
     """Attention of new tokens over a paged cache (sdpa_paged_forward).
 
     q: [total_q, n_heads, head_dim] bf16/fp16, the sequences' rows one after
@@ -656,7 +661,10 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
     number of rows for each sequence, one for a decoding step); kv_lens: int32
     [n_seqs] cached tokens, the new ones among them; page_table: int32
     [n_seqs, max_pages].  is_causal: row i of n sees keys up to kv_lens - n +
-    i.  Returns ``out`` [total_q, n_heads, head_dim], or ``(out, lse)`` with
+    i.  window (with is_causal): of these only the last ``window``, its own
+    among them, and the sequence's first ``sinks`` (sdpa_paged_forward_window);
+    pages that no row of a sequence then sees need not exist (their entries may
+    be anything).  Returns ``out`` [total_q, n_heads, head_dim], or ``(out, lse)`` with
     lse fp32 [total_q, n_heads].  Rows of q outside every sequence are not
     written: they hold whatever the memory held where ``out`` and ``lse`` are
     allocated here.  (A sequence's own rows are all read and written, those that
@@ -680,6 +688,11 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
         raise SdpaError(3, where)
     if max_seqlen_q > total:
         max_seqlen_q = total
+    if window is None:
+        if sinks != 0:
+            raise SdpaError(6, where)
+    elif not is_causal or window < 1 or sinks < 0:
+        raise SdpaError(6, where)
     if out is not None and (out.dtype is not q.dtype or out.shape != shape):
         raise SdpaError(3, where)
     if lse is not None and (lse.dtype is not _torch.float32 or tuple(lse.shape) != (total, heads)):
@@ -712,11 +725,14 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
         work = empty(size, dtype=_torch.uint8, device=dev)
         strides = _Strides(*qs, *_two_strides(o, where), *(ls.stride() if ls is not None else ()))
         at = _address(strides)
-        rc = lib.sdpa_paged_forward(
-            q.data_ptr(), o.data_ptr(), ls.data_ptr() if ls is not None else None, dt, cache._ref, total, heads, at,
-            at + 16, at + 32, page_table.data_ptr(), page_table.stride(0), max_pages, kv_lens.data_ptr(),
-            cu_seqlens_q.data_ptr() if cu_seqlens_q is not None else None, n_seqs, max_seqlen_q,
-            1 if is_causal else 0, math.nan if scale is None else scale, work.data_ptr(), size, st)
+        args = (q.data_ptr(), o.data_ptr(), ls.data_ptr() if ls is not None else None, dt, cache._ref, total, heads, at,
+                at + 16, at + 32, page_table.data_ptr(), page_table.stride(0), max_pages, kv_lens.data_ptr(),
+                cu_seqlens_q.data_ptr() if cu_seqlens_q is not None else None, n_seqs, max_seqlen_q)
+        tail = (math.nan if scale is None else scale, work.data_ptr(), size, st)
+        if window is None:
+            rc = lib.sdpa_paged_forward(*args, 1 if is_causal else 0, *tail)
+        else:
+            rc = lib.sdpa_paged_forward_window(*args, min(window, _I64_MAX), min(sinks, _I64_MAX), *tail)
         if rc != 0:
             raise SdpaError(rc, where)
         return o if ls is None else (o, ls)

@@ -95,8 +95,27 @@ __device__ __forceinline__ int unit_keys(const PagedParams& p, const Seq& s, int
   const int last = by_G(p, min((t + 1) * rt, s.nq * p.G) - 1);
   return min(max(s.len - s.nq + last + 1, 0), s.len);
 }
+// With a window (WIN, causal): first key of the window of tile t's first row, which
+// reaches back the farthest.  The unit's rows see no key between the sinks and it.
+__device__ __forceinline__ int unit_from(const PagedParams& p, const Seq& s, int t, int rt) {
+  const int seen = min(max(s.len - s.nq + by_G(p, t * rt) + 1, 0), s.len);
+  return max(seen - p.window, 0);
+}
+// Steps without a key that the unit's rows see, between the sinks' steps and the
+// window's: step s of the unit stands for run step_run(..) of its keys.
+template <bool WIN>
+__device__ __forceinline__ int unit_skip(const PagedParams& p, const Seq& s, int t, int rt) {
+  if constexpr (!WIN) return 0;
+  return max((unit_from(p, s, t, rt) >> p.step_shift) - p.sink_steps, 0);
+}
+template <bool WIN>
+__device__ __forceinline__ int step_run(const PagedParams& p, int skip, int s) {
+  if constexpr (!WIN) return s;
+  return s < p.sink_steps ? s : s + skip;
+}
+template <bool WIN>
 __device__ __forceinline__ int unit_steps(const PagedParams& p, const Seq& s, int t, int rt) {
-  return max((unit_keys(p, s, t, rt) + (1 << p.step_shift) - 1) >> p.step_shift, 1);
+  return max(((unit_keys(p, s, t, rt) + (1 << p.step_shift) - 1) >> p.step_shift) - unit_skip<WIN>(p, s, t, rt), 1);
 }
 
 // A position in the division: unit (b, h, t) (h: the group of heads), whose
@@ -130,7 +149,7 @@ __device__ __forceinline__ int range_start(int total, int i, int n) {
 // block calls it.  A group of W lanes adds up a sequence's units, as many
 // sequences at a time as the block has groups; a batch of at most that many is
 // read once.
-template <int NT, class At>
+template <int NT, bool WIN, class At>
 __device__ __forceinline__ int divide(const PagedParams& p, int rt, DivideScratch* sc, At&& at, int& total,
                                       Cursor& c) {
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -148,10 +167,10 @@ __device__ __forceinline__ int divide(const PagedParams& p, int rt, DivideScratc
     if (b < p.n_seqs) {
       seq = load_seq(p, b, rt);
       if (!p.is_causal)
-        mine = seq.nt == 0 ? 0 : seq.nt * unit_steps(p, seq, 0, rt);
+        mine = seq.nt == 0 ? 0 : seq.nt * unit_steps<WIN>(p, seq, 0, rt);
       else
 #pragma unroll 1
-        for (int t = sub; t < seq.nt; t += w) mine += unit_steps(p, seq, t, rt);
+        for (int t = sub; t < seq.nt; t += w) mine += unit_steps<WIN>(p, seq, t, rt);
     }
     for (int o = 1; o < w; o <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     incl = sub == 0 ? mine * p.n_groups : 0;
@@ -197,7 +216,7 @@ __device__ __forceinline__ int divide(const PagedParams& p, int rt, DivideScratc
   c.t = 0;
 #pragma unroll 1
   while (c.s.nt > 1) {
-    const int n = c.t + lane < c.s.nt ? unit_steps(p, c.s, c.t + lane, rt) : 0;
+    const int n = c.t + lane < c.s.nt ? unit_steps<WIN>(p, c.s, c.t + lane, rt) : 0;
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -218,8 +237,9 @@ __device__ __forceinline__ int divide(const PagedParams& p, int rt, DivideScratc
 }
 
 // The next unit (its steps begin where this one's end).
+template <bool WIN>
 __device__ __forceinline__ void advance(const PagedParams& p, int rt, Cursor& c) {
-  c.u0 += unit_steps(p, c.s, c.t, rt);
+  c.u0 += unit_steps<WIN>(p, c.s, c.t, rt);
   if (++c.t < c.s.nt) return;
   c.t = 0;
   if (++c.h < p.n_groups) return;
@@ -251,10 +271,11 @@ __device__ __forceinline__ float* part_rows(const PagedParams& p, int i, int slo
 
 // CTA i's note: its last unit, if that begins here (with its first or a later
 // segment) and goes on behind its range.
+template <bool WIN>
 __device__ __forceinline__ void leave_note(const PagedParams& p, int i, int total, int n, int rt,
                                            const Cursor& c, int s0, int s1, bool first) {
   JoinNote j{};
-  const int steps = unit_steps(p, c.s, c.t, rt);
+  const int steps = unit_steps<WIN>(p, c.s, c.t, rt);
   if (s0 == 0 && s1 < steps) {
     // the range that holds the unit's last step
     const long long last = (static_cast<long long>(c.u0 + steps) * n - 1) / total;

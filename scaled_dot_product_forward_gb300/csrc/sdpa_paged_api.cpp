@@ -165,6 +165,139 @@ uint64_t workspace_bytes(const sdpa_impl::PagedForm& f, int64_t head_dim) {
          (sdpa_impl::kJoinNoteBytes + 2u * static_cast<uint64_t>(f.heads) * static_cast<uint64_t>(f.rows) * static_cast<uint64_t>(head_dim + 2) * 4u);
 }
 
+// window 0: every key (up to the causal limit).
+sdpa_status paged_forward(const void* q, void* out, float* lse, sdpa_dtype dtype, const sdpa_paged_cache* cache, int64_t total_q,
+                          int64_t n_heads, const int64_t* q_stride, const int64_t* o_stride, const int64_t* lse_stride,
+                          const int32_t* page_table, int64_t page_table_stride, int64_t max_pages, const int32_t* kv_lens,
+                          const int32_t* cu_seqlens_q, int64_t n_seqs, int64_t max_seqlen_q, int is_causal, int64_t window,
+                          int64_t sinks, float scale, void* workspace, uint64_t workspace_size, void* stream) {
+  sdpa_status s = check_cache(cache, dtype);
+  if (s != SDPA_OK) return s;
+  if (!q || !out || !q_stride || !o_stride || !workspace || (lse && !lse_stride)) return SDPA_ERR_NULL;
+  if ((s = check_batch(cache, total_q, page_table, page_table_stride, max_pages, kv_lens, cu_seqlens_q,
+                       n_seqs)) != SDPA_OK)
+    return s;
+  const int64_t D = cache->head_dim, hkv = cache->n_kv_heads;
+  if (n_heads < 1 || n_heads % hkv != 0 || max_seqlen_q < 1) return SDPA_ERR_SHAPE;
+  const int64_t G = n_heads / hkv;
+  if (total_q > (kIntMax - 1024) / G || max_pages * cache->page_size > kIntMax - 4096) return SDPA_ERR_SHAPE;
+  Rows rq, ro;
+  if ((s = check_rows(q, total_q, n_heads, D, q_stride, &rq)) != SDPA_OK) return s;
+  if ((s = check_rows(out, total_q, n_heads, D, o_stride, &ro)) != SDPA_OK) return s;
+  if (!aligned(workspace, 16)) return SDPA_ERR_LAYOUT;
+  Block ls;
+  int64_t lt = 0, lh = 0;
+  if (lse) {
+    lt = total_q > 1 ? lse_stride[0] : 0;
+    lh = n_heads > 1 ? lse_stride[1] : 0;
+    if (!aligned(lse, 4) || (total_q > 1 && lt <= 0) || (n_heads > 1 && lh <= 0)) return SDPA_ERR_LAYOUT;
+    if (lt >= (int64_t(1) << 38) || lh >= (int64_t(1) << 38)) return SDPA_ERR_LAYOUT;
+    ls = block_of(lse, 4);
+    ls.add(total_q, 4 * lt), ls.add(n_heads, 4 * lh);
+  }
+  if (std::isinf(scale)) return SDPA_ERR_ARG;
+  const bool e4m3 = cache->elem == SDPA_CACHE_E4M3;
+  {
+    const uint64_t sb = 4ull * static_cast<uint64_t>(cache->n_pages) * static_cast<uint64_t>(hkv);
+    const Block ins[8] = {rq.block(),
+                          cache_block(cache, cache->k, cache->k_stride),
+                          cache_block(cache, cache->v, cache->v_stride),
+                          block_of(e4m3 ? cache->k_scale : nullptr, sb),
+                          block_of(e4m3 ? cache->v_scale : nullptr, sb),
+                          block_of(page_table, 4ull * static_cast<uint64_t>((n_seqs - 1) * page_table_stride + max_pages)),
+                          block_of(kv_lens, 4ull * static_cast<uint64_t>(n_seqs)),
+                          block_of(cu_seqlens_q, 4ull * static_cast<uint64_t>(n_seqs + 1))};
+    const Block outs[3] = {ro.block(), ls, block_of(workspace, workspace_size)};
+    for (const Block& o : outs)
+      for (const Block& i : ins)
+        if (overlap(o, i)) return SDPA_ERR_ARG;
+    if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2])) return SDPA_ERR_ARG;
+  }
+  int dev = 0, sms = 0;
+  s = static_cast<sdpa_status>(sdpa_impl::current_device(&dev, &sms));
+  if (s != SDPA_OK) return s;
+  const int64_t max_rows = (max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
+  const sdpa_impl::PagedForm form = sdpa_impl::paged_form(max_rows, static_cast<int>(D), e4m3, hkv, sms);
+  {
+    // the kernels count their steps in 31 bits
+    const double units = static_cast<double>(total_q) * static_cast<double>(G) / form.rows + static_cast<double>(n_seqs);
+    const double steps = static_cast<double>((max_pages * cache->page_size) >> form.step_shift) + 1.0;
+    if (units * static_cast<double>(hkv / form.heads) * steps > 2.0e9) return SDPA_ERR_SHAPE;
+  }
+  if (workspace_size < workspace_bytes(form, D)) return SDPA_ERR_ARG;
+  sdpa_impl::PagedParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.q_st = rq.st, p.q_sh = rq.sh;
+  p.out = out;
+  p.o_st = ro.st, p.o_sh = ro.sh;
+  p.out_sectors = aligned(out, 32) && ro.st % 16 == 0 && ro.sh % 16 == 0;
+  p.lse = lse;
+  p.lse_st = lt, p.lse_sh = lh;
+  p.k = static_cast<const uint8_t*>(cache->k);
+  p.v = static_cast<const uint8_t*>(cache->v);
+  byte_strides(cache, cache->k_stride, &p.k_sp, &p.k_st, &p.k_sh);
+  byte_strides(cache, cache->v_stride, &p.v_sp, &p.v_st, &p.v_sh);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.table = page_table;
+  p.table_st = n_seqs > 1 ? page_table_stride : 0;
+  p.kv_lens = kv_lens;
+  p.cu = cu_seqlens_q;
+  p.total_q = static_cast<int>(total_q);
+  p.n_seqs = static_cast<int>(n_seqs);
+  p.n_kv = static_cast<int>(hkv);
+  p.G = static_cast<int>(G);
+  // m = floor(2^(31+s) / G) + 1 with 2^s >= G: n m is off from n 2^(31+s) / G by
+  // at most n < 2^31 parts of G <= 2^s, too little to reach the next multiple
+  p.g_shift = 31;
+  while ((int64_t(1) << (p.g_shift - 31)) < G) ++p.g_shift;
+  p.g_mul = static_cast<unsigned int>((uint64_t(1) << p.g_shift) / static_cast<uint64_t>(G) + 1);
+  p.seq_q = static_cast<int>(total_q / n_seqs);
+  p.n_pages = static_cast<int>(cache->n_pages);
+  p.max_len = static_cast<int>(max_pages * cache->page_size);
+  p.page_shift = log2_of(cache->page_size);
+  p.is_causal = is_causal ? 1 : 0;
+  // (a window over all that the tables hold is none: the same keys, the same kernel)
+  p.window = window < p.max_len ? static_cast<int>(window) : 0;
+  p.sinks = static_cast<int>(sinks < p.max_len ? sinks : p.max_len);
+  const double sc = std::isnan(scale) ? 1.0 / std::sqrt(static_cast<double>(D)) : static_cast<double>(scale);
+  p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);  // log2(e)
+  p.part = static_cast<float*>(workspace);
+  p.n_ctas = form.ctas;
+  p.max_rows = static_cast<int>(max_rows);
+  p.unit_heads = form.heads;
+  p.n_groups = static_cast<int>(hkv) / form.heads;
+  p.step_shift = form.step_shift;
+  p.sink_steps = (p.sinks + (1 << p.step_shift) - 1) >> p.step_shift;
+  p.min_steps = form.min_steps;
+  p.min_steps_shift = log2_of(form.min_steps);
+  p.device = dev;
+  cudaError_t e;
+  if (form.tc) {
+    // a zero scale: the smallest normal multiplier rounds every finite score
+    // to 0 and keeps a removed one infinite (its sign does not matter)
+    if (p.scale_log2 == 0.0f) p.scale_log2 = FLT_MIN;
+    p.debug_withhold_q = sdpa_impl::withhold_q();
+    p.wait_limit_ns = sdpa_impl::wait_limit_ns();
+    CUtensorMap tm_k, tm_v;
+    const int64_t ext[4] = {D, cache->page_size, hkv, cache->n_pages};
+    const int64_t ks[3] = {p.k_st, p.k_sh, p.k_sp}, vs[3] = {p.v_st, p.v_sh, p.v_sp};
+    const int box = static_cast<int>(cache->page_size < 128 ? cache->page_size : 128);
+    const bool bf16 = dtype == SDPA_BF16;
+    s = static_cast<sdpa_status>(sdpa_impl::encode_pages(cache->k, e4m3, bf16, ext, ks, box,
+                                                         e4m3 ? static_cast<int>(D) : 128, &tm_k));
+    if (s == SDPA_OK)
+      s = static_cast<sdpa_status>(sdpa_impl::encode_pages(cache->v, e4m3, bf16, ext, vs, box, e4m3 ? 0 : 128, &tm_v));
+    if (s != SDPA_OK) return s;
+    e = sdpa_impl::launch_paged_tc(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, form.rows, tm_k, tm_v,
+                                   static_cast<cudaStream_t>(stream));
+  } else {
+    e = sdpa_impl::launch_paged(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, static_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -297,127 +430,24 @@ sdpa_status sdpa_paged_forward(const void* q, void* out, float* lse, sdpa_dtype 
                                const int32_t* kv_lens, const int32_t* cu_seqlens_q,
                                int64_t n_seqs, int64_t max_seqlen_q, int is_causal, float scale,
                                void* workspace, uint64_t workspace_size, void* stream) {
-  sdpa_status s = check_cache(cache, dtype);
-  if (s != SDPA_OK) return s;
-  if (!q || !out || !q_stride || !o_stride || !workspace || (lse && !lse_stride)) return SDPA_ERR_NULL;
-  if ((s = check_batch(cache, total_q, page_table, page_table_stride, max_pages, kv_lens, cu_seqlens_q,
-                       n_seqs)) != SDPA_OK)
-    return s;
-  const int64_t D = cache->head_dim, hkv = cache->n_kv_heads;
-  if (n_heads < 1 || n_heads % hkv != 0 || max_seqlen_q < 1) return SDPA_ERR_SHAPE;
-  const int64_t G = n_heads / hkv;
-  if (total_q > (kIntMax - 1024) / G || max_pages * cache->page_size > kIntMax - 4096) return SDPA_ERR_SHAPE;
-  Rows rq, ro;
-  if ((s = check_rows(q, total_q, n_heads, D, q_stride, &rq)) != SDPA_OK) return s;
-  if ((s = check_rows(out, total_q, n_heads, D, o_stride, &ro)) != SDPA_OK) return s;
-  if (!aligned(workspace, 16)) return SDPA_ERR_LAYOUT;
-  Block ls;
-  int64_t lt = 0, lh = 0;
-  if (lse) {
-    lt = total_q > 1 ? lse_stride[0] : 0;
-    lh = n_heads > 1 ? lse_stride[1] : 0;
-    if (!aligned(lse, 4) || (total_q > 1 && lt <= 0) || (n_heads > 1 && lh <= 0)) return SDPA_ERR_LAYOUT;
-    if (lt >= (int64_t(1) << 38) || lh >= (int64_t(1) << 38)) return SDPA_ERR_LAYOUT;
-    ls = block_of(lse, 4);
-    ls.add(total_q, 4 * lt), ls.add(n_heads, 4 * lh);
-  }
-  if (std::isinf(scale)) return SDPA_ERR_ARG;
-  const bool e4m3 = cache->elem == SDPA_CACHE_E4M3;
-  {
-    const uint64_t sb = 4ull * static_cast<uint64_t>(cache->n_pages) * static_cast<uint64_t>(hkv);
-    const Block ins[8] = {rq.block(),
-                          cache_block(cache, cache->k, cache->k_stride),
-                          cache_block(cache, cache->v, cache->v_stride),
-                          block_of(e4m3 ? cache->k_scale : nullptr, sb),
-                          block_of(e4m3 ? cache->v_scale : nullptr, sb),
-                          block_of(page_table, 4ull * static_cast<uint64_t>((n_seqs - 1) * page_table_stride + max_pages)),
-                          block_of(kv_lens, 4ull * static_cast<uint64_t>(n_seqs)),
-                          block_of(cu_seqlens_q, 4ull * static_cast<uint64_t>(n_seqs + 1))};
-    const Block outs[3] = {ro.block(), ls, block_of(workspace, workspace_size)};
-    for (const Block& o : outs)
-      for (const Block& i : ins)
-        if (overlap(o, i)) return SDPA_ERR_ARG;
-    if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2])) return SDPA_ERR_ARG;
-  }
-  int dev = 0, sms = 0;
-  s = static_cast<sdpa_status>(sdpa_impl::current_device(&dev, &sms));
-  if (s != SDPA_OK) return s;
-  const int64_t max_rows = (max_seqlen_q < total_q ? max_seqlen_q : total_q) * G;
-  const sdpa_impl::PagedForm form = sdpa_impl::paged_form(max_rows, static_cast<int>(D), e4m3, hkv, sms);
-  {
-    // the kernels count their steps in 31 bits
-    const double units = static_cast<double>(total_q) * static_cast<double>(G) / form.rows + static_cast<double>(n_seqs);
-    const double steps = static_cast<double>((max_pages * cache->page_size) >> form.step_shift) + 1.0;
-    if (units * static_cast<double>(hkv / form.heads) * steps > 2.0e9) return SDPA_ERR_SHAPE;
-  }
-  if (workspace_size < workspace_bytes(form, D)) return SDPA_ERR_ARG;
-  sdpa_impl::PagedParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.q = q;
-  p.q_st = rq.st, p.q_sh = rq.sh;
-  p.out = out;
-  p.o_st = ro.st, p.o_sh = ro.sh;
-  p.out_sectors = aligned(out, 32) && ro.st % 16 == 0 && ro.sh % 16 == 0;
-  p.lse = lse;
-  p.lse_st = lt, p.lse_sh = lh;
-  p.k = static_cast<const uint8_t*>(cache->k);
-  p.v = static_cast<const uint8_t*>(cache->v);
-  byte_strides(cache, cache->k_stride, &p.k_sp, &p.k_st, &p.k_sh);
-  byte_strides(cache, cache->v_stride, &p.v_sp, &p.v_st, &p.v_sh);
-  p.k_scale = cache->k_scale;
-  p.v_scale = cache->v_scale;
-  p.table = page_table;
-  p.table_st = n_seqs > 1 ? page_table_stride : 0;
-  p.kv_lens = kv_lens;
-  p.cu = cu_seqlens_q;
-  p.total_q = static_cast<int>(total_q);
-  p.n_seqs = static_cast<int>(n_seqs);
-  p.n_kv = static_cast<int>(hkv);
-  p.G = static_cast<int>(G);
-  // m = floor(2^(31+s) / G) + 1 with 2^s >= G: n m is off from n 2^(31+s) / G by
-  // at most n < 2^31 parts of G <= 2^s, too little to reach the next multiple
-  p.g_shift = 31;
-  while ((int64_t(1) << (p.g_shift - 31)) < G) ++p.g_shift;
-  p.g_mul = static_cast<unsigned int>((uint64_t(1) << p.g_shift) / static_cast<uint64_t>(G) + 1);
-  p.seq_q = static_cast<int>(total_q / n_seqs);
-  p.n_pages = static_cast<int>(cache->n_pages);
-  p.max_len = static_cast<int>(max_pages * cache->page_size);
-  p.page_shift = log2_of(cache->page_size);
-  p.is_causal = is_causal ? 1 : 0;
-  const double sc = std::isnan(scale) ? 1.0 / std::sqrt(static_cast<double>(D)) : static_cast<double>(scale);
-  p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);  // log2(e)
-  p.part = static_cast<float*>(workspace);
-  p.n_ctas = form.ctas;
-  p.max_rows = static_cast<int>(max_rows);
-  p.unit_heads = form.heads;
-  p.n_groups = static_cast<int>(hkv) / form.heads;
-  p.step_shift = form.step_shift;
-  p.min_steps = form.min_steps;
-  p.min_steps_shift = log2_of(form.min_steps);
-  p.device = dev;
-  cudaError_t e;
-  if (form.tc) {
-    // a zero scale: the smallest normal multiplier rounds every finite score
-    // to 0 and keeps a removed one infinite (its sign does not matter)
-    if (p.scale_log2 == 0.0f) p.scale_log2 = FLT_MIN;
-    p.debug_withhold_q = sdpa_impl::withhold_q();
-    p.wait_limit_ns = sdpa_impl::wait_limit_ns();
-    CUtensorMap tm_k, tm_v;
-    const int64_t ext[4] = {D, cache->page_size, hkv, cache->n_pages};
-    const int64_t ks[3] = {p.k_st, p.k_sh, p.k_sp}, vs[3] = {p.v_st, p.v_sh, p.v_sp};
-    const int box = static_cast<int>(cache->page_size < 128 ? cache->page_size : 128);
-    const bool bf16 = dtype == SDPA_BF16;
-    s = static_cast<sdpa_status>(sdpa_impl::encode_pages(cache->k, e4m3, bf16, ext, ks, box,
-                                                         e4m3 ? static_cast<int>(D) : 128, &tm_k));
-    if (s == SDPA_OK)
-      s = static_cast<sdpa_status>(sdpa_impl::encode_pages(cache->v, e4m3, bf16, ext, vs, box, e4m3 ? 0 : 128, &tm_v));
-    if (s != SDPA_OK) return s;
-    e = sdpa_impl::launch_paged_tc(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, form.rows, tm_k, tm_v,
-                                   static_cast<cudaStream_t>(stream));
-  } else {
-    e = sdpa_impl::launch_paged(p, static_cast<int>(D), dtype == SDPA_BF16, e4m3, static_cast<cudaStream_t>(stream));
-  }
-  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+  return paged_forward(q, out, lse, dtype, cache, total_q, n_heads, q_stride, o_stride, lse_stride, page_table, page_table_stride,
+                       max_pages, kv_lens, cu_seqlens_q, n_seqs, max_seqlen_q, is_causal, 0, 0, scale, workspace, workspace_size,
+                       stream);
+}
+
+sdpa_status sdpa_paged_forward_window(const void* q, void* out, float* lse, sdpa_dtype dtype,
+                                      const sdpa_paged_cache* cache, int64_t total_q, int64_t n_heads,
+                                      const int64_t* q_stride, const int64_t* o_stride,
+                                      const int64_t* lse_stride, const int32_t* page_table,
+                                      int64_t page_table_stride, int64_t max_pages,
+                                      const int32_t* kv_lens, const int32_t* cu_seqlens_q,
+                                      int64_t n_seqs, int64_t max_seqlen_q, int64_t window,
+                                      int64_t sinks, float scale, void* workspace,
+                                      uint64_t workspace_size, void* stream) {
+  if (window < 1 || sinks < 0) return SDPA_ERR_ARG;
+  return paged_forward(q, out, lse, dtype, cache, total_q, n_heads, q_stride, o_stride, lse_stride, page_table, page_table_stride,
+                       max_pages, kv_lens, cu_seqlens_q, n_seqs, max_seqlen_q, 1, window, sinks, scale, workspace, workspace_size,
+                       stream);
 }
 
 }  // extern "C"

@@ -162,7 +162,7 @@ __device__ __forceinline__ void store_out4(uint16_t* at, const float4& o, float 
   *reinterpret_cast<uint2*>(at) = make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
 }
 
-template <int D, bool E4M3, bool BF16>
+template <int D, bool E4M3, bool BF16, bool WIN>
 __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
     paged_kernel(const __grid_constant__ PagedParams p) {
   using S = Smem<D, E4M3>;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
   const int cta = static_cast<int>(blockIdx.x);
   int total;
   Cursor c;
-  int v = divide<kThreads>(
+  int v = divide<kThreads, WIN>(
       p, RT, sc,
       [&](int all) {
         const int n = range_count(p, all);
@@ -217,12 +217,16 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
     const uint8_t *kh, *vh;
     int64_t scale_at;
     int s0, s1, keys, len;
+    int skip, from;              // WIN: steps left out, first key of the rows' windows
     int ids_at, ids, ids_next;   // lane i: the page entry of step ids_at + i
   };
-  auto key_of = [&](int s) { return (s << p.step_shift) + slice * kWarpKeys; };
+  auto key_of = [&](int skip, int s) { return (step_run<WIN>(p, skip, s) << p.step_shift) + slice * kWarpKeys; };
+  // (16 keys that no row sees may lie in a page that is gone: they are taken for
+  // keys without a page)
   auto load_ids = [&](const Loads& a, int s) {
-    const int key0 = key_of(s + lane);
-    return (s + lane < a.s1 && key0 < a.keys) ? __ldg(a.trow + (key0 >> p.page_shift)) : -1;
+    const int key0 = key_of(a.skip, s + lane);
+    const bool seen = !WIN || key0 + kWarpKeys > a.from || key0 < p.sinks;
+    return (s + lane < a.s1 && key0 < a.keys && seen) ? __ldg(a.trow + (key0 >> p.page_shift)) : -1;
   };
   auto issue = [&](Loads& a, int s, int stage) {
     if (s < a.s1) {
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
         a.ids_next = load_ids(a, a.ids_at + 32);
       }
       const int page = __shfl_sync(0xffffffffu, a.ids, s - a.ids_at);
-      const int key0 = key_of(s);
+      const int key0 = key_of(a.skip, s);
       const bool ok = page >= 0 && page < p.n_pages;
       const int64_t pg = ok ? page : 0;
       const int tok = key0 & page_mask;
@@ -283,7 +287,9 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
     a.keys = unit_keys(p, cu.s, cu.t, RT);
     a.len = cu.s.len;
     a.s0 = from - cu.u0;
-    a.s1 = min(unit_steps(p, cu.s, cu.t, RT), v_end - cu.u0);
+    a.s1 = min(unit_steps<WIN>(p, cu.s, cu.t, RT), v_end - cu.u0);
+    a.skip = unit_skip<WIN>(p, cu.s, cu.t, RT);
+    a.from = WIN ? unit_from(p, cu.s, cu.t, RT) : 0;
     a.ids_at = a.s0;
     a.ids = load_ids(a, a.s0);
     a.ids_next = load_ids(a, a.s0 + 32);
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
   bool first_segment = true;
   while (true) {
     const int s0 = ld.s0, s1 = ld.s1, keys = ld.keys;
-    const bool whole = s0 == 0 && s1 == unit_steps(p, c.s, c.t, RT);
+    const bool whole = s0 == 0 && s1 == unit_steps<WIN>(p, c.s, c.t, RT);
     const int rows = min(RT, c.s.nq * p.G - c.t * RT);
     const int head = c.h * p.unit_heads + hsub;
 
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
     uint32_t qf[NK][4];
     float mul[2];
     int lim[2];
-    int lim_min = keys;
+    int lim_min = keys, lim_max = 0;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const int r = hf * 8 + g8;
@@ -314,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
       const int i = by_G(p, rr), g = rr - i * p.G;
       lim[hf] = live ? (p.is_causal ? min(max(c.s.len - c.s.nq + i + 1, 0), c.s.len) : c.s.len) : 0;
       if (live) lim_min = min(lim_min, lim[hf]);
+      if (WIN) lim_max = max(lim_max, lim[hf]);
       const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) +
                             (static_cast<int64_t>(c.s.q0) + i) * p.q_st +
                             (static_cast<int64_t>(head) * p.G + g) * p.q_sh;
@@ -353,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
       }
     }
     lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+    if (WIN) lim_max = __reduce_max_sync(0xffffffffu, lim_max);
 
     float o[NV][4];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
       cp_async_wait<R::kStages - 2>();
       __syncwarp();
       issue(ld, s + R::kStages - 1, stage == 0 ? R::kStages - 1 : stage - 1);
-      const int key0 = key_of(s);
+      const int key0 = key_of(ld.skip, s);
       if (key0 < keys && notes->ok[stage] != 0) {
         const uint8_t* kt = ring + stage * 2 * R::kTile;
         const uint8_t* vt = kt + R::kTile;
@@ -414,13 +422,15 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
           y[0] = fmaf(y[0], f, lv);
           y[1] = fmaf(y[1], f, lv);
         }
-        if (key0 + kWarpKeys > lim_min) {
+        if (key0 + kWarpKeys > lim_min || (WIN && key0 < lim_max - p.window && key0 + kWarpKeys > p.sinks)) {
           // some row does not see some of these keys
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key0 + n * 8 + t4 * 2 + (e & 1) >= lim[e >> 1]) acc[n][e] = -INFINITY;
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + n * 8 + t4 * 2 + (e & 1);
+              if (key >= lim[e >> 1] || (WIN && key < lim[e >> 1] - p.window && key >= p.sinks)) acc[n][e] = -INFINITY;
+            }
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
@@ -516,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
     if (!more) grid_launch_dependents();
     Cursor next = c;
     if (more) {
-      advance(p, RT, next);
+      advance<WIN>(p, RT, next);
       if (slices == 1) ld = open(next, v_next);
     } else if (threadIdx.x == 0) {
-      leave_note(p, cta, total, n_ranges, RT, c, s0, s1, first_segment);
+      leave_note<WIN>(p, cta, total, n_ranges, RT, c, s0, s1, first_segment);
     }
 
     // Accumulator columns 2 t4 and 2 t4 + 1 of group j are elements j of the
@@ -708,10 +718,10 @@ cudaError_t launch_join(const PagedParams& p, int rt, cudaStream_t stream) {
                     0, stream, p, rt);
 }
 
-template <int D, bool E4M3, bool BF16>
+template <int D, bool E4M3, bool BF16, bool WIN>
 cudaError_t launch_one(const PagedParams& p, cudaStream_t stream) {
   using S = Smem<D, E4M3>;
-  auto kern = paged_kernel<D, E4M3, BF16>;
+  auto kern = paged_kernel<D, E4M3, BF16, WIN>;
   static std::atomic<uint64_t> configured{0};  // a bit a device
   const uint64_t bit = 1ull << p.device;
   cudaError_t e = cudaSuccess;
@@ -725,10 +735,10 @@ cudaError_t launch_one(const PagedParams& p, cudaStream_t stream) {
   return launch_join<D, BF16>(p, RT, stream);
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_dim(const PagedParams& p, bool bf16, bool e4m3, cudaStream_t s) {
-  if (e4m3) return bf16 ? launch_one<D, true, true>(p, s) : launch_one<D, true, false>(p, s);
-  return bf16 ? launch_one<D, false, true>(p, s) : launch_one<D, false, false>(p, s);
+  if (e4m3) return bf16 ? launch_one<D, true, true, WIN>(p, s) : launch_one<D, true, false, WIN>(p, s);
+  return bf16 ? launch_one<D, false, true, WIN>(p, s) : launch_one<D, false, false, WIN>(p, s);
 }
 
 }  // namespace
@@ -736,7 +746,9 @@ cudaError_t launch_dim(const PagedParams& p, bool bf16, bool e4m3, cudaStream_t 
 namespace sdpa_impl {
 
 cudaError_t launch_paged(const PagedParams& p, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
-  return head_dim == 64 ? launch_dim<64>(p, bf16, e4m3, stream) : launch_dim<128>(p, bf16, e4m3, stream);
+  if (p.window != 0)
+    return head_dim == 64 ? launch_dim<64, true>(p, bf16, e4m3, stream) : launch_dim<128, true>(p, bf16, e4m3, stream);
+  return head_dim == 64 ? launch_dim<64, false>(p, bf16, e4m3, stream) : launch_dim<128, false>(p, bf16, e4m3, stream);
 }
 
 cudaError_t launch_paged_join(const PagedParams& p, int head_dim, bool bf16, int rt, cudaStream_t stream) {

@@ -188,10 +188,10 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
-template <int RT>
+template <int RT, bool WIN>
 __device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor& c, int v, int v_end,
                                               bool first) {
-  const int steps = unit_steps(p, c.s, c.t, RT);
+  const int steps = unit_steps<WIN>(p, c.s, c.t, RT);
   Segment g;
   g.s0 = v - c.u0;
   g.s1 = min(steps, v_end - c.u0);
@@ -204,16 +204,16 @@ __device__ __forceinline__ Segment segment_of(const PagedParams& p, const Cursor
 
 // Calls f(cursor, segment) for the CTA's segments in order until it returns
 // false.
-template <int RT, class F>
+template <int RT, bool WIN, class F>
 __device__ __forceinline__ void for_each_segment(const PagedParams& p, Cursor c, int v,
                                                  int v_end, F&& f) {
   bool first = true;
   while (v < v_end) {
-    const Segment g = segment_of<RT>(p, c, v, v_end, first);
+    const Segment g = segment_of<RT, WIN>(p, c, v, v_end, first);
     if (!f(c, g)) return;
     first = false;
     v = c.u0 + g.s1;
-    if (v < v_end) advance(p, RT, c);
+    if (v < v_end) advance<WIN>(p, RT, c);
   }
 }
 
@@ -550,7 +550,7 @@ __device__ __forceinline__ void mma_codes_x2(uint32_t d_tmem, uint32_t a_lo, uin
       : "memory");
 }
 
-template <int D, bool E4M3, bool BF16, bool HALF>
+template <int D, bool E4M3, bool BF16, bool HALF, bool WIN>
 __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v) {
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
   const int cta = static_cast<int>(blockIdx.x);
   int total;
   Cursor c0{};
-  const int v0 = divide<Split<E4M3>::kThreads>(
+  const int v0 = divide<Split<E4M3>::kThreads, WIN>(
       p, RT, reinterpret_cast<DivideScratch*>(sQ),
       [&](int all) {
         const int n = range_count(p, all);
@@ -674,24 +674,26 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     };
     save(c0, v0);
     bool first = true;
-    if (v0 < v1) ask(c0, segment_of<RT>(p, c0, v0, v1, true));
+    if (v0 < v1) ask(c0, segment_of<RT, WIN>(p, c0, v0, v1, true));
     for (bool ok = v0 < v1; ok;) {
       float f = 0.0f;
-      int seen, s0, s1;
+      int seen, s0, s1, skip;
       bool split, idle;
       {
         Cursor c;
         int v, v_end;
         load(c, v, v_end);
-        const Segment g = segment_of<RT>(p, c, v, v_end, first);
+        const Segment g = segment_of<RT, WIN>(p, c, v, v_end, first);
         s0 = g.s0, s1 = g.s1, split = HALF || g.split;
+        skip = unit_skip<WIN>(p, c.s, c.t, RT);
         const int ru = row_of(g);
         int64_t token, head;
-        const int tok = place(c, ru, token, head);
         // rows that the unit has not: nothing of theirs is removed (a removed
-        // key costs the whole warp), and a warp of them alone only keeps step
+        // key costs the whole warp; with a window, what is removed for the last
+        // row), and a warp of them alone only keeps step
+        const int tok = place(c, WIN ? min(ru, g.rows - 1) : ru, token, head);
         idle = ru - (HALF ? lane & 15 : lane) >= g.rows;
-        seen = ru >= g.rows ? 0x7fffffff : p.is_causal ? min(max(c.s.len - c.s.nq + tok + 1, 0), c.s.len) : c.s.len;
+        seen = !WIN && ru >= g.rows ? 0x7fffffff : p.is_causal ? min(max(c.s.len - c.s.nq + tok + 1, 0), c.s.len) : c.s.len;
         cp_async_wait<0>();
         if (!idle) {
           __syncwarp();
@@ -735,8 +737,12 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kPer; ++i) x[i] = __uint_as_float(u[i]);
         }
-        const int left = seen - s * KT;   // keys of this tile that the row sees
-        if (__any_sync(0xffffffffu, left < KT) || bad != 0u) {
+        // keys of this tile that the row sees, and with a window the first ones that
+        // lie before it, but for the sinks
+        const int tile0 = step_run<WIN>(p, skip, s) * KT;
+        const int left = seen - tile0;
+        const bool cut = WIN && left > p.window && tile0 + KT > p.sinks;
+        if (__any_sync(0xffffffffu, left < KT || cut) || bad != 0u) {
           const int mine_left = left - half * kPer;
           const uint32_t mine_bad = bad >> (half * (kPer / 16));
           uint32_t keep[kPer / 32];
@@ -744,6 +750,14 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
           for (int i = 0; i < kPer / 32; ++i) {
             const int n = min(max(mine_left - 32 * i, 0), 32);
             keep[i] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+            if constexpr (WIN) {
+              // (left is at least -KT here: what lies further makes no difference)
+              const int b = min(max(max(mine_left, -KT) - p.window - 32 * i, 0), 32);
+              const int c = min(max(p.sinks - tile0 - half * kPer - 32 * i, 0), 32);
+              const uint32_t before = b == 32 ? 0xffffffffu : (1u << b) - 1u;
+              const uint32_t stay = c == 32 ? 0xffffffffu : (1u << c) - 1u;
+              keep[i] &= ~before | stay;
+            }
             if ((mine_bad >> (2 * i)) & 1u) keep[i] &= 0xffff0000u;
             if ((mine_bad >> (2 * i)) & 2u) keep[i] &= 0x0000ffffu;
           }
@@ -779,13 +793,13 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       Cursor c;
       int v, v_end;
       load(c, v, v_end);
-      const Segment g = segment_of<RT>(p, c, v, v_end, first);
+      const Segment g = segment_of<RT, WIN>(p, c, v, v_end, first);
       Cursor next = c;
       const int v_next = c.u0 + g.s1;
       if (v_next < v_end) {
-        advance(p, RT, next);
+        advance<WIN>(p, RT, next);
         // its query, while this one's rows are written (S of this tile is complete)
-        ask(next, segment_of<RT>(p, next, v_next, v_end, false));
+        ask(next, segment_of<RT, WIN>(p, next, v_next, v_end, false));
       }
       // n_s completions of s_full[t] so far, as many of o_done[t]
       if (mine > 0 && !warp_wait(&bars->o_done[t], (n_s - 1) & 1, bars, limit, kSiteO)) break;
@@ -892,7 +906,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       tc_fence_before();
       if (v_next >= v_end) {
         grid_launch_dependents();
-        if (t == 0 && r == 0) leave_note(p, blockIdx.x, total, n_ranges, RT, c, g.s0, g.s1, first);
+        if (t == 0 && r == 0) leave_note<WIN>(p, blockIdx.x, total, n_ranges, RT, c, g.s0, g.s1, first);
         break;
       }
       first = false;
@@ -910,24 +924,37 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     struct Window {
       const int* row;
       int n, at, ids, next;
+      int gone0, gone1;   // WIN: entries whose keys none of the unit's rows sees
     };
-    auto entries = [&](const Window& w, int from) {
-      const int id = from + lane < w.n ? __ldg(w.row + from + lane) : -1;
+    auto entry = [&](const Window& w, int e) {
+      const bool wanted = e < w.n && (!WIN || e < w.gone0 || e >= w.gone1);
+      const int id = wanted ? __ldg(w.row + e) : -1;
       return id >= 0 && id < p.n_pages ? id : p.n_pages;
     };
-    auto open_window = [&](const Cursor& c, int s) {
+    auto entries = [&](const Window& w, int from) { return entry(w, from + lane); };
+    auto move_to = [&](Window& w, int e) {
+      w.at = e;
+      w.ids = entries(w, e);
+      w.next = entries(w, e + 32);
+    };
+    auto open_window = [&](const Cursor& c, int run) {
       Window w;
       w.row = p.table + static_cast<int64_t>(c.b) * p.table_st;
       w.n = (c.s.len + P - 1) >> p.page_shift;
-      w.at = (s * KT) >> p.page_shift;
-      w.ids = entries(w, w.at);
-      w.next = entries(w, w.at + 32);
+      w.gone0 = w.gone1 = 0;
+      if constexpr (WIN) {
+        w.gone0 = (p.sinks + P - 1) >> p.page_shift;
+        w.gone1 = unit_from(p, c.s, c.t, RT) >> p.page_shift;
+      }
+      move_to(w, (run * KT) >> p.page_shift);
       return w;
     };
     // (a step's entries lie in one window: their number divides 32)
-    auto reach = [&](Window& w, int s) {
-      const int e = (s * KT) >> p.page_shift;
-      if (e - w.at >= 32) {
+    auto reach = [&](Window& w, int run) {
+      const int e = (run * KT) >> p.page_shift;
+      if (WIN && e - w.at >= 64) {
+        move_to(w, e);
+      } else if (e - w.at >= 32) {
         w.at += 32;
         w.ids = w.next;
         w.next = entries(w, w.at + 32);
@@ -948,17 +975,21 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       uint32_t phase = 0;
       bool lapped = false;
       RingAt<L::kNotes> note_at;
-      for_each_segment<RT>(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
-        Window w = open_window(c, g.s0);
+      for_each_segment<RT, WIN>(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
+        const int skip = unit_skip<WIN>(p, c.s, c.t, RT);
+        Window w = open_window(c, step_run<WIN>(p, skip, g.s0));
         // keys' warp: lane i < 8 looks after keys 16 i .. of a step; its page's
         // scales are asked for a step ahead (the entry may lie in the window
         // behind)
         int id = 0;
         float ks = 1.0f, vs = 1.0f;
         auto ask = [&](int s) {
-          const int e = ((s * KT + (lane & 7) * 16) >> p.page_shift) - w.at;
+          const int run = step_run<WIN>(p, skip, s);
+          const int e = ((run * KT + (lane & 7) * 16) >> p.page_shift) - w.at;
           const int a = __shfl_sync(0xffffffffu, w.ids, e & 31), b = __shfl_sync(0xffffffffu, w.next, e & 31);
           id = e < 32 ? a : b;
+          // (over the gap behind the sinks)
+          if (WIN && e >= 64) id = entry(w, w.at + e);
           if (E4M3 && lane < 8 && id < p.n_pages) {
             const int64_t at = static_cast<int64_t>(id) * p.n_kv + c.h;
             ks = __ldg(p.k_scale + at);
@@ -967,14 +998,15 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         };
         if (is_k) ask(g.s0);
         for (int s = g.s0; s < g.s1; ++s) {
-          const int e0 = reach(w, s), row0 = (s * KT) & (P - 1);
+          const int run = step_run<WIN>(p, skip, s);
+          const int e0 = reach(w, run), row0 = (run * KT) & (P - 1);
           if (lapped && !warp_wait(empty0 + at, phase ^ 1u, bars, limit, kSiteEmpty)) return false;
           uint64_t* full = full0 + at;
           const uint32_t dst = dst0 + static_cast<uint32_t>(at) * (E4M3 ? L::kCodes : L::kTile);
           // one elected lane issues the tile's boxes
           const bool leader = elect_one();
           if (leader) {
-            if (E4M3 && !is_k) *reinterpret_cast<volatile int*>(&bars->valid[at]) = c.s.len - s * KT;
+            if (E4M3 && !is_k) *reinterpret_cast<volatile int*>(&bars->valid[at]) = c.s.len - run * KT;
             mbar_arrive_expect_tx(full, E4M3 ? L::kCodes : L::kTile);
           }
 #pragma unroll 2
@@ -1091,8 +1123,9 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         tc_fence_after();
         return true;
       };
-      for_each_segment<RT>(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
+      for_each_segment<RT, WIN>(p, c0, v0, v1, [&](const Cursor& c, const Segment& g) -> bool {
         if (p.debug_withhold_q) return false;
+        const int skip = unit_skip<WIN>(p, c.s, c.t, RT);
         const int n = g.s1 - g.s0;
         issued = true;
         // One place each for the two products, whatever the mode (the code of
@@ -1107,7 +1140,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
           const int ahead = j + (split ? 2 : 1);
           const bool head = split || t == 0, tail = split || t == 1;   // of the step's events
           if (e >= 0) {
-            if (head && !next_v(c.s.len - (g.s0 + j) * KT)) return false;
+            if (head && !next_v(c.s.len - step_run<WIN>(p, skip, g.s0 + j) * KT)) return false;
             if (!next_p(t)) return false;
             issue_pv(t, j > (split ? 1 : 0));
             if (tail) {
@@ -1167,9 +1200,9 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
   }
 }
 
-template <int D, bool E4M3, bool BF16, bool HALF>
+template <int D, bool E4M3, bool BF16, bool HALF, bool WIN>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
-  auto kern = paged_tc_kernel<D, E4M3, BF16, HALF>;
+  auto kern = paged_tc_kernel<D, E4M3, BF16, HALF, WIN>;
   static std::atomic<uint64_t> configured{0};  // a bit a device
   const uint64_t bit = 1ull << p.device;
   cudaError_t e = cudaSuccess;
@@ -1199,11 +1232,18 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUte
   return sdpa_impl::launch_paged_join(p, D, BF16, unit_rows(HALF), stream);
 }
 
-template <int D, bool HALF>
+template <int D, bool HALF, bool WIN>
 cudaError_t launch_dim(const PagedParams& p, bool bf16, bool e4m3, const CUtensorMap& k, const CUtensorMap& v,
                        cudaStream_t s) {
-  if (e4m3) return bf16 ? launch_one<D, true, true, HALF>(p, k, v, s) : launch_one<D, true, false, HALF>(p, k, v, s);
-  return bf16 ? launch_one<D, false, true, HALF>(p, k, v, s) : launch_one<D, false, false, HALF>(p, k, v, s);
+  if (e4m3) return bf16 ? launch_one<D, true, true, HALF, WIN>(p, k, v, s) : launch_one<D, true, false, HALF, WIN>(p, k, v, s);
+  return bf16 ? launch_one<D, false, true, HALF, WIN>(p, k, v, s) : launch_one<D, false, false, HALF, WIN>(p, k, v, s);
+}
+template <bool WIN>
+cudaError_t launch_tile(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile, const CUtensorMap& k,
+                        const CUtensorMap& v, cudaStream_t s) {
+  if (tile == unit_rows(true))
+    return head_dim == 64 ? launch_dim<64, true, WIN>(p, bf16, e4m3, k, v, s) : launch_dim<128, true, WIN>(p, bf16, e4m3, k, v, s);
+  return head_dim == 64 ? launch_dim<64, false, WIN>(p, bf16, e4m3, k, v, s) : launch_dim<128, false, WIN>(p, bf16, e4m3, k, v, s);
 }
 
 }  // namespace
@@ -1212,11 +1252,8 @@ namespace sdpa_impl {
 
 cudaError_t launch_paged_tc(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile, const CUtensorMap& tm_k,
                             const CUtensorMap& tm_v, cudaStream_t stream) {
-  if (tile == unit_rows(true))
-    return head_dim == 64 ? launch_dim<64, true>(p, bf16, e4m3, tm_k, tm_v, stream)
-                          : launch_dim<128, true>(p, bf16, e4m3, tm_k, tm_v, stream);
-  return head_dim == 64 ? launch_dim<64, false>(p, bf16, e4m3, tm_k, tm_v, stream)
-                        : launch_dim<128, false>(p, bf16, e4m3, tm_k, tm_v, stream);
+  return p.window != 0 ? launch_tile<true>(p, head_dim, bf16, e4m3, tile, tm_k, tm_v, stream)
+                       : launch_tile<false>(p, head_dim, bf16, e4m3, tile, tm_k, tm_v, stream);
 }
 
 cudaError_t read_and_clear_paged_status(unsigned int* status) {
