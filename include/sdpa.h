@@ -424,6 +424,57 @@ SDPA_API sdpa_status sdpa_cache_append(
     const int64_t* q_stride, const int64_t* q_out_stride, void* stream);
 
 /*
+ * sdpa_cache_append_norm -- sdpa_cache_append, the keys and queries normalised
+ * head by head before they are rotated: x becomes x / sqrt(mean(x^2) + eps) * w
+ * over the head's head_dim elements, in fp32 (nothing is rounded before the
+ * rotation's end).
+ *
+ * q_norm,
+ * k_norm       : NULL (not normalised), or DEVICE fp32 [head_dim], contiguous, 16-byte
+ *                aligned: the weights w of every query (key) head.  q_norm needs q.
+ * eps          : 2^-100 .. 1 where a norm is wanted (else not used).
+ *
+ * An infinite element becomes NaN and its head's others zeros, a NaN makes all of
+ * the head NaN; the rotation carries a NaN to the other element of its pair.  Errors as sdpa_cache_append, NULL for q_norm without q, ARG for
+ * an eps out of range.
+ */
+SDPA_API sdpa_status sdpa_cache_append_norm(
+    const sdpa_paged_cache* cache, const void* k, const void* v, sdpa_dtype dtype, int64_t total,
+    const int64_t* k_stride, const int64_t* v_stride, const int32_t* page_table,
+    int64_t page_table_stride, int64_t max_pages, const int32_t* kv_lens,
+    const int32_t* cu_seqlens, int64_t n_seqs, const float* cos, const float* sin, int64_t n_pos,
+    int64_t rot_dim, int interleaved, const void* q, void* q_out, int64_t n_heads,
+    const int64_t* q_stride, const int64_t* q_out_stride, const float* q_norm, const float* k_norm,
+    float eps, void* stream);
+
+/*
+ * sdpa_norm_rotate -- the same norm and rotation of queries and keys that go to no
+ * cache (in front of sdpa_forward_varlen, say).  One kernel launch,
+ * asynchronous on `stream`.
+ *
+ * q, q_out     : DEVICE [total, n_heads, head_dim] of `dtype`; 2 strides each in
+ *                ELEMENTS (token, head), multiples of 8.  q_out may be q with q's
+ *                strides (in place).  head_dim: 64 or 128.
+ * k, k_out     : both NULL, or the same with n_kv_heads heads.
+ * positions    : DEVICE int32 [total], the rows' positions, or NULL: 0, 1, 2, ..
+ * cos, sin     : both NULL (no rotation), or tables as in sdpa_cache_append.
+ * q_norm,
+ * k_norm, eps  : as in sdpa_cache_append_norm; k_norm needs k.
+ *
+ * A row whose position is not in [0, n_pos) is left out: its rows of q_out and
+ * k_out are not written.  (Without a rotation positions are not read.)  Errors:
+ * NULL, DTYPE, SHAPE, LAYOUT, ARG (an output overlaps another operand; eps), CUDA,
+ * DEVICE.
+ */
+SDPA_API sdpa_status sdpa_norm_rotate(
+    const void* q, void* q_out, int64_t n_heads, const int64_t* q_stride,
+    const int64_t* q_out_stride, const void* k, void* k_out, int64_t n_kv_heads,
+    const int64_t* k_stride, const int64_t* k_out_stride, sdpa_dtype dtype, int64_t total,
+    int64_t head_dim, const int32_t* positions, const float* cos, const float* sin, int64_t n_pos,
+    int64_t rot_dim, int interleaved, const float* q_norm, const float* k_norm, float eps,
+    void* stream);
+
+/*
  * sdpa_paged_forward -- attention of each sequence's new tokens over its pages.
  *
  * q, out       : DEVICE [total_q, n_heads, head_dim] of `dtype`; 2 strides in

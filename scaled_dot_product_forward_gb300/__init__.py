@@ -22,7 +22,8 @@ __all__ = ["sdpa_forward", "sdpa_forward_raw", "sdpa_status_string", "sdpa_last_
            "sdpa_debug_set_wait_limit_ns", "sdpa_debug_withhold_q_load",
            "sdpa_forward_varlen", "sdpa_sparse_forward", "sdpa_sparse_compact", "SdpaPlan",
            "sdpa_mask_tiles", "sdpa_forward_masked_noalloc", "head_range",
-           "sdpa_forward_heads", "SdpaPagedCache", "sdpa_cache_append", "sdpa_paged_forward"]
+           "sdpa_forward_heads", "SdpaPagedCache", "sdpa_cache_append", "sdpa_paged_forward",
+           "sdpa_norm_rotate"]
 
 LIB_PATH = _build.LIB_PATH
 
@@ -119,6 +120,11 @@ def load_library(path: str | None = None):
     lib.sdpa_cache_append.argtypes = [vp, vp, vp, ctypes.c_int, i64, vp, vp, vp, i64, i64, vp, vp, i64, vp, vp,
                                       i64, i64, ctypes.c_int, vp, vp, i64, vp, vp, vp]
     lib.sdpa_cache_append.restype = ctypes.c_int
+    lib.sdpa_cache_append_norm.argtypes = [*lib.sdpa_cache_append.argtypes[:-1], vp, vp, ctypes.c_float, vp]
+    lib.sdpa_cache_append_norm.restype = ctypes.c_int
+    lib.sdpa_norm_rotate.argtypes = [vp, vp, i64, vp, vp, vp, vp, i64, vp, vp, ctypes.c_int, i64, i64, vp, vp, vp, i64, i64,
+                                     ctypes.c_int, vp, vp, ctypes.c_float, vp]
+    lib.sdpa_norm_rotate.restype = ctypes.c_int
     lib.sdpa_paged_forward.argtypes = [vp, vp, vp, ctypes.c_int, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp,
                                        i64, i64, ctypes.c_int, ctypes.c_float, vp, ctypes.c_uint64, vp]
     lib.sdpa_paged_forward.restype = ctypes.c_int
@@ -522,7 +528,15 @@ class SdpaPagedCache:
         self._workspace = {}   # bytes that a forward needs, by (query heads, rows)
 
 
-_torch = None      # set by the first SdpaPagedCache (the calls below come after one)
+_torch = None      # set by the first SdpaPagedCache, or the first call below that comes without one
+
+
+def _need_torch():
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
 
 
 def _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, rows):
@@ -557,6 +571,33 @@ def _two_strides(t, where):
     return a, b
 
 
+def _angles(cos, sin, where):
+    """Positions and rotated elements of the tables."""
+    f32 = _torch.float32
+    if cos.dtype is not f32 or sin.dtype is not f32:
+        raise SdpaError(4, where)
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise SdpaError(3, where)
+    if not cos.is_contiguous() or not sin.is_contiguous():
+        raise SdpaError(5, where)
+    n_pos, pairs = cos.shape
+    return n_pos, 2 * pairs
+
+
+def _check_norms(q_norm, k_norm, dim, device, where):
+    for w in (q_norm, k_norm):
+        if w is None:
+            continue
+        if w.dtype is not _torch.float32:
+            raise SdpaError(4, where)
+        if w.dim() != 1 or w.shape[0] != dim:
+            raise SdpaError(3, where)
+        if not w.is_contiguous():
+            raise SdpaError(5, where)
+        if w.get_device() != device:
+            raise SdpaError(6, where)
+
+
 def _on_device(device, where, stream, call):
     """call(stream handle) with ``device`` current, memory that it allocates
     belonging to the stream it launches on."""
@@ -574,7 +615,8 @@ def _on_device(device, where, stream, call):
 
 
 def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=None, sin=None,
-                      interleaved: bool = False, q=None, q_out=None, stream=None):
+                      interleaved: bool = False, q=None, q_out=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+                      stream=None):
     """Append new tokens' keys and values to a paged cache (sdpa_cache_append).
 
     k, v: [total, n_kv_heads, head_dim] bf16/fp16, the sequences' new tokens
@@ -584,7 +626,9 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
     rot_dim / 2] rotation tables (None: no rotation), pairs (j, j + rot_dim /
     2), or neighbours when ``interleaved``.  q: the tokens' queries [total,
     n_heads, head_dim], rotated too, into ``q_out`` (allocated if None; may be
-    ``q``).  Returns ``q_out`` (None without q).
+    ``q``).  q_norm, k_norm: fp32 [head_dim] weights; each query (key) head x is
+    then x / sqrt(mean(x^2) + eps) * weight before it is rotated
+    (sdpa_cache_append_norm).  Returns ``q_out`` (None without q).
 
     A token whose position is negative, past the page table or past the angles
     is left out, and so are rows behind the last sequence: their rows of
@@ -611,15 +655,12 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
         heads = q_shape[1]
     n_pos = rot = 0
     if cos is not None:
-        f32 = _torch.float32
-        if cos.dtype is not f32 or sin.dtype is not f32:
-            raise SdpaError(4, where)
-        if cos.dim() != 2 or cos.shape != sin.shape:
-            raise SdpaError(3, where)
-        n_pos, rot = cos.shape
-        if not cos.is_contiguous() or not sin.is_contiguous():
-            raise SdpaError(5, where)
-        rot *= 2
+        n_pos, rot = _angles(cos, sin, where)
+    normed = q_norm is not None or k_norm is not None
+    if normed:
+        if q is None and q_norm is not None:
+            raise SdpaError(1, where)
+        _check_norms(q_norm, k_norm, shape[2], cache.device, where)
     ks, vs = _two_strides(k, where), _two_strides(v, where)
     device = cache.device
     # all on the cache's CUDA device (a host pointer would fault)
@@ -637,15 +678,86 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
             qs, qos = _two_strides(q, where), _two_strides(qo, where)
         strides = _Strides(*ks, *vs, *qs, *qos)
         at = _address(strides)
-        rc = load_library().sdpa_cache_append(
-            cache._ref, k.data_ptr(), v.data_ptr(), dt, total, at, at + 16, page_table.data_ptr(), page_table.stride(0),
-            max_pages, kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None, n_seqs,
-            cos.data_ptr() if cos is not None else None, sin.data_ptr() if cos is not None else None, n_pos, rot,
-            1 if interleaved else 0, q.data_ptr() if q is not None else None,
-            qo.data_ptr() if q is not None else None, heads, at + 32, at + 48, st)
+        args = (cache._ref, k.data_ptr(), v.data_ptr(), dt, total, at, at + 16, page_table.data_ptr(), page_table.stride(0),
+                max_pages, kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None, n_seqs,
+                cos.data_ptr() if cos is not None else None, sin.data_ptr() if cos is not None else None, n_pos, rot,
+                1 if interleaved else 0, q.data_ptr() if q is not None else None,
+                qo.data_ptr() if q is not None else None, heads, at + 32, at + 48)
+        if normed:
+            rc = load_library().sdpa_cache_append_norm(*args, q_norm.data_ptr() if q_norm is not None else None,
+                                                       k_norm.data_ptr() if k_norm is not None else None, eps, st)
+        else:
+            rc = load_library().sdpa_cache_append(*args, st)
         if rc != 0:
             raise SdpaError(rc, where)
         return qo
+
+    return _on_device(device, where, stream, call)
+
+
+def sdpa_norm_rotate(q, k=None, positions=None, *, cos=None, sin=None, interleaved: bool = False, q_norm=None, k_norm=None,
+                     eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Norm and rotation of query and key heads that go to no cache
+    (sdpa_norm_rotate), in one pass.
+
+    q, k: [total, heads, head_dim] bf16/fp16 (k with its own number of heads,
+    or None); positions: int32 [total] (None: 0, 1, 2, ..); cos, sin,
+    interleaved, q_norm, k_norm, eps as in sdpa_cache_append.  q_out, k_out:
+    allocated if None; may be q and k.  Returns ``(q_out, k_out)``.  Rows whose
+    position is not in the tables are left out: not written (they hold whatever
+    the memory held where the outputs are allocated here)."""
+    _need_torch()
+    where = "sdpa_norm_rotate"
+    dtype, shape = q.dtype, q.shape
+    dt = SDPA_BF16 if dtype is _torch.bfloat16 else SDPA_FP16 if dtype is _torch.float16 else -1
+    if dt < 0 or any(t is not None and t.dtype is not dtype for t in (k, q_out, k_out)) or \
+            (positions is not None and positions.dtype is not _torch.int32):
+        raise SdpaError(4, where)
+    if k is None and (k_out is not None or k_norm is not None) or (cos is None) != (sin is None):
+        raise SdpaError(1, where)
+    if len(shape) != 3 or (q_out is not None and q_out.shape != shape):
+        raise SdpaError(3, where)
+    total, heads, dim = shape
+    kv_heads = 0
+    if k is not None:
+        k_shape = k.shape
+        if len(k_shape) != 3 or k_shape[0] != total or k_shape[2] != dim or (k_out is not None and k_out.shape != k_shape):
+            raise SdpaError(3, where)
+        kv_heads = k_shape[1]
+    if positions is not None:
+        if positions.dim() != 1 or positions.shape[0] != total:
+            raise SdpaError(3, where)
+        if not positions.is_contiguous():
+            raise SdpaError(5, where)
+    n_pos = rot = 0
+    device = q.get_device()
+    if cos is not None:
+        n_pos, rot = _angles(cos, sin, where)
+    _check_norms(q_norm, k_norm, dim, device, where)
+    # all on one CUDA device (a host pointer would fault)
+    if device < 0 or any(t is not None and t.get_device() != device for t in (k, positions, cos, sin, q_out, k_out)):
+        raise SdpaError(6, where)
+    qs, ks = _two_strides(q, where), _two_strides(k, where) if k is not None else (0, 0)
+
+    def call(st):
+        qo, ko, kos = q_out, k_out, (0, 0)
+        if qo is None:
+            qo = _torch.empty(shape, dtype=dtype, device=q.device)
+        if k is not None:
+            if ko is None:
+                ko = _torch.empty(k_shape, dtype=dtype, device=q.device)
+            kos = _two_strides(ko, where)
+        strides = _Strides(*qs, *_two_strides(qo, where), *ks, *kos)
+        at = _address(strides)
+        rc = load_library().sdpa_norm_rotate(
+            q.data_ptr(), qo.data_ptr(), heads, at, at + 16, k.data_ptr() if k is not None else None,
+            ko.data_ptr() if k is not None else None, kv_heads, at + 32, at + 48, dt, total, dim,
+            positions.data_ptr() if positions is not None else None, cos.data_ptr() if cos is not None else None,
+            sin.data_ptr() if cos is not None else None, n_pos, rot, 1 if interleaved else 0,
+            q_norm.data_ptr() if q_norm is not None else None, k_norm.data_ptr() if k_norm is not None else None, eps, st)
+        if rc != 0:
+            raise SdpaError(rc, where)
+        return qo, ko
 
     return _on_device(device, where, stream, call)
 

@@ -15,6 +15,12 @@
 // type's least normal: when a token arrives that does not fit, the page's
 // earlier codes are multiplied by old / new in place.
 //
+// With norms (NORM) a key's or query's head is first divided by the root mean
+// square of its D elements and multiplied by the weights, x rsqrt(sum x^2 / D +
+// eps) w, in fp32: the row's lanes add up their squares by log2(D / 8) exchanges,
+// and nothing is rounded before the rotation's end.  norm_rotate_kernel does the
+// same to rows that go to no cache.
+//
 // Bound by memory: each new row is read once and written once.  Two kinds of
 // work share one launch:
 //   * rows without a scale (the queries; 16-bit keys and values): a warp takes a
@@ -128,6 +134,70 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const float4& c, const fl
   }
 }
 
+// The lane's weights (of elements ea .. ea + 3, eb .. eb + 3).
+__device__ __forceinline__ void load_weights(const float* weight, const Lane& l, float (&w)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(weight + l.ea));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(weight + l.eb));
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+// Sum over a row's LANES lanes, the same in each of them.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Rows x[0 .. N) normalised; LANES lanes hold a row, the whole warp calls it.
+// Squares below 2^-126 do not matter beside eps >= 2^-100; those of values above
+// 2^60 (bf16) may overflow, and such rows are summed again 2^-70 times as large.
+template <int LANES, int N>
+__device__ __forceinline__ void normalise(float (&x)[N][8], const float (&w)[8], float eps) {
+  float ss[N];
+  bool over = false;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float a = x[k][0] * x[k][0], b = x[k][1] * x[k][1];
+#pragma unroll
+    for (int e = 2; e < 8; e += 2) {
+      a = fmaf(x[k][e], x[k][e], a);
+      b = fmaf(x[k][e + 1], x[k][e + 1], b);
+    }
+    ss[k] = a + b;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    ss[k] = row_sum<LANES>(ss[k]);
+    over |= ss[k] == INFINITY;
+    ss[k] = rsqrtf(fmaf(ss[k], 1.0f / (8 * LANES), eps));
+  }
+  if (__any_sync(0xffffffffu, over)) {
+    const float down = 8.470329472543003e-22f;   // 2^-70
+#pragma unroll 1
+    for (int k = 0; k < N; ++k) {
+      float a = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) y = i == k ? x[i][e] : y;
+        a = fmaf(y * down, y * down, a);
+      }
+      a = row_sum<LANES>(a);
+      // (from 2^60 on, where the plain sum overflows, eps is nothing)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i == k && ss[i] == 0.0f) ss[i] = rsqrtf(a * (1.0f / (8 * LANES))) * down;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[k][e] = x[k][e] * ss[k] * w[e];
+}
+
 // The page's new tokens: positions [lo, hi), the first being row t0 of k, v, q.
 struct PageTokens {
   int lo, hi, t0;
@@ -162,14 +232,14 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __int_as_float((e + 127) << 23);
 }
 
-// Rows r, r + stride, .. (kBatch of them) of a unit of n rows, rotated (ROT), in
-// registers; rows from n on are zeros.  src, cos, sin: this lane's part of row
-// r; steps in elements.
+// Rows r, r + stride, .. (kBatch of them) of a unit of n rows, normalised (NORM)
+// and rotated (ROT), in registers; rows from n on are zeros.  src, cos, sin: this
+// lane's part of row r; steps in elements.
 constexpr int kBatch = 4;
-template <bool BF16, bool ROT>
+template <int D, bool BF16, bool ROT, bool NORM>
 __device__ __forceinline__ void load_rows(const uint16_t* src, int64_t src_step, const float* cos, const float* sin,
                                           int64_t angle_step, const Lane& at, int interleaved, int r, int stride, int n,
-                                          float (&x)[kBatch][8]) {
+                                          const float* weight, float eps, float (&x)[kBatch][8]) {
 #pragma unroll
   for (int k = 0; k < kBatch; ++k) {
     if (r + k * stride < n) {
@@ -179,6 +249,11 @@ __device__ __forceinline__ void load_rows(const uint16_t* src, int64_t src_step,
       for (int e = 0; e < 8; ++e) x[k][e] = 0.0f;
     }
     src += src_step;
+  }
+  if (NORM && weight != nullptr) {
+    float w[8];
+    load_weights(weight, at, w);
+    normalise<D / 8, kBatch>(x, w, eps);
   }
   if (ROT && at.rotated) {
 #pragma unroll
@@ -209,7 +284,7 @@ __device__ __forceinline__ void store_codes(uint8_t* to, int64_t step, const Lan
 
 // A unit: the page's new rows of one head, quantised under the page's scale, by
 // WARPS warps (part: this one's number, red: their shared scratch).
-template <int D, bool BF16, bool ROT, int WARPS>
+template <int D, bool BF16, bool ROT, bool NORM, int WARPS>
 __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, const PageTokens& pt,
                                              const uint16_t* src, int64_t src_st, uint8_t* dst,
                                              int64_t dst_st, float* scale_at, int part, float* red) {
@@ -230,9 +305,9 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
   const float* const cos = ROT ? p.cos + angle : nullptr;
   const float* const sin = ROT ? p.sin + angle : nullptr;
   auto load = [&](int batch, float (&x)[kBatch][8]) {
-    load_rows<BF16, ROT>(rows + batch * (kBatch * row_step), row_step, cos + batch * (kBatch * angle_step),
+    load_rows<D, BF16, ROT, NORM>(rows + batch * (kBatch * row_step), row_step, cos + batch * (kBatch * angle_step),
                          sin + batch * (kBatch * angle_step), angle_step, at, p.interleaved,
-                         first + batch * kBatch * kStride, kStride, n, x);
+                         first + batch * kBatch * kStride, kStride, n, p.k_norm, p.eps, x);
   };
   float x[kBatch][8];
   float amax = 0.0f;
@@ -297,30 +372,42 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
   }
 }
 
-// One warp: heads [h0, h1) of one token, rotated (ROT) or copied, four rows a
-// lane at a time.  (c, s): the lane's angles.
-template <int D, bool BF16, bool ROT>
-__device__ __forceinline__ void token_rows(const sdpa_impl::AppendParams& p, const Lane& at, const float4& c,
-                                           const float4& s, const uint16_t* src, int64_t src_sh, uint8_t* dst,
-                                           int64_t dst_sh_bytes, int h0, int h1) {
+// One warp: heads [h0, h1) of one token, normalised (NORM, with weights), rotated
+// (ROT) or copied, four rows a lane at a time.  (c, s): the lane's angles.
+template <int D, bool BF16, bool ROT, bool NORM>
+__device__ __forceinline__ void token_rows(int interleaved, const Lane& at, const float4& c, const float4& s,
+                                           const uint16_t* src, int64_t src_sh, uint8_t* dst, int64_t dst_sh_bytes,
+                                           const float* weight, float eps, int h0, int h1) {
   constexpr int kLanes = D / 8;
   constexpr int kRows = 32 / kLanes;
-  int h = h0 + static_cast<int>(threadIdx.x & 31) / kLanes;
+  const int sub = static_cast<int>(threadIdx.x & 31) / kLanes;
+  int h = h0 + sub;
   src += h * src_sh;
   dst += h * dst_sh_bytes;
   const int64_t src_step = kRows * src_sh, dst_step = kRows * dst_sh_bytes;
+  // (a norm's sums are exchanged: the warp stays together)
 #pragma unroll 1
-  for (; h < h1; h += kBatch * kRows) {
+  for (; (NORM ? h - sub : h) < h1; h += kBatch * kRows) {
     float x[kBatch][8];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (h + u * kRows < h1) load8<BF16>(src, at, x[u]);
+      if (h + u * kRows < h1) {
+        load8<BF16>(src, at, x[u]);
+      } else if (NORM) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
+      }
       src += src_step;
+    }
+    if (NORM && weight != nullptr) {
+      float w[8];
+      load_weights(weight, at, w);
+      normalise<kLanes, kBatch>(x, w, eps);
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (h + u * kRows < h1) {
-        if (ROT && at.rotated) rotate8(x[u], c, s, p.interleaved);
+        if (ROT && at.rotated) rotate8(x[u], c, s, interleaved);
         store8<BF16>(reinterpret_cast<uint16_t*>(dst), at, x[u]);
       }
       dst += dst_step;
@@ -347,7 +434,7 @@ __device__ __forceinline__ int last_at_most(int n, int x, F&& f) {
 // tokens can touch, so a slot finds its sequence without a prefix sum over
 // lengths; a slot's units are its value and key heads.  The other blocks: a
 // warp takes a share (1 / parts) of one token's rows.
-template <int D, bool BF16, bool E4M3, bool ROT, int UNIT_WARPS>
+template <int D, bool BF16, bool E4M3, bool ROT, bool NORM, int UNIT_WARPS>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     append_kernel(const __grid_constant__ sdpa_impl::AppendParams p, int kv_blocks, int parts) {
   __shared__ float red[kWarps];
@@ -385,10 +472,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       const int64_t at = static_cast<int64_t>(page) * p.n_kv + h;
       const int part = warp % UNIT_WARPS;
       if (hv < p.n_kv)
-        append_codes<D, BF16, false, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.v) + h * p.v_sh, p.v_st,
+        append_codes<D, BF16, false, false, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.v) + h * p.v_sh, p.v_st,
                                                  p.cv + page * p.cv_sp + h * p.cv_sh, p.cv_st, p.v_scale + at, part, red + warp - part);
       else
-        append_codes<D, BF16, ROT, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.k) + h * p.k_sh, p.k_st,
+        append_codes<D, BF16, ROT, NORM, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.k) + h * p.k_sh, p.k_st,
                                                p.ck + page * p.ck_sp + h * p.ck_sh, p.ck_st, p.k_scale + at, part, red + warp - part);
       return;
     }
@@ -412,36 +499,62 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
   }
   if (p.q != nullptr)
-    token_rows<D, BF16, ROT>(p, at, c, s, reinterpret_cast<const uint16_t*>(p.q) + tok * p.q_st, p.q_sh,
-                             reinterpret_cast<uint8_t*>(p.q_out) + tok * p.qo_st * 2, p.qo_sh * 2, p.H * share / parts,
-                             p.H * (share + 1) / parts);
+    token_rows<D, BF16, ROT, NORM>(p.interleaved, at, c, s, reinterpret_cast<const uint16_t*>(p.q) + tok * p.q_st, p.q_sh,
+                                   reinterpret_cast<uint8_t*>(p.q_out) + tok * p.qo_st * 2, p.qo_sh * 2, p.q_norm, p.eps,
+                                   p.H * share / parts, p.H * (share + 1) / parts);
   if constexpr (!E4M3) {
     const int page = __ldg(p.table + b * p.table_st + (pos >> p.page_shift));
     if (page < 0 || page >= p.n_pages) return;
     const int row = pos & (P - 1), h0 = p.n_kv * share / parts, h1 = p.n_kv * (share + 1) / parts;
-    token_rows<D, BF16, ROT>(p, at, c, s, reinterpret_cast<const uint16_t*>(p.k) + tok * p.k_st, p.k_sh,
-                             p.ck + page * p.ck_sp + row * p.ck_st, p.ck_sh, h0, h1);
+    token_rows<D, BF16, ROT, NORM>(p.interleaved, at, c, s, reinterpret_cast<const uint16_t*>(p.k) + tok * p.k_st, p.k_sh,
+                                   p.ck + page * p.ck_sp + row * p.ck_st, p.ck_sh, p.k_norm, p.eps, h0, h1);
     // (plain copies: every lane takes eight elements that lie together)
-    token_rows<D, BF16, false>(p, lane_of(j, 0, 0), c, s, reinterpret_cast<const uint16_t*>(p.v) + tok * p.v_st, p.v_sh,
-                               p.cv + page * p.cv_sp + row * p.cv_st, p.cv_sh, h0, h1);
+    token_rows<D, BF16, false, false>(0, lane_of(j, 0, 0), c, s, reinterpret_cast<const uint16_t*>(p.v) + tok * p.v_st, p.v_sh,
+                                      p.cv + page * p.cv_sp + row * p.cv_st, p.cv_sh, nullptr, 0.0f, h0, h1);
   }
 }
 
-template <int D, bool BF16, bool E4M3, bool ROT, int UNIT_WARPS>
-cudaError_t launch_one(const sdpa_impl::AppendParams& p, int sms, cudaStream_t stream) {
-  long long kv_blocks = 0;
-  if (E4M3) {
-    const long long units = ((p.total >> p.page_shift) + 2LL * p.n_seqs) * 2 * p.n_kv;
-    kv_blocks = (units + kWarps / UNIT_WARPS - 1) / (kWarps / UNIT_WARPS);
+// Rows without a cache: a warp takes a share (1 / parts) of one token's query and
+// key heads.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, kPerSm)
+    norm_rotate_kernel(const __grid_constant__ sdpa_impl::RowsParams p, int parts) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t tok = w / static_cast<unsigned>(parts);
+  const int share = static_cast<int>(w % static_cast<unsigned>(parts));
+  if (tok >= p.total) return;
+  const int j = (threadIdx.x & 31) % (D / 8);
+  const Lane at = lane_of(j, p.rot, p.interleaved);
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.rot > 0) {
+    const int pos = p.positions != nullptr ? __ldg(p.positions + tok) : static_cast<int>(tok);
+    if (pos < 0 || pos >= p.n_pos) return;
+    if (at.rotated) {
+      const int64_t o = static_cast<int64_t>(pos) * (p.rot / 2) + 4 * j;
+      c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
+      s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
+    }
   }
-  // Tokens' rows: a warp a token, or a share of its heads each where that
-  // leaves SMs without work.
+  token_rows<D, BF16, true, true>(p.interleaved, at, c, s, reinterpret_cast<const uint16_t*>(p.q) + tok * p.q_st, p.q_sh,
+                                  reinterpret_cast<uint8_t*>(p.q_out) + tok * p.qo_st * 2, p.qo_sh * 2, p.q_norm, p.eps,
+                                  p.H * share / parts, p.H * (share + 1) / parts);
+  if (p.k != nullptr)
+    token_rows<D, BF16, true, true>(p.interleaved, at, c, s, reinterpret_cast<const uint16_t*>(p.k) + tok * p.k_st, p.k_sh,
+                                    reinterpret_cast<uint8_t*>(p.k_out) + tok * p.ko_st * 2, p.ko_sh * 2, p.k_norm, p.eps,
+                                    p.n_kv * share / parts, p.n_kv * (share + 1) / parts);
+}
+
+// Warps a token: one, or several that share its heads where tokens are few.
+int token_parts(long long total, int heads, int sms) {
   int parts = 1;
-  const int heads = p.H > p.n_kv ? p.H : p.n_kv;
-  while (parts < 16 && static_cast<long long>(p.total) * parts < 16LL * sms && parts * 2 <= heads) parts *= 2;
-  const bool rows = !E4M3 || p.q != nullptr;
-  const long long row_blocks = rows ? (static_cast<long long>(p.total) * parts + kWarps - 1) / kWarps : 0;
-  const long long blocks = kv_blocks + row_blocks;
+  while (parts < 16 && total * parts < 16LL * sms && parts * 2 <= heads) parts *= 2;
+  return parts;
+}
+
+template <class K, class... A>
+cudaError_t launch_pdl(K kern, long long blocks, cudaStream_t stream, const A&... args) {
   if (blocks > 0x7fffffffLL / kWarps) return cudaErrorInvalidValue;   // (units and warps are counted in 32 bits)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -452,20 +565,50 @@ cudaError_t launch_one(const sdpa_impl::AppendParams& p, int sms, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<D, BF16, E4M3, ROT, UNIT_WARPS>, p, static_cast<int>(kv_blocks), parts);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, bool BF16, bool ROT>
+template <int D, bool BF16>
+cudaError_t launch_rows(const sdpa_impl::RowsParams& p, int sms, cudaStream_t stream) {
+  const int parts = token_parts(p.total, p.H > p.n_kv ? p.H : p.n_kv, sms);
+  return launch_pdl(norm_rotate_kernel<D, BF16>, (static_cast<long long>(p.total) * parts + kWarps - 1) / kWarps, stream, p, parts);
+}
+
+template <int D, bool BF16, bool E4M3, bool ROT, bool NORM, int UNIT_WARPS>
+cudaError_t launch_one(const sdpa_impl::AppendParams& p, int sms, cudaStream_t stream) {
+  long long kv_blocks = 0;
+  if (E4M3) {
+    const long long units = ((p.total >> p.page_shift) + 2LL * p.n_seqs) * 2 * p.n_kv;
+    kv_blocks = (units + kWarps / UNIT_WARPS - 1) / (kWarps / UNIT_WARPS);
+  }
+  // Tokens' rows: a warp a token, or a share of its heads each where that
+  // leaves SMs without work.
+  const int parts = token_parts(p.total, p.H > p.n_kv ? p.H : p.n_kv, sms);
+  const bool rows = !E4M3 || p.q != nullptr;
+  const long long row_blocks = rows ? (static_cast<long long>(p.total) * parts + kWarps - 1) / kWarps : 0;
+  return launch_pdl(append_kernel<D, BF16, E4M3, ROT, NORM, UNIT_WARPS>, kv_blocks + row_blocks, stream, p,
+                    static_cast<int>(kv_blocks), parts);
+}
+
+template <int D, bool BF16, bool ROT, bool NORM>
 cudaError_t launch_typed(const sdpa_impl::AppendParams& p, bool e4m3, int sms, cudaStream_t s) {
-  if (!e4m3) return launch_one<D, BF16, false, ROT, 1>(p, sms, s);
+  if (!e4m3) return launch_one<D, BF16, false, ROT, NORM, 1>(p, sms, s);
   // as many warps a unit as hold its rows in registers (the most it can have:
   // a page's, or about a sequence's when those are fewer)
   const int P = 1 << p.page_shift, n = p.total / p.n_seqs, rows = P < n ? P : n;
   const int warp_rows = kBatch * 32 / (D / 8);
-  if (rows <= warp_rows) return launch_one<D, BF16, true, ROT, 1>(p, sms, s);
-  if (rows <= 2 * warp_rows) return launch_one<D, BF16, true, ROT, 2>(p, sms, s);
-  if (rows <= 4 * warp_rows) return launch_one<D, BF16, true, ROT, 4>(p, sms, s);
-  return launch_one<D, BF16, true, ROT, 8>(p, sms, s);
+  if (rows <= warp_rows) return launch_one<D, BF16, true, ROT, NORM, 1>(p, sms, s);
+  if (rows <= 2 * warp_rows) return launch_one<D, BF16, true, ROT, NORM, 2>(p, sms, s);
+  if (rows <= 4 * warp_rows) return launch_one<D, BF16, true, ROT, NORM, 4>(p, sms, s);
+  return launch_one<D, BF16, true, ROT, NORM, 8>(p, sms, s);
+}
+
+// (With norms there is one form for rotated rows and others: rot = 0.)
+template <int D, bool BF16>
+cudaError_t launch_dim(const sdpa_impl::AppendParams& p, bool e4m3, int sms, cudaStream_t s) {
+  if (p.q_norm != nullptr || p.k_norm != nullptr) return launch_typed<D, BF16, true, true>(p, e4m3, sms, s);
+  if (p.cos != nullptr) return launch_typed<D, BF16, true, false>(p, e4m3, sms, s);
+  return launch_typed<D, BF16, false, false>(p, e4m3, sms, s);
 }
 
 }  // namespace
@@ -474,12 +617,13 @@ namespace sdpa_impl {
 
 cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, bool e4m3, int sms,
                                 cudaStream_t stream) {
-  if (head_dim == 64) {
-    if (p.cos) return bf16 ? launch_typed<64, true, true>(p, e4m3, sms, stream) : launch_typed<64, false, true>(p, e4m3, sms, stream);
-    return bf16 ? launch_typed<64, true, false>(p, e4m3, sms, stream) : launch_typed<64, false, false>(p, e4m3, sms, stream);
-  }
-  if (p.cos) return bf16 ? launch_typed<128, true, true>(p, e4m3, sms, stream) : launch_typed<128, false, true>(p, e4m3, sms, stream);
-  return bf16 ? launch_typed<128, true, false>(p, e4m3, sms, stream) : launch_typed<128, false, false>(p, e4m3, sms, stream);
+  if (head_dim == 64) return bf16 ? launch_dim<64, true>(p, e4m3, sms, stream) : launch_dim<64, false>(p, e4m3, sms, stream);
+  return bf16 ? launch_dim<128, true>(p, e4m3, sms, stream) : launch_dim<128, false>(p, e4m3, sms, stream);
+}
+
+cudaError_t launch_norm_rotate(const RowsParams& p, int head_dim, bool bf16, int sms, cudaStream_t stream) {
+  if (head_dim == 64) return bf16 ? launch_rows<64, true>(p, sms, stream) : launch_rows<64, false>(p, sms, stream);
+  return bf16 ? launch_rows<128, true>(p, sms, stream) : launch_rows<128, false>(p, sms, stream);
 }
 
 }  // namespace sdpa_impl

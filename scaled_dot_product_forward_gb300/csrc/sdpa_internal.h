@@ -181,6 +181,26 @@ struct AppendParams {
   const int* kv_lens;
   const int* cu;
   int total, n_seqs, n_kv, H, n_pages, max_len, n_pos, rot, interleaved, page_shift;
+  // Norms: the heads' weights [D], null: not normalised.
+  const float* q_norm;
+  const float* k_norm;
+  float eps;
+};
+
+// Rows of queries and keys, normalised and rotated without a cache.
+struct RowsParams {
+  const void* q;            // [total, H, D] 16-bit, element strides
+  void* q_out;
+  const void* k;            // optional [total, n_kv, D]
+  void* k_out;
+  int64_t q_st, q_sh, qo_st, qo_sh, k_st, k_sh, ko_st, ko_sh;
+  const int* positions;     // [total], null: the row's number
+  const float* cos;         // [n_pos, rot / 2], null: no rotation
+  const float* sin;
+  const float* q_norm;      // [D], null: not normalised
+  const float* k_norm;
+  float eps;
+  int total, H, n_kv, n_pos, rot, interleaved;
 };
 
 // The scales a cache may hold: positive, 2^-50 .. 2^50 (others are taken as
@@ -189,6 +209,7 @@ constexpr int kScaleMinExp = -50, kScaleMaxExp = 50;
 
 cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, bool e4m3, int sms,
                                 cudaStream_t stream);
+cudaError_t launch_norm_rotate(const RowsParams& p, int head_dim, bool bf16, int sms, cudaStream_t stream);
 constexpr int kJoinNoteBytes = 32;  // a CTA's note at the workspace's start
 
 // How a launch is divided: CTAs, rows and key/value heads of a unit, keys of
