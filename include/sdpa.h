@@ -552,6 +552,126 @@ SDPA_API sdpa_status sdpa_paged_forward_window(
 SDPA_API uint64_t sdpa_paged_workspace_bytes(int64_t head_dim, int64_t n_heads,
                                              int64_t n_kv_heads, int64_t max_seqlen_q);
 
+/*
+ * Pages as a whole.  A program that answers several ways from one prompt, gives
+ * back what a window has left behind, or drops tokens, shares, copies and frees
+ * pages.  The accounts are two arrays of the caller's: refs, DEVICE int32
+ * [n_pages], 16-byte aligned, the number of table entries that name a page (plus
+ * whatever else holds it), none for a free one; and page tables, DEVICE int32
+ * [n_rows, max_pages], row stride >= max_pages, -1 for no page.  All calls are
+ * asynchronous on `stream`, read every length on the device and do not depend on
+ * timing: free pages are given out in rising order of their numbers, to the
+ * requests in their order.  Calls that write to the same arrays must be ordered
+ * by the caller.
+ *
+ * sdpa_pages_take -- pages for row i's tokens [from_lens[i], to_lens[i]): entries
+ * ceil(from / page_size) .. ceil(to / page_size) - 1 each get a free page, with one
+ * reference.  (The page that token from - 1 lies in has room for the next ones.)
+ * Lengths are limited to [0, max_pages * page_size]; what the entries held before
+ * is not looked at.
+ *
+ * from_lens,
+ * to_lens      : DEVICE int32 [n_rows].
+ * missing      : DEVICE int32 [1], written: pages that there were too few of.  The
+ *                last requests' entries are then -1.
+ *
+ * sdpa_pages_fork -- row dst[i] of new_table becomes a copy of row src[i] of
+ * page_table.  What it held loses a reference; the floor(kv_lens[src] / page_size)
+ * full pages are shared, each with a reference more; the begun one, if there is
+ * any, becomes a free page of the row's own, into which its rows are still to be
+ * copied (sdpa_cache_copy_pages with copy_src, copy_dst, copy_rows, for the cache of
+ * every layer); later entries are -1.
+ *
+ * new_table    : [n_new_rows, max_pages]; page_table itself (same rows and stride),
+ *                or apart from it.
+ * kv_lens      : DEVICE int32 [n_rows], lengths of page_table's rows, limited as above.
+ * src, dst     : DEVICE int32 [n], n <= 32768.  No two dst are the same, and in one
+ *                table none is another pair's src (the results are then some
+ *                mixture, within the arrays).  A pair that names no row, or one row
+ *                of one table twice, does nothing.
+ * copy_src,
+ * copy_dst,
+ * copy_rows    : DEVICE int32 [n], written: page, new page and number of tokens to
+ *                copy; -1, -1, 0 where there is nothing (no begun page, an entry that
+ *                is no page, or no free page left).
+ * missing      : as above, also for the entry of a begun page that has none (-1).
+ *
+ * sdpa_pages_release -- row rows[i] (rows NULL: row i) gives up the pages that lie
+ * wholly within its tokens [from_lens[i], to_lens[i]): entries ceil(from /
+ * page_size) .. floor(to / page_size) - 1 become -1, their pages lose a
+ * reference.  from_lens NULL: from 0; to_lens NULL: to the row's end.
+ * rows, from_lens,
+ * to_lens      : DEVICE int32 [n].
+ *
+ * Table entries outside [0, n_pages) count as none; rows outside [0, n_rows) are
+ * left out.  page_size: 16 .. 1024, a power of two; n_pages at most 2^30, at most
+ * 32768 rows in sdpa_pages_take.  Errors: NULL, SHAPE, LAYOUT, ARG (an output
+ * overlaps another operand), CUDA, DEVICE.
+ */
+SDPA_API sdpa_status sdpa_pages_take(int32_t* refs, int64_t n_pages, int32_t* page_table,
+                                     int64_t page_table_stride, int64_t n_rows, int64_t max_pages,
+                                     int64_t page_size, const int32_t* from_lens,
+                                     const int32_t* to_lens, int32_t* missing, void* stream);
+SDPA_API sdpa_status sdpa_pages_fork(int32_t* refs, int64_t n_pages, const int32_t* page_table,
+                                     int64_t page_table_stride, int64_t n_rows, int32_t* new_table,
+                                     int64_t new_table_stride, int64_t n_new_rows,
+                                     int64_t max_pages, int64_t page_size, const int32_t* kv_lens,
+                                     const int32_t* src, const int32_t* dst, int64_t n,
+                                     int32_t* copy_src, int32_t* copy_dst, int32_t* copy_rows,
+                                     int32_t* missing, void* stream);
+SDPA_API sdpa_status sdpa_pages_release(int32_t* refs, int64_t n_pages, int32_t* page_table,
+                                        int64_t page_table_stride, int64_t n_rows,
+                                        int64_t max_pages, int64_t page_size, const int32_t* rows,
+                                        const int32_t* from_lens, const int32_t* to_lens, int64_t n,
+                                        void* stream);
+
+/*
+ * sdpa_cache_copy_pages -- copy pages of a cache: keys, values and scales of page
+ * src[i] to page dst[i], bit for bit.  One kernel launch, asynchronous.
+ *
+ * src, dst     : DEVICE int32 [n].  No page is dst twice, or dst and src.  A pair
+ *                with an entry outside [0, n_pages), or with both the same, does
+ *                nothing.
+ * rows         : NULL (whole pages), or DEVICE int32 [n]: only the page's first
+ *                rows[i] tokens (limited to [0, page_size]; none: nothing, else the
+ *                scales whole).
+ * Errors: NULL, DTYPE, SHAPE, LAYOUT, ARG (the cache overlaps the lists, or its
+ * keys' pages its values'), CUDA, DEVICE.
+ */
+SDPA_API sdpa_status sdpa_cache_copy_pages(const sdpa_paged_cache* cache, const int32_t* src,
+                                           const int32_t* dst, const int32_t* rows, int64_t n,
+                                           void* stream);
+
+/*
+ * sdpa_cache_compact -- move the tokens of each sequence that are kept together,
+ * into new pages: token i of sequence b's new pages (page new_table[b, i /
+ * page_size], row i % page_size) is the one at position kept[b, i] of its old
+ * ones (page_table).  Keys stay as they are, rotated by their old positions.  One
+ * kernel launch, asynchronous.
+ *
+ * page_table   : DEVICE int32 [n_seqs, max_pages], row stride page_table_stride.
+ * kept         : DEVICE int32 [n_seqs, max_kept], row stride kept_stride; any
+ *                positions in any order.
+ * kept_lens    : DEVICE int32 [n_seqs], limited to [0, max_kept], or NULL: max_kept each.
+ * new_table    : DEVICE int32 [n_seqs, new_max_pages].  The pages with new tokens are
+ *                none of those that are read, and no two entries name one.
+ *
+ * SDPA_CACHE_E4M3: the scale of a new (page, head) is the largest of those that its
+ * tokens' old pages have, and codes that came under a smaller one are multiplied
+ * by old / new and rounded once (with powers of two exact but for codes below the
+ * type's least normal).  A position outside the old pages, or whose entry is no
+ * page, leaves its token out (its row is not written), and so does a new entry
+ * that is no page; rows of a new page behind the last kept token are not
+ * written.  Errors: NULL, DTYPE, SHAPE, LAYOUT, ARG (the cache overlaps the
+ * tables, or its keys' pages its values'), CUDA, DEVICE.
+ */
+SDPA_API sdpa_status sdpa_cache_compact(const sdpa_paged_cache* cache, const int32_t* page_table,
+                                        int64_t page_table_stride, int64_t max_pages,
+                                        const int32_t* kept, int64_t kept_stride, int64_t max_kept,
+                                        const int32_t* kept_lens, const int32_t* new_table,
+                                        int64_t new_table_stride, int64_t new_max_pages,
+                                        int64_t n_seqs, void* stream);
+
 /* Adds (lse != NULL) or removes (lse == NULL) the log-sum-exp output of a
  * plan; same layout rules as sdpa_forward_lse. */
 SDPA_API sdpa_status sdpa_plan_set_lse(sdpa_plan* plan, float* lse, const int64_t* lse_stride);

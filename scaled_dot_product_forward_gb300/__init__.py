@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 from . import _build
 
@@ -23,7 +24,8 @@ __all__ = ["sdpa_forward", "sdpa_forward_raw", "sdpa_status_string", "sdpa_last_
            "sdpa_forward_varlen", "sdpa_sparse_forward", "sdpa_sparse_compact", "SdpaPlan",
            "sdpa_mask_tiles", "sdpa_forward_masked_noalloc", "head_range",
            "sdpa_forward_heads", "SdpaPagedCache", "sdpa_cache_append", "sdpa_paged_forward",
-           "sdpa_norm_rotate"]
+           "sdpa_norm_rotate", "PageCopies", "sdpa_pages_take", "sdpa_pages_fork", "sdpa_pages_release",
+           "sdpa_cache_copy_pages", "sdpa_cache_compact"]
 
 LIB_PATH = _build.LIB_PATH
 
@@ -131,6 +133,16 @@ def load_library(path: str | None = None):
     lib.sdpa_paged_forward_window.argtypes = [vp, vp, vp, ctypes.c_int, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp,
                                               i64, i64, i64, i64, ctypes.c_float, vp, ctypes.c_uint64, vp]
     lib.sdpa_paged_forward_window.restype = ctypes.c_int
+    lib.sdpa_pages_take.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp]
+    lib.sdpa_pages_take.restype = ctypes.c_int
+    lib.sdpa_pages_fork.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    lib.sdpa_pages_fork.restype = ctypes.c_int
+    lib.sdpa_pages_release.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, i64, vp]
+    lib.sdpa_pages_release.restype = ctypes.c_int
+    lib.sdpa_cache_copy_pages.argtypes = [vp, vp, vp, vp, i64, vp]
+    lib.sdpa_cache_copy_pages.restype = ctypes.c_int
+    lib.sdpa_cache_compact.argtypes = [vp, vp, i64, i64, vp, i64, i64, vp, vp, i64, i64, i64, vp]
+    lib.sdpa_cache_compact.restype = ctypes.c_int
     lib.sdpa_paged_workspace_bytes.argtypes = [i64, i64, i64, i64]
     lib.sdpa_paged_workspace_bytes.restype = ctypes.c_uint64
     if path is None:
@@ -848,6 +860,197 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
         if rc != 0:
             raise SdpaError(rc, where)
         return o if ls is None else (o, ls)
+
+    return _on_device(device, where, stream, call)
+
+
+class PageCopies(NamedTuple):
+    """What sdpa_pages_fork leaves to be copied: int32 pages ``src`` and
+    ``dst`` and the number of their tokens, ``rows`` (-1, -1, 0: nothing), for
+    sdpa_cache_copy_pages; ``missing``, int32 [1]: pages that there were too
+    few of."""
+    src: object
+    dst: object
+    rows: object
+    missing: object
+
+
+def _int_vectors(where, device, n, *vectors):
+    """int32 [n] each (or None), contiguous, on the device."""
+    for t in vectors:
+        if t is None:
+            continue
+        if t.dtype is not _torch.int32:
+            raise SdpaError(4, where)
+        if t.dim() != 1 or t.shape[0] != n:
+            raise SdpaError(3, where)
+        if not t.is_contiguous():
+            raise SdpaError(5, where)
+        if t.get_device() != device:
+            raise SdpaError(6, where)
+
+
+def _int_table(where, device, t, rows=None):
+    """int32 [rows, columns] on the device; (rows, columns, row stride)."""
+    if t.dtype is not _torch.int32:
+        raise SdpaError(4, where)
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows):
+        raise SdpaError(3, where)
+    if t.stride(1) != 1 and shape[1] != 1:
+        raise SdpaError(5, where)
+    if t.get_device() != device:
+        raise SdpaError(6, where)
+    return shape[0], shape[1], t.stride(0)
+
+
+def _accounts(where, refs, page_table):
+    _need_torch()
+    if refs.dtype is not _torch.int32:
+        raise SdpaError(4, where)
+    if refs.dim() != 1:
+        raise SdpaError(3, where)
+    if not refs.is_contiguous():
+        raise SdpaError(5, where)
+    device = refs.get_device()
+    return device, *_int_table(where, device, page_table)
+
+
+def sdpa_pages_take(refs, page_table, from_lens, to_lens, page_size, *, stream=None):
+    """Free pages for new tokens (sdpa_pages_take): row i of ``page_table``
+    (int32 [n_rows, max_pages]) gets pages for its tokens [from_lens[i],
+    to_lens[i]) (int32 [n_rows]) that do not lie in the page of token
+    from_lens[i] - 1, the lowest ones without references first, each with one
+    reference in ``refs`` (int32 [n_pages]) then.  Returns ``missing``, int32
+    [1]: pages that there were too few of (their entries are -1)."""
+    where = "sdpa_pages_take"
+    device, rows, columns, stride = _accounts(where, refs, page_table)
+    _int_vectors(where, device, rows, from_lens, to_lens)
+    if device < 0:
+        raise SdpaError(6, where)
+
+    def call(st):
+        missing = _torch.empty(1, dtype=_torch.int32, device=refs.device)
+        rc = load_library().sdpa_pages_take(refs.data_ptr(), refs.shape[0], page_table.data_ptr(), stride, rows, columns, page_size,
+                                            from_lens.data_ptr(), to_lens.data_ptr(), missing.data_ptr(), st)
+        if rc != 0:
+            raise SdpaError(rc, where)
+        return missing
+
+    return _on_device(device, where, stream, call)
+
+
+def sdpa_pages_fork(refs, page_table, kv_lens, src, dst, page_size, new_table=None, *, stream=None):
+    """Sequences as copies of others (sdpa_pages_fork): row dst[i] of
+    ``new_table`` (None: ``page_table`` itself) gives up what it held, shares the
+    full pages of row src[i] of ``page_table`` (length kv_lens[src[i]]) and gets
+    a free page of its own for the one that is begun.  refs: int32 [n_pages]
+    references; kv_lens: int32 [n_rows]; src, dst: int32 [n], no dst twice or
+    (in one table) another's src.  Returns PageCopies: what sdpa_cache_copy_pages
+    has to copy in every layer's cache."""
+    where = "sdpa_pages_fork"
+    device, rows, columns, stride = _accounts(where, refs, page_table)
+    new_rows, new_stride = rows, stride
+    if new_table is not None:
+        new_rows, new_columns, new_stride = _int_table(where, device, new_table)
+        if new_columns != columns:
+            raise SdpaError(3, where)
+    _int_vectors(where, device, rows, kv_lens)
+    if src.dim() != 1:
+        raise SdpaError(3, where)
+    n = src.shape[0]
+    _int_vectors(where, device, n, src, dst)
+    if device < 0:
+        raise SdpaError(6, where)
+
+    def call(st):
+        dev = refs.device
+        copies = PageCopies(*_torch.empty((3, n), dtype=_torch.int32, device=dev).unbind(0),
+                            _torch.empty(1, dtype=_torch.int32, device=dev))
+        rc = load_library().sdpa_pages_fork(
+            refs.data_ptr(), refs.shape[0], page_table.data_ptr(), stride, rows,
+            (page_table if new_table is None else new_table).data_ptr(), new_stride, new_rows, columns, page_size,
+            kv_lens.data_ptr(), src.data_ptr(), dst.data_ptr(), n, copies.src.data_ptr(), copies.dst.data_ptr(),
+            copies.rows.data_ptr(), copies.missing.data_ptr(), st)
+        if rc != 0:
+            raise SdpaError(rc, where)
+        return copies
+
+    return _on_device(device, where, stream, call)
+
+
+def sdpa_pages_release(refs, page_table, from_lens, to_lens, page_size, rows=None, *, stream=None):
+    """Pages given back (sdpa_pages_release): row rows[i] (None: row i) of
+    ``page_table`` loses those that lie wholly within its tokens [from_lens[i],
+    to_lens[i]) (None: from the first, to the row's end), and they a reference
+    each in ``refs``.  What a window leaves behind before the next token:
+    from_lens = sinks, to_lens = kv_lens + 1 - window."""
+    where = "sdpa_pages_release"
+    device, n_rows, columns, stride = _accounts(where, refs, page_table)
+    n = n_rows
+    if rows is not None:
+        if rows.dim() != 1:
+            raise SdpaError(3, where)
+        n = rows.shape[0]
+    _int_vectors(where, device, n, rows, from_lens, to_lens)
+    if device < 0:
+        raise SdpaError(6, where)
+
+    def call(st):
+        rc = load_library().sdpa_pages_release(
+            refs.data_ptr(), refs.shape[0], page_table.data_ptr(), stride, n_rows, columns, page_size,
+            rows.data_ptr() if rows is not None else None, from_lens.data_ptr() if from_lens is not None else None,
+            to_lens.data_ptr() if to_lens is not None else None, n, st)
+        if rc != 0:
+            raise SdpaError(rc, where)
+
+    return _on_device(device, where, stream, call)
+
+
+def sdpa_cache_copy_pages(cache, src, dst, rows=None, *, stream=None):
+    """Copies pages (sdpa_cache_copy_pages): keys, values and scales of page
+    src[i] to page dst[i] (int32 [n]), or of its first rows[i] tokens.  No page
+    is dst twice, or dst and src; entries that are no pages do nothing."""
+    where = "sdpa_cache_copy_pages"
+    device = cache.device
+    if src.dim() != 1:
+        raise SdpaError(3, where)
+    n = src.shape[0]
+    _int_vectors(where, device, n, src, dst, rows)
+    if device < 0:
+        raise SdpaError(6, where)
+
+    def call(st):
+        rc = load_library().sdpa_cache_copy_pages(cache._ref, src.data_ptr(), dst.data_ptr(),
+                                                  rows.data_ptr() if rows is not None else None, n, st)
+        if rc != 0:
+            raise SdpaError(rc, where)
+
+    return _on_device(device, where, stream, call)
+
+
+def sdpa_cache_compact(cache, page_table, kept, new_table, kept_lens=None, *, stream=None):
+    """Moves the tokens that are kept together (sdpa_cache_compact): token i of
+    sequence b in the pages new_table[b] is the one at position kept[b, i] in the
+    pages page_table[b], for i < kept_lens[b] (None: all of kept's row).
+    page_table, kept, new_table: int32 [n_seqs, ..]; kept_lens: int32 [n_seqs].
+    The new pages are none of those that are read.  Keys stay rotated by their
+    old positions."""
+    where = "sdpa_cache_compact"
+    device = cache.device
+    n_seqs, max_pages, stride = _int_table(where, device, page_table)
+    _, max_kept, kept_stride = _int_table(where, device, kept, n_seqs)
+    _, new_pages, new_stride = _int_table(where, device, new_table, n_seqs)
+    _int_vectors(where, device, n_seqs, kept_lens)
+    if device < 0:
+        raise SdpaError(6, where)
+
+    def call(st):
+        rc = load_library().sdpa_cache_compact(
+            cache._ref, page_table.data_ptr(), stride, max_pages, kept.data_ptr(), kept_stride, max_kept,
+            kept_lens.data_ptr() if kept_lens is not None else None, new_table.data_ptr(), new_stride, new_pages, n_seqs, st)
+        if rc != 0:
+            raise SdpaError(rc, where)
 
     return _on_device(device, where, stream, call)
 

@@ -210,6 +210,81 @@ constexpr int kScaleMinExp = -50, kScaleMaxExp = 50;
 cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, bool e4m3, int sms,
                                 cudaStream_t stream);
 cudaError_t launch_norm_rotate(const RowsParams& p, int head_dim, bool bf16, int sms, cudaStream_t stream);
+
+// A cache's pages as bytes.
+struct PageBytes {
+  uint8_t* p[2];            // keys, values
+  float* scale[2];          // e4m3: [n_pages, n_kv] (null for 16-bit caches)
+  int64_t sp[2], st[2], sh[2];   // BYTE strides of pages, tokens, heads
+  int n_pages, n_kv, page_shift;
+  int row_shift;            // 16-byte pieces of a head's row = 1 << row_shift
+  unsigned int h_mul;       // n / n_kv = n h_mul >> h_shift, for 31-bit n
+  int h_shift;
+};
+struct CopyPagesParams {
+  PageBytes c;
+  const int* src;           // [n] pages
+  const int* dst;
+  const int* rows;          // [n] first tokens to copy, or null: all
+  int n;
+  int slabs;                // blocks a page of keys (or values)
+};
+struct CompactPagesParams {
+  PageBytes c;
+  const int* table;         // [n_seqs, max_len / page size]
+  int64_t table_st;
+  const int* kept;          // [n_seqs, max_kept] positions
+  int64_t kept_st;
+  const int* kept_lens;     // [n_seqs], or null: max_kept each
+  const int* new_table;     // [n_seqs, ..], at least `entries` columns
+  int64_t new_st;
+  int n_seqs, max_kept, max_len;
+  int entries;              // new pages of a sequence, at most
+  int unit_shift, groups;   // heads of a block = 1 << unit_shift, groups of them
+};
+// References to pages: refs[page] of them, none: the page is free.
+struct PageTable {
+  int* refs;                // [n_pages]
+  int* table;               // [rows, max_pages]
+  int64_t st;
+  int n_pages, rows, max_pages, page_shift;
+};
+struct ForkParams {
+  PageTable t;              // the source rows (only read), and the counts
+  int* new_table;           // the rows to write, as many columns
+  int64_t new_st;
+  int new_rows;
+  int same;                 // new_table is the table
+  const int* lens;          // [rows]
+  const int* src;           // [n] rows
+  const int* dst;           // [n] rows of new_table
+  int n;
+  int* copy_src;            // [n] pages to copy (-1: none)
+  int* copy_dst;
+  int* copy_rows;
+  int* missing;             // pages that there were too few of
+};
+struct TakeParams {
+  PageTable t;
+  const int* from;          // [rows]
+  const int* to;
+  int* missing;
+};
+struct ReleaseParams {
+  PageTable t;
+  const int* which;         // [n] rows, or null: 0 .. n - 1
+  const int* from;          // [n], or null: 0
+  const int* to;            // [n], or null: the row's end
+  int n;
+};
+cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream);
+cudaError_t launch_compact_pages(const CompactPagesParams& p, bool e4m3, cudaStream_t stream);
+constexpr int kSlabPieces = 2048;    // 16-byte pieces of a block of launch_copy_pages
+// Rows (pairs) of a call that takes pages: a prefix sum over them lies in shared memory.
+constexpr int kMostRequests = 32768;
+cudaError_t launch_fork(const ForkParams& p, int device, cudaStream_t stream);
+cudaError_t launch_take(const TakeParams& p, int device, cudaStream_t stream);
+cudaError_t launch_release(const ReleaseParams& p, cudaStream_t stream);
 constexpr int kJoinNoteBytes = 32;  // a CTA's note at the workspace's start
 
 // How a launch is divided: CTAs, rows and key/value heads of a unit, keys of
