@@ -877,12 +877,13 @@ class PageCopies(NamedTuple):
 
 def _int_vectors(where, device, n, *vectors):
     """int32 [n] each (or None), contiguous, on the device."""
+    i32 = _torch.int32
     for t in vectors:
         if t is None:
             continue
-        if t.dtype is not _torch.int32:
+        if t.dtype is not i32:
             raise SdpaError(4, where)
-        if t.dim() != 1 or t.shape[0] != n:
+        if t.dim() != 1 or t.numel() != n:
             raise SdpaError(3, where)
         if not t.is_contiguous():
             raise SdpaError(5, where)
@@ -894,18 +895,23 @@ def _int_table(where, device, t, rows=None):
     """int32 [rows, columns] on the device; (rows, columns, row stride)."""
     if t.dtype is not _torch.int32:
         raise SdpaError(4, where)
-    shape = t.shape
-    if len(shape) != 2 or (rows is not None and shape[0] != rows):
+    if t.dim() != 2:
         raise SdpaError(3, where)
-    if t.stride(1) != 1 and shape[1] != 1:
+    n_rows, columns = t.shape
+    if rows is not None and n_rows != rows:
+        raise SdpaError(3, where)
+    stride, last = t.stride()
+    if last != 1 and columns != 1:
         raise SdpaError(5, where)
     if t.get_device() != device:
         raise SdpaError(6, where)
-    return shape[0], shape[1], t.stride(0)
+    return n_rows, columns, stride
 
 
 def _accounts(where, refs, page_table):
-    _need_torch()
+    """(device, number of pages, rows, columns, row stride)"""
+    if _torch is None:
+        _need_torch()
     if refs.dtype is not _torch.int32:
         raise SdpaError(4, where)
     if refs.dim() != 1:
@@ -913,7 +919,7 @@ def _accounts(where, refs, page_table):
     if not refs.is_contiguous():
         raise SdpaError(5, where)
     device = refs.get_device()
-    return device, *_int_table(where, device, page_table)
+    return device, refs.numel(), *_int_table(where, device, page_table)
 
 
 def sdpa_pages_take(refs, page_table, from_lens, to_lens, page_size, *, stream=None):
@@ -924,14 +930,14 @@ def sdpa_pages_take(refs, page_table, from_lens, to_lens, page_size, *, stream=N
     reference in ``refs`` (int32 [n_pages]) then.  Returns ``missing``, int32
     [1]: pages that there were too few of (their entries are -1)."""
     where = "sdpa_pages_take"
-    device, rows, columns, stride = _accounts(where, refs, page_table)
+    device, n_pages, rows, columns, stride = _accounts(where, refs, page_table)
     _int_vectors(where, device, rows, from_lens, to_lens)
     if device < 0:
         raise SdpaError(6, where)
 
     def call(st):
-        missing = _torch.empty(1, dtype=_torch.int32, device=refs.device)
-        rc = load_library().sdpa_pages_take(refs.data_ptr(), refs.shape[0], page_table.data_ptr(), stride, rows, columns, page_size,
+        missing = refs.new_empty(1)
+        rc = load_library().sdpa_pages_take(refs.data_ptr(), n_pages, page_table.data_ptr(), stride, rows, columns, page_size,
                                             from_lens.data_ptr(), to_lens.data_ptr(), missing.data_ptr(), st)
         if rc != 0:
             raise SdpaError(rc, where)
@@ -949,7 +955,7 @@ def sdpa_pages_fork(refs, page_table, kv_lens, src, dst, page_size, new_table=No
     (in one table) another's src.  Returns PageCopies: what sdpa_cache_copy_pages
     has to copy in every layer's cache."""
     where = "sdpa_pages_fork"
-    device, rows, columns, stride = _accounts(where, refs, page_table)
+    device, n_pages, rows, columns, stride = _accounts(where, refs, page_table)
     new_rows, new_stride = rows, stride
     if new_table is not None:
         new_rows, new_columns, new_stride = _int_table(where, device, new_table)
@@ -958,17 +964,15 @@ def sdpa_pages_fork(refs, page_table, kv_lens, src, dst, page_size, new_table=No
     _int_vectors(where, device, rows, kv_lens)
     if src.dim() != 1:
         raise SdpaError(3, where)
-    n = src.shape[0]
+    n = src.numel()
     _int_vectors(where, device, n, src, dst)
     if device < 0:
         raise SdpaError(6, where)
 
     def call(st):
-        dev = refs.device
-        copies = PageCopies(*_torch.empty((3, n), dtype=_torch.int32, device=dev).unbind(0),
-                            _torch.empty(1, dtype=_torch.int32, device=dev))
+        copies = PageCopies(refs.new_empty(n), refs.new_empty(n), refs.new_empty(n), refs.new_empty(1))
         rc = load_library().sdpa_pages_fork(
-            refs.data_ptr(), refs.shape[0], page_table.data_ptr(), stride, rows,
+            refs.data_ptr(), n_pages, page_table.data_ptr(), stride, rows,
             (page_table if new_table is None else new_table).data_ptr(), new_stride, new_rows, columns, page_size,
             kv_lens.data_ptr(), src.data_ptr(), dst.data_ptr(), n, copies.src.data_ptr(), copies.dst.data_ptr(),
             copies.rows.data_ptr(), copies.missing.data_ptr(), st)
@@ -986,19 +990,19 @@ def sdpa_pages_release(refs, page_table, from_lens, to_lens, page_size, rows=Non
     each in ``refs``.  What a window leaves behind before the next token:
     from_lens = sinks, to_lens = kv_lens + 1 - window."""
     where = "sdpa_pages_release"
-    device, n_rows, columns, stride = _accounts(where, refs, page_table)
+    device, n_pages, n_rows, columns, stride = _accounts(where, refs, page_table)
     n = n_rows
     if rows is not None:
         if rows.dim() != 1:
             raise SdpaError(3, where)
-        n = rows.shape[0]
+        n = rows.numel()
     _int_vectors(where, device, n, rows, from_lens, to_lens)
     if device < 0:
         raise SdpaError(6, where)
 
     def call(st):
         rc = load_library().sdpa_pages_release(
-            refs.data_ptr(), refs.shape[0], page_table.data_ptr(), stride, n_rows, columns, page_size,
+            refs.data_ptr(), n_pages, page_table.data_ptr(), stride, n_rows, columns, page_size,
             rows.data_ptr() if rows is not None else None, from_lens.data_ptr() if from_lens is not None else None,
             to_lens.data_ptr() if to_lens is not None else None, n, st)
         if rc != 0:
@@ -1015,7 +1019,7 @@ def sdpa_cache_copy_pages(cache, src, dst, rows=None, *, stream=None):
     device = cache.device
     if src.dim() != 1:
         raise SdpaError(3, where)
-    n = src.shape[0]
+    n = src.numel()
     _int_vectors(where, device, n, src, dst, rows)
     if device < 0:
         raise SdpaError(6, where)

@@ -34,6 +34,8 @@
 // rotation needs no exchange.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "sdpa_paged.cuh"
 
 using namespace sdpa_dev;
@@ -134,6 +136,12 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const float4& c, const fl
   }
 }
 
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // The lane's weights (of elements ea .. ea + 3, eb .. eb + 3).
 __device__ __forceinline__ void load_weights(const float* weight, const Lane& l, float (&w)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(weight + l.ea));
@@ -149,53 +157,57 @@ __device__ __forceinline__ float row_sum(float x) {
   for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+__device__ __forceinline__ float square_sum(const uint64_t (&v)[4]) {
+  float a, b;
+  unpair(fma2(v[3], v[3], fma2(v[2], v[2], fma2(v[1], v[1], mul2(v[0], v[0])))), a, b);
+  return a + b;
+}
 
-// Rows x[0 .. N) normalised; LANES lanes hold a row, the whole warp calls it.
-// Squares below 2^-126 do not matter beside eps >= 2^-100; those of values above
-// 2^60 (bf16) may overflow, and such rows are summed again 2^-70 times as large.
+// 1 / sqrt(mean of squares + eps) of rows v[0 .. N), LANES lanes a row; the whole
+// warp calls it.  Squares below 2^-126 do not matter beside eps >= 2^-100; those of
+// values above 2^60 (bf16) may overflow: such a row becomes 2^-70 times as large
+// and is summed again, without eps (nothing beside squares above 2^120).
+template <int LANES, int N>
+__device__ __forceinline__ void row_factors(uint64_t (&v)[N][4], float eps, float (&r)[N]) {
+  float most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) r[k] = square_sum(v[k]);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    r[k] = row_sum<LANES>(r[k]);
+    most = fmaxf(most, r[k]);   // (drops a NaN)
+  }
+  if (__any_sync(0xffffffffu, most == INFINITY)) {
+    const float down = 8.470329472543003e-22f;   // 2^-70
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const bool large = r[k] == INFINITY;
+      const float f = large ? down : 1.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[k][e] = mul2(v[k][e], pair(f, f));
+      r[k] = rsqrtf(fmaf(row_sum<LANES>(square_sum(v[k])), 1.0f / (8 * LANES), large ? 0.0f : eps));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k] = rsqrtf(fmaf(r[k], 1.0f / (8 * LANES), eps));
+  }
+}
+
+// Rows x[0 .. N) normalised.
 template <int LANES, int N>
 __device__ __forceinline__ void normalise(float (&x)[N][8], const float (&w)[8], float eps) {
-  float ss[N];
-  bool over = false;
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    float a = x[k][0] * x[k][0], b = x[k][1] * x[k][1];
-#pragma unroll
-    for (int e = 2; e < 8; e += 2) {
-      a = fmaf(x[k][e], x[k][e], a);
-      b = fmaf(x[k][e + 1], x[k][e + 1], b);
-    }
-    ss[k] = a + b;
-  }
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    ss[k] = row_sum<LANES>(ss[k]);
-    over |= ss[k] == INFINITY;
-    ss[k] = rsqrtf(fmaf(ss[k], 1.0f / (8 * LANES), eps));
-  }
-  if (__any_sync(0xffffffffu, over)) {
-    const float down = 8.470329472543003e-22f;   // 2^-70
-#pragma unroll 1
-    for (int k = 0; k < N; ++k) {
-      float a = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float y = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) y = i == k ? x[i][e] : y;
-        a = fmaf(y * down, y * down, a);
-      }
-      a = row_sum<LANES>(a);
-      // (from 2^60 on, where the plain sum overflows, eps is nothing)
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i == k && ss[i] == 0.0f) ss[i] = rsqrtf(a * (1.0f / (8 * LANES))) * down;
-    }
-  }
+  uint64_t v[N][4];
 #pragma unroll
   for (int k = 0; k < N; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[k][e] = x[k][e] * ss[k] * w[e];
+    for (int e = 0; e < 4; ++e) v[k][e] = pair(x[k][2 * e], x[k][2 * e + 1]);
+  float r[N];
+  row_factors<LANES, N>(v, eps, r);
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      unpair(mul2(mul2(v[k][e], pair(r[k], r[k])), pair(w[2 * e], w[2 * e + 1])), x[k][2 * e], x[k][2 * e + 1]);
 }
 
 // The page's new tokens: positions [lo, hi), the first being row t0 of k, v, q.
@@ -372,37 +384,25 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
   }
 }
 
-// One warp: heads [h0, h1) of one token, normalised (NORM, with weights), rotated
-// (ROT) or copied, four rows a lane at a time.  (c, s): the lane's angles.
-template <int D, bool BF16, bool ROT, bool NORM>
+// One warp: heads [h0, h1) of one token, rotated (ROT) or copied, four rows a
+// lane at a time.  (c, s): the lane's angles.
+template <int D, bool BF16, bool ROT>
 __device__ __forceinline__ void token_rows(int interleaved, const Lane& at, const float4& c, const float4& s,
                                            const uint16_t* src, int64_t src_sh, uint8_t* dst, int64_t dst_sh_bytes,
-                                           const float* weight, float eps, int h0, int h1) {
+                                           int h0, int h1) {
   constexpr int kLanes = D / 8;
   constexpr int kRows = 32 / kLanes;
-  const int sub = static_cast<int>(threadIdx.x & 31) / kLanes;
-  int h = h0 + sub;
+  int h = h0 + static_cast<int>(threadIdx.x & 31) / kLanes;
   src += h * src_sh;
   dst += h * dst_sh_bytes;
   const int64_t src_step = kRows * src_sh, dst_step = kRows * dst_sh_bytes;
-  // (a norm's sums are exchanged: the warp stays together)
 #pragma unroll 1
-  for (; (NORM ? h - sub : h) < h1; h += kBatch * kRows) {
+  for (; h < h1; h += kBatch * kRows) {
     float x[kBatch][8];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (h + u * kRows < h1) {
-        load8<BF16>(src, at, x[u]);
-      } else if (NORM) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
-      }
+      if (h + u * kRows < h1) load8<BF16>(src, at, x[u]);
       src += src_step;
-    }
-    if (NORM && weight != nullptr) {
-      float w[8];
-      load_weights(weight, at, w);
-      normalise<kLanes, kBatch>(x, w, eps);
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -413,6 +413,138 @@ __device__ __forceinline__ void token_rows(int interleaved, const Lane& at, cons
       dst += dst_step;
     }
   }
+}
+
+// The same heads normalised, then rotated.  The weights go into the angles, once a
+// token, and a row's factor comes last: an element is (x m + x' n) r, m and n the
+// products of its weight and its pair's with cosine and sine, x' the pair's other
+// element (as many roundings as with the factor first).  The next rows are on
+// their way while these are turned, and the first before the token's place is
+// known: angles(c, s) looks it up, false for a token that is left out.
+// PAIRED: neighbours are pairs.  ALL: all of a head is rotated.
+constexpr int kNormBatch = 2;
+template <int D, bool BF16, bool PAIRED, bool ALL, class Angles>
+__device__ __forceinline__ void norm_rows_as(const Lane& at, Angles&& angles, const uint16_t* src, int64_t src_sh,
+                                             uint8_t* dst, int64_t dst_sh_bytes, const float* weight, float eps, int h0, int h1) {
+  constexpr int kLanes = D / 8;
+  constexpr int kRows = 32 / kLanes;
+  const int sub = static_cast<int>(threadIdx.x & 31) / kLanes;
+  // from a lane's first four elements to its others (bytes)
+  const int apart = PAIRED ? 8 : ALL ? D : 2 * (at.eb - at.ea);
+  const uint8_t* from = reinterpret_cast<const uint8_t*>(src + (h0 + sub) * src_sh + at.ea);
+  const int64_t from_step = kRows * src_sh * 2, to_step = kRows * dst_sh_bytes;
+  uint2 raw[kNormBatch][2];
+  auto ask = [&](int h) {
+    // (plain loads: the queries may be rotated in place)
+    if (h + kNormBatch * kRows <= h1) {
+#pragma unroll
+      for (int u = 0; u < kNormBatch; ++u) {
+        raw[u][0] = *reinterpret_cast<const uint2*>(from);
+        raw[u][1] = *reinterpret_cast<const uint2*>(from + apart);
+        from += from_step;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kNormBatch; ++u) {
+        raw[u][0] = raw[u][1] = make_uint2(0u, 0u);
+        if (h + sub + u * kRows < h1) {
+          raw[u][0] = *reinterpret_cast<const uint2*>(from);
+          raw[u][1] = *reinterpret_cast<const uint2*>(from + apart);
+        }
+        from += from_step;
+      }
+    }
+  };
+  ask(h0);
+  float w[8];
+  load_weights(weight, at, w);
+  float4 c, s;
+  if (!angles(c, s)) return;
+  uint64_t m[4], n[4];
+  if (!ALL && !at.rotated) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = pair(w[2 * e], w[2 * e + 1]), n[e] = 0;
+  } else if (PAIRED) {
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      m[e] = pair(w[2 * e] * cc[e], w[2 * e + 1] * cc[e]);
+      n[e] = pair(-w[2 * e + 1] * ss[e], w[2 * e] * ss[e]);
+    }
+  } else {
+    const uint64_t cc[2] = {pair(c.x, c.y), pair(c.z, c.w)}, ss[2] = {pair(s.x, s.y), pair(s.z, s.w)};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[e] = mul2(pair(w[2 * e], w[2 * e + 1]), cc[e]);
+      n[2 + e] = mul2(pair(w[2 * e], w[2 * e + 1]), ss[e]);
+      m[2 + e] = mul2(pair(w[4 + 2 * e], w[5 + 2 * e]), cc[e]);
+      n[e] = mul2(pair(-w[4 + 2 * e], -w[5 + 2 * e]), ss[e]);
+    }
+  }
+  uint8_t* to = dst + (h0 + sub) * dst_sh_bytes + 2 * at.ea;
+  // (the sums are exchanged: the warp stays together)
+#pragma unroll 1
+  for (int h = h0; h < h1; h += kNormBatch * kRows) {
+    uint64_t v[kNormBatch][4];
+    float r[kNormBatch];
+#pragma unroll
+    for (int u = 0; u < kNormBatch; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint2 x = raw[u][e >> 1];
+        const float2 f = unpack2<BF16>((e & 1) ? x.y : x.x);
+        v[u][e] = pair(f.x, f.y);
+      }
+    if (h + kNormBatch * kRows < h1) ask(h + kNormBatch * kRows);
+    row_factors<kLanes, kNormBatch>(v, eps, r);
+#pragma unroll
+    for (int u = 0; u < kNormBatch; ++u) {
+      uint64_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint64_t other = v[u][e ^ 2];
+        if (PAIRED) {
+          float a, b;
+          unpair(v[u][e], a, b);
+          other = pair(b, a);
+        }
+        // (an infinite element has no part in one that it is no pair of)
+        y[e] = !ALL && !at.rotated ? mul2(v[u][e], m[e]) : fma2(v[u][e], m[e], mul2(other, n[e]));
+      }
+      uint32_t out[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a, b;
+        unpair(mul2(y[e], pair(r[u], r[u])), a, b);
+        out[e] = pack2<BF16>(a, b);
+      }
+      if (h + sub + u * kRows < h1) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
+        *reinterpret_cast<uint2*>(to + apart) = make_uint2(out[2], out[3]);
+      }
+      to += to_step;
+    }
+  }
+}
+// (Knowing the form saves instructions: 8 x 4096 tokens of 32 + 8 heads 142 -> 139 us,
+// 17700 rows of 16 + 16 heads of 64 29.2 -> 27.7.  Two rows a lane at a time and four
+// blocks an SM: with four rows and three blocks 144 and 30.5, with one row 160 and
+// 34.5; without the next rows on their way 145 and 29.4.  Rows by asynchronous
+// copies into a ring in shared memory, eight a lane on their way: 136 and 27.6, with
+// twice the code and spills: not kept.)
+template <int D, bool BF16, class Angles>
+__device__ __forceinline__ void norm_rows(int rot, int interleaved, const Lane& at, Angles&& angles, const uint16_t* src,
+                                          int64_t src_sh, uint8_t* dst, int64_t dst_sh_bytes, const float* weight, float eps,
+                                          int h0, int h1) {
+  auto go = [&](auto paired, auto all) {
+    norm_rows_as<D, BF16, paired.value, all.value>(at, angles, src, src_sh, dst, dst_sh_bytes, weight, eps, h0, h1);
+  };
+  using std::false_type;
+  using std::true_type;
+  if (interleaved)
+    rot == D ? go(true_type{}, true_type{}) : go(true_type{}, false_type{});
+  else
+    rot == D ? go(false_type{}, true_type{}) : go(false_type{}, false_type{});
 }
 
 // The last of n values, f(0) <= f(1) <= .., that is at most x (-1: none); the
@@ -484,66 +616,116 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   const int64_t tok = w / static_cast<unsigned>(parts);
   const int share = static_cast<int>(w % static_cast<unsigned>(parts));
   if (tok >= p.total) return;
-  const int b = last_at_most(p.n_seqs, static_cast<int>(tok), first_token);
-  if (b < 0) return;
-  const int q0 = first_token(b), q1 = first_token(b + 1);
-  if (tok >= q1) return;   // behind the last sequence
-  const int pos = __ldg(p.kv_lens + b) - (q1 - q0) + (static_cast<int>(tok) - q0);
-  if (pos < 0 || pos >= p.max_len || (p.cos != nullptr && pos >= p.n_pos)) return;
   const int j = (threadIdx.x & 31) % (D / 8);
   const Lane at = lane_of(j, ROT ? p.rot : 0, p.interleaved);
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ROT && at.rotated) {
-    const int64_t o = static_cast<int64_t>(pos) * (p.rot / 2) + 4 * j;
-    c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
-    s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
+  int b = -1, pos = -1;
+  // the token's sequence and position; false: it is left out
+  auto look_up = [&]() {
+    b = last_at_most(p.n_seqs, static_cast<int>(tok), first_token);
+    if (b < 0) return false;
+    const int q0 = first_token(b), q1 = first_token(b + 1);
+    if (tok >= q1) return false;   // behind the last sequence
+    pos = __ldg(p.kv_lens + b) - (q1 - q0) + (static_cast<int>(tok) - q0);
+    return pos >= 0 && pos < p.max_len && (p.cos == nullptr || pos < p.n_pos);
+  };
+  auto angles = [&](float4& c, float4& s) {
+    c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ROT && at.rotated) {
+      const int64_t o = static_cast<int64_t>(pos) * (p.rot / 2) + 4 * j;
+      c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
+      s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
+    }
+  };
+  float4 c, s;
+  const uint16_t* const q = reinterpret_cast<const uint16_t*>(p.q) + tok * p.q_st;
+  uint8_t* const q_out = reinterpret_cast<uint8_t*>(p.q_out) + tok * p.qo_st * 2;
+  const int qh0 = p.H * share / parts, qh1 = p.H * (share + 1) / parts;
+  if (NORM && p.q_norm != nullptr) {
+    bool there = false;
+    norm_rows<D, BF16>(
+        p.rot, p.interleaved, at,
+        [&](float4& cc, float4& ss) {
+          there = look_up();
+          if (there) angles(cc, ss);
+          return there;
+        },
+        q, p.q_sh, q_out, p.qo_sh * 2, p.q_norm, p.eps, qh0, qh1);
+    if (!there) return;
+  } else {
+    if (!look_up()) return;
+    angles(c, s);
+    if (p.q != nullptr) token_rows<D, BF16, ROT>(p.interleaved, at, c, s, q, p.q_sh, q_out, p.qo_sh * 2, qh0, qh1);
   }
-  if (p.q != nullptr)
-    token_rows<D, BF16, ROT, NORM>(p.interleaved, at, c, s, reinterpret_cast<const uint16_t*>(p.q) + tok * p.q_st, p.q_sh,
-                                   reinterpret_cast<uint8_t*>(p.q_out) + tok * p.qo_st * 2, p.qo_sh * 2, p.q_norm, p.eps,
-                                   p.H * share / parts, p.H * (share + 1) / parts);
   if constexpr (!E4M3) {
     const int page = __ldg(p.table + b * p.table_st + (pos >> p.page_shift));
     if (page < 0 || page >= p.n_pages) return;
     const int row = pos & (P - 1), h0 = p.n_kv * share / parts, h1 = p.n_kv * (share + 1) / parts;
-    token_rows<D, BF16, ROT, NORM>(p.interleaved, at, c, s, reinterpret_cast<const uint16_t*>(p.k) + tok * p.k_st, p.k_sh,
-                                   p.ck + page * p.ck_sp + row * p.ck_st, p.ck_sh, p.k_norm, p.eps, h0, h1);
+    const uint16_t* const k = reinterpret_cast<const uint16_t*>(p.k) + tok * p.k_st;
+    uint8_t* const ck = p.ck + page * p.ck_sp + row * p.ck_st;
+    if (NORM && p.k_norm != nullptr) {
+      norm_rows<D, BF16>(
+          p.rot, p.interleaved, at,
+          [&](float4& cc, float4& ss) {
+            angles(cc, ss);
+            return true;
+          },
+          k, p.k_sh, ck, p.ck_sh, p.k_norm, p.eps, h0, h1);
+    } else {
+      if (NORM) angles(c, s);   // (the queries' norm did not leave them)
+      token_rows<D, BF16, ROT>(p.interleaved, at, c, s, k, p.k_sh, ck, p.ck_sh, h0, h1);
+    }
     // (plain copies: every lane takes eight elements that lie together)
-    token_rows<D, BF16, false, false>(0, lane_of(j, 0, 0), c, s, reinterpret_cast<const uint16_t*>(p.v) + tok * p.v_st, p.v_sh,
-                                      p.cv + page * p.cv_sp + row * p.cv_st, p.cv_sh, nullptr, 0.0f, h0, h1);
+    token_rows<D, BF16, false>(0, lane_of(j, 0, 0), c, s, reinterpret_cast<const uint16_t*>(p.v) + tok * p.v_st, p.v_sh,
+                               p.cv + page * p.cv_sp + row * p.cv_st, p.cv_sh, h0, h1);
   }
 }
 
-// Rows without a cache: a warp takes a share (1 / parts) of one token's query and
-// key heads.
+// Rows without a cache: a warp takes a share (1 / 2^parts_shift) of one token's query
+// and key heads.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, kPerSm)
-    norm_rotate_kernel(const __grid_constant__ sdpa_impl::RowsParams p, int parts) {
+    norm_rotate_kernel(const __grid_constant__ sdpa_impl::RowsParams p, int parts_shift) {
   grid_dependency_wait();
   grid_launch_dependents();
   const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t tok = w / static_cast<unsigned>(parts);
-  const int share = static_cast<int>(w % static_cast<unsigned>(parts));
+  const int64_t tok = w >> parts_shift;
+  const int share = static_cast<int>(w & ((1u << parts_shift) - 1u));
   if (tok >= p.total) return;
   const int j = (threadIdx.x & 31) % (D / 8);
   const Lane at = lane_of(j, p.rot, p.interleaved);
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.rot > 0) {
-    const int pos = p.positions != nullptr ? __ldg(p.positions + tok) : static_cast<int>(tok);
-    if (pos < 0 || pos >= p.n_pos) return;
+  // the row's position (before: none yet), and its angles; false: it is left out
+  int pos = -1;
+  auto angles = [&](float4& c, float4& s) {
+    c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.rot == 0) return true;
+    if (pos < 0) pos = p.positions != nullptr ? __ldg(p.positions + tok) : static_cast<int>(tok);
+    if (pos < 0 || pos >= p.n_pos) return false;
     if (at.rotated) {
       const int64_t o = static_cast<int64_t>(pos) * (p.rot / 2) + 4 * j;
       c = __ldg(reinterpret_cast<const float4*>(p.cos + o));
       s = __ldg(reinterpret_cast<const float4*>(p.sin + o));
     }
-  }
-  token_rows<D, BF16, true, true>(p.interleaved, at, c, s, reinterpret_cast<const uint16_t*>(p.q) + tok * p.q_st, p.q_sh,
-                                  reinterpret_cast<uint8_t*>(p.q_out) + tok * p.qo_st * 2, p.qo_sh * 2, p.q_norm, p.eps,
-                                  p.H * share / parts, p.H * (share + 1) / parts);
-  if (p.k != nullptr)
-    token_rows<D, BF16, true, true>(p.interleaved, at, c, s, reinterpret_cast<const uint16_t*>(p.k) + tok * p.k_st, p.k_sh,
-                                    reinterpret_cast<uint8_t*>(p.k_out) + tok * p.ko_st * 2, p.ko_sh * 2, p.k_norm, p.eps,
-                                    p.n_kv * share / parts, p.n_kv * (share + 1) / parts);
+    return true;
+  };
+  auto rows = [&](const void* x, int64_t st, int64_t sh, void* out, int64_t ost, int64_t osh, const float* weight, int heads) {
+    const uint16_t* const from = reinterpret_cast<const uint16_t*>(x) + tok * st;
+    uint8_t* const to = reinterpret_cast<uint8_t*>(out) + tok * ost * 2;
+    const int h0 = (heads * share) >> parts_shift, h1 = (heads * (share + 1)) >> parts_shift;
+    bool there = true;
+    if (weight != nullptr) {
+      norm_rows<D, BF16>(
+          p.rot, p.interleaved, at,
+          [&](float4& c, float4& s) { return there = angles(c, s); },
+          from, sh, to, osh * 2, weight, p.eps, h0, h1);
+    } else {
+      float4 c, s;
+      there = angles(c, s);
+      if (there) token_rows<D, BF16, true>(p.interleaved, at, c, s, from, sh, to, osh * 2, h0, h1);
+    }
+    return there;
+  };
+  if (rows(p.q, p.q_st, p.q_sh, p.q_out, p.qo_st, p.qo_sh, p.q_norm, p.H) && p.k != nullptr)
+    rows(p.k, p.k_st, p.k_sh, p.k_out, p.ko_st, p.ko_sh, p.k_norm, p.n_kv);
 }
 
 // Warps a token: one, or several that share its heads where tokens are few.
@@ -571,7 +753,9 @@ cudaError_t launch_pdl(K kern, long long blocks, cudaStream_t stream, const A&..
 template <int D, bool BF16>
 cudaError_t launch_rows(const sdpa_impl::RowsParams& p, int sms, cudaStream_t stream) {
   const int parts = token_parts(p.total, p.H > p.n_kv ? p.H : p.n_kv, sms);
-  return launch_pdl(norm_rotate_kernel<D, BF16>, (static_cast<long long>(p.total) * parts + kWarps - 1) / kWarps, stream, p, parts);
+  int shift = 0;
+  while ((1 << shift) < parts) ++shift;
+  return launch_pdl(norm_rotate_kernel<D, BF16>, (static_cast<long long>(p.total) * parts + kWarps - 1) / kWarps, stream, p, shift);
 }
 
 template <int D, bool BF16, bool E4M3, bool ROT, bool NORM, int UNIT_WARPS>

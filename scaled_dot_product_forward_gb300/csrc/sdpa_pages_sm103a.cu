@@ -73,27 +73,67 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
       c.scale[which][static_cast<int64_t>(dst) * c.n_kv + h] = c.scale[which][static_cast<int64_t>(src) * c.n_kv + h];
 }
 
-// Sixteen e4m3 codes times a factor <= 1, each rounded once.
-__device__ __forceinline__ uint32_t scaled4(uint32_t w, float f) {
-  auto two = [&](uint32_t x) -> uint32_t {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffffu), __NV_E4M3);
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return __nv_cvt_float2_to_fp8x2(make_float2(v.x * f, v.y * f), __NV_SATFINITE, __NV_E4M3);
-  };
-  return two(w) | (two(w >> 16) << 16);
+// Sixteen e4m3 codes times a factor <= 1, each rounded once: in fp16, where a
+// power of two down to 2^-14 makes no other rounding (a product that fp16 does not
+// hold is far below half of e4m3's least step), else in fp32.
+__device__ __forceinline__ uint4 scaled16(const uint4& x, float f) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const bool exact = (__float_as_uint(f) & 0x7fffffu) == 0 && f >= 6.103515625e-5f;
+  const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2 h(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((w[e] >> (16 * i)) & 0xffffu), __NV_E4M3)));
+      uint32_t two;
+      if (exact) {
+        two = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hmul2(h, f2)), __NV_SATFINITE, __NV_E4M3);
+      } else {
+        const float2 v = __half22float2(h);
+        two = __nv_cvt_float2_to_fp8x2(make_float2(v.x * f, v.y * f), __NV_SATFINITE, __NV_E4M3);
+      }
+      out |= two << (16 * i);
+    }
+    w[e] = out;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void copy_16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
 // A block: the tokens of one new page, 1 << unit_shift of their key or value
-// heads.  e4m3: the new scale of a (page, head) is the largest of those under
-// which its tokens came, so that no value grows; each block finds it for its
-// heads, codes that came under that very scale are moved as they are.
+// heads, of which a thread has one 16-byte piece of every so many tokens.  e4m3:
+// the new scale of a (page, head) is the largest of those under which its tokens
+// came, so that no value grows; each block finds it for its heads, codes that
+// came under that very scale are moved as they are.
+//
+// Bound by latency before memory: a row's place is behind two lists (a third for
+// its scale), so what counts is that much is asked for at once.  The lists are
+// read together, then eight pieces a thread go to shared memory by asynchronous
+// copies, while the scales are compared.
+constexpr int kMove = 8;        // pieces of a thread at a time
+struct CompactSmem {
+  int data, from, old, total;   // byte offsets
+  __host__ __device__ CompactSmem(bool e4m3, int tokens, int unit_shift) {
+    data = 64;
+    from = data + kMove * kThreads * 16;
+    old = from + tokens * 8;
+    total = old + (e4m3 ? (tokens << unit_shift) * 4 : 0);
+  }
+};
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) compact_pages_kernel(const __grid_constant__ CompactPagesParams p) {
-  __shared__ int2 s_from[1024];      // page (-1: none) and row of each token
-  __shared__ float s_scale[16];
+__global__ void __launch_bounds__(kThreads, 6) compact_pages_kernel(const __grid_constant__ CompactPagesParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const PageBytes& c = p.c;
+  const CompactSmem at(E4M3, 1 << c.page_shift, p.unit_shift);
+  float* const s_scale = reinterpret_cast<float*>(smem);                 // [16] new scales
+  int2* const s_from = reinterpret_cast<int2*>(smem + at.from);          // each token's old page (-1: none) and row
+  float* const s_old = reinterpret_cast<float*>(smem + at.old);          // its scales, by head
   grid_dependency_wait();
   grid_launch_dependents();
-  const PageBytes& c = p.c;
   const int tid = static_cast<int>(threadIdx.x);
   unsigned block = blockIdx.x;
   const int group = static_cast<int>(block % static_cast<unsigned>(p.groups));
@@ -103,68 +143,83 @@ __global__ void __launch_bounds__(kThreads) compact_pages_kernel(const __grid_co
   const int entry = static_cast<int>(block % static_cast<unsigned>(p.entries));
   const int b = static_cast<int>(block / static_cast<unsigned>(p.entries));
   const int P = 1 << c.page_shift;
+  const int* const kept = p.kept + b * p.kept_st + (static_cast<int64_t>(entry) << c.page_shift);
+  const int* const table = p.table + b * p.table_st;
+  const int listed = min(P, p.max_kept - (entry << c.page_shift));
+  auto place = [&](int pos) { return pos >= 0 && pos < p.max_len ? __ldg(table + (pos >> c.page_shift)) : -1; };
+  int pos = tid < listed ? __ldg(kept + tid) : -1;
   const int n = p.kept_lens != nullptr ? min(max(__ldg(p.kept_lens + b), 0), p.max_kept) : p.max_kept;
-  const int count = min(P, n - (entry << c.page_shift));
-  if (count <= 0) return;
   const int page = __ldg(p.new_table + b * p.new_st + entry);
-  if (page < 0 || page >= c.n_pages) return;
+  int from = place(pos);
+  const int count = min(P, n - (entry << c.page_shift));
+  if (count <= 0 || page < 0 || page >= c.n_pages) return;
+  const int unit = 1 << p.unit_shift, h0 = group << p.unit_shift, heads = min(unit, c.n_kv - h0);
+  if (E4M3 && tid < 16) s_scale[tid] = 0.0f;
   for (int i = tid; i < count; i += kThreads) {
-    const int pos = __ldg(p.kept + b * p.kept_st + (entry << c.page_shift) + i);
-    int from = pos >= 0 && pos < p.max_len ? __ldg(p.table + b * p.table_st + (pos >> c.page_shift)) : -1;
+    if (i != tid) {
+      pos = __ldg(kept + i);
+      from = place(pos);
+    }
     if (from >= c.n_pages) from = -1;
     s_from[i] = make_int2(from, pos & (P - 1));
   }
-  if (tid < 16) s_scale[tid] = 0.0f;
   __syncthreads();
-  const int unit = 1 << p.unit_shift, h0 = group << p.unit_shift, heads = min(unit, c.n_kv - h0);
-  const float* const scales = c.scale[which] + h0;
-  if constexpr (E4M3) {
-    // (kThreads is a multiple of the heads: a thread stays with one)
-    const int h = tid & (unit - 1);
-    float top = 0.0f;
-    if (h < heads)
-      for (int i = tid >> p.unit_shift; i < count; i += kThreads >> p.unit_shift)
-        if (s_from[i].x >= 0) top = fmaxf(top, clamp_scale(scales[static_cast<int64_t>(s_from[i].x) * c.n_kv + h]));
-    for (int o = 16; o >= unit; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // (positive: ordered as their bits are)
-    if ((tid & 31) < unit) atomicMax(reinterpret_cast<int*>(s_scale + h), __float_as_int(top));
-    __syncthreads();
-    if (tid < heads && s_scale[tid] > 0.0f) c.scale[which][static_cast<int64_t>(page) * c.n_kv + h0 + tid] = s_scale[tid];
-  }
-  const uint8_t* const from0 = c.p[which] + h0 * c.sh[which];
-  uint8_t* const to0 = c.p[which] + page * c.sp[which] + h0 * c.sh[which];
-  const int pieces = count << (p.unit_shift + c.row_shift);
-  constexpr int kPer = 4;
-#pragma unroll 1
-  for (int u0 = tid; u0 < pieces; u0 += kPer * kThreads) {
-    uint4 x[kPer];
-    float f[kPer];
-    int64_t to[kPer];
+  // this thread's piece of a token, and its tokens (a token has at most 256 pieces)
+  const int per_token = p.unit_shift + c.row_shift;
+  const int h = (tid >> c.row_shift) & (unit - 1);
+  const int64_t piece = (h0 + h) * c.sh[which] + ((tid & ((1 << c.row_shift) - 1)) << 4);
+  const uint8_t* const from0 = c.p[which] + piece;
+  const int first = tid >> per_token, step = kThreads >> per_token;
+  const int tokens = h < heads ? count : 0;
+  uint8_t* const mine = smem + at.data + tid * 16;   // (a thread reads what it has asked for)
+  const uint32_t mine_at = smem_addr(mine);
+  auto ask = [&](int i0) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int u = u0 + k * kThreads;
-      const int r = u >> c.row_shift, h = r & (unit - 1), i = r >> p.unit_shift;
-      to[k] = -1;
-      f[k] = 1.0f;
-      if (u >= pieces || h >= heads) continue;
-      const int2 from = s_from[i];
-      if (from.x < 0) continue;
-      const int64_t piece = h * c.sh[which] + ((u & ((1 << c.row_shift) - 1)) << 4);
-      to[k] = i * c.st[which] + piece;
-      x[k] = *reinterpret_cast<const uint4*>(from0 + from.x * c.sp[which] + from.y * c.st[which] + piece);
-      if constexpr (E4M3) f[k] = clamp_scale(scales[static_cast<int64_t>(from.x) * c.n_kv + h]);
+    for (int k = 0; k < kMove; ++k) {
+      const int i = i0 + k * step;
+      const int2 o = i < tokens ? s_from[i] : make_int2(-1, 0);
+      if (o.x >= 0) copy_16(mine_at + k * (kThreads * 16), from0 + (o.x * c.sp[which] + o.y * c.st[which]));
     }
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (to[k] < 0) continue;
-      if constexpr (E4M3) {
-        const float now = s_scale[((u0 + k * kThreads) >> c.row_shift) & (unit - 1)];
-        if (f[k] != now) {
-          const float ratio = f[k] / now;
-          x[k] = make_uint4(scaled4(x[k].x, ratio), scaled4(x[k].y, ratio), scaled4(x[k].z, ratio), scaled4(x[k].w, ratio));
-        }
+    cp_async_commit();
+  };
+  ask(first);
+  if constexpr (E4M3) {
+    // (a warp's lanes: as many tokens, head by head)
+    for (int i0 = tid & ~31; i0 < count; i0 += kThreads) {
+      const int i = i0 + (tid & 31), page_i = i < count ? s_from[i].x : -1;
+      const float* const scales = c.scale[which] + static_cast<int64_t>(max(page_i, 0)) * c.n_kv + h0;
+#pragma unroll 4
+      for (int e = 0; e < heads; ++e) {
+        const float y = page_i >= 0 ? clamp_scale(__ldg(scales + e)) : 0.0f;
+        if (i < count) s_old[(i << p.unit_shift) + e] = y;
+        // (positive: ordered as their bits are)
+        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(y));
+        if ((tid & 31) == 0) atomicMax(reinterpret_cast<unsigned*>(s_scale + e), top);
       }
-      *reinterpret_cast<uint4*>(to0 + to[k]) = x[k];
+    }
+    __syncthreads();
+    if (tid < heads && s_scale[tid] > 0.0f)
+      c.scale[which][static_cast<int64_t>(page) * c.n_kv + h0 + tid] = s_scale[tid];
+  }
+  uint8_t* to = c.p[which] + piece + page * c.sp[which] + first * c.st[which];
+  const int64_t to_step = step * c.st[which];
+  const float now = E4M3 ? s_scale[h] : 1.0f;
+#pragma unroll 1
+  for (int i0 = first; i0 < tokens; i0 += kMove * step) {
+    if (i0 != first) ask(i0);
+    cp_async_wait<0>();
+#pragma unroll 4
+    for (int k = 0; k < kMove; ++k) {
+      const int i = i0 + k * step;
+      if (i < tokens && s_from[i].x >= 0) {
+        uint4 x = *reinterpret_cast<const uint4*>(mine + k * (kThreads * 16));
+        if constexpr (E4M3) {
+          const float old = s_old[(i << p.unit_shift) + h];
+          if (old != now) x = scaled16(x, old / now);
+        }
+        *reinterpret_cast<uint4*>(to) = x;
+      }
+      to += to_step;
     }
   }
 }
@@ -191,30 +246,41 @@ __device__ __forceinline__ bool fork_rows(const ForkParams& p, int i, int& src, 
 
 constexpr int kEntries = 4 * kThreads;   // of a block
 
-// A block: kEntries entries of a fork's new row, which lose what they held and
-// share the source's full pages.
-__global__ void __launch_bounds__(kThreads) fork_entries_kernel(const __grid_constant__ ForkParams p, int slabs) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int i = static_cast<int>(blockIdx.x / static_cast<unsigned>(slabs));
-  const int slab = static_cast<int>(blockIdx.x % static_cast<unsigned>(slabs));
+// Entries e0, e0 + step, .. (four of them, below the row's end) of fork i's new
+// row, which lose what they held and share the source's full pages.
+__device__ __forceinline__ void fork_entries(const ForkParams& p, int i, int e0, int step) {
   int src, dst, full, begun;
   if (!fork_rows(p, i, src, dst)) return;
   pages_of(p.t, __ldg(p.lens + src), full, begun);
   const int* const from = p.t.table + src * p.t.st;
   int* const to = p.new_table + dst * p.new_st;
+  int old[4], now[4];
 #pragma unroll
-  for (int k = 0; k < kEntries / kThreads; ++k) {
-    const int e = slab * kEntries + k * kThreads + static_cast<int>(threadIdx.x);
-    if (e >= p.t.max_pages) break;
-    const int old = to[e];
-    int now = e < full ? from[e] : -1;
-    if (!is_page(p.t, now)) now = -1;
-    if (now == old) continue;
-    if (is_page(p.t, old)) atomicAdd(p.t.refs + old, -1);
-    if (now >= 0) atomicAdd(p.t.refs + now, 1);
-    to[e] = now;
+  for (int k = 0; k < 4; ++k) {
+    const int e = e0 + k * step;
+    old[k] = now[k] = -1;
+    if (e >= p.t.max_pages) continue;
+    old[k] = to[e];
+    if (e < full) now[k] = from[e];
+    if (!is_page(p.t, now[k])) now[k] = -1;
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int e = e0 + k * step;
+    if (e >= p.t.max_pages || now[k] == old[k]) continue;
+    if (is_page(p.t, old[k])) atomicAdd(p.t.refs + old[k], -1);
+    if (now[k] >= 0) atomicAdd(p.t.refs + now[k], 1);
+    to[e] = now[k];
+  }
+}
+
+// A block: kEntries entries of a fork's new row.
+__global__ void __launch_bounds__(kThreads) fork_entries_kernel(const __grid_constant__ ForkParams p, int slabs) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int i = static_cast<int>(blockIdx.x / static_cast<unsigned>(slabs));
+  const int slab = static_cast<int>(blockIdx.x % static_cast<unsigned>(slabs));
+  fork_entries(p, i, slab * kEntries + static_cast<int>(threadIdx.x), kThreads);
 }
 
 // A block: kEntries entries of a row; those of pages wholly within [from, to) are
@@ -287,7 +353,8 @@ __device__ __forceinline__ void entries_to_take(const TakeParams& p, int i, int&
   n = max(f1 + (b1 != 0 ? 1 : 0) - e0, 0);
 }
 
-template <bool FORK, class Params>
+// FUSED: the forks' other entries too, a warp's 128 at a time.
+template <bool FORK, bool FUSED, class Params>
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPickThreads)
     pick_kernel(const __grid_constant__ Params p, int n) {
   extern __shared__ int prefix[];   // [n + 1]
@@ -295,9 +362,16 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPickThreads)
   __shared__ int found[2][kCtas], wants[kCtas];
   const int tid = static_cast<int>(threadIdx.x), cta = static_cast<int>(blockIdx.x);
   const PageTable& t = p.t;
-  cluster_arrive();
+  if constexpr (!FUSED) cluster_arrive();
   grid_dependency_wait();
   grid_launch_dependents();
+  if constexpr (FUSED) {
+    const unsigned runs = static_cast<unsigned>((t.max_pages + 127) / 128);
+    for (unsigned w = cta * (kPickThreads / 32) + (tid >> 5); w < runs * n; w += kCtas * (kPickThreads / 32))
+      fork_entries(p, static_cast<int>(w / runs), static_cast<int>(w % runs) * 128 + (tid & 31), 32);
+    __threadfence();
+    cluster_arrive();   // (waited for below, before the counts are read)
+  }
   // the requests
   auto request = [&](int i) -> int {
     if constexpr (FORK) {
@@ -410,9 +484,9 @@ cudaError_t launch_pdl(K kern, long long blocks, int threads, size_t smem, cudaS
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <bool FORK, class Params>
+template <bool FORK, bool FUSED, class Params>
 cudaError_t launch_pick(const Params& p, int n, int device, cudaStream_t stream) {
-  auto kern = pick_kernel<FORK, Params>;
+  auto kern = pick_kernel<FORK, FUSED, Params>;
   static std::atomic<uint64_t> configured{0};  // a bit a device
   const uint64_t bit = 1ull << device;
   if ((configured.load(std::memory_order_relaxed) & bit) == 0) {
@@ -423,6 +497,9 @@ cudaError_t launch_pick(const Params& p, int n, int device, cudaStream_t stream)
   }
   return launch_pdl(kern, kCtas, kPickThreads, static_cast<size_t>(n + 1) * 4, stream, p, n);
 }
+
+// Forks with so many table entries at most are one launch, by eight blocks.
+constexpr long long kFusedEntries = 65536;
 
 int slabs_of(int max_pages) { return (max_pages + kEntries - 1) / kEntries; }
 
@@ -436,18 +513,20 @@ cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream) {
 
 cudaError_t launch_compact_pages(const CompactPagesParams& p, bool e4m3, cudaStream_t stream) {
   const long long blocks = 2LL * p.n_seqs * p.entries * p.groups;
-  return e4m3 ? launch_pdl(compact_pages_kernel<true>, blocks, kThreads, 0, stream, p)
-              : launch_pdl(compact_pages_kernel<false>, blocks, kThreads, 0, stream, p);
+  const CompactSmem at(e4m3, 1 << p.c.page_shift, p.unit_shift);
+  return e4m3 ? launch_pdl(compact_pages_kernel<true>, blocks, kThreads, at.total, stream, p)
+              : launch_pdl(compact_pages_kernel<false>, blocks, kThreads, at.total, stream, p);
 }
 
 cudaError_t launch_fork(const ForkParams& p, int device, cudaStream_t stream) {
+  if (static_cast<long long>(p.n) * p.t.max_pages <= kFusedEntries) return launch_pick<true, true>(p, p.n, device, stream);
   const int slabs = slabs_of(p.t.max_pages);
   const cudaError_t e = launch_pdl(fork_entries_kernel, static_cast<long long>(p.n) * slabs, kThreads, 0, stream, p, slabs);
-  return e != cudaSuccess ? e : launch_pick<true>(p, p.n, device, stream);
+  return e != cudaSuccess ? e : launch_pick<true, false>(p, p.n, device, stream);
 }
 
 cudaError_t launch_take(const TakeParams& p, int device, cudaStream_t stream) {
-  return launch_pick<false>(p, p.t.rows, device, stream);
+  return launch_pick<false, false>(p, p.t.rows, device, stream);
 }
 
 cudaError_t launch_release(const ReleaseParams& p, cudaStream_t stream) {
