@@ -936,7 +936,7 @@ def sdpa_pages_take(refs, page_table, from_lens, to_lens, page_size, *, stream=N
         raise SdpaError(6, where)
 
     def call(st):
-        missing = refs.new_empty(1)
+        missing = _torch.empty(1, dtype=_torch.int32, device=refs.device)
         rc = load_library().sdpa_pages_take(refs.data_ptr(), n_pages, page_table.data_ptr(), stride, rows, columns, page_size,
                                             from_lens.data_ptr(), to_lens.data_ptr(), missing.data_ptr(), st)
         if rc != 0:
@@ -970,15 +970,16 @@ def sdpa_pages_fork(refs, page_table, kv_lens, src, dst, page_size, new_table=No
         raise SdpaError(6, where)
 
     def call(st):
-        copies = PageCopies(refs.new_empty(n), refs.new_empty(n), refs.new_empty(n), refs.new_empty(1))
+        empty, i32, dev = _torch.empty, _torch.int32, refs.device
+        copy_src, copy_dst, copy_rows, missing = (empty(k, dtype=i32, device=dev) for k in (n, n, n, 1))
         rc = load_library().sdpa_pages_fork(
             refs.data_ptr(), n_pages, page_table.data_ptr(), stride, rows,
             (page_table if new_table is None else new_table).data_ptr(), new_stride, new_rows, columns, page_size,
-            kv_lens.data_ptr(), src.data_ptr(), dst.data_ptr(), n, copies.src.data_ptr(), copies.dst.data_ptr(),
-            copies.rows.data_ptr(), copies.missing.data_ptr(), st)
+            kv_lens.data_ptr(), src.data_ptr(), dst.data_ptr(), n, copy_src.data_ptr(), copy_dst.data_ptr(),
+            copy_rows.data_ptr(), missing.data_ptr(), st)
         if rc != 0:
             raise SdpaError(rc, where)
-        return copies
+        return PageCopies(copy_src, copy_dst, copy_rows, missing)
 
     return _on_device(device, where, stream, call)
 
