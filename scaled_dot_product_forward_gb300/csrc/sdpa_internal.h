@@ -150,12 +150,13 @@ struct PagedParams {
   int is_causal;
   float scale_log2;
   int out_sectors;          // rows of out begin on 32-byte boundaries
+  int part_sectors;         // so does the workspace (and with it the rows in it)
   int max_rows;             // the caller's bound on a sequence's rows a head (>= 1)
   // A causal row that sees keys below `seen` sees those from seen - window on, and
   // those below sinks; 0: all of them.
   int window, sinks;
   int sink_steps;           // steps that hold the sinks
-  float* part;              // workspace: n_ctas notes, [n_ctas][2][unit_heads][rows of a unit][D + 2] floats
+  float* part;              // workspace: n_ctas notes, [n_ctas][2] pieces of unit_heads * (rows of a unit) * (D + 2) floats
   int n_ctas;               // ranges of the division (grid of the main kernel)
   int device;               // the current device (below 64)
   int debug_withhold_q;     // test hook: 1 = no products are issued, so the waits run out

@@ -252,7 +252,8 @@ __device__ __forceinline__ void advance(const PagedParams& p, int rt, Cursor& c)
 }
 
 // The workspace: what to join, a note of each CTA's, then the partial units,
-// two a CTA of rt rows a head of D sums and their maximum and sum.
+// two a CTA: rt rows a head of D sums, behind them the rows' maxima and sums (so
+// that a row begins where a sector does).
 struct JoinNote {
   int pieces;        // 0: no unit begins in this CTA's range and ends behind it
   int slot;          // of its piece here; the following CTAs' pieces are their first
@@ -267,6 +268,11 @@ template <int D>
 __device__ __forceinline__ float* part_rows(const PagedParams& p, int i, int slot, int rt) {
   return p.part + static_cast<int64_t>(p.n_ctas) * (sizeof(JoinNote) / 4) +
          (static_cast<int64_t>(i) * 2 + slot) * p.unit_heads * rt * (D + 2);
+}
+// Of the piece at `rows`: row hr's maximum and sum.
+template <int D>
+__device__ __forceinline__ float2* part_sums(float* rows, int heads, int rt, int hr) {
+  return reinterpret_cast<float2*>(rows + heads * rt * D) + hr;
 }
 
 // CTA i's note: its last unit, if that begins here (with its first or a later

@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
     auto column = [](int n, int j) {
       return (E4M3 || D == 64) ? n * NV + j : (j < 8 ? 8 * n + j : 64 + 8 * n + j - 8);
     };
-    float* part = part_rows<D>(p, cta, first_segment ? 0 : 1, RT) + hsub * RT * (D + 2);
+    float* part = part_rows<D>(p, cta, first_segment ? 0 : 1, RT);
     if (slices > 1) {
       // join the head's warps: each leaves its rows' maximum, sum and O (over
       // its own ring, which holds no copies in flight any more)
@@ -560,14 +560,14 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
       }
       if (r >= rows) continue;
       if (slices > 1 || !whole) {
-        float* row = slices > 1 ? join + (warp * RT + r) * S::kJoinRow : part + r * (D + 2);
+        float* row = slices > 1 ? join + (warp * RT + r) * S::kJoinRow : part + (hsub * RT + r) * D;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int j = 0; j < NV; j += 2)
             *reinterpret_cast<float2*>(row + column(2 * t4 + e, j)) =
                 make_float2(o[j][2 * hf + e], o[j + 1][2 * hf + e]);
-        if (slices == 1 && t4 == 0) *reinterpret_cast<float2*>(row + D) = make_float2(mx, ls);
+        if (slices == 1 && t4 == 0) *part_sums<D>(part, p.unit_heads, RT, hsub * RT + r) = make_float2(mx, ls);
       } else {
         const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
 #pragma unroll
@@ -608,10 +608,8 @@ __global__ void __launch_bounds__(kThreads, sdpa_impl::paged_per_sm(D, E4M3))
           store_out4<D, BF16>(out_row(p, c.s.q0, hd, c.t * RT + r) + d, sum, ls == 0.0f ? 0.0f : 1.0f / ls);
           if (d == 0 && p.lse != nullptr) store_lse(p, c.s.q0, hd, c.t * RT + r, mx, ls);
         } else {
-          float* row = part_rows<D>(p, cta, first_segment ? 0 : 1, RT) + (hs * RT + r) * (D + 2);
-          *reinterpret_cast<float2*>(row + d) = make_float2(sum.x, sum.y);
-          *reinterpret_cast<float2*>(row + d + 2) = make_float2(sum.z, sum.w);
-          if (d == 0) *reinterpret_cast<float2*>(row + D) = make_float2(mx, ls);
+          *reinterpret_cast<float4*>(part + (hs * RT + r) * D + d) = sum;
+          if (d == 0) *part_sums<D>(part, p.unit_heads, RT, hs * RT + r) = make_float2(mx, ls);
         }
       }
       __syncthreads();
@@ -642,15 +640,15 @@ __global__ void __launch_bounds__(kThreads)
   for (int hr = static_cast<int>(blockIdx.y * kWarps + (threadIdx.x >> 5)); hr < note.heads * note.rows;
        hr += static_cast<int>(gridDim.y) * kWarps) {
     const int hs = hr / note.rows, r = hr - hs * note.rows;
-    const float* row0 = part_rows<D>(p, i, note.slot, rt) + (hs * rt + r) * (D + 2);
-    const float* row1 = part_rows<D>(p, i + 1, 0, rt) + (hs * rt + r) * (D + 2);
-    auto piece = [&](int k) { return k == 0 ? row0 : row1 + (k - 1) * step; };
+    float* const rows0 = part_rows<D>(p, i, note.slot, rt);
+    float* const rows1 = part_rows<D>(p, i + 1, 0, rt);
+    auto piece = [&](int k) { return k == 0 ? rows0 : rows1 + (k - 1) * step; };
     float mx = -INFINITY, ls = 0.0f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < note.pieces; k0 += 32) {
       const int n = min(note.pieces - k0, 32);
       float2 ml = make_float2(-INFINITY, 0.0f);
-      if (lane < n) ml = *reinterpret_cast<const float2*>(piece(k0 + lane) + D);
+      if (lane < n) ml = *part_sums<D>(piece(k0 + lane), note.heads, rt, hs * rt + r);
       float top = ml.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -669,13 +667,11 @@ __global__ void __launch_bounds__(kThreads)
       for (int k = 0; k < n; k += kSplit) {
         const float fk = __shfl_sync(0xffffffffu, f, (k + first) & 31);
         if (kSplit == 1 || k + first < n) {
-          const float* row = piece(k0 + k + first) + d;
-          const float2 x0 = *reinterpret_cast<const float2*>(row);
-          const float2 x1 = *reinterpret_cast<const float2*>(row + 2);
-          sum.x = fmaf(x0.x, fk, sum.x);
-          sum.y = fmaf(x0.y, fk, sum.y);
-          sum.z = fmaf(x1.x, fk, sum.z);
-          sum.w = fmaf(x1.y, fk, sum.w);
+          const float4 x = *reinterpret_cast<const float4*>(piece(k0 + k + first) + (hs * rt + r) * D + d);
+          sum.x = fmaf(x.x, fk, sum.x);
+          sum.y = fmaf(x.y, fk, sum.y);
+          sum.z = fmaf(x.z, fk, sum.z);
+          sum.w = fmaf(x.w, fk, sum.w);
         }
       }
     }

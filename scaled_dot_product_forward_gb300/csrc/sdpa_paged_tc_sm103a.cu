@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       fa *= inv;
       fb *= inv;
       uint16_t* orow = reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh;
-      float* prow = part_rows<D>(p, blockIdx.x, g.first ? 0 : 1, RT) + static_cast<int64_t>(ru) * (D + 2);
+      float* const part = part_rows<D>(p, blockIdx.x, g.first ? 0 : 1, RT);
       // this thread's runs of 32 columns: all, or half of them (HALF: of its
       // half row's; where that is one run, the first warpgroup's)
       constexpr int kRuns = HALF ? D / 64 : D / 32;
@@ -882,9 +882,14 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
                 *reinterpret_cast<uint4*>(to + e * 8) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             }
           } else {
+            float* to = part + ru * D + col0 + i * 32;
+            if (p.part_sectors) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              *reinterpret_cast<float2*>(prow + col0 + i * 32 + e) = make_float2(of[e], of[e + 1]);
+              for (int e = 0; e < 32; e += 8) store_sector(to + e, o + e);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(of[e], of[e + 1], of[e + 2], of[e + 3]);
+            }
           }
         }
       }
@@ -897,7 +902,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
       }
       if (live && half == 0 && (!split || t == 0)) {
         if (!g.whole) {
-          *reinterpret_cast<float2*>(prow + D) = make_float2(m, l);
+          *part_sums<D>(part, 1, RT, ru) = make_float2(m, l);
         } else if (p.lse != nullptr) {
           constexpr float kLn2 = 0.693147180559945309f;
           p.lse[token * p.lse_st + head * p.lse_sh] = l == 0.0f ? -INFINITY : (log2f(l) + m) * kLn2;
