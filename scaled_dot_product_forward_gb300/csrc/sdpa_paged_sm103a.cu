@@ -27,6 +27,13 @@
 // of 128 rows would be 7/8 padding here.  The order of D inside both products
 // is free, so each thread takes 16 consecutive bytes of a key's row as they
 // lie in memory, and the output's columns come out in runs of D / 4.
+//
+// With a window (WIN; a kernel of its own, since the loop is bound by its issue
+// slots) a unit's steps are those that hold the sinks and those from its first
+// row's window on; keys of these that a row does not see are removed as those
+// behind its causal limit are.  64 sequences in a window of 4096 (H 32/8, D 128,
+// e4m3): 102 us, 20 of which are the start, uneven ends and the join (2048 more
+// keys of a window cost 40.6, 97% of the measured copy rate).
 #include <atomic>
 
 #include "sdpa_paged.cuh"

@@ -26,6 +26,13 @@
 // fp16 tiles (exact); a key's weight carries its page's value scale, so the
 // scales touch eight constants a row and step, not the elements.
 //
+// With a window (WIN) a unit's steps are the sinks' and, from its first row's
+// window on, the others; entries of pages between them read as no page.  4096
+// tokens in a window of 4096 behind 12288 (H 32/8, D 128): e4m3 315 us, 872
+// TFLOP/s, 16-bit pages 250, 1100.  A unit is 34 steps of 2.2 us here, and 8 us
+// around them (queries 2.3, the first scores 0.9, the last products 1.2, output
+// 3.2), without its masked keys 7 us less in all; the join is 15.
+//
 // The steps of all units are divided equally over the CTAs (one an SM), the
 // two cut units of a CTA joined by a second kernel (sdpa_paged.cuh).  Every
 // wait is bounded in time; on expiry the CTA records a status bit, stops, lets

@@ -637,3 +637,32 @@ def test_refusals_of_the_c_entries():
         assert compact(**kw) == LAYOUT, kw
     for kw in (dict(table=base), dict(kept=base + 64), dict(lens=base + 64 * M), dict(new=base + 32 * 1024)):
         assert compact(**kw) == ARG, kw
+
+
+@gpu
+def test_far_pages(sdpa_lib):
+    """Pages that begin behind 2^31 elements and 2^32 bytes: copied, compacted, read in a window."""
+    D, hkv, P, n_pages = 128, 8, 1024, 2200
+    k, v = (torch.empty(n_pages, P, hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    c = sdpa_lib.SdpaPagedCache(k, v)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for x in (k, v):
+        x[5].normal_(generator=g)
+        x[2150].normal_(generator=g)
+    sdpa_lib.sdpa_cache_copy_pages(c, i32([5, 2150]), i32([2199, 9]))
+    for x in (k, v):
+        assert torch.equal(x[2199], x[5]) and torch.equal(x[9], x[2150])
+    pos = torch.randperm(2 * P, generator=torch.Generator().manual_seed(3))[:700]
+    sdpa_lib.sdpa_cache_compact(c, i32([[2199, 2150]]), pos[None].to(torch.int32).cuda(), i32([[2180]]))
+    for x in (k, v):
+        want = torch.cat([x[5], x[9]])[pos.cuda()]
+        assert torch.equal(x[2180, :700], want)
+    q = torch.randn(3, 16, D, generator=g, device="cuda").bfloat16()
+    lens = i32([1500])
+    near, far = i32([[5, 9]]), i32([[2199, 2150]])
+    for rows in (1, 3):
+        a, b = (sdpa_lib.sdpa_paged_forward(q[:rows], c, t, lens, is_causal=True, window=700, sinks=5) for t in (near, far))
+        assert torch.equal(a, b)
+    wide = torch.randn(90, 16, D, generator=g, device="cuda").bfloat16()
+    a, b = (sdpa_lib.sdpa_paged_forward(wide, c, t, lens, is_causal=True, window=700, sinks=5) for t in (near, far))
+    assert torch.equal(a, b)
