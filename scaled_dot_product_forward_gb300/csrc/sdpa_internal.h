@@ -211,6 +211,11 @@ constexpr int kScaleMinExp = -50, kScaleMaxExp = 50;
 cudaError_t launch_cache_append(const AppendParams& p, int head_dim, bool bf16, bool e4m3, int sms,
                                 cudaStream_t stream);
 cudaError_t launch_norm_rotate(const RowsParams& p, int head_dim, bool bf16, int sms, cudaStream_t stream);
+// (translation units of their own; the two above call them)
+cudaError_t launch_append_norm64(const AppendParams& p, bool bf16, bool e4m3, int sms, cudaStream_t stream);
+cudaError_t launch_append_norm128(const AppendParams& p, bool bf16, bool e4m3, int sms, cudaStream_t stream);
+cudaError_t launch_norm_rotate64(const RowsParams& p, bool bf16, int sms, cudaStream_t stream);
+cudaError_t launch_norm_rotate128(const RowsParams& p, bool bf16, int sms, cudaStream_t stream);
 
 // A cache's pages as bytes.
 struct PageBytes {
