@@ -79,23 +79,34 @@ __device__ __forceinline__ Lane lane_of(int j, int rot, int interleaved) {
   return l;
 }
 
-template <bool BF16>
+// TOGETHER: the lane's eight elements are one run (nothing is rotated).
+template <bool BF16, bool TOGETHER = false>
 __device__ __forceinline__ void load8(const uint16_t* row, const Lane& l, float (&x)[8]) {
   // (plain loads: the queries may be rotated in place)
-  const uint2 a = *reinterpret_cast<const uint2*>(row + l.ea);
-  const uint2 b = *reinterpret_cast<const uint2*>(row + l.eb);
+  uint2 a, b;
+  if constexpr (TOGETHER) {
+    const uint4 w = *reinterpret_cast<const uint4*>(row + l.ea);
+    a = make_uint2(w.x, w.y), b = make_uint2(w.z, w.w);
+  } else {
+    a = *reinterpret_cast<const uint2*>(row + l.ea);
+    b = *reinterpret_cast<const uint2*>(row + l.eb);
+  }
   const float2 f0 = unpack2<BF16>(a.x), f1 = unpack2<BF16>(a.y);
   const float2 f2 = unpack2<BF16>(b.x), f3 = unpack2<BF16>(b.y);
   x[0] = f0.x, x[1] = f0.y, x[2] = f1.x, x[3] = f1.y;
   x[4] = f2.x, x[5] = f2.y, x[6] = f3.x, x[7] = f3.y;
 }
 
-template <bool BF16>
+template <bool BF16, bool TOGETHER = false>
 __device__ __forceinline__ void store8(uint16_t* row, const Lane& l, const float (&x)[8]) {
-  *reinterpret_cast<uint2*>(row + l.ea) =
-      make_uint2(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]));
-  *reinterpret_cast<uint2*>(row + l.eb) =
-      make_uint2(pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+  const uint2 a = make_uint2(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]));
+  const uint2 b = make_uint2(pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+  if constexpr (TOGETHER) {
+    *reinterpret_cast<uint4*>(row + l.ea) = make_uint4(a.x, a.y, b.x, b.y);
+  } else {
+    *reinterpret_cast<uint2*>(row + l.ea) = a;
+    *reinterpret_cast<uint2*>(row + l.eb) = b;
+  }
 }
 
 // Two fp32 values an instruction.
@@ -259,7 +270,7 @@ __device__ __forceinline__ void load_rows(const uint16_t* src, int64_t src_step,
 #pragma unroll
   for (int k = 0; k < kBatch; ++k) {
     if (r + k * stride < n) {
-      load8<BF16>(src, at, x[k]);
+      load8<BF16, !ROT>(src, at, x[k]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[k][e] = 0.0f;
@@ -282,6 +293,7 @@ __device__ __forceinline__ void load_rows(const uint16_t* src, int64_t src_step,
   }
 }
 
+template <bool TOGETHER>
 __device__ __forceinline__ void store_codes(uint8_t* to, int64_t step, const Lane& at, int r, int stride, int n, float inv,
                                             const float (&x)[kBatch][8]) {
   const uint64_t f = pair(inv, inv);
@@ -291,8 +303,13 @@ __device__ __forceinline__ void store_codes(uint8_t* to, int64_t step, const Lan
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; e += 2) unpair(mul2(pair(x[k][e], x[k][e + 1]), f), y[e], y[e + 1]);
-      *reinterpret_cast<uint32_t*>(to + at.ea) = codes4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint32_t*>(to + at.eb) = codes4(y[4], y[5], y[6], y[7]);
+      const uint32_t a = codes4(y[0], y[1], y[2], y[3]), b = codes4(y[4], y[5], y[6], y[7]);
+      if constexpr (TOGETHER) {
+        *reinterpret_cast<uint2*>(to + at.ea) = make_uint2(a, b);
+      } else {
+        *reinterpret_cast<uint32_t*>(to + at.ea) = a;
+        *reinterpret_cast<uint32_t*>(to + at.eb) = b;
+      }
     }
     to += step;
   }
@@ -384,7 +401,7 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
 #pragma unroll 1
   for (int i = 0; i < batches; ++i) {
     if (batches > 1) load(i, x);
-    store_codes(to + i * (kBatch * to_step), to_step, at, first + i * kBatch * kStride, kStride, n, inv, x);
+    store_codes<!ROT>(to + i * (kBatch * to_step), to_step, at, first + i * kBatch * kStride, kStride, n, inv, x);
   }
 }
 
@@ -405,14 +422,14 @@ __device__ __forceinline__ void token_rows(int interleaved, const Lane& at, cons
     float x[kBatch][8];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (h + u * kRows < h1) load8<BF16>(src, at, x[u]);
+      if (h + u * kRows < h1) load8<BF16, !ROT>(src, at, x[u]);
       src += src_step;
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (h + u * kRows < h1) {
         if (ROT && at.rotated) rotate8(x[u], c, s, interleaved);
-        store8<BF16>(reinterpret_cast<uint16_t*>(dst), at, x[u]);
+        store8<BF16, !ROT>(reinterpret_cast<uint16_t*>(dst), at, x[u]);
       }
       dst += dst_step;
     }
@@ -585,29 +602,49 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   };
   if constexpr (E4M3) {
     if (static_cast<int>(blockIdx.x) < kv_blocks) {
-      const unsigned unit = blockIdx.x * (kWarps / UNIT_WARPS) + warp / UNIT_WARPS;
-      const int slot = static_cast<int>(unit / (2u * p.n_kv));
-      const int hv = static_cast<int>(unit - slot * 2u * p.n_kv);
-      auto first_slot = [&](int b) { return (first_token(b) >> p.page_shift) + 2 * b; };
-      const int b = last_at_most(p.n_seqs, slot, first_slot);
-      if (b < 0) return;
-      const int q0 = first_token(b), q1 = max(first_token(b + 1), q0);
-      const int len = __ldg(p.kv_lens + b), n = q1 - q0;
-      const int p0 = max(len - n, 0);          // position of the first token that has one
-      const int page_i = (p0 >> p.page_shift) + (slot - first_slot(b));
-      if (page_i < 0 || page_i > (p.max_len - 1) >> p.page_shift) return;
+      const int part = warp % UNIT_WARPS;
       PageTokens pt;
-      pt.lo = max(p0, page_i << p.page_shift);
-      // a position past the table's pages or the angles' table is left out
-      pt.hi = min(min(len, p.max_len), (page_i << p.page_shift) + P);
-      if (p.cos != nullptr) pt.hi = min(pt.hi, p.n_pos);
-      if (pt.lo >= pt.hi) return;
-      pt.t0 = q0 + (pt.lo - (len - n));
-      const int page = __ldg(p.table + b * p.table_st + page_i);
+      int hv = 0, page = -1;
+      // the unit's page (-1: nothing to do) and its new tokens
+      auto look_up = [&]() {
+        const unsigned unit = blockIdx.x * (kWarps / UNIT_WARPS) + warp / UNIT_WARPS;
+        const int slot = static_cast<int>(unit / (2u * p.n_kv));
+        hv = static_cast<int>(unit - slot * 2u * p.n_kv);
+        auto first_slot = [&](int b) { return (first_token(b) >> p.page_shift) + 2 * b; };
+        const int b = last_at_most(p.n_seqs, slot, first_slot);
+        if (b < 0) return;
+        const int q0 = first_token(b), q1 = max(first_token(b + 1), q0);
+        const int len = __ldg(p.kv_lens + b), n = q1 - q0;
+        const int p0 = max(len - n, 0);          // position of the first token that has one
+        const int page_i = (p0 >> p.page_shift) + (slot - first_slot(b));
+        if (page_i < 0 || page_i > (p.max_len - 1) >> p.page_shift) return;
+        pt.lo = max(p0, page_i << p.page_shift);
+        // a position past the table's pages or the angles' table is left out
+        pt.hi = min(min(len, p.max_len), (page_i << p.page_shift) + P);
+        if (p.cos != nullptr) pt.hi = min(pt.hi, p.n_pos);
+        if (pt.lo >= pt.hi) return;
+        pt.t0 = q0 + (pt.lo - (len - n));
+        page = __ldg(p.table + b * p.table_st + page_i);
+      };
+      if constexpr (UNIT_WARPS > 1) {
+        // the first of the unit's warps looks for all of them (each for itself was a
+        // fifth of the instructions: MEASURE)
+        __shared__ int4 found[kWarps / UNIT_WARPS];
+        __shared__ int found_hv[kWarps / UNIT_WARPS];
+        const int u = warp / UNIT_WARPS;
+        if (part == 0) {
+          look_up();
+          if ((threadIdx.x & 31) == 0) found[u] = make_int4(pt.lo, pt.hi, pt.t0, page), found_hv[u] = hv;
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + u), "n"(UNIT_WARPS * 32) : "memory");
+        const int4 f = found[u];
+        pt.lo = f.x, pt.hi = f.y, pt.t0 = f.z, page = f.w, hv = found_hv[u];
+      } else {
+        look_up();
+      }
       if (page < 0 || page >= p.n_pages) return;
       const int h = hv < p.n_kv ? hv : hv - p.n_kv;
       const int64_t at = static_cast<int64_t>(page) * p.n_kv + h;
-      const int part = warp % UNIT_WARPS;
       if (hv < p.n_kv)
         append_codes<D, BF16, false, false, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.v) + h * p.v_sh, p.v_st,
                                                  p.cv + page * p.cv_sp + h * p.cv_sh, p.cv_st, p.v_scale + at, part, red + warp - part);
