@@ -49,6 +49,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kUnitHeads = 4;   // of a unit of eight warps, at most
 constexpr int kPerSm = 4;   // blocks an SM: the loads' latency is hidden by warps, not by registers
 
 // Where lane j of a row keeps its eight elements: a[0..3] from `ea`, b[0..3]
@@ -316,11 +317,15 @@ __device__ __forceinline__ void store_codes(uint8_t* to, int64_t step, const Lan
 }
 
 // A unit: the page's new rows of one head, quantised under the page's scale, by
-// WARPS warps (part: this one's number, red: their shared scratch).
+// WARPS warps (part: this one's number, red: their shared scratch); with eight warps,
+// of `heads` heads after one another, so that the page is looked up once for
+// them (8 x 4096 tokens with norms, 8 heads: one a unit 138 us, two 131, four 127,
+// eight 125 but 63 without queries, where four take 56).
 template <int D, bool BF16, bool ROT, bool NORM, int WARPS>
 __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, const PageTokens& pt,
-                                             const uint16_t* src, int64_t src_st, uint8_t* dst,
-                                             int64_t dst_st, float* scale_at, int part, float* red) {
+                                             const uint16_t* src, int64_t src_st, int64_t src_sh, uint8_t* dst,
+                                             int64_t dst_st, int64_t dst_sh, float* scale_at, int heads, int part,
+                                             float* red) {
   constexpr int kLanes = D / 8;                  // lanes a row
   constexpr int kStride = WARPS * 32 / kLanes;   // rows a step
   const int lane = threadIdx.x & 31;
@@ -328,11 +333,8 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
   const Lane at = lane_of(j, ROT ? p.rot : 0, p.interleaved);
   const int n = pt.hi - pt.lo;
   const int row0 = pt.lo & ((1 << p.page_shift) - 1);
-  // the page's scale, if earlier rows have made one
-  float old = 0.0f;
-  if (row0 > 0) old = clamp_scale(*scale_at);
   // this lane's part of its first row, and from one of its rows to the next
-  const uint16_t* const rows = src + (static_cast<int64_t>(pt.t0) + first) * src_st;
+  const uint16_t* rows = src + (static_cast<int64_t>(pt.t0) + first) * src_st;
   const int64_t row_step = kStride * src_st, angle_step = static_cast<int64_t>(kStride) * (p.rot / 2);
   const int64_t angle = (static_cast<int64_t>(pt.lo) + first) * (p.rot / 2) + 4 * j;
   const float* const cos = ROT ? p.cos + angle : nullptr;
@@ -342,66 +344,77 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
                          sin + batch * (kBatch * angle_step), angle_step, at, p.interleaved,
                          first + batch * kBatch * kStride, kStride, n, p.k_norm, p.eps, x);
   };
-  float x[kBatch][8];
-  float amax = 0.0f;
   // (more rows than the registers hold are read again below)
   const int batches = (n + kBatch * kStride - 1) / (kBatch * kStride);
 #pragma unroll 1
-  for (int i = 0; i < batches; ++i) {
-    load(i, x);
-    float top = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) top = abs_max(top, x[k][e], x[k][e + 1]);
-    if (top == INFINITY) {
-      top = 0.0f;
+  for (int h = 0; h < (WARPS == kWarps ? heads : 1); ++h) {
+    // the page's scale, if earlier rows have made one
+    float old = 0.0f;
+    if (row0 > 0) old = clamp_scale(*scale_at);
+    float x[kBatch][8];
+    float amax = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < batches; ++i) {
+      load(i, x);
+      float top = 0.0f;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(x[k][e]));
-    }
-    amax = fmaxf(amax, top);
-  }
+        for (int e = 0; e < 8; e += 2) top = abs_max(top, x[k][e], x[k][e + 1]);
+      if (top == INFINITY) {
+        top = 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if constexpr (WARPS > 1) {
-    if (lane == 0) red[part] = amax;
-    // the unit's warps (also: all have read the old scale)
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / (WARPS * 32)), "n"(WARPS * 32) : "memory");
+        for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, red[w]);
-  } else {
-    __syncwarp();
-  }
-  float scale = scale_for(amax);
-  if (row0 > 0) {
-    if (scale > old) {
-      // raise the scale: the page's earlier codes of this head
-      const float ratio = old / scale;
-      for (int i = part * 32 + lane; i < row0 * (D / 16); i += WARPS * 32) {
-        uint4* at16 = reinterpret_cast<uint4*>(dst + (i / (D / 16)) * dst_st + (i % (D / 16)) * 16);
-        const uint4 w = *at16;
-        uint32_t in[4] = {w.x, w.y, w.z, w.w}, res[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 a = values2(in[e]), b = values2(in[e] >> 16);
-          res[e] = codes4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
-        }
-        *at16 = make_uint4(res[0], res[1], res[2], res[3]);
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(x[k][e]));
       }
-    } else {
-      scale = old;
+      amax = fmaxf(amax, top);
     }
-  }
-  if (part == 0 && lane == 0) *scale_at = scale;
-  const float inv = 1.0f / scale;
-  uint8_t* const to = dst + (row0 + first) * dst_st;
-  const int64_t to_step = kStride * dst_st;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if constexpr (WARPS > 1) {
+      // (heads in turn use two places: one barrier a head)
+      float* const tops = red + (WARPS == kWarps ? (h & 1) * kWarps : 0);
+      if (lane == 0) tops[part] = amax;
+      // the unit's warps (also: all have read the old scale)
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / (WARPS * 32)), "n"(WARPS * 32) : "memory");
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, tops[w]);
+    } else {
+      __syncwarp();
+    }
+    float scale = scale_for(amax);
+    if (row0 > 0) {
+      if (scale > old) {
+        // raise the scale: the page's earlier codes of this head
+        const float ratio = old / scale;
+        for (int i = part * 32 + lane; i < row0 * (D / 16); i += WARPS * 32) {
+          uint4* at16 = reinterpret_cast<uint4*>(dst + (i / (D / 16)) * dst_st + (i % (D / 16)) * 16);
+          const uint4 w = *at16;
+          uint32_t in[4] = {w.x, w.y, w.z, w.w}, res[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = values2(in[e]), b = values2(in[e] >> 16);
+            res[e] = codes4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+          }
+          *at16 = make_uint4(res[0], res[1], res[2], res[3]);
+        }
+      } else {
+        scale = old;
+      }
+    }
+    if (part == 0 && lane == 0) *scale_at = scale;
+    const float inv = 1.0f / scale;
+    uint8_t* const to = dst + (row0 + first) * dst_st;
+    const int64_t to_step = kStride * dst_st;
 #pragma unroll 1
-  for (int i = 0; i < batches; ++i) {
-    if (batches > 1) load(i, x);
-    store_codes<!ROT>(to + i * (kBatch * to_step), to_step, at, first + i * kBatch * kStride, kStride, n, inv, x);
+    for (int i = 0; i < batches; ++i) {
+      if (batches > 1) load(i, x);
+      store_codes<!ROT>(to + i * (kBatch * to_step), to_step, at, first + i * kBatch * kStride, kStride, n, inv, x);
+    }
+    rows += src_sh;
+    dst += dst_sh;
+    ++scale_at;
   }
 }
 
@@ -582,7 +595,8 @@ __device__ __forceinline__ int last_at_most(int n, int x, F&& f) {
   return count - 1;
 }
 
-// Blocks [0, kv_blocks): units of 8-bit pages, UNIT_WARPS warps each.  A slot
+// Blocks [0, kv_blocks): units of 8-bit pages, UNIT_WARPS warps each.  (Evenly among
+// the others, they are no faster: 8 x 4096 tokens with norms 130 us against 127.)  A slot
 // stands for a (sequence, page with new tokens): sequence b has the slots
 // [f(b), f(b+1)), f(b) = cu[b] / P + 2 b, at least as many as the pages its new
 // tokens can touch, so a slot finds its sequence without a prefix sum over
@@ -591,7 +605,7 @@ __device__ __forceinline__ int last_at_most(int n, int x, F&& f) {
 template <int D, bool BF16, bool E4M3, bool ROT, bool NORM, int UNIT_WARPS>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     append_kernel(const __grid_constant__ sdpa_impl::AppendParams p, int kv_blocks, int parts) {
-  __shared__ float red[kWarps];
+  __shared__ float red[2 * kWarps];
   grid_dependency_wait();
   grid_launch_dependents();
   const int P = 1 << p.page_shift;
@@ -608,8 +622,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       // the unit's page (-1: nothing to do) and its new tokens
       auto look_up = [&]() {
         const unsigned unit = blockIdx.x * (kWarps / UNIT_WARPS) + warp / UNIT_WARPS;
-        const int slot = static_cast<int>(unit / (2u * p.n_kv));
-        hv = static_cast<int>(unit - slot * 2u * p.n_kv);
+        const unsigned each = 2u * p.n_kv / (UNIT_WARPS == kWarps ? p.unit_heads : 1);   // units of a slot
+        const int slot = static_cast<int>(unit / each);
+        hv = static_cast<int>(unit - slot * each) * (UNIT_WARPS == kWarps ? p.unit_heads : 1);
         auto first_slot = [&](int b) { return (first_token(b) >> p.page_shift) + 2 * b; };
         const int b = last_at_most(p.n_seqs, slot, first_slot);
         if (b < 0) return;
@@ -627,8 +642,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         page = __ldg(p.table + b * p.table_st + page_i);
       };
       if constexpr (UNIT_WARPS > 1) {
-        // the first of the unit's warps looks for all of them (each for itself was a
-        // fifth of the instructions: MEASURE)
+        // (the first of the unit's warps looks for all of them)
         __shared__ int4 found[kWarps / UNIT_WARPS];
         __shared__ int found_hv[kWarps / UNIT_WARPS];
         const int u = warp / UNIT_WARPS;
@@ -646,11 +660,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       const int h = hv < p.n_kv ? hv : hv - p.n_kv;
       const int64_t at = static_cast<int64_t>(page) * p.n_kv + h;
       if (hv < p.n_kv)
-        append_codes<D, BF16, false, false, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.v) + h * p.v_sh, p.v_st,
-                                                 p.cv + page * p.cv_sp + h * p.cv_sh, p.cv_st, p.v_scale + at, part, red + warp - part);
+        append_codes<D, BF16, false, false, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.v) + h * p.v_sh, p.v_st, p.v_sh,
+                                                 p.cv + page * p.cv_sp + h * p.cv_sh, p.cv_st, p.cv_sh, p.v_scale + at,
+                                                 p.unit_heads, part, red + warp - part);
       else
-        append_codes<D, BF16, ROT, NORM, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.k) + h * p.k_sh, p.k_st,
-                                               p.ck + page * p.ck_sp + h * p.ck_sh, p.ck_st, p.k_scale + at, part, red + warp - part);
+        append_codes<D, BF16, ROT, NORM, UNIT_WARPS>(p, pt, reinterpret_cast<const uint16_t*>(p.k) + h * p.k_sh, p.k_st, p.k_sh,
+                                               p.ck + page * p.ck_sp + h * p.ck_sh, p.ck_st, p.ck_sh, p.k_scale + at,
+                                               p.unit_heads, part, red + warp - part);
       return;
     }
   }
@@ -745,10 +761,13 @@ cudaError_t launch_pdl(K kern, long long blocks, cudaStream_t stream, const A&..
 }
 
 template <int D, bool BF16, bool E4M3, bool ROT, bool NORM, int UNIT_WARPS>
-cudaError_t launch_one(const sdpa_impl::AppendParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_one(sdpa_impl::AppendParams p, int sms, cudaStream_t stream) {
   long long kv_blocks = 0;
+  p.unit_heads = 1;
   if (E4M3) {
-    const long long units = ((p.total >> p.page_shift) + 2LL * p.n_seqs) * 2 * p.n_kv;
+    long long units = ((p.total >> p.page_shift) + 2LL * p.n_seqs) * 2 * p.n_kv;
+    while (UNIT_WARPS == kWarps && p.unit_heads < kUnitHeads && p.n_kv % (2 * p.unit_heads) == 0 && units >= 8LL * sms)
+      p.unit_heads *= 2, units /= 2;
     kv_blocks = (units + kWarps / UNIT_WARPS - 1) / (kWarps / UNIT_WARPS);
   }
   // Tokens' rows: a warp a token, or a share of its heads each where that
