@@ -21,8 +21,8 @@
 // square of its D elements and multiplied by the weights, x rsqrt(sum x^2 / D +
 // eps) w, in fp32: the row's lanes add up their squares by log2(D / 8) exchanges,
 // and nothing is rounded before the rotation's end.  norm_rotate_kernel does the
-// same to rows that go to no cache.  8 x 4096 tokens (H 32/8, D 128, e4m3): 139 us,
-// 5.3 TB/s; 17700 rows of 16 + 16 heads of 64: 26 us, 5.6 TB/s.
+// same to rows that go to no cache.  8 x 4096 tokens (H 32/8, D 128, e4m3): 127 us,
+// 5.8 TB/s; 17700 rows of 16 + 16 heads of 64: 26 us, 5.6 TB/s.
 //
 // Bound by memory: each new row is read once and written once.  Two kinds of
 // work share one launch:
