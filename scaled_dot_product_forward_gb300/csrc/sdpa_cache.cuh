@@ -49,7 +49,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnitHeads = 4;   // of a unit of eight warps, at most
+constexpr int kUnitHeads = 4;   // of a unit of several warps, at most
 constexpr int kPerSm = 4;   // blocks an SM: the loads' latency is hidden by warps, not by registers
 
 // Where lane j of a row keeps its eight elements: a[0..3] from `ea`, b[0..3]
@@ -317,10 +317,12 @@ __device__ __forceinline__ void store_codes(uint8_t* to, int64_t step, const Lan
 }
 
 // A unit: the page's new rows of one head, quantised under the page's scale, by
-// WARPS warps (part: this one's number, red: their shared scratch); with eight warps,
-// of `heads` heads after one another, so that the page is looked up once for
-// them (8 x 4096 tokens with norms, 8 heads: one a unit 138 us, two 131, four 127,
-// eight 125 but 63 without queries, where four take 56).
+// WARPS warps (part: this one's number, red: their shared scratch); with several
+// warps, of `heads` heads after one another, so that the page is looked up once
+// for them.  8 x 4096 tokens with norms, 8 heads, pages of 64: one a unit 138 us, two
+// 131, four 127, eight 125 but 63 without queries, where four take 56; pages of 32
+// 151 and 133, of 16 151 and 139.  (Units of one warp gain 1%, a single token's
+// append loses 5.)
 template <int D, bool BF16, bool ROT, bool NORM, int WARPS>
 __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, const PageTokens& pt,
                                              const uint16_t* src, int64_t src_st, int64_t src_sh, uint8_t* dst,
@@ -347,7 +349,7 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
   // (more rows than the registers hold are read again below)
   const int batches = (n + kBatch * kStride - 1) / (kBatch * kStride);
 #pragma unroll 1
-  for (int h = 0; h < (WARPS == kWarps ? heads : 1); ++h) {
+  for (int h = 0; h < (WARPS > 1 ? heads : 1); ++h) {
     // the page's scale, if earlier rows have made one
     float old = 0.0f;
     if (row0 > 0) old = clamp_scale(*scale_at);
@@ -374,7 +376,7 @@ __device__ __forceinline__ void append_codes(const sdpa_impl::AppendParams& p, c
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if constexpr (WARPS > 1) {
       // (heads in turn use two places: one barrier a head)
-      float* const tops = red + (WARPS == kWarps ? (h & 1) * kWarps : 0);
+      float* const tops = red + (h & 1) * kWarps;
       if (lane == 0) tops[part] = amax;
       // the unit's warps (also: all have read the old scale)
       asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / (WARPS * 32)), "n"(WARPS * 32) : "memory");
@@ -622,9 +624,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       // the unit's page (-1: nothing to do) and its new tokens
       auto look_up = [&]() {
         const unsigned unit = blockIdx.x * (kWarps / UNIT_WARPS) + warp / UNIT_WARPS;
-        const unsigned each = 2u * p.n_kv / (UNIT_WARPS == kWarps ? p.unit_heads : 1);   // units of a slot
+        const int unit_heads = UNIT_WARPS > 1 ? p.unit_heads : 1;
+        const unsigned each = 2u * p.n_kv / unit_heads;   // units of a slot
         const int slot = static_cast<int>(unit / each);
-        hv = static_cast<int>(unit - slot * each) * (UNIT_WARPS == kWarps ? p.unit_heads : 1);
+        hv = static_cast<int>(unit - slot * each) * unit_heads;
         auto first_slot = [&](int b) { return (first_token(b) >> p.page_shift) + 2 * b; };
         const int b = last_at_most(p.n_seqs, slot, first_slot);
         if (b < 0) return;
@@ -766,7 +769,9 @@ cudaError_t launch_one(sdpa_impl::AppendParams p, int sms, cudaStream_t stream) 
   p.unit_heads = 1;
   if (E4M3) {
     long long units = ((p.total >> p.page_shift) + 2LL * p.n_seqs) * 2 * p.n_kv;
-    while (UNIT_WARPS == kWarps && p.unit_heads < kUnitHeads && p.n_kv % (2 * p.unit_heads) == 0 && units >= 8LL * sms)
+    // (while they still fill the SMs twice over)
+    while (UNIT_WARPS > 1 && p.unit_heads < kUnitHeads && p.n_kv % (2 * p.unit_heads) == 0 &&
+           units * UNIT_WARPS / kWarps >= 8LL * sms)
       p.unit_heads *= 2, units /= 2;
     kv_blocks = (units + kWarps / UNIT_WARPS - 1) / (kWarps / UNIT_WARPS);
   }

@@ -182,7 +182,7 @@ struct AppendParams {
   const int* kv_lens;
   const int* cu;
   int total, n_seqs, n_kv, H, n_pages, max_len, n_pos, rot, interleaved, page_shift;
-  int unit_heads;           // heads of a unit of eight warps
+  int unit_heads;           // heads of a unit of several warps
   // Norms: the heads' weights [D], null: not normalised.
   const float* q_norm;
   const float* k_norm;
