@@ -28,10 +28,10 @@
 //
 // With a window (WIN) a unit's steps are the sinks' and, from its first row's
 // window on, the others; entries of pages between them read as no page.  4096
-// tokens in a window of 4096 behind 12288 (H 32/8, D 128): e4m3 315 us, 872
-// TFLOP/s, 16-bit pages 250, 1100.  A unit is 34 steps of 2.2 us here, and 8 us
+// tokens in a window of 4096 behind 12288 (H 32/8, D 128): e4m3 305 us, 902
+// TFLOP/s, 16-bit pages 249, 1105.  A unit is 34 steps of 2.1 us here, and 8 us
 // around them (queries 2.3, the first scores 0.9, the last products 1.2, output
-// 3.2), without its masked keys 7 us less in all; the join is 15.
+// 3.2), without its masked keys 7 us less in all; the join is 11.
 //
 // The steps of all units are divided equally over the CTAs (one an SM), the
 // two cut units of a CTA joined by a second kernel (sdpa_paged.cuh).  Every
@@ -320,19 +320,23 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* tile, 
 // it is not 1).
 // With N = 64 a row's other half is the partner thread's (lane ^ 16): both take
 // the same maximum, and l is this half's sum.
-template <bool E4M3, bool MBF, int N>
+// PAGE64: pages of 64 tokens and more, so that four groups have one page's scales,
+// read and multiplied once (chunks of prompts in a window 316 -> 305 us, without
+// 427 -> 416; every value is what it was).
+template <bool E4M3, bool MBF, int N, bool PAGE64>
 __device__ __forceinline__ float weights(float (&s)[N], float f, const float4* note, float& m, float& l,
                                          bool& need, uint32_t (&pk)[N / 2]) {
   float top = -INFINITY;
   // never zero: a removed score, an infinity, has to stay one
-  auto mul = [&](int g) { return fmaxf(f * note[g].x, 1.17549435e-38f); };
+  auto of = [&](int g) -> const float4& { return note[PAGE64 ? g / 4 * 4 : g]; };
+  auto mul = [&](int g) { return fmaxf(f * of(g).x, 1.17549435e-38f); };
   if constexpr (E4M3) {
 #pragma unroll
     for (int g = 0; g < N / 16; ++g) {
       const float* x = s + g * 16;
       const float a = max3f(x[0], x[1], x[2]), b = max3f(x[3], x[4], x[5]), c = max3f(x[6], x[7], x[8]);
       const float d = max3f(x[9], x[10], x[11]), e = max3f(x[12], x[13], x[14]);
-      top = fmaxf(top, fmaf(fmaxf(max3f(a, b, c), max3f(d, e, x[15])), mul(g), note[g].y));
+      top = fmaxf(top, fmaf(fmaxf(max3f(a, b, c), max3f(d, e, x[15])), mul(g), of(g).y));
     }
   } else {
     float e8[8];
@@ -358,7 +362,7 @@ __device__ __forceinline__ float weights(float (&s)[N], float f, const float4* n
   if constexpr (E4M3) {
 #pragma unroll
     for (int g = 0; g < N / 16; ++g) {
-      const float a = mul(g), b = note[g].y + neg_m;
+      const float a = mul(g), b = of(g).y + neg_m;
 #pragma unroll
       for (int c = 16 * g; c < 16 * g + 16; c += 2) fma2_bcast(s[c], s[c + 1], s[c], s[c + 1], a, b);
     }
@@ -379,7 +383,7 @@ __device__ __forceinline__ float weights(float (&s)[N], float f, const float4* n
         pk[e / 2] = pack2<MBF>(s[e], s[e + 1]);
       }
       add2_acc(r[0], r[1], r[2], r[3]);
-      l = fmaf(r[0] + r[1], note[g].z, l);
+      l = fmaf(r[0] + r[1], of(g).z, l);
     }
   } else {
     float rs[8];
@@ -557,7 +561,7 @@ __device__ __forceinline__ void mma_codes_x2(uint32_t d_tmem, uint32_t a_lo, uin
       : "memory");
 }
 
-template <int D, bool E4M3, bool BF16, bool HALF, bool WIN>
+template <int D, bool E4M3, bool BF16, bool HALF, bool WIN, bool PAGE64>
 __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v) {
@@ -773,7 +777,7 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
         }
         bool need;
         uint32_t pk[kPer / 2];
-        const float alpha = weights<E4M3, MBF, kPer>(x, f, notes + slot * kGroups + half * (kPer / 16), m, l, need, pk);
+        const float alpha = weights<E4M3, MBF, kPer, PAGE64>(x, f, notes + slot * kGroups + half * (kPer / 16), m, l, need, pk);
         if (mine > 0 && __any_sync(0xffffffffu, need)) {
           // the earlier products of this tile are complete: S of this step was
           // issued behind them (rolled, as whatever seldom runs)
@@ -1212,9 +1216,9 @@ __global__ void __launch_bounds__(Split<E4M3>::kThreads, 1)
   }
 }
 
-template <int D, bool E4M3, bool BF16, bool HALF, bool WIN>
+template <int D, bool E4M3, bool BF16, bool HALF, bool WIN, bool PAGE64>
 cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
-  auto kern = paged_tc_kernel<D, E4M3, BF16, HALF, WIN>;
+  auto kern = paged_tc_kernel<D, E4M3, BF16, HALF, WIN, PAGE64>;
   static std::atomic<uint64_t> configured{0};  // a bit a device
   const uint64_t bit = 1ull << p.device;
   cudaError_t e = cudaSuccess;
@@ -1247,8 +1251,11 @@ cudaError_t launch_one(const PagedParams& p, const CUtensorMap& tm_k, const CUte
 template <int D, bool HALF, bool WIN>
 cudaError_t launch_dim(const PagedParams& p, bool bf16, bool e4m3, const CUtensorMap& k, const CUtensorMap& v,
                        cudaStream_t s) {
-  if (e4m3) return bf16 ? launch_one<D, true, true, HALF, WIN>(p, k, v, s) : launch_one<D, true, false, HALF, WIN>(p, k, v, s);
-  return bf16 ? launch_one<D, false, true, HALF, WIN>(p, k, v, s) : launch_one<D, false, false, HALF, WIN>(p, k, v, s);
+  if (e4m3 && p.page_shift >= 6)
+    return bf16 ? launch_one<D, true, true, HALF, WIN, true>(p, k, v, s) : launch_one<D, true, false, HALF, WIN, true>(p, k, v, s);
+  if (e4m3)
+    return bf16 ? launch_one<D, true, true, HALF, WIN, false>(p, k, v, s) : launch_one<D, true, false, HALF, WIN, false>(p, k, v, s);
+  return bf16 ? launch_one<D, false, true, HALF, WIN, false>(p, k, v, s) : launch_one<D, false, false, HALF, WIN, false>(p, k, v, s);
 }
 template <bool WIN>
 cudaError_t launch_tile(const PagedParams& p, int head_dim, bool bf16, bool e4m3, int tile, const CUtensorMap& k,
