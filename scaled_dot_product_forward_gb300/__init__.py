@@ -2,7 +2,10 @@
 
 A thin ctypes binding over the C ABI declared in ``include/sdpa.h``: the
 Python functions carry the C names and only marshal arguments (pointers,
-shapes, strides, the current stream).  Every step of the computation runs in
+shapes, strides, the current stream).  The paged cache's operators, whose calls
+are as short as the host is quick, look at their arguments in a compiled module
+first (``_sdpa_binding``) and here only to name an error or for another stream or
+device.  Every step of the computation runs in
 the CUDA kernel of ``libsdpa_gb300.so``; there is no Python or CPU fallback,
 and importing this package fails loudly when the library is missing.
 
@@ -502,10 +505,8 @@ class SdpaPagedCache:
     sdpa_paged_forward; it owns no device memory of its own."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        global _torch
-        import torch
-
-        _torch = torch
+        _need_torch()
+        torch = _torch
         elem = {torch.bfloat16: SDPA_BF16, torch.float16: SDPA_FP16, torch.float8_e4m3fn: SDPA_CACHE_E4M3}.get(k.dtype)
         if elem is None or v.dtype != k.dtype:
             raise SdpaError(4, "SdpaPagedCache")
@@ -540,15 +541,22 @@ class SdpaPagedCache:
         self._workspace = {}   # bytes that a forward needs, by (query heads, rows)
 
 
-_torch = None      # set by the first SdpaPagedCache, or the first call below that comes without one
+# Set by the first SdpaPagedCache, or the first call below that comes without one.
+_torch = _native = None
 
 
 def _need_torch():
-    global _torch
-    if _torch is None:
+    global _torch, _native
+    if _native is None:
         import torch
 
         _torch = torch
+        if not os.path.exists(_build.BINDING_PATH):
+            raise ImportError(
+                f"{_build.BINDING_PATH} is missing: build it with scaled_dot_product_forward_gb300._build.build()")
+        from . import _sdpa_binding
+
+        _native = _sdpa_binding
 
 
 def _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, rows):
@@ -648,6 +656,11 @@ def sdpa_cache_append(cache, k, v, page_table, kv_lens, cu_seqlens=None, *, cos=
     perhaps) if it is allocated here, the queries as they were with
     ``q_out=q``."""
     where = "sdpa_cache_append"
+    if stream is None:
+        done = _native.append(cache._ref, cache.device, k, v, page_table, kv_lens, cu_seqlens, cos, sin, interleaved, q, q_out,
+                              q_norm, k_norm, eps)
+        if done is not NotImplemented:
+            return done
     n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens, k)
     dtype, shape = k.dtype, k.shape
     if v.dtype is not dtype or (q is not None and q.dtype is not dtype) or \
@@ -720,6 +733,10 @@ def sdpa_norm_rotate(q, k=None, positions=None, *, cos=None, sin=None, interleav
     the memory held where the outputs are allocated here)."""
     _need_torch()
     where = "sdpa_norm_rotate"
+    if stream is None:
+        done = _native.norm_rotate(q.get_device(), q, k, positions, cos, sin, interleaved, q_norm, k_norm, eps, q_out, k_out)
+        if done is not NotImplemented:
+            return done
     dtype, shape = q.dtype, q.shape
     dt = SDPA_BF16 if dtype is _torch.bfloat16 else SDPA_FP16 if dtype is _torch.float16 else -1
     if dt < 0 or any(t is not None and t.dtype is not dtype for t in (k, q_out, k_out)) or \
@@ -795,6 +812,12 @@ def sdpa_paged_forward(q, cache, page_table, kv_lens, cu_seqlens_q=None, max_seq
     an append left out too.)  The workspace is allocated from torch's pool for
     this call and stream."""
     where = "sdpa_paged_forward"
+    if stream is None:
+        done = _native.forward(cache._ref, cache.device, q, page_table, kv_lens, cu_seqlens_q,
+                               0 if cu_seqlens_q is None else max_seqlen_q, out, is_causal, 0 if window is None else window or -1,
+                               sinks, scale, return_lse, lse)
+        if done is not NotImplemented:
+            return done
     n_seqs, max_pages, dt = _paged_batch(where, cache, page_table, kv_lens, cu_seqlens_q, q)
     shape = q.shape
     if len(shape) != 3 or shape[2] != cache.head_dim or shape[1] % cache.n_kv_heads != 0:
@@ -910,8 +933,6 @@ def _int_table(where, device, t, rows=None):
 
 def _accounts(where, refs, page_table):
     """(device, number of pages, rows, columns, row stride)"""
-    if _torch is None:
-        _need_torch()
     if refs.dtype is not _torch.int32:
         raise SdpaError(4, where)
     if refs.dim() != 1:
@@ -930,6 +951,11 @@ def sdpa_pages_take(refs, page_table, from_lens, to_lens, page_size, *, stream=N
     reference in ``refs`` (int32 [n_pages]) then.  Returns ``missing``, int32
     [1]: pages that there were too few of (their entries are -1)."""
     where = "sdpa_pages_take"
+    _need_torch()
+    if stream is None:
+        done = _native.take(refs.get_device(), refs, page_table, from_lens, to_lens, page_size)
+        if done is not NotImplemented:
+            return done
     device, n_pages, rows, columns, stride = _accounts(where, refs, page_table)
     _int_vectors(where, device, rows, from_lens, to_lens)
     if device < 0:
@@ -955,6 +981,11 @@ def sdpa_pages_fork(refs, page_table, kv_lens, src, dst, page_size, new_table=No
     (in one table) another's src.  Returns PageCopies: what sdpa_cache_copy_pages
     has to copy in every layer's cache."""
     where = "sdpa_pages_fork"
+    _need_torch()
+    if stream is None:
+        done = _native.fork(refs.get_device(), refs, page_table, kv_lens, src, dst, page_size, new_table)
+        if done is not NotImplemented:
+            return PageCopies._make(done)
     device, n_pages, rows, columns, stride = _accounts(where, refs, page_table)
     new_rows, new_stride = rows, stride
     if new_table is not None:
@@ -991,6 +1022,10 @@ def sdpa_pages_release(refs, page_table, from_lens, to_lens, page_size, rows=Non
     each in ``refs``.  What a window leaves behind before the next token:
     from_lens = sinks, to_lens = kv_lens + 1 - window."""
     where = "sdpa_pages_release"
+    _need_torch()
+    if stream is None and _native.release(refs.get_device(), refs, page_table, from_lens, to_lens, page_size,
+                                          rows) is not NotImplemented:
+        return
     device, n_pages, n_rows, columns, stride = _accounts(where, refs, page_table)
     n = n_rows
     if rows is not None:
@@ -1017,6 +1052,8 @@ def sdpa_cache_copy_pages(cache, src, dst, rows=None, *, stream=None):
     src[i] to page dst[i] (int32 [n]), or of its first rows[i] tokens.  No page
     is dst twice, or dst and src; entries that are no pages do nothing."""
     where = "sdpa_cache_copy_pages"
+    if stream is None and _native.copy_pages(cache._ref, cache.device, src, dst, rows) is not NotImplemented:
+        return
     device = cache.device
     if src.dim() != 1:
         raise SdpaError(3, where)
@@ -1042,6 +1079,8 @@ def sdpa_cache_compact(cache, page_table, kept, new_table, kept_lens=None, *, st
     The new pages are none of those that are read.  Keys stay rotated by their
     old positions."""
     where = "sdpa_cache_compact"
+    if stream is None and _native.compact(cache._ref, cache.device, page_table, kept, new_table, kept_lens) is not NotImplemented:
+        return
     device = cache.device
     n_seqs, max_pages, stride = _int_table(where, device, page_table)
     _, max_kept, kept_stride = _int_table(where, device, kept, n_seqs)
