@@ -906,7 +906,7 @@ def _int_vectors(where, device, n, *vectors):
             continue
         if t.dtype is not i32:
             raise SdpaError(4, where)
-        if t.dim() != 1 or t.numel() != n:
+        if t.dim() != 1 or t.numel() != n or n < 1:
             raise SdpaError(3, where)
         if not t.is_contiguous():
             raise SdpaError(5, where)
@@ -921,7 +921,7 @@ def _int_table(where, device, t, rows=None):
     if t.dim() != 2:
         raise SdpaError(3, where)
     n_rows, columns = t.shape
-    if rows is not None and n_rows != rows:
+    if n_rows < 1 or columns < 1 or (rows is not None and n_rows != rows):
         raise SdpaError(3, where)
     stride, last = t.stride()
     if last != 1 and columns != 1:
@@ -935,7 +935,7 @@ def _accounts(where, refs, page_table):
     """(device, number of pages, rows, columns, row stride)"""
     if refs.dtype is not _torch.int32:
         raise SdpaError(4, where)
-    if refs.dim() != 1:
+    if refs.dim() != 1 or refs.numel() < 1:
         raise SdpaError(3, where)
     if not refs.is_contiguous():
         raise SdpaError(5, where)

@@ -561,6 +561,12 @@ def test_refusals():
     assert status(f, c, t, n, t) == SHAPE
     assert status(f, c, z(3, 4).t(), t, t) == LAYOUT
     assert status(f, c, t, t, t) == ARG
+    # nothing to do is a wrong shape
+    for g, args in ((sdpa.sdpa_pages_take, (z(0), t, n, n, 16)), (sdpa.sdpa_pages_take, (refs, z(0, 3), z(0), z(0), 16)),
+                    (sdpa.sdpa_pages_take, (refs, z(4, 0), n, n, 16)), (sdpa.sdpa_pages_fork, (refs, t, n, z(0), z(0), 16)),
+                    (sdpa.sdpa_pages_release, (refs, t, None, None, 16, z(0))), (sdpa.sdpa_cache_copy_pages, (c, z(0), z(0))),
+                    (f, (c, t, z(4, 0), t)), (f, (c, z(0, 3), z(0, 3), z(0, 3)))):
+        assert status(g, *args) == SHAPE
 
 
 def test_refusals_of_the_c_entries():
