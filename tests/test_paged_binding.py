@@ -145,3 +145,38 @@ def test_refusals_on_the_device(sdpa_lib):
         with pytest.raises(lib.SdpaError) as e:
             f(*args, **kw)
         assert e.value.status == status, (f.__name__, status, e.value.status)
+
+
+def test_two_streams_at_once(sdpa_lib):
+    """Calls that run beside each other share nothing: attention (a workspace each), norms, moves of other pages."""
+    lib = sdpa_lib
+    g = torch.Generator().manual_seed(7)
+    n_pages, P = 400, 16
+    c = make_cache(lib, n_pages, P, 2, 128, "e4m3", torch.bfloat16, 4)
+    lens = i32([1500, 700, 1, 40])
+    tabs = [tables(4, 94, n_pages, s).cuda() for s in (1, 2)]
+    qs = [torch.randn(4, 8, 128, generator=g).bfloat16().cuda() for _ in range(2)]
+    many = [torch.randn(200, 8, 128, generator=g).bfloat16().cuda() for _ in range(2)]
+    cu = i32([0, 90, 91, 92, 200])
+    moved = [make_cache(lib, 40, P, 2, 128, "e4m3", torch.bfloat16, 4) for _ in range(2)]
+    w = torch.rand(128, generator=g).cuda()
+
+    def work(i):
+        lib.sdpa_cache_copy_pages(moved[i], i32([1, 2, 3]), i32([11, 12, 13]))
+        lib.sdpa_cache_compact(moved[i], i32([[11, 12]]), i32([list(range(1, 32, 2))]), i32([[20]]))
+        return [lib.sdpa_paged_forward(qs[i], c, tabs[i], lens, is_causal=True, window=300, sinks=4),
+                lib.sdpa_paged_forward(many[i], c, tabs[i], lens, cu, 108, is_causal=True, window=100, sinks=20),
+                lib.sdpa_norm_rotate(many[i], q_norm=w)[0], moved[i].k[20].view(torch.uint8).clone()]
+
+    want = [work(0), work(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(work(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for x in got[i]:
+            same(x, want[i])
