@@ -6,6 +6,9 @@
 // current device and stream, and answers Py_NotImplemented for everything that is
 // not plainly in order (another device, a wrong type, shape or layout, a status of
 // the C entry): the Python function then looks itself and names the error.
+//
+// Other Python threads run while a call allocates and launches, either of which may
+// wait: for memory, for room in a full queue, for a kernel to be loaded.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -23,6 +26,17 @@ namespace {
 
 #define NEED(condition) \
   if (!(condition)) Py_RETURN_NOTIMPLEMENTED
+
+// Gives the interpreter's lock up for as long as it lives (an exception takes it back
+// on its way out).  What it spans touches no Python object; the arguments' tensors
+// stay, the caller holds them.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 // The call's arguments, in order.
 struct Args {
@@ -139,21 +153,24 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const int64_t seqs = tab->size(0), total = k->size(0);
   NEED(ints(lens, seqs) && (!cu || ints(cu, seqs + 1)));
   NEED((!qn || floats(qn, cache->head_dim)) && (!kn || floats(kn, cache->head_dim)));
+  NEED(!q || (rows(q, type) && q->size(0) == total && q->size(2) == cache->head_dim));
+  NEED(!q_out || (rows(q_out, type) && q_out->sizes() == q->sizes()));
   at::Tensor made;
-  if (q) {
-    NEED(rows(q, type) && q->size(0) == total && q->size(2) == cache->head_dim);
-    if (!q_out) {
+  sdpa_status status;
+  {
+    Unlocked others;
+    if (q && !q_out) {
       made = at::empty(q->sizes(), q->options());
       q_out = &made;
     }
-    NEED(rows(q_out, type) && q_out->sizes() == q->sizes());
+    const int64_t ks[2] = {k->stride(0), k->stride(1)}, vs[2] = {v->stride(0), v->stride(1)};
+    const int64_t qs[2] = {q ? q->stride(0) : 0, q ? q->stride(1) : 0}, os[2] = {q ? q_out->stride(0) : 0, q ? q_out->stride(1) : 0};
+    status = sdpa_cache_append_norm(cache, k->data_ptr(), v->data_ptr(), dt, total, ks, vs, as<int32_t>(tab), tab->stride(0), tab->size(1),
+                                    as<int32_t>(lens), as<int32_t>(cu), seqs, as<float>(cos), as<float>(sin), cos ? cos->size(0) : 0,
+                                    cos ? 2 * cos->size(1) : 0, interleaved, at_or_null(q), at_or_null(q_out), q ? q->size(1) : 0, qs, os,
+                                    as<float>(qn), as<float>(kn), eps, stream(a.device));
   }
-  const int64_t ks[2] = {k->stride(0), k->stride(1)}, vs[2] = {v->stride(0), v->stride(1)};
-  const int64_t qs[2] = {q ? q->stride(0) : 0, q ? q->stride(1) : 0}, os[2] = {q ? q_out->stride(0) : 0, q ? q_out->stride(1) : 0};
-  NEED(sdpa_cache_append_norm(cache, k->data_ptr(), v->data_ptr(), dt, total, ks, vs, as<int32_t>(tab), tab->stride(0), tab->size(1),
-                              as<int32_t>(lens), as<int32_t>(cu), seqs, as<float>(cos), as<float>(sin), cos ? cos->size(0) : 0,
-                              cos ? 2 * cos->size(1) : 0, interleaved, at_or_null(q), at_or_null(q_out), q ? q->size(1) : 0, qs, os,
-                              as<float>(qn), as<float>(kn), eps, stream(a.device)) == SDPA_OK);
+  NEED(status == SDPA_OK);
   if (!q) Py_RETURN_NONE;
   return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(args[11]);
   END_HANDLE_TH_ERRORS
@@ -186,27 +203,32 @@ PyObject* forward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (most > total) most = total;
   const uint64_t size = sdpa_paged_workspace_bytes(cache->head_dim, heads, cache->n_kv_heads, most);
   NEED(size != 0);
-  at::Tensor made, made_lse;
-  if (!out) {
-    made = at::empty(q->sizes(), q->options());
-    out = &made;
-  }
-  NEED(rows(out, type) && out->sizes() == q->sizes());
-  if (!lse && return_lse) {
-    made_lse = at::empty({total, heads}, q->options().dtype(at::kFloat));
-    lse = &made_lse;
-  }
+  NEED(!out || (rows(out, type) && out->sizes() == q->sizes()));
   NEED(!lse || (lse->scalar_type() == at::kFloat && lse->dim() == 2 && lse->size(0) == total && lse->size(1) == heads));
-  const at::Tensor work = at::empty({static_cast<int64_t>(size)}, q->options().dtype(at::kByte));
-  const int64_t qs[2] = {q->stride(0), q->stride(1)}, os[2] = {out->stride(0), out->stride(1)};
-  const int64_t ls[2] = {lse ? lse->stride(0) : 0, lse ? lse->stride(1) : 0};
-  void* const st = stream(a.device);
-  NEED((window == 0 ? sdpa_paged_forward(q->data_ptr(), out->data_ptr(), as<float>(lse), dt, cache, total, heads, qs, os, ls,
-                                         as<int32_t>(tab), tab->stride(0), tab->size(1), as<int32_t>(lens), as<int32_t>(cu), seqs, most,
-                                         causal, scale, work.data_ptr(), size, st)
-                    : sdpa_paged_forward_window(q->data_ptr(), out->data_ptr(), as<float>(lse), dt, cache, total, heads, qs, os, ls,
-                                                as<int32_t>(tab), tab->stride(0), tab->size(1), as<int32_t>(lens), as<int32_t>(cu), seqs,
-                                                most, window, sinks, scale, work.data_ptr(), size, st)) == SDPA_OK);
+  at::Tensor made, made_lse;
+  sdpa_status status;
+  {
+    Unlocked others;
+    if (!out) {
+      made = at::empty(q->sizes(), q->options());
+      out = &made;
+    }
+    if (!lse && return_lse) {
+      made_lse = at::empty({total, heads}, q->options().dtype(at::kFloat));
+      lse = &made_lse;
+    }
+    const at::Tensor work = at::empty({static_cast<int64_t>(size)}, q->options().dtype(at::kByte));
+    const int64_t qs[2] = {q->stride(0), q->stride(1)}, os[2] = {out->stride(0), out->stride(1)};
+    const int64_t ls[2] = {lse ? lse->stride(0) : 0, lse ? lse->stride(1) : 0};
+    void* const st = stream(a.device);
+    status = window == 0 ? sdpa_paged_forward(q->data_ptr(), out->data_ptr(), as<float>(lse), dt, cache, total, heads, qs, os, ls,
+                                              as<int32_t>(tab), tab->stride(0), tab->size(1), as<int32_t>(lens), as<int32_t>(cu), seqs,
+                                              most, causal, scale, work.data_ptr(), size, st)
+                         : sdpa_paged_forward_window(q->data_ptr(), out->data_ptr(), as<float>(lse), dt, cache, total, heads, qs, os, ls,
+                                                     as<int32_t>(tab), tab->stride(0), tab->size(1), as<int32_t>(lens), as<int32_t>(cu),
+                                                     seqs, most, window, sinks, scale, work.data_ptr(), size, st);
+  }
+  NEED(status == SDPA_OK);
   PyObject* o = made.defined() ? THPVariable_Wrap(made) : Py_NewRef(args[7]);
   if (!lse) return o;
   PyObject* l = made_lse.defined() ? THPVariable_Wrap(made_lse) : Py_NewRef(args[13]);
@@ -234,21 +256,27 @@ PyObject* norm_rotate(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const int64_t total = q->size(0), dim = q->size(2);
   NEED((!k || (k->size(0) == total && k->size(2) == dim)) && (!pos || ints(pos, total)));
   NEED((!qn || floats(qn, dim)) && (!kn || floats(kn, dim)));
+  NEED(!q_out || (rows(q_out, type) && q_out->sizes() == q->sizes()));
+  NEED(!k_out || (rows(k_out, type) && k_out->sizes() == k->sizes()));
   at::Tensor made_q, made_k;
-  if (!q_out) {
-    made_q = at::empty(q->sizes(), q->options());
-    q_out = &made_q;
+  sdpa_status status;
+  {
+    Unlocked others;
+    if (!q_out) {
+      made_q = at::empty(q->sizes(), q->options());
+      q_out = &made_q;
+    }
+    if (k && !k_out) {
+      made_k = at::empty(k->sizes(), k->options());
+      k_out = &made_k;
+    }
+    const int64_t qs[2] = {q->stride(0), q->stride(1)}, qos[2] = {q_out->stride(0), q_out->stride(1)};
+    const int64_t ks[2] = {k ? k->stride(0) : 0, k ? k->stride(1) : 0}, kos[2] = {k ? k_out->stride(0) : 0, k ? k_out->stride(1) : 0};
+    status = sdpa_norm_rotate(q->data_ptr(), q_out->data_ptr(), q->size(1), qs, qos, at_or_null(k), at_or_null(k_out), k ? k->size(1) : 0,
+                              ks, kos, dt, total, dim, as<int32_t>(pos), as<float>(cos), as<float>(sin), cos ? cos->size(0) : 0,
+                              cos ? 2 * cos->size(1) : 0, interleaved, as<float>(qn), as<float>(kn), eps, stream(a.device));
   }
-  if (k && !k_out) {
-    made_k = at::empty(k->sizes(), k->options());
-    k_out = &made_k;
-  }
-  NEED(rows(q_out, type) && q_out->sizes() == q->sizes() && (!k || (rows(k_out, type) && k_out->sizes() == k->sizes())));
-  const int64_t qs[2] = {q->stride(0), q->stride(1)}, qos[2] = {q_out->stride(0), q_out->stride(1)};
-  const int64_t ks[2] = {k ? k->stride(0) : 0, k ? k->stride(1) : 0}, kos[2] = {k ? k_out->stride(0) : 0, k ? k_out->stride(1) : 0};
-  NEED(sdpa_norm_rotate(q->data_ptr(), q_out->data_ptr(), q->size(1), qs, qos, at_or_null(k), at_or_null(k_out), k ? k->size(1) : 0, ks,
-                        kos, dt, total, dim, as<int32_t>(pos), as<float>(cos), as<float>(sin), cos ? cos->size(0) : 0,
-                        cos ? 2 * cos->size(1) : 0, interleaved, as<float>(qn), as<float>(kn), eps, stream(a.device)) == SDPA_OK);
+  NEED(status == SDPA_OK);
   PyObject* o = made_q.defined() ? THPVariable_Wrap(made_q) : Py_NewRef(args[10]);
   PyObject* l = made_k.defined() ? THPVariable_Wrap(made_k) : Py_NewRef(k ? args[11] : Py_None);
   PyObject* both = PyTuple_Pack(2, o, l);
@@ -270,9 +298,15 @@ PyObject* take(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const at::Tensor *refs = a.required(), *tab = a.required(), *lo = a.required(), *hi = a.required();
   const int64_t P = a.integer();
   NEED(a.all() && accounts(refs, tab) && ints(lo, tab->size(0)) && ints(hi, tab->size(0)));
-  const at::Tensor missing = vector_of(*refs, 1);
-  NEED(sdpa_pages_take(as<int32_t>(refs), refs->size(0), as<int32_t>(tab), tab->stride(0), tab->size(0), tab->size(1), P, as<int32_t>(lo),
-                       as<int32_t>(hi), as<int32_t>(&missing), stream(a.device)) == SDPA_OK);
+  at::Tensor missing;
+  sdpa_status status;
+  {
+    Unlocked others;
+    missing = vector_of(*refs, 1);
+    status = sdpa_pages_take(as<int32_t>(refs), refs->size(0), as<int32_t>(tab), tab->stride(0), tab->size(0), tab->size(1), P,
+                             as<int32_t>(lo), as<int32_t>(hi), as<int32_t>(&missing), stream(a.device));
+  }
+  NEED(status == SDPA_OK);
   return THPVariable_Wrap(missing);
   END_HANDLE_TH_ERRORS
 }
@@ -289,10 +323,17 @@ PyObject* fork_rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!to) to = tab;
   const int64_t pairs = src->size(0);
   NEED(ints(src, pairs) && ints(dst, pairs) && table(to) && to->size(1) == tab->size(1));
-  const at::Tensor made[4] = {vector_of(*refs, pairs), vector_of(*refs, pairs), vector_of(*refs, pairs), vector_of(*refs, 1)};
-  NEED(sdpa_pages_fork(as<int32_t>(refs), refs->size(0), as<int32_t>(tab), tab->stride(0), tab->size(0), as<int32_t>(to), to->stride(0),
-                       to->size(0), tab->size(1), P, as<int32_t>(lens), as<int32_t>(src), as<int32_t>(dst), pairs, as<int32_t>(&made[0]),
-                       as<int32_t>(&made[1]), as<int32_t>(&made[2]), as<int32_t>(&made[3]), stream(a.device)) == SDPA_OK);
+  at::Tensor made[4];
+  sdpa_status status;
+  {
+    Unlocked others;
+    for (int i = 0; i < 4; ++i) made[i] = vector_of(*refs, i < 3 ? pairs : 1);
+    status = sdpa_pages_fork(as<int32_t>(refs), refs->size(0), as<int32_t>(tab), tab->stride(0), tab->size(0), as<int32_t>(to),
+                             to->stride(0), to->size(0), tab->size(1), P, as<int32_t>(lens), as<int32_t>(src), as<int32_t>(dst), pairs,
+                             as<int32_t>(&made[0]), as<int32_t>(&made[1]), as<int32_t>(&made[2]), as<int32_t>(&made[3]),
+                             stream(a.device));
+  }
+  NEED(status == SDPA_OK);
   PyObject* four = PyTuple_New(4);
   for (int i = 0; four && i < 4; ++i) PyTuple_SET_ITEM(four, i, THPVariable_Wrap(made[i]));
   return four;
@@ -310,8 +351,13 @@ PyObject* release(PyObject*, PyObject* const* args, Py_ssize_t n) {
   NEED(a.all() && accounts(refs, tab) && (!which || which->dim() == 1));
   const int64_t count = which ? which->size(0) : tab->size(0);
   NEED((!which || ints(which, count)) && (!lo || ints(lo, count)) && (!hi || ints(hi, count)));
-  NEED(sdpa_pages_release(as<int32_t>(refs), refs->size(0), as<int32_t>(tab), tab->stride(0), tab->size(0), tab->size(1), P,
-                          as<int32_t>(which), as<int32_t>(lo), as<int32_t>(hi), count, stream(a.device)) == SDPA_OK);
+  sdpa_status status;
+  {
+    Unlocked others;
+    status = sdpa_pages_release(as<int32_t>(refs), refs->size(0), as<int32_t>(tab), tab->stride(0), tab->size(0), tab->size(1), P,
+                                as<int32_t>(which), as<int32_t>(lo), as<int32_t>(hi), count, stream(a.device));
+  }
+  NEED(status == SDPA_OK);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -326,7 +372,12 @@ PyObject* copy_pages(PyObject*, PyObject* const* args, Py_ssize_t n) {
   NEED(a.all() && src->dim() == 1);
   const int64_t count = src->size(0);
   NEED(ints(src, count) && ints(dst, count) && (!part || ints(part, count)));
-  NEED(sdpa_cache_copy_pages(cache, as<int32_t>(src), as<int32_t>(dst), as<int32_t>(part), count, stream(a.device)) == SDPA_OK);
+  sdpa_status status;
+  {
+    Unlocked others;
+    status = sdpa_cache_copy_pages(cache, as<int32_t>(src), as<int32_t>(dst), as<int32_t>(part), count, stream(a.device));
+  }
+  NEED(status == SDPA_OK);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -341,8 +392,13 @@ PyObject* compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
   NEED(a.all() && table(tab) && table(kept) && table(to));
   const int64_t seqs = tab->size(0);
   NEED(kept->size(0) == seqs && to->size(0) == seqs && (!lens || ints(lens, seqs)));
-  NEED(sdpa_cache_compact(cache, as<int32_t>(tab), tab->stride(0), tab->size(1), as<int32_t>(kept), kept->stride(0), kept->size(1),
-                          as<int32_t>(lens), as<int32_t>(to), to->stride(0), to->size(1), seqs, stream(a.device)) == SDPA_OK);
+  sdpa_status status;
+  {
+    Unlocked others;
+    status = sdpa_cache_compact(cache, as<int32_t>(tab), tab->stride(0), tab->size(1), as<int32_t>(kept), kept->stride(0), kept->size(1),
+                                as<int32_t>(lens), as<int32_t>(to), to->stride(0), to->size(1), seqs, stream(a.device));
+  }
+  NEED(status == SDPA_OK);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
