@@ -4,7 +4,8 @@
 unit is compiled by its own nvcc process, in parallel, for exactly one target:
 ``-gencode arch=compute_103a,code=sm_103a``.  Then ``_sdpa_binding.so``, the
 paged operators' binding on torch tensors (g++ with torch's headers; its
-compilation runs beside the others).
+compilation runs beside the others).  The library, a C ABI, needs no torch:
+where there is none, it is all that is built.
 """
 from __future__ import annotations
 
@@ -39,9 +40,18 @@ def _nvcc() -> str:
 
 
 def _inputs():
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    """Sources of the library (the header last)."""
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING_SOURCE]
     deps.append(os.path.join(INCLUDE, "sdpa.h"))
     return deps
+
+
+def _have_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
 
 
 def _binding_commands(obj: str, out: str):
@@ -59,49 +69,69 @@ def _binding_commands(obj: str, out: str):
              "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
 
 
+def _newer(built: str, inputs) -> bool:
+    return os.path.exists(built) and all(os.path.getmtime(d) <= os.path.getmtime(built) for d in inputs)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB_PATH, _inputs())
+
+
+def _binding_up_to_date() -> bool:
+    return _newer(BINDING_PATH, [os.path.join(CSRC, BINDING_SOURCE), os.path.join(INCLUDE, "sdpa.h")])
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(d) <= t for d in _inputs())
+    return _library_up_to_date() and (not _have_torch() or _binding_up_to_date())
+
+
+def _finish(proc, cmd, what: str) -> None:
+    out, _ = proc.communicate()
+    if proc.returncode != 0:
+        raise RuntimeError(f"{what} failed ({' '.join(cmd)}):\n{out.decode()}")
+
+
+def _start(cmd, verbose: bool):
+    if verbose:
+        print(" ".join(cmd))
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _install(made: str, path: str) -> None:
+    shutil.copyfile(made, path + ".tmp")
+    os.replace(path + ".tmp", path)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build ``libsdpa_gb300.so`` and the binding if any source is newer; return the library's path."""
-    if not force and up_to_date():
+    """Build ``libsdpa_gb300.so`` and, with torch, the binding, each if one of its
+    sources is newer; return the library's path."""
+    library = force or not _library_up_to_date()
+    binding = _have_torch() and (force or not _binding_up_to_date())
+    if not library and not binding:
         return LIB_PATH
-    nvcc = _nvcc()
     with tempfile.TemporaryDirectory(prefix="sdpa_build_") as tmp:
         procs, objs = [], []
-        binding, link_binding = _binding_commands(os.path.join(tmp, "binding.o"), os.path.join(tmp, "binding.so"))
-        binding_proc = subprocess.Popen(binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-        for src in SOURCES:
-            obj = os.path.join(tmp, os.path.splitext(src)[0] + ".o")
-            cmd = [nvcc, *GENCODE, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
-            if verbose:
-                print(" ".join(cmd))
-            procs.append((subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                           stderr=subprocess.STDOUT), cmd))
-            objs.append(obj)
-        for p, cmd in procs:
-            out, _ = p.communicate()
-            if p.returncode != 0:
-                raise RuntimeError(f"nvcc failed ({' '.join(cmd)}):\n{out.decode()}")
-        tmp_lib = os.path.join(tmp, LIB_NAME)
-        link = [nvcc, *GENCODE, "-shared", "-o", tmp_lib, *objs]
-        r = subprocess.run(link, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
-        shutil.copyfile(tmp_lib, LIB_PATH + ".tmp")
-        os.replace(LIB_PATH + ".tmp", LIB_PATH)
-        out, _ = binding_proc.communicate()
-        if binding_proc.returncode != 0:
-            raise RuntimeError(f"g++ failed ({' '.join(binding)}):\n{out.decode()}")
-        r = subprocess.run(link_binding, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
-        shutil.copyfile(os.path.join(tmp, "binding.so"), BINDING_PATH + ".tmp")
-        os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+        if binding:
+            made = os.path.join(tmp, "binding.so")
+            compile_binding, link_binding = _binding_commands(os.path.join(tmp, "binding.o"), made)
+            binding_proc = _start(compile_binding, verbose)
+        if library:
+            nvcc = _nvcc()
+            for src in SOURCES:
+                obj = os.path.join(tmp, os.path.splitext(src)[0] + ".o")
+                cmd = [nvcc, *GENCODE, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
+                procs.append((_start(cmd, verbose), cmd))
+                objs.append(obj)
+            for p, cmd in procs:
+                _finish(p, cmd, "nvcc")
+            tmp_lib = os.path.join(tmp, LIB_NAME)
+            link = [nvcc, *GENCODE, "-shared", "-o", tmp_lib, *objs]
+            _finish(_start(link, verbose), link, "link")
+            _install(tmp_lib, LIB_PATH)
+        if binding:
+            _finish(binding_proc, compile_binding, "g++")
+            _finish(_start(link_binding, verbose), link_binding, "link")
+            _install(made, BINDING_PATH)
     return LIB_PATH
 
 
