@@ -554,6 +554,10 @@ def _need_torch():
         if not os.path.exists(_build.BINDING_PATH):
             raise ImportError(
                 f"{_build.BINDING_PATH} is missing: build it with scaled_dot_product_forward_gb300._build.build()")
+        key, built_for = _build.binding_key(), _build.binding_built_for()
+        if built_for != key:
+            raise ImportError(f"{_build.BINDING_PATH} was built for {built_for or 'something that it does not say'}, and this is "
+                              f"{key}: build it again with scaled_dot_product_forward_gb300._build.build()")
         from . import _sdpa_binding
 
         _native = _sdpa_binding

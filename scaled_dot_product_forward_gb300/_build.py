@@ -54,6 +54,28 @@ def _have_torch() -> bool:
     return True
 
 
+def binding_key() -> str:
+    """What a binding belongs to: its code reads torch's and Python's objects as the headers lay them out."""
+    import torch
+
+    # (the suffix names Python's version and the machine)
+    return (f"{sysconfig.get_config_var('EXT_SUFFIX')}, torch {torch.__version__} {torch.version.git_version}, C++ ABI "
+            f"{int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
+def binding_key_path() -> str:
+    return BINDING_PATH + ".built_for"
+
+
+def binding_built_for() -> str | None:
+    """The key of the binding that is there (None: it does not say)."""
+    try:
+        with open(binding_key_path(), encoding="utf-8") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def _binding_commands(obj: str, out: str):
     """Compiler and linker commands of the binding."""
     import torch
@@ -78,7 +100,8 @@ def _library_up_to_date() -> bool:
 
 
 def _binding_up_to_date() -> bool:
-    return _newer(BINDING_PATH, [os.path.join(CSRC, BINDING_SOURCE), os.path.join(INCLUDE, "sdpa.h")])
+    return binding_built_for() == binding_key() and \
+        _newer(BINDING_PATH, [os.path.join(CSRC, BINDING_SOURCE), os.path.join(INCLUDE, "sdpa.h")])
 
 
 def up_to_date() -> bool:
@@ -104,7 +127,8 @@ def _install(made: str, path: str) -> None:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Build ``libsdpa_gb300.so`` and, with torch, the binding, each if one of its
-    sources is newer; return the library's path."""
+    sources is newer (the binding also if it belongs to another torch or Python);
+    return the library's path."""
     library = force or not _library_up_to_date()
     binding = _have_torch() and (force or not _binding_up_to_date())
     if not library and not binding:
@@ -131,7 +155,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if binding:
             _finish(binding_proc, compile_binding, "g++")
             _finish(_start(link_binding, verbose), link_binding, "link")
+            key = os.path.join(tmp, "key")
+            with open(key, "w", encoding="utf-8") as f:
+                f.write(binding_key())
+            # (one that is cut short here says nothing, and is made again)
+            if os.path.exists(binding_key_path()):
+                os.unlink(binding_key_path())
             _install(made, BINDING_PATH)
+            _install(key, binding_key_path())
     return LIB_PATH
 
 

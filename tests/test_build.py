@@ -81,3 +81,37 @@ def test_a_failed_compiler_is_named(compilers, tmp_path):
     with pytest.raises(RuntimeError, match="nvcc failed(.|\n)*no such thing"):
         _build.build()
     assert not os.path.exists(_build.LIB_PATH) and not os.path.exists(_build.BINDING_PATH)
+
+
+@pytest.fixture
+def torch():
+    return pytest.importorskip("torch")
+
+
+def test_a_binding_of_another_torch_is_built_again(compilers, torch, monkeypatch):
+    _build.build()
+    compilers()
+    with monkeypatch.context() as other:
+        other.setattr(torch, "__version__", "0.0.1+other")
+        assert not _build.up_to_date()
+        _build.build()
+        assert compilers() == BINDING and _build.up_to_date()
+    assert not _build.up_to_date()      # (made for that one now)
+    _build.build()
+    assert compilers() == BINDING and _build.up_to_date()
+    # one that does not say what it was made for
+    os.unlink(_build.binding_key_path())
+    assert not _build.up_to_date()
+
+
+def test_a_binding_of_another_torch_is_not_loaded(torch, monkeypatch):
+    import scaled_dot_product_forward_gb300 as sdpa
+    _build.build()
+    monkeypatch.setattr(sdpa, "_native", None)
+    with monkeypatch.context() as other:
+        other.setattr(torch, "__version__", "0.0.1+other")
+        with pytest.raises(ImportError, match="built for .*torch.*build it again"):
+            sdpa.SdpaPagedCache(None, None)
+        assert sdpa._native is None
+    sdpa._need_torch()
+    assert sdpa._native is not None
