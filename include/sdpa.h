@@ -649,12 +649,21 @@ SDPA_API sdpa_status sdpa_cache_copy_pages(const sdpa_paged_cache* cache, const 
  * ones (page_table).  Keys stay as they are, rotated by their old positions.  One
  * kernel launch, asynchronous.
  *
+ * From now on a sequence's length in the cache (kv_lens) is not its length in the
+ * text, and sdpa_cache_append takes a token's position from the first: keys that it
+ * rotated would be at wrong distances from the kept ones.  New tokens' keys and
+ * queries are rotated before (and normalised), by sdpa_norm_rotate with their
+ * positions in the text, and appended without tables and norms; the keys are then
+ * rounded to `dtype` on the way to an SDPA_CACHE_E4M3 cache.  A causal limit or a
+ * window counts places in the cache, not positions.
+ *
  * page_table   : DEVICE int32 [n_seqs, max_pages], row stride page_table_stride.
  * kept         : DEVICE int32 [n_seqs, max_kept], row stride kept_stride; any
  *                positions in any order.
  * kept_lens    : DEVICE int32 [n_seqs], limited to [0, max_kept], or NULL: max_kept each.
  * new_table    : DEVICE int32 [n_seqs, new_max_pages].  The pages with new tokens are
- *                none of those that are read, and no two entries name one.
+ *                none of those that are read, and no two entries name one.  Kept
+ *                tokens from new_max_pages * page_size on are left out.
  *
  * SDPA_CACHE_E4M3: the scale of a new (page, head) is the largest of those that its
  * tokens' old pages have, and codes that came under a smaller one are multiplied

@@ -1080,8 +1080,11 @@ def sdpa_cache_compact(cache, page_table, kept, new_table, kept_lens=None, *, st
     sequence b in the pages new_table[b] is the one at position kept[b, i] in the
     pages page_table[b], for i < kept_lens[b] (None: all of kept's row).
     page_table, kept, new_table: int32 [n_seqs, ..]; kept_lens: int32 [n_seqs].
-    The new pages are none of those that are read.  Keys stay rotated by their
-    old positions."""
+    The new pages are none of those that are read; kept tokens that they have no
+    room for are left out.  Keys stay rotated by their old positions, and
+    sdpa_cache_append would rotate later tokens by their places in the cache:
+    rotate (and normalise) those with sdpa_norm_rotate and their positions in the
+    text, and append them without ``cos``, ``sin`` and norms."""
     where = "sdpa_cache_compact"
     if stream is None and _native.compact(cache._ref, cache.device, page_table, kept, new_table, kept_lens) is not NotImplemented:
         return
