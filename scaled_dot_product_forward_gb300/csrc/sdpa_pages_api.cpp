@@ -145,8 +145,8 @@ sdpa_status sdpa_cache_compact(const sdpa_paged_cache* cache, const int32_t* pag
   sdpa_impl::CompactPagesParams p;
   std::memset(&p, 0, sizeof(p));
   p.c = page_bytes(cache);
-  // a block takes as many heads as make 64 KB of a full page, at most 16 (8 x 8192 of
-  // 16384 tokens, us: 16 KB 49.7, its look at the lists weighs more; 32 KB 42.7; 64 KB 41.9)
+  // a block takes as many heads as make 64 KB of a full page, at most 16 (8 x about
+  // 7400 of 16384 tokens, us: 16 KB 49.7, its look at the lists weighs more; 32 KB 42.7; 64 KB 41.9)
   const int64_t head_bytes = cache->page_size << (p.c.row_shift + 4);
   while (p.unit_shift < 4 && (int64_t(1) << p.unit_shift) < cache->n_kv_heads && (head_bytes << p.unit_shift) < 65536)
     ++p.unit_shift;

@@ -114,8 +114,8 @@ __device__ __forceinline__ void copy_16(uint32_t to, const void* from) {
 // Bound by latency before memory: a row's place is behind two lists (a third for
 // its scale), so what counts is that much is asked for at once.  The lists are
 // read together, then eight pieces a thread go to shared memory by asynchronous
-// copies, while the scales are compared.  8 x 8192 of 16384 tokens, 8 heads of 128
-// codes: 42 us, 5.8 TB/s (47 with a batch of pieces in registers; without any
+// copies, while the scales are compared.  8 x about 7400 of 16384 tokens, 8 heads of
+// 128 codes: 42 us, 5.8 TB/s (47 with a batch of pieces in registers; without any
 // conversion the same).
 constexpr int kMove = 8;        // pieces of a thread at a time
 struct CompactSmem {
